@@ -15,7 +15,9 @@
  * (moe_expand_cast_fp8_ex, swiglu_cast_fp8_ex), the FP4 E2M1 casts
  * (moe_expand_cast_fp4, swiglu_cast_fp4), steps 1-3 in one call with a fused
  * decode launch (moe_route_expand_cast_fp8), and the route map without a
- * workspace (moe_route_map_noalloc).
+ * workspace (moe_route_map_noalloc); and the operators around the routed
+ * experts (moe_block_norm, moe_balance_loss and moe_combine's gradient, with
+ * their backward passes, and moe_expert_matvec_fp4).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -484,6 +486,206 @@ moe_status_t moe_route_expand_cast_fp8(const float *scores, int64_t num_tokens,
 /* 256 + moe_route_map_workspace_bytes(T, E, k). */
 size_t moe_route_expand_cast_fp8_workspace_bytes(int64_t num_tokens, int32_t num_experts,
                                                  int32_t num_topk);
+
+/*
+ * ------------------------------------------------------------------------
+ * The operators around the routed experts: the block's norms with its gate and
+ * residual scale, the router's balance loss with its gradient, the combine's
+ * gradient, and the experts' products with 4-bit weights for decode batches.
+ * They have no counterpart on the pages; the formulas are given in full here.
+ * The conventions above hold, with one widening: where a float argument says
+ * "-inf allowed", -inf is an ordinary value.
+ * ------------------------------------------------------------------------
+ */
+
+/* Element types of the norms' tensors, and of the combine's gradient. */
+typedef enum moe_dtype {
+    MOE_DT_BF16 = 0,
+    MOE_DT_F32 = 1
+} moe_dtype_t;
+
+/* Shape of the block's gate, and what is applied to it first. */
+#define MOE_GATE_NONE 0     /* no gate: g = 1                                 */
+#define MOE_GATE_CHANNEL 1  /* [H] f32: one value per channel                 */
+#define MOE_GATE_TOKEN 2    /* [T] f32: one value per token                   */
+#define MOE_GATE_ELEMENT 3  /* [T, H] in the block's type                     */
+#define MOE_GATE_ACT_NONE 0
+#define MOE_GATE_ACT_SIGMOID 1 /* g = 1 / (1 + exp(-gate))                    */
+
+/* Largest hidden size of the norms. */
+#define MOE_NORM_MAX_HIDDEN 16384
+
+/*
+ * moe_block_norm -- the norms before and after a block, in one pass:
+ *   rstd_post[t] = 1 / sqrt(mean_c y[t,c]^2 + eps)
+ *   z[t,c] = y[t,c] * rstd_post[t] * post_weight[c]     (post_weight NULL: z = y)
+ *   h[t,c] = residual[t,c] + scale * g[t,c] * z[t,c]    (y NULL: h = residual)
+ *   rstd_pre[t] = 1 / sqrt(mean_c h[t,c]^2 + eps)
+ *   n[t,c] = h[t,c] * rstd_pre[t] * pre_weight[c]       (pre_weight NULL: no n)
+ * h is rounded to the stream's type when stored, and n is computed from h
+ * before that rounding; every sum and product is f32.
+ *   residual, h      [T, H] in stream_dtype; h may be residual itself (in place)
+ *   y, n             [T, H] in block_dtype; y may be NULL (h is then not written)
+ *   gate             see MOE_GATE_*; NULL exactly when gate_kind is MOE_GATE_NONE
+ *   post_weight, pre_weight  [H] f32, each may be NULL (post_weight needs y)
+ *   rstd_post, rstd_pre      [T] f32 out, each may be NULL; kept for the backward
+ * Requires T >= 0, 1 <= H <= MOE_NORM_MAX_HIDDEN, T * H < 2^40, eps > 0 and
+ * finite, scale finite, y or pre_weight given, n non-NULL exactly when
+ * pre_weight is, and every tensor aligned to its element.  (16-byte aligned
+ * tensors with H % 8 == 0 take 16-byte accesses.)
+ */
+moe_status_t moe_block_norm(const void *residual, int32_t stream_dtype, const void *y,
+                            int32_t block_dtype, int64_t num_tokens, int32_t hidden,
+                            const float *post_weight, const void *gate, int32_t gate_kind,
+                            int32_t gate_act, float scale, const float *pre_weight, float eps,
+                            void *h, void *n, float *rstd_post, float *rstd_pre, void *stream);
+
+/*
+ * moe_block_norm_backward -- gradients of moe_block_norm for the gradients
+ * grad_h of h and grad_n of n, from the saved h, y and inverse norms:
+ *   u = grad_n * pre_weight
+ *   d[t,c] = grad_h + rstd_pre * u - h * rstd_pre^3 * mean_c(u * h)
+ *   grad_residual = d
+ *   grad_pre_weight[c] = sum_t grad_n * h * rstd_pre
+ *   grad_gate = scale * d * z * g'     (g' = 1, or g (1 - g) for the sigmoid),
+ *               summed over the tokens (CHANNEL) or the channels (TOKEN)
+ *   b = scale * g * d
+ *   grad_post_weight[c] = sum_t b * y * rstd_post
+ *   grad_y = rstd_post * b * post_weight
+ *            - y * rstd_post^3 * mean_c(b * post_weight * y)   (no post_weight: b)
+ *   grad_h [T, H] stream_dtype, may be NULL (zero); grad_n [T, H] block_dtype and
+ *   h [T, H] stream_dtype, both needed with pre_weight; y, gate as above;
+ *   rstd_post needed with post_weight, rstd_pre with pre_weight.
+ *   grad_residual [T, H] stream_dtype (may be grad_h itself); grad_y [T, H]
+ *   block_dtype, needed with y; grad_post_weight, grad_pre_weight [H] f32, needed
+ *   with their weights; grad_gate in the gate's shape and type, needed with it.
+ * Sums over tokens are f32 partial sums of fixed runs of tokens, added in a fixed order:
+ * the same inputs give the same bits.  T == 0 zero-fills the [H] gradients.
+ *   workspace: moe_block_norm_backward_workspace_bytes(T, H) bytes, 16-byte aligned.
+ */
+moe_status_t moe_block_norm_backward(
+    const void *grad_h, const void *grad_n, const void *h, int32_t stream_dtype, const void *y,
+    int32_t block_dtype, int64_t num_tokens, int32_t hidden, const float *post_weight,
+    const void *gate, int32_t gate_kind, int32_t gate_act, float scale, const float *pre_weight,
+    const float *rstd_post, const float *rstd_pre, void *grad_residual, void *grad_y,
+    float *grad_post_weight, void *grad_gate, float *grad_pre_weight, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+size_t moe_block_norm_backward_workspace_bytes(int64_t num_tokens, int32_t hidden);
+
+/* The router's probabilities in the balance loss. */
+#define MOE_SCORE_SOFTMAX 0 /* p = softmax(scores)                             */
+#define MOE_SCORE_SIGMOID 1 /* p = sigmoid(scores) / sum of the row's sigmoids  */
+
+/*
+ * moe_balance_loss -- per-expert counts and the router's auxiliary losses over
+ * packed sequences.  Sequence i holds the tokens seq_offsets[i] <= t <
+ * seq_offsets[i+1].  A token counts if it lies in a sequence, token_mask (if
+ * given) is nonzero there, and its row has a score above -inf; n_i is the
+ * number of such tokens of sequence i.  Scores of a token that does not count
+ * may hold anything.  Over the tokens that count:
+ *   counts[i,e] = #{(t,j) : topk_idx[t,j] == e}
+ *   probs[i,e]  = (1/n_i) sum_t p[t,e]
+ *   balance[i]  = sum_e (E counts[i,e] / (k n_i)) * probs[i,e]
+ *   z[i]        = (1/n_i) sum_t (log sum_e exp(scores[t,e]))^2
+ * and all of them are 0 where n_i = 0.
+ *   scores [T, E] f32 (-inf allowed, +inf not); topk_idx [T, k] i32
+ *   seq_offsets [S+1] i32, non-decreasing, within [0, T]; NULL for one sequence
+ *   of all T tokens (num_seqs 1);  token_mask [T] u8, may be NULL
+ *   balance, z [S] f32; counts [S, E] i32; probs [S, E] f32; tokens [S] i32 (n_i)
+ *   workspace: moe_balance_loss_workspace_bytes(T, E, S) bytes, 16-byte aligned
+ * An index outside [0, E) is not counted and sets MOE_DEVERR_EXPERT_RANGE.
+ * The same inputs give the same bits.  Requires the E and k limits of
+ * moe_topk_gate, 1 <= num_seqs <= 65535 and 0 <= T < 2^31.
+ */
+moe_status_t moe_balance_loss(const float *scores, const int32_t *topk_idx, int64_t num_tokens,
+                              int32_t num_experts, int32_t num_topk, int32_t score_func,
+                              const int32_t *seq_offsets, int32_t num_seqs,
+                              const uint8_t *token_mask, float *balance, float *z,
+                              int32_t *counts, float *probs, int32_t *tokens, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+size_t moe_balance_loss_workspace_bytes(int64_t num_tokens, int32_t num_experts,
+                                        int32_t num_seqs);
+
+/*
+ * moe_balance_loss_backward -- the router's score gradient: of both losses, and
+ * (where grad_topk_weights is given) of the softmax weights of the selected
+ * scores that moe_topk_gate returns.  With f_e = E counts[i,e] / (k n_i), taken
+ * as constant, and q = softmax(scores):
+ *   a_e = grad_balance[i] f_e / n_i
+ *   grad_scores[t,e] = p_e (a_e - sum_e' p_e' a_e') [* (1 - sigmoid(scores)) for
+ *                      MOE_SCORE_SIGMOID]
+ *                    + (2 grad_z[i] / n_i) lse_t q_e
+ *                    + w_j (grad_w_j - sum_j' w_j' grad_w_j')   where e = topk_idx[t,j]
+ * A token that does not count (see moe_balance_loss) gets a row of zeros.
+ *   counts, tokens: as moe_balance_loss returned them
+ *   grad_balance, grad_z [S] f32, each may be NULL (zero)
+ *   topk_idx [T, k] i32 (a token's experts distinct), topk_weights and
+ *   grad_topk_weights [T, k] f32: all three, or grad_topk_weights NULL
+ *   grad_scores [T, E] f32 out
+ */
+moe_status_t moe_balance_loss_backward(const float *scores, int64_t num_tokens,
+                                       int32_t num_experts, int32_t num_topk, int32_t score_func,
+                                       const int32_t *seq_offsets, int32_t num_seqs,
+                                       const uint8_t *token_mask, const int32_t *counts,
+                                       const int32_t *tokens, const float *grad_balance,
+                                       const float *grad_z, const int32_t *topk_idx,
+                                       const float *topk_weights, const float *grad_topk_weights,
+                                       float *grad_scores, void *stream);
+
+/*
+ * moe_combine_backward -- gradients of moe_combine:
+ *   grad_y[pos[t,j], c] = bf16(topk_weights[t,j] * grad_out[t,c])   for pos[t,j] >= 0
+ *   grad_topk_weights[t,j] = sum_c grad_out[t,c] * y[pos[t,j], c]   (f32; 0 for pos < 0)
+ *   grad_out [T, H] in grad_dtype (MOE_DT_*), y and grad_y [num_rows, H] bf16, all
+ *   16-byte aligned; topk_weights, grad_topk_weights [T, k] f32; pos [T, k] i32, each
+ *   row named at most once
+ *   sorted_src: NULL (rows no pos names are not written), or [num_rows] i32 as the
+ *   route map returns it: rows with a negative entry are zero-filled
+ * Requirements and error bits as moe_combine.
+ */
+moe_status_t moe_combine_backward(const void *grad_out, int32_t grad_dtype, const void *y,
+                                  const float *topk_weights, const int32_t *pos,
+                                  const int32_t *sorted_src, int64_t num_tokens, int32_t hidden,
+                                  int32_t num_topk, int64_t num_rows, void *grad_y,
+                                  float *grad_topk_weights, void *stream);
+
+#define MOE_MATVEC_MAX_ROWS (1 << 18) /* most rows of moe_expert_matvec_fp4 */
+
+/* Scale types of moe_expert_matvec_fp4's weights: the row-major layouts that
+ * moe_expand_cast_fp4 writes. */
+#define MOE_WSF_F32 0   /* [E][M][K/group] f32                                     */
+#define MOE_WSF_UE8M0 1 /* [E][M][K/group] u8, value 2^(byte - 127)                */
+
+/*
+ * moe_expert_matvec_fp4 -- products of routed rows with their expert's 4-bit
+ * weights, for decode batches (few rows per expert):
+ *   o[r, m] = sum_c x[src(r), c] * E2M1(w[e(r), m, c]) * w_sf[e(r), m, c / group]
+ *   out[r, n] = o[r, n]                                        (M = N), or
+ *   out[r, n] = o[r, n] / (1 + exp(-o[r, n])) * o[r, N + n]    (swiglu: M = 2N)
+ * for the rows offsets[e] <= r < offsets[e+1] of every expert e, in f32, rounded
+ * once to out_dtype.  Rows at or past offsets[E] are not written.
+ *   x [num_x, K] bf16, finite, 16-byte aligned
+ *   w [E, M, K/2] u8, two E2M1 codes per byte, element 2i in the low nibble (the
+ *   layout moe_expand_cast_fp4 writes), 16-byte aligned; w_sf as MOE_WSF_*
+ *   offsets [E+1] i32, non-decreasing, within [0, num_rows], as the route maps
+ *   return it; NULL (E == 1 only): all num_rows rows
+ *   sorted_src: NULL: src(r) = r (num_x >= num_rows); or [num_rows] i32 as the route
+ *   maps return it: src(r) = sorted_src[r] / num_topk, and a negative entry gives
+ *   a row of zeros
+ *   out [num_rows, N] in out_dtype (MOE_OUT_*)
+ * group is 16, 32, 64 or 128; K % 32 == 0, K % group == 0, K <= 65536, N <= 2^24,
+ * num_rows <= MOE_MATVEC_MAX_ROWS.  offsets
+ * beyond num_rows or a src outside [0, num_x) set MOE_DEVERR_POS_RANGE; such rows
+ * are not written, or are zero.
+ */
+moe_status_t moe_expert_matvec_fp4(const void *x, int64_t num_x, const uint8_t *w,
+                                   const void *w_sf, int32_t sf_type, int32_t group,
+                                   const int32_t *offsets, const int32_t *sorted_src,
+                                   int32_t num_experts, int32_t num_topk, int64_t num_rows,
+                                   int32_t k_dim, int32_t n_dim, int32_t swiglu, void *out,
+                                   int32_t out_dtype, void *stream);
 
 /* Test hooks of the fused path, process-wide, read at each launch:
  *   MOE_DEBUG_WAIT_TIMEOUT_NS: the bound of every wait (default 1e9 ns);

@@ -1,0 +1,195 @@
+// block_ops.cuh -- what the operators around the routed experts share: element
+// access, and the launchers that api_block.cu validates for and calls.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+// bf16 in memory; f32 is float itself.
+struct Bf16 {
+  uint16_t bits;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
+  const uint32_t l = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
+  const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
+  return l | (h << 16);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& a, float (&v)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+// 16-byte load of data read once, through the coherent path: an output may
+// share its address (in-place updates), each element read before it is stored.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// VEC consecutive elements as f32: one element, or eight through 16-byte
+// accesses (p 16-byte aligned).  Loads are read-once (no L1 allocation);
+// stores are evict-first.
+template <int VEC>
+__device__ __forceinline__ void load_elems(const Bf16* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    unpack8(ld_once_v4(p), v);
+  } else {
+    static_assert(VEC == 1, "one or eight elements");
+    v[0] = __uint_as_float((uint32_t)p->bits << 16);
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_elems(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const uint4 a = ld_once_v4(p), b = ld_once_v4(p + 4);
+    v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y);
+    v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+    v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y);
+    v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+  } else {
+    static_assert(VEC == 1, "one or eight elements");
+    v[0] = *p;
+  }
+}
+
+// f32 values other rows re-read (weights, per-channel gates): the cached path.
+template <int VEC>
+__device__ __forceinline__ void load_shared_f32(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    v[0] = __ldg(p);
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_elems(Bf16* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8)
+    st_stream_v4(p, make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
+                               pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7])));
+  else
+    p->bits = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_elems(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    st_stream_v4(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                               __float_as_uint(v[2]), __float_as_uint(v[3])));
+    st_stream_v4(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
+                                   __float_as_uint(v[6]), __float_as_uint(v[7])));
+  } else {
+    *p = v[0];
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// ------------------------------------------------------------- launchers
+
+// moe_block_norm and its backward (block_norm.cu); the fields are the
+// arguments of the C calls, checked by the caller.
+struct NormArgs {
+  const void* residual = nullptr;  // forward only
+  const void* y = nullptr;
+  const void* gate = nullptr;
+  const float* post_w = nullptr;
+  const float* pre_w = nullptr;
+  int64_t T = 0;
+  int H = 0;
+  int gate_kind = 0;
+  int gate_act = 0;
+  float scale = 1.0f;
+  float eps = 0.0f;
+  void* h = nullptr;  // written by the forward, read by the backward
+  void* n = nullptr;
+  float* rstd_post = nullptr;
+  float* rstd_pre = nullptr;
+  // backward
+  const void* grad_h = nullptr;
+  const void* grad_n = nullptr;
+  void* grad_residual = nullptr;
+  void* grad_y = nullptr;
+  void* grad_gate = nullptr;
+  float* grad_post_w = nullptr;
+  float* grad_pre_w = nullptr;
+  float* partials = nullptr;  // workspace: [3][blocks][H] sums over a block's tokens
+};
+cudaError_t launch_block_norm(const LaunchCtx& c, const NormArgs& a, bool stream_f32,
+                              bool block_f32);
+cudaError_t launch_block_norm_backward(const LaunchCtx& c, const NormArgs& a, bool stream_f32,
+                                       bool block_f32);
+// Blocks of the backward that leave partial sums over tokens: at most this
+// many, and at most one per token.
+constexpr int kNormMaxPartials = 320;
+
+// moe_balance_loss (balance_loss.cu).
+struct BalanceArgs {
+  const float* scores = nullptr;
+  const int32_t* idx = nullptr;
+  int64_t T = 0;
+  int E = 0, k = 0, func = 0, S = 1;
+  const int32_t* seq = nullptr;
+  const uint8_t* mask = nullptr;
+  float* balance = nullptr;
+  float* z = nullptr;
+  int32_t* counts = nullptr;
+  float* probs = nullptr;
+  int32_t* tokens = nullptr;
+  void* ws = nullptr;
+  // backward
+  const float* grad_balance = nullptr;
+  const float* grad_z = nullptr;
+  const float* w = nullptr;
+  const float* grad_w = nullptr;
+  float* grad_scores = nullptr;
+};
+size_t balance_workspace_bytes(int64_t T, int E, int S);
+cudaError_t launch_balance_loss(const LaunchCtx& c, const BalanceArgs& a);
+cudaError_t launch_balance_loss_backward(const LaunchCtx& c, const BalanceArgs& a);
+
+cudaError_t launch_combine_backward(const LaunchCtx& c, const void* grad_out, bool grad_f32,
+                                    const void* y, const float* w, const int32_t* pos,
+                                    const int32_t* src, int64_t T, int H, int k, int64_t R,
+                                    void* grad_y, float* grad_w);
+
+// moe_expert_matvec_fp4 (expert_matvec_fp4.cu).
+struct MatvecArgs {
+  const void* x = nullptr;
+  int64_t num_x = 0;
+  const uint8_t* w = nullptr;
+  const void* sf = nullptr;
+  int sf_type = 0, group = 0;
+  const int32_t* offsets = nullptr;
+  const int32_t* src = nullptr;
+  int E = 1, k = 1;
+  int64_t R = 0;
+  int K = 0, N = 0, swiglu = 0;
+  void* out = nullptr;
+  bool out_f32 = false;
+};
+cudaError_t launch_expert_matvec_fp4(const LaunchCtx& c, const MatvecArgs& a);
+
+}  // namespace moe

@@ -58,6 +58,21 @@ SIGNATURES = {
     "swiglu_cast_fp8_ex": (ctypes.c_int, [_P, _i64, _i32, _P, _P, ctypes.c_uint32, _i64, _i32,
                                           ctypes.c_float, _P, _P, _i32, _P]),
     "moe_combine": (ctypes.c_int, [_P, _P, _P, _i64, _i32, _i32, _i64, _P, _i32, _P]),
+    "moe_block_norm": (ctypes.c_int, [_P, _i32, _P, _i32, _i64, _i32, _P, _P, _i32, _i32,
+                                      ctypes.c_float, _P, ctypes.c_float, _P, _P, _P, _P, _P]),
+    "moe_block_norm_backward": (ctypes.c_int, [_P, _P, _P, _i32, _P, _i32, _i64, _i32, _P, _P,
+                                               _i32, _i32, ctypes.c_float, _P, _P, _P, _P, _P, _P,
+                                               _P, _P, _P, _sz, _P]),
+    "moe_block_norm_backward_workspace_bytes": (_sz, [_i64, _i32]),
+    "moe_balance_loss": (ctypes.c_int, [_P, _P, _i64, _i32, _i32, _i32, _P, _i32, _P, _P, _P, _P,
+                                        _P, _P, _P, _sz, _P]),
+    "moe_balance_loss_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "moe_balance_loss_backward": (ctypes.c_int, [_P, _i64, _i32, _i32, _i32, _P, _i32, _P, _P, _P,
+                                                 _P, _P, _P, _P, _P, _P, _P]),
+    "moe_combine_backward": (ctypes.c_int, [_P, _i32, _P, _P, _P, _P, _i64, _i32, _i32, _i64, _P,
+                                            _P, _P]),
+    "moe_expert_matvec_fp4": (ctypes.c_int, [_P, _i64, _P, _P, _i32, _i32, _P, _P, _i32, _i32,
+                                             _i64, _i32, _i32, _i32, _P, _i32, _P]),
     "moe_peak_copy": (ctypes.c_int, [_P, _P, _sz, _P]),
     "moe_get_device_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -493,6 +508,331 @@ def combine(y: torch.Tensor, topk_weights: torch.Tensor, pos: torch.Tensor,
     return o
 
 
+# --------------------------------------------------------------------------
+# The operators around the routed experts.
+
+DT_BF16, DT_F32 = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = range(4)
+_GATE_ACT = {"none": 0, "sigmoid": 1}
+_SCORE_FUNC = {"softmax": 0, "sigmoid": 1}
+WSF_F32, WSF_UE8M0 = 0, 1
+
+
+def _dt(t: torch.Tensor, name: str) -> int:
+    """MOE_DT_* of a bfloat16 or float32 tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == torch.bfloat16:
+        return DT_BF16
+    if t.dtype == torch.float32:
+        return DT_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _choice(value: str, table: dict, name: str) -> int:
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def _gate_kind(gate, T: int, H: int, block_dtype) -> int:
+    """MOE_GATE_* from the gate's shape: [H] float32, [T, 1] float32, or
+    [T, H] in the block's type."""
+    if gate is None:
+        return GATE_NONE
+    if not isinstance(gate, torch.Tensor):
+        raise TypeError("gate must be a torch.Tensor")
+    if gate.dim() == 1:
+        _dev(gate, "gate", torch.float32, (H,))
+        return GATE_CHANNEL
+    if gate.dim() == 2 and gate.shape[1] == 1 and gate.dtype == torch.float32:
+        _dev(gate, "gate", torch.float32, (T, 1))
+        return GATE_TOKEN
+    _dev(gate, "gate", block_dtype, (T, H))
+    return GATE_ELEMENT
+
+
+def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_weight=None,
+               gate=None, gate_act: str = "none", scale: float = 1.0, pre_weight=None,
+               eps: float = 1e-6, block_dtype=None, out=None, stream=None):
+    """The norms before and after a block, with its gate and residual scale:
+
+        z = y * rstd_post * post_weight          (post_weight None: z = y)
+        h = residual + scale * g * z             (y None: h is residual)
+        n = h * rstd_pre * pre_weight            (pre_weight None: no n)
+
+    with rstd = 1 / sqrt(mean(row^2) + eps) and g the gate: None, [H] or [T, 1]
+    float32, or [T, H] in y's type; gate_act "none" or "sigmoid".  residual and
+    h are [T, H] bfloat16 or float32, y and n [T, H] bfloat16 or float32
+    (block_dtype, y's own by default, else bfloat16); weights are [H] float32.
+    out: None or (h, n), where h may be residual itself.
+    -> (h, n, rstd_post, rstd_pre), None for what there is not."""
+    sd = _dt(residual, "residual")
+    _dev(residual, "residual", residual.dtype)
+    T, H = residual.shape
+    if block_dtype is None:
+        block_dtype = torch.bfloat16 if y is None else y.dtype
+    if block_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("block_dtype must be bfloat16 or float32")
+    if y is not None:
+        _dev(y, "y", block_dtype, (T, H))
+    elif post_weight is not None or gate is not None:
+        raise ValueError("post_weight and gate need y")
+    elif pre_weight is None:
+        raise ValueError("nothing to do: neither y nor pre_weight given")
+    for name, wt in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if wt is not None:
+            _dev(wt, name, torch.float32, (H,))
+    kind = _gate_kind(gate, T, H, block_dtype)
+    h, n = out if out is not None else (None, None)
+    if y is None:
+        h = residual
+    elif h is None:
+        h = torch.empty_like(residual)
+    else:
+        _dev(h, "out[0]", residual.dtype, (T, H))
+    if pre_weight is None:
+        n = None
+    elif n is None:
+        n = _empty((T, H), block_dtype, residual)
+    else:
+        _dev(n, "out[1]", block_dtype, (T, H))
+    rp = _empty((T,), torch.float32, residual) if post_weight is not None else None
+    rn = _empty((T,), torch.float32, residual) if pre_weight is not None else None
+    rc = lib().moe_block_norm(_ptr(residual), sd, _ptr(y),
+                              DT_F32 if block_dtype == torch.float32 else DT_BF16, T, H,
+                              _ptr(post_weight), _ptr(gate), kind,
+                              _choice(gate_act, _GATE_ACT, "gate_act"), scale, _ptr(pre_weight),
+                              eps, _ptr(h), _ptr(n), _ptr(rp), _ptr(rn), _stream(stream))
+    _check(rc, "moe_block_norm")
+    return h, n, rp, rn
+
+
+def block_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().moe_block_norm_backward_workspace_bytes(T, H))
+
+
+def block_norm_backward(grad_h, grad_n, h: torch.Tensor, *, y=None, post_weight=None, gate=None,
+                        gate_act: str = "none", scale: float = 1.0, pre_weight=None,
+                        rstd_post=None, rstd_pre=None, workspace=None, stream=None):
+    """Gradients of block_norm for grad_h (of h, or None) and grad_n (of n, or
+    None without pre_weight), from the saved h, y and inverse norms.
+    -> (grad_residual, grad_y, grad_post_weight, grad_gate, grad_pre_weight),
+    None for what there is not; each in its tensor's type and shape."""
+    sd = _dt(h, "h")
+    _dev(h, "h", h.dtype)
+    T, H = h.shape
+    if grad_h is not None:
+        _dev(grad_h, "grad_h", h.dtype, (T, H))
+    if (pre_weight is None) != (grad_n is None) or (pre_weight is None) != (rstd_pre is None):
+        raise ValueError("pre_weight, grad_n and rstd_pre go together")
+    if (post_weight is None) != (rstd_post is None):
+        raise ValueError("post_weight and rstd_post go together")
+    block = y if y is not None else grad_n
+    if block is None:
+        raise ValueError("nothing to do: neither y nor grad_n given")
+    bd = _dt(block, "y or grad_n")
+    if y is not None:
+        _dev(y, "y", block.dtype, (T, H))
+    elif post_weight is not None or gate is not None:
+        raise ValueError("post_weight and gate need y")
+    if grad_n is not None:
+        _dev(grad_n, "grad_n", block.dtype, (T, H))
+    for name, wt in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if wt is not None:
+            _dev(wt, name, torch.float32, (H,))
+    for name, r in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
+        if r is not None:
+            _dev(r, name, torch.float32, (T,))
+    kind = _gate_kind(gate, T, H, block.dtype)
+    gr = torch.empty_like(h)
+    gy = None if y is None else torch.empty_like(y)
+    gpw = None if post_weight is None else torch.empty_like(post_weight)
+    gg = None if gate is None else torch.empty_like(gate)
+    gnw = None if pre_weight is None else torch.empty_like(pre_weight)
+    if workspace is None:
+        workspace = _empty((block_norm_backward_workspace_bytes(T, H),), torch.uint8, h)
+    _dev(workspace, "workspace", torch.uint8)
+    rc = lib().moe_block_norm_backward(
+        _ptr(grad_h), _ptr(grad_n), _ptr(h), sd, _ptr(y), bd, T, H, _ptr(post_weight), _ptr(gate),
+        kind, _choice(gate_act, _GATE_ACT, "gate_act"), scale, _ptr(pre_weight), _ptr(rstd_post),
+        _ptr(rstd_pre), _ptr(gr), _ptr(gy), _ptr(gpw), _ptr(gg), _ptr(gnw), _ptr(workspace),
+        workspace.numel(), _stream(stream))
+    _check(rc, "moe_block_norm_backward")
+    return gr, gy, gpw, gg, gnw
+
+
+def _sequences(seq_offsets, token_mask, T: int) -> int:
+    """Checks of what the balance loss and its backward share; the sequences."""
+    if seq_offsets is not None:
+        _dev(seq_offsets, "seq_offsets", torch.int32)
+        if seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+            raise ValueError("seq_offsets must be [S + 1] with S >= 1")
+    if token_mask is not None:
+        if not isinstance(token_mask, torch.Tensor) or token_mask.dtype not in (torch.bool,
+                                                                                torch.uint8):
+            raise TypeError("token_mask must be a bool or uint8 tensor")
+        _dev(token_mask, "token_mask", token_mask.dtype, (T,))
+    return 1 if seq_offsets is None else seq_offsets.numel() - 1
+
+
+def balance_loss_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    return int(lib().moe_balance_loss_workspace_bytes(T, E, S))
+
+
+def balance_loss(scores: torch.Tensor, topk_idx: torch.Tensor, *, score_func: str = "softmax",
+                 seq_offsets=None, token_mask=None, workspace=None, stream=None):
+    """Per-expert counts, balance loss and z-loss of the router per sequence.
+
+    scores [T, E] float32 (-inf allowed), topk_idx [T, k] int32; seq_offsets
+    [S+1] int32 (None: one sequence of all T tokens); token_mask [T] bool or
+    uint8, zero where a token does not count.  With p = softmax(scores), or
+    sigmoid(scores) over its row sum:
+        balance[i] = sum_e E counts[i,e] / (k n_i) * probs[i,e],  probs = mean p
+        z[i]       = mean of logsumexp(scores)^2
+    -> (balance [S], z [S], counts [S, E] int32, probs [S, E], tokens [S] int32)."""
+    _dev(scores, "scores", torch.float32)
+    T, E = scores.shape
+    _dev(topk_idx, "topk_idx", torch.int32)
+    k = topk_idx.shape[1]
+    _dev(topk_idx, "topk_idx", torch.int32, (T, k))
+    S = _sequences(seq_offsets, token_mask, T)
+    bal, z = _empty((S,), torch.float32, scores), _empty((S,), torch.float32, scores)
+    counts = _empty((S, E), torch.int32, scores)
+    probs = _empty((S, E), torch.float32, scores)
+    tokens = _empty((S,), torch.int32, scores)
+    if workspace is None:
+        workspace = _empty((balance_loss_workspace_bytes(T, E, S),), torch.uint8, scores)
+    _dev(workspace, "workspace", torch.uint8)
+    rc = lib().moe_balance_loss(_ptr(scores), _ptr(topk_idx), T, E, k,
+                                _choice(score_func, _SCORE_FUNC, "score_func"), _ptr(seq_offsets),
+                                S, _ptr(token_mask), _ptr(bal), _ptr(z), _ptr(counts),
+                                _ptr(probs), _ptr(tokens), _ptr(workspace), workspace.numel(),
+                                _stream(stream))
+    _check(rc, "moe_balance_loss")
+    return bal, z, counts, probs, tokens
+
+
+def balance_loss_backward(scores: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor,
+                          grad_balance=None, grad_z=None, *, k: int | None = None,
+                          score_func: str = "softmax", seq_offsets=None, token_mask=None,
+                          topk_idx=None, topk_weights=None, grad_topk_weights=None, out=None,
+                          stream=None):
+    """The router's score gradient [T, E] float32: of balance_loss's two losses
+    (grad_balance, grad_z [S] float32, or None) and, with grad_topk_weights
+    [T, k], of topk_gate's softmax weights of the selected scores (topk_idx and
+    topk_weights as topk_gate returned them).  counts and tokens as
+    balance_loss returned them; k from topk_idx or, without it, given."""
+    _dev(scores, "scores", torch.float32)
+    T, E = scores.shape
+    S = _sequences(seq_offsets, token_mask, T)
+    _dev(counts, "counts", torch.int32, (S, E))
+    _dev(tokens, "tokens", torch.int32, (S,))
+    for name, g in (("grad_balance", grad_balance), ("grad_z", grad_z)):
+        if g is not None:
+            _dev(g, name, torch.float32, (S,))
+    if topk_idx is not None:
+        _dev(topk_idx, "topk_idx", torch.int32)
+        if k is not None and k != topk_idx.shape[1]:
+            raise ValueError(f"k is {k} but topk_idx has {topk_idx.shape[1]} columns")
+        k = topk_idx.shape[1]
+        _dev(topk_idx, "topk_idx", torch.int32, (T, k))
+    elif k is None:
+        raise ValueError("k is needed without topk_idx")
+    if grad_topk_weights is not None:
+        if topk_idx is None or topk_weights is None:
+            raise ValueError("grad_topk_weights needs topk_idx and topk_weights")
+        _dev(topk_weights, "topk_weights", torch.float32, (T, k))
+        _dev(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k))
+    g = out if out is not None else torch.empty_like(scores)
+    _dev(g, "out", torch.float32, (T, E))
+    rc = lib().moe_balance_loss_backward(
+        _ptr(scores), T, E, k, _choice(score_func, _SCORE_FUNC, "score_func"), _ptr(seq_offsets),
+        S, _ptr(token_mask), _ptr(counts), _ptr(tokens), _ptr(grad_balance), _ptr(grad_z),
+        _ptr(topk_idx), _ptr(topk_weights), _ptr(grad_topk_weights), _ptr(g), _stream(stream))
+    _check(rc, "moe_balance_loss_backward")
+    return g
+
+
+def combine_backward(grad_out: torch.Tensor, y: torch.Tensor, topk_weights: torch.Tensor,
+                     pos: torch.Tensor, *, sorted_src=None, out=None, stream=None):
+    """Gradients of combine: grad_y[pos[t, j]] = w[t, j] * grad_out[t] and
+    grad_w[t, j] = <grad_out[t], y[pos[t, j]]>.
+
+    grad_out [T, H] bfloat16 or float32, y [R, H] bfloat16, w [T, k] float32,
+    pos [T, k] int32; sorted_src [R] int32 zero-fills grad_y's rows with a
+    negative entry (without it, rows no pos names are not written).
+    -> (grad_y [R, H] bfloat16, grad_w [T, k] float32)."""
+    gd = _dt(grad_out, "grad_out")
+    _dev(grad_out, "grad_out", grad_out.dtype)
+    T, H = grad_out.shape
+    _dev(y, "y", torch.bfloat16)
+    R = y.shape[0]
+    _dev(y, "y", torch.bfloat16, (R, H))
+    _dev(topk_weights, "topk_weights", torch.float32)
+    k = topk_weights.shape[1]
+    _dev(topk_weights, "topk_weights", torch.float32, (T, k))
+    _dev(pos, "pos", torch.int32, (T, k))
+    if sorted_src is not None:
+        _dev(sorted_src, "sorted_src", torch.int32, (R,))
+    gy, gw = out if out is not None else (torch.empty_like(y), torch.empty_like(topk_weights))
+    _dev(gy, "out[0]", torch.bfloat16, (R, H))
+    _dev(gw, "out[1]", torch.float32, (T, k))
+    rc = lib().moe_combine_backward(_ptr(grad_out), gd, _ptr(y), _ptr(topk_weights), _ptr(pos),
+                                    _ptr(sorted_src), T, H, k, R, _ptr(gy), _ptr(gw),
+                                    _stream(stream))
+    _check(rc, "moe_combine_backward")
+    return gy, gw
+
+
+def expert_matvec_fp4(x: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, offsets=None, *,
+                      sorted_src=None, k: int = 1, group: int = 32, swiglu: bool = False,
+                      out_dtype=torch.bfloat16, out=None, stream=None):
+    """Products of routed rows with their expert's 4-bit weights, for decode
+    batches (few rows per expert).
+
+    w [E, M, K/2] uint8 E2M1 codes (element 2i in the low nibble) and w_sf
+    [E, M, K/group] float32 or uint8 (UE8M0), as expand_cast_fp4 writes them.
+    Rows are in the route map's order: offsets [E+1] int32 (None: one expert,
+    all rows).  x [num_x, K] bfloat16: row r of the output reads x[r], or with
+    sorted_src [R] int32 x[sorted_src[r] // k] (a negative entry: a row of zeros).
+    swiglu: M = 2N, the gate's outputs first; out = silu(gate) * up.
+    -> out [R, N] bfloat16 or float32 (rows past offsets[E] not written)."""
+    _dev(x, "x", torch.bfloat16)
+    _dev(w, "w", torch.uint8)
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [rows, K] and w [E, M, K/2]")
+    K = x.shape[1]
+    E, M = w.shape[0], w.shape[1]
+    if group not in (16, 32, 64, 128):
+        raise ValueError(f"group must be 16, 32, 64 or 128, got {group}")
+    _dev(w, "w", torch.uint8, (E, M, K // 2))
+    if w_sf.dtype not in (torch.float32, torch.uint8):
+        raise TypeError(f"w_sf must be float32 or uint8, got {w_sf.dtype}")
+    _dev(w_sf, "w_sf", w_sf.dtype, (E, M, K // group))
+    if swiglu and M % 2:
+        raise ValueError("swiglu needs an even number of weight rows")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bfloat16 or float32")
+    if offsets is not None:
+        _dev(offsets, "offsets", torch.int32, (E + 1,))
+    if sorted_src is not None:
+        _dev(sorted_src, "sorted_src", torch.int32)
+        R = sorted_src.shape[0]
+    else:
+        R = x.shape[0]
+    N = M // 2 if swiglu else M
+    o = out if out is not None else _empty((R, N), out_dtype, x)
+    _dev(o, "out", out_dtype, (R, N))
+    rc = lib().moe_expert_matvec_fp4(_ptr(x), x.shape[0], _ptr(w), _ptr(w_sf),
+                                     WSF_UE8M0 if w_sf.dtype == torch.uint8 else WSF_F32, group,
+                                     _ptr(offsets), _ptr(sorted_src), E, k, R, K, N, int(swiglu),
+                                     _ptr(o), MOE_OUT_F32 if out_dtype == torch.float32 else
+                                     MOE_OUT_BF16, _stream(stream))
+    _check(rc, "moe_expert_matvec_fp4")
+    return o
+
+
 def peak_copy(src: torch.Tensor, dst: torch.Tensor, *, stream=None):
     """Device copy of src's bytes into dst (the HBM roofline probe)."""
     if src.device.type != "cuda" or dst.device.type != "cuda":
@@ -521,4 +861,6 @@ __all__ = ["lib", "MoeError", "topk_gate", "route_map", "route_map_workspace_byt
            "expand_cast_fp8_ex_workspace_bytes", "swiglu_cast_fp8_ex", "sf_empty",
            "route_expand_cast_fp8", "route_expand_cast_workspace", "debug_set", "debug_cvt", "expand_cast_fp4", "swiglu_cast_fp4",
            "expand_cast_fp8", "swiglu_cast_fp8", "combine", "peak_copy", "device_status",
-           "launch_count", "SIGNATURES"]
+           "launch_count", "SIGNATURES", "block_norm", "block_norm_backward",
+           "block_norm_backward_workspace_bytes", "balance_loss", "balance_loss_backward",
+           "balance_loss_workspace_bytes", "combine_backward", "expert_matvec_fp4"]
