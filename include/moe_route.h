@@ -668,7 +668,8 @@ moe_status_t moe_combine_backward(const void *grad_out, int32_t grad_dtype, cons
  * once to out_dtype.  Rows at or past offsets[E] are not written.
  *   x [num_x, K] bf16, finite, 16-byte aligned
  *   w [E, M, K/2] u8, two E2M1 codes per byte, element 2i in the low nibble (the
- *   layout moe_expand_cast_fp4 writes), 16-byte aligned; w_sf as MOE_WSF_*
+ *   layout moe_expand_cast_fp4 writes), 16-byte aligned; w_sf as MOE_WSF_*, 4-byte
+ *   aligned
  *   offsets [E+1] i32, non-decreasing, within [0, num_rows], as the route maps
  *   return it; NULL (E == 1 only): all num_rows rows
  *   sorted_src: NULL: src(r) = r (num_x >= num_rows); or [num_rows] i32 as the route

@@ -314,7 +314,7 @@ moe_status_t moe_expert_matvec_fp4(const void* x, int64_t num_x, const uint8_t* 
   if (num_rows == 0) return MOE_OK;
   if ((num_x > 0 && !x) || !w || !w_sf || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(offsets, 4) || !aligned(sorted_src, 4) ||
-      !aligned(w_sf, sf_type == MOE_WSF_F32 ? 4 : 1) ||
+      !aligned(w_sf, 4) ||
       !aligned(out, out_dtype == MOE_OUT_F32 ? 4 : 2))
     return MOE_ERR_INVALID_ARG;
   LaunchCtx c;

@@ -4,11 +4,31 @@
 //   o[r, m] = sum_g w_sf[e, m, g] * sum_{c in g} x[src(r), c] * E2M1(w[e, m, c])
 //
 // With few rows per expert the weights are read once for little arithmetic,
-// so HBM bounds it: K/2 bytes of codes and K/group scales per output.
+// so HBM bounds it: K/2 bytes of codes and K/group scales per output.  At that
+// rate an SM receives about 47 weights per clock.  Decoding them to f32 and
+// multiplying on the FP32 lanes costs more issue slots than there are, so the
+// products go to the tensor cores (mma.sync m16n8k16, f16 inputs, f32 sums):
+// 16 outputs by up to 8 rows of x, the codes decoded two at a time by the
+// hardware conversion E2M1 -> f16, which is exact.  (tcgen05.mma takes 4-bit
+// weights only beside activations of 8 bits or fewer, which would round x.)
 //
-// One CTA takes up to kRows rows of one expert (the route map left them
-// adjacent) and a tile of outputs; each warp computes one output at a time,
-// its lanes walking the weight row 16 bytes (32 codes) apiece.
+// x is bf16, which f16 cannot hold in range, so each block of 128 channels of
+// a row is scaled by the power of two that brings its largest magnitude to
+// [2^14, 2^15).  bf16's 8 significant bits fit f16's 11: a channel is exact
+// unless it is below 2^-31 of its block's largest, and then off by less than
+// 2^-39 of that largest.  The power of two is undone in f32.
+//
+// One CTA per SM.  Each computes, from the offsets, the list of (expert, run
+// of up to C rows) items, and takes an equal share of all (item, tile of 16
+// outputs) units.  For each item the CTA converts the run's rows of x into
+// shared memory once; then its 16 warps work through tiles, s warps splitting
+// a tile's channels (s chosen so that the units fill the warps; their sums are
+// added through shared memory in a fixed order).  Each warp streams its codes
+// and scales through a ring of its own in shared memory with cp.async, several
+// blocks of 128 channels ahead, so no barrier stands in the stream.
+//
+// With SwiGLU a tile is 8 gate outputs and the 8 up outputs of the same
+// channels, which the fragment layout leaves in one lane.
 #include "block_ops.cuh"
 
 #include <cuda_fp16.h>
@@ -16,67 +36,109 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 8;
-constexpr int kOutPerWarp = 2;
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxRows = 8;   // columns of one mma
+constexpr int kBlockK = 128;  // channels per ring stage
+constexpr int kStages = 4;
+
+// Bytes of scales of one stage: f32 [16][128 / G], or the aligned 32-bit words
+// that hold 128 / G bytes at any offset, [16][words].
+template <int G, bool U8>
+struct Stage {
+  static constexpr int kGroups = kBlockK / G;
+  static constexpr int kWords = U8 ? (kGroups + 3 + 3) / 4 : kGroups;
+  static constexpr int kCodeBytes = 16 * 64;
+  static constexpr int kBytes = kCodeBytes + 16 * kWords * 4;
+};
 
 // The two E2M1 codes of byte `i` of w as f16x2, element 0 (the low nibble) in
 // the low half: the hardware conversion, exact.
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w, int i) {
-  const uint16_t b = (uint16_t)((w >> (8 * i)) & 0xFFu);
   uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.u8.u16 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}" : "=r"(r) : "h"(b));
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n .reg .b8 t;\n mov.b32 {b0, b1, b2, b3}, %1;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n}"
+      : "=r"(r)
+      : "r"(w >> (8 * i)));
   return r;
 }
 
-// The item-th run of up to kRows rows of one expert, experts ascending; every
-// thread of the block calls it.  Empty (n == 0) past the last.
-struct Item {
-  int e, r0, n;
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1, bool from_zero) {
+  const float c[4] = {from_zero ? 0.0f : d[0], from_zero ? 0.0f : d[1], from_zero ? 0.0f : d[2],
+                      from_zero ? 0.0f : d[3]};
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+        "f"(c[2]), "f"(c[3]));
+}
+
+// Asynchronous copies of 16 or 4 bytes into shared memory; only the first
+// `bytes` are read, the rest is zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void group_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// 2^(b - 127): the exponent field itself, and 2^-127 as the denormal it is.
+__device__ __forceinline__ float ue8m0(uint32_t b) {
+  return __uint_as_float(b ? b << 23 : 0x00400000u);
+}
+
+// Shared memory: the warps' rings, the x rows (f16, row stride 2 Kp + 64 bytes
+// so that neighbouring rows fall into different halves of the banks), the
+// powers of two [Kp / 128][8], two buffers of partial sums, the items' prefix.
+struct Smem {
+  uint32_t ring, x, xs, red, first, total;
 };
-__device__ __forceinline__ Item find_item(const MatvecArgs& a, int item, Item* shared,
-                                          unsigned* err) {
-  if (a.offsets == nullptr) {
-    const int64_t r0 = (int64_t)item * kRows;
-    const int64_t left = a.R - r0;
-    return Item{0, (int)r0, left < 0 ? 0 : left < kRows ? (int)left : kRows};
-  }
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    if (lane == 0) *shared = Item{0, 0, 0};
-    __syncwarp();
-    int before = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      int lo = 0, hi = 0;
-      if (e < a.E) {
-        lo = __ldg(a.offsets + e);
-        hi = __ldg(a.offsets + e + 1);
-        if (lo < 0 || hi > a.R) {
-          flag_error(err, MOE_DEVERR_POS_RANGE);
-          lo = lo < 0 ? 0 : lo;
-          hi = hi > a.R ? (int)a.R : hi;
-        }
-      }
-      const int runs = hi > lo ? (hi - lo + kRows - 1) / kRows : 0;
-      int sum = runs;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      const int first = before + sum - runs;
-      if (item >= first && item < first + runs) {
-        const int r0 = lo + (item - first) * kRows;
-        *shared = Item{e, r0, hi - r0 < kRows ? hi - r0 : kRows};
-      }
-      before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-      if (item < before) break;
-    }
-  }
-  __syncthreads();
-  return *shared;
+__host__ __device__ inline int padded_k(int K) { return (K + kBlockK - 1) / kBlockK * kBlockK; }
+__host__ __device__ inline uint32_t x_stride(int K) { return (uint32_t)padded_k(K) * 2 + 64; }
+__host__ __device__ inline Smem smem_layout(int stage_bytes, int K, int E, int C) {
+  Smem s;
+  s.ring = 0;
+  s.x = (uint32_t)(kWarps * kStages * stage_bytes);
+  s.xs = s.x + (uint32_t)C * x_stride(K);
+  s.red = s.xs + (uint32_t)(padded_k(K) / kBlockK) * kMaxRows * 4;
+  s.first = s.red + 2 * kWarps * 512;
+  s.total = s.first + (uint32_t)(E + 1) * 4;
+  return s;
 }
 
 // Row r's row of x, or -1 for a row of zeros.
@@ -94,97 +156,355 @@ __device__ __forceinline__ int64_t source_row(const MatvecArgs& a, int r, unsign
   return s;
 }
 
-__device__ __forceinline__ float scale_at(const MatvecArgs& a, int64_t i) {
-  if (a.sf_type == MOE_WSF_F32) return __ldg(static_cast<const float*>(a.sf) + i);
-  const uint32_t b = __ldg(static_cast<const uint8_t*>(a.sf) + i);
-  // 2^(b - 127): the exponent field itself, and 2^-127 as the denormal it is
-  return __uint_as_float(b ? b << 23 : 0x00400000u);
-}
-
-__global__ void __launch_bounds__(kThreads)
-    expert_matvec_kernel(const MatvecArgs a, unsigned* err) {
+template <int G, bool U8>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_matvec_kernel(const MatvecArgs a, const int C, unsigned* err) {
   pdl_enter();
-  __shared__ Item shared;
-  __shared__ int64_t xrow[kRows];
-  const Item it = find_item(a, blockIdx.y, &shared, err);
-  if (it.n <= 0) return;
-  if (threadIdx.x < kRows)
-    xrow[threadIdx.x] = (int)threadIdx.x < it.n ? source_row(a, it.r0 + threadIdx.x, err) : -1;
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int M = a.swiglu ? 2 * a.N : a.N, blocks = a.K / 32;
-  const uint16_t* x = static_cast<const uint16_t*>(a.x);
-  for (int i = 0; i < kOutPerWarp; ++i) {
-    const int n = (blockIdx.x * kWarps + warp) * kOutPerWarp + i;
-    if (n >= a.N) return;
-    float acc[2][kRows];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) acc[h][r] = 0.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1 && !a.swiglu) break;
-      const int64_t m = (int64_t)it.e * M + n + h * a.N;
-      for (int b = lane; b < blocks; b += 32) {
-        const uint4 q = ld_stream_v4(a.w + m * (a.K / 2) + b * 16);
-        const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int c = b * 32 + half * 16;
-          const float s = scale_at(a, m * (a.K / a.group) + c / a.group);
-          float w[16];
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const uint32_t f = e2m1x2_to_f16x2(qw[half * 2 + p / 4], p % 4);
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-            w[2 * p] = v.x;
-            w[2 * p + 1] = v.y;
-          }
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            if (r >= it.n || xrow[r] < 0) continue;
-            float v[16];
-            const uint16_t* xp = x + xrow[r] * a.K + c;
-            unpack16(ld_v4(xp), ld_v4(xp + 8), v);
-            float d = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) d = __fmaf_rn(v[j], w[j], d);
-            acc[h][r] = __fmaf_rn(s, d, acc[h][r]);
-          }
+  using St = Stage<G, U8>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Smem L = smem_layout(St::kBytes, a.K, a.E, C);
+  const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
+  int* first = reinterpret_cast<int*>(smem + L.first);
+  float* xs = reinterpret_cast<float*>(smem + L.xs);
+  float4* red = reinterpret_cast<float4*>(smem + L.red);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int M = a.swiglu ? 2 * a.N : a.N;
+  const int per_tile = a.swiglu ? 8 : 16;  // outputs of one tile
+  const int tiles = (a.N + per_tile - 1) / per_tile;
+  const int nblk = padded_k(a.K) / kBlockK;
+  const uint32_t xrow_bytes = x_stride(a.K);
+  const int64_t sf_row = a.K / G;  // scales of one weight row
+
+  // first[e]: items of the experts before e
+  if (warp == 0) {
+    int before = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      int runs = 0;
+      if (e < a.E) {
+        int64_t lo = 0, hi = a.R;
+        if (a.offsets != nullptr) {
+          lo = __ldg(a.offsets + e);
+          hi = __ldg(a.offsets + e + 1);
+          if (lo < 0 || hi > a.R) flag_error(err, MOE_DEVERR_POS_RANGE);
+          if (lo < 0) lo = 0;
+          if (hi > a.R) hi = a.R;
         }
+        runs = hi > lo ? (int)((hi - lo + C - 1) / C) : 0;
       }
-    }
+      int sum = runs;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if (r >= it.n) break;
-      float o = warp_sum(acc[0][r]);
-      if (a.swiglu) {
-        const float up = warp_sum(acc[1][r]);
-        o = o / (1.0f + expf(-o)) * up;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
       }
-      if (lane == 0) {
-        const int64_t at = (int64_t)(it.r0 + r) * a.N + n;
-        if (a.out_f32)
-          static_cast<float*>(a.out)[at] = o;
-        else
-          static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-      }
+      if (e < a.E) first[e] = before + sum - runs;
+      before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (lane == 0) first[a.E] = before;
+  }
+  __syncthreads();
+  const int64_t units = (int64_t)first[a.E] * tiles;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+
+  // warps per tile: the split with the fewest block steps for this share
+  int split = 1;
+  {
+    const int64_t share = u1 - u0;
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= kWarps; s <<= 1) {
+      const int64_t rounds = (share * s + kWarps - 1) / kWarps;
+      const int64_t cost = rounds * ((nblk + s - 1) / s + (s > 1 ? 1 : 0));
+      if (cost < best) best = cost, split = s;
     }
   }
+  const int sub = warp % split, team = warp / split, teams = kWarps / split;
+  const int bpw = (nblk + split - 1) / split;
+  const int b_lo = sub * bpw < nblk ? sub * bpw : nblk;
+  const int b_hi = b_lo + bpw < nblk ? b_lo + bpw : nblk;
+  const int mine = b_hi - b_lo;  // blocks of each tile this warp sums
+
+  const uint32_t ring = sbase + L.ring + (uint32_t)(warp * kStages * St::kBytes);
+  int parity = 0;
+
+  int64_t u = u0;
+  while (u < u1) {
+    // the item of unit u, and the part of this CTA's share in it
+    const int item = (int)(u / tiles);
+    int e = 0;  // the last expert with first[e] <= item
+    for (int hi = a.E; hi - e > 1;) {
+      const int mid = (e + hi) >> 1;
+      if (first[mid] <= item)
+        e = mid;
+      else
+        hi = mid;
+    }
+    const int tile0 = (int)(u - (int64_t)item * tiles);
+    int64_t left = u1 - u;
+    const int ntiles = (int)(left < tiles - tile0 ? left : tiles - tile0);
+    u += ntiles;
+    int64_t lo = 0, hi = a.R;
+    if (a.offsets != nullptr) {
+      lo = __ldg(a.offsets + e);
+      hi = __ldg(a.offsets + e + 1);
+      if (lo < 0) lo = 0;
+      if (hi > a.R) hi = a.R;
+    }
+    const int r0 = (int)lo + (item - first[e]) * C;
+    const int n = hi - r0 < C ? (int)(hi - r0) : C;
+
+    // this team's tiles: tile0 + team, + teams, ...; its steps are (tile, block)
+    const int my_tiles = ntiles > team ? (ntiles - team + teams - 1) / teams : 0;
+    const int steps = my_tiles * mine;
+    const int64_t m_base = (int64_t)e * M;
+    // weight row of tile row i (0..15), or -1
+    auto weight_row = [&](int tile, int i) -> int64_t {
+      int nn;
+      if (a.swiglu) {
+        nn = tile * 8 + (i & 7);
+        if (nn >= a.N) return -1;
+        return m_base + nn + (i >> 3) * a.N;
+      }
+      nn = tile * 16 + i;
+      return nn < a.N ? m_base + nn : -1;
+    };
+    int ld_tile = tile0 + team, ld_blk = b_lo;
+    auto issue = [&](int step) {
+      if (step < steps) {
+        const uint32_t st = ring + (uint32_t)((step % kStages) * St::kBytes);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = g + 8 * i;
+          const int64_t m = weight_row(ld_tile, row);
+          const int c = ld_blk * 64 + q * 16;
+          const bool ok = m >= 0 && c < a.K / 2;
+          cp_async16(st + row * 64 + ((q ^ ((row >> 1) & 3)) << 4),
+                     a.w + (ok ? m * (a.K / 2) + c : 0), ok ? 16 : 0);
+        }
+        const uint32_t sst = st + St::kCodeBytes;
+        if (U8) {
+          const uint8_t* sf = static_cast<const uint8_t*>(a.sf);
+          const int64_t end = (int64_t)a.E * M * sf_row;
+          for (int p = lane; p < 16 * St::kWords; p += 32) {
+            const int row = p / St::kWords, wi = p % St::kWords;
+            const int64_t m = weight_row(ld_tile, row);
+            const int64_t at = ((m * sf_row + ld_blk * St::kGroups) & ~(int64_t)3) + 4 * wi;
+            int64_t bytes = m >= 0 ? end - at : 0;
+            bytes = bytes < 0 ? 0 : bytes > 4 ? 4 : bytes;
+            cp_async4(sst + p * 4, sf + (bytes > 0 ? at : 0), (int)bytes);
+          }
+        } else {
+          const float* sf = static_cast<const float*>(a.sf);
+          for (int p = lane; p < 16 * St::kGroups; p += 32) {
+            const int row = p / St::kGroups, j = p % St::kGroups;
+            const int64_t m = weight_row(ld_tile, row);
+            const int gi = ld_blk * St::kGroups + j;
+            const bool ok = m >= 0 && gi < sf_row;
+            cp_async4(sst + p * 4, sf + (ok ? m * sf_row + gi : 0), ok ? 4 : 0);
+          }
+        }
+        if (++ld_blk == b_hi) {
+          ld_blk = b_lo;
+          ld_tile += teams;
+        }
+      }
+      cp_async_commit();
+    };
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    // x: each half warp converts one block of 128 channels of one row
+    for (int t = tid >> 4; t < n * nblk; t += kThreads / 16) {
+      const int col = t / nblk, b = t - col * nblk, l16 = tid & 15;
+      const unsigned half = 0xFFFFu << (lane & 16);
+      const int64_t sr = source_row(a, r0 + col, err);
+      const int c = b * kBlockK + l16 * 8;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (sr >= 0 && c < a.K) v = ld_v4(static_cast<const uint16_t*>(a.x) + sr * a.K + c);
+      float f[8];
+      unpack8(v, f);
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
+      // 2^ex brings m's exponent to 14; kept to 126 so that 2^-ex is normal
+      int ex = 14 + 127 - (int)(__float_as_uint(m) >> 23);
+      ex = ex > 126 ? 126 : ex;
+      const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+      uint4 h;
+      uint32_t* hw = reinterpret_cast<uint32_t*>(&h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 p = __floats2half2_rn(f[2 * i] * up, f[2 * i + 1] * up);
+        hw[i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      *reinterpret_cast<uint4*>(smem + L.x + col * xrow_bytes + c * 2) = h;
+      if (l16 == 0) xs[b * kMaxRows + col] = __uint_as_float((uint32_t)(127 - ex) << 23);
+    }
+    __syncthreads();
+
+    const uint32_t xcol = sbase + L.x + g * xrow_bytes;
+    const bool has_col = g < n;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int tile = tile0 + team, blk = b_lo;
+    // a team whose warps have no block left still joins its tiles' sums
+    const int loop = mine > 0 ? steps : my_tiles;
+    for (int step = 0; step < loop; ++step) {
+      if (mine > 0) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        issue(step + kStages - 1);
+        const uint32_t st = ring + (uint32_t)((step % kStages) * St::kBytes);
+        const uint32_t sst = st + St::kCodeBytes;
+        const float2 xc = *reinterpret_cast<const float2*>(xs + blk * kMaxRows + 2 * q);
+        // scales of rows g and g + 8
+        float s[2][St::kGroups];
+        if (U8) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = g + 8 * i;
+            const int64_t m = weight_row(tile, row);
+            const int sh = 8 * (int)((m * sf_row + blk * St::kGroups) & 3);
+            uint32_t w[St::kWords];
+#pragma unroll
+            for (int j = 0; j < St::kWords; ++j) w[j] = lds32(sst + (row * St::kWords + j) * 4);
+#pragma unroll
+            for (int j = 0; j < St::kGroups; ++j) {
+              const int wi = j >> 2;
+              const uint32_t word =
+                  wi + 1 < St::kWords ? __funnelshift_r(w[wi], w[wi + 1], sh) : w[wi] >> sh;
+              s[i][j] = ue8m0((word >> (8 * (j & 3))) & 0xFFu);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < St::kGroups; ++j)
+              s[i][j] = __uint_as_float(lds32(sst + ((g + 8 * i) * St::kGroups + j) * 4));
+        }
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        auto flush = [&](int gi) {  // a group is complete: scale its sums
+          acc[0] = __fmaf_rn(s[0][gi] * xc.x, part[0], acc[0]);
+          acc[1] = __fmaf_rn(s[0][gi] * xc.y, part[1], acc[1]);
+          acc[2] = __fmaf_rn(s[1][gi] * xc.x, part[2], acc[2]);
+          acc[3] = __fmaf_rn(s[1][gi] * xc.y, part[3], acc[3]);
+        };
+        const uint32_t xb = xcol + (uint32_t)blk * 256;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t unit = (uint32_t)((j ^ (g >> 1)) << 4);  // rows g and g + 8 alike
+          const uint32_t lo_row = st + g * 64 + unit, hi_row = lo_row + 8 * 64;
+          uint32_t a0[4], a1[4];
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (G == 16) {
+            // the 16 channels of a group: 2 bytes of codes per lane
+            const uint32_t w0 = lds16(lo_row + 2 * q), w1 = lds16(lo_row + 8 + 2 * q);
+            const uint32_t w2 = lds16(hi_row + 2 * q), w3 = lds16(hi_row + 8 + 2 * q);
+            a0[0] = e2m1x2_to_f16x2(w0, 0), a0[2] = e2m1x2_to_f16x2(w0, 1);
+            a0[1] = e2m1x2_to_f16x2(w2, 0), a0[3] = e2m1x2_to_f16x2(w2, 1);
+            a1[0] = e2m1x2_to_f16x2(w1, 0), a1[2] = e2m1x2_to_f16x2(w1, 1);
+            a1[1] = e2m1x2_to_f16x2(w3, 0), a1[3] = e2m1x2_to_f16x2(w3, 1);
+            if (has_col) {
+              const uint2 p = lds64(xb + j * 64 + q * 8), r = lds64(xb + j * 64 + 32 + q * 8);
+              x = make_uint4(p.x, p.y, r.x, r.y);
+            }
+          } else {
+            const uint32_t w0 = lds32(lo_row + 4 * q), w1 = lds32(hi_row + 4 * q);
+            a0[0] = e2m1x2_to_f16x2(w0, 0), a0[2] = e2m1x2_to_f16x2(w0, 1);
+            a0[1] = e2m1x2_to_f16x2(w1, 0), a0[3] = e2m1x2_to_f16x2(w1, 1);
+            a1[0] = e2m1x2_to_f16x2(w0, 2), a1[2] = e2m1x2_to_f16x2(w0, 3);
+            a1[1] = e2m1x2_to_f16x2(w1, 2), a1[3] = e2m1x2_to_f16x2(w1, 3);
+            if (has_col) x = lds128(xb + j * 64 + q * 16);
+          }
+          const bool start = G <= 32 || (j * 32) % G == 0;
+          mma_16816(part, a0, x.x, x.y, start);
+          if (G == 16) flush(2 * j);
+          mma_16816(part, a1, x.z, x.w, G == 16);
+          if (G == 16)
+            flush(2 * j + 1);
+          else if ((j * 32 + 32) % G == 0)
+            flush((j * 32) / G);
+        }
+        if (++blk < b_hi) continue;
+        blk = b_lo;
+      }
+      // the tile is complete for this warp
+      bool writer = true;
+      if (split > 1) {
+        float4* buf = red + parity * kWarps * 32;
+        buf[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        group_barrier(1 + team, split * 32);
+        writer = sub == 0;
+        if (writer) {
+          for (int w = 1; w < split; ++w) {
+            const float4 v = buf[(warp + w) * 32 + lane];
+            acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
+          }
+        }
+        parity ^= 1;
+      }
+      if (writer) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = 2 * q + (i & 1);
+          float o = acc[i];
+          int nn;
+          if (a.swiglu) {
+            if (i >= 2) break;
+            o = o / (1.0f + expf(-o)) * acc[i + 2];
+            nn = tile * 8 + g;
+          } else {
+            nn = tile * 16 + g + (i >> 1) * 8;
+          }
+          if (col >= n || nn >= a.N) continue;
+          const int64_t at = (int64_t)(r0 + col) * a.N + nn;
+          if (a.out_f32)
+            static_cast<float*>(a.out)[at] = o;
+          else
+            static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+        }
+      }
+      acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+      tile += teams;
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // x and the rings are free for the next item
+  }
+}
+
+template <int G, bool U8>
+cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
+  // rows per item: 8 columns of the mma, fewer where a long x would not fit
+  int C = kMaxRows;
+  while (C > 1 && smem_layout(Stage<G, U8>::kBytes, a.K, a.E, C).total > 220 * 1024) C >>= 1;
+  const size_t smem = smem_layout(Stage<G, U8>::kBytes, a.K, a.E, C).total;
+  cudaError_t e = allow_max_dynamic_smem(expert_matvec_kernel<G, U8>);
+  if (e != cudaSuccess) return e;
+  int64_t items = (a.offsets ? a.E : 1) + a.R / C;
+  if (items > a.R) items = a.R;
+  const int per_tile = a.swiglu ? 8 : 16;
+  const int64_t units = items * ((a.N + per_tile - 1) / per_tile);
+  const int64_t blocks = units < c.num_sms ? units : c.num_sms;
+  return launch_pdl(expert_matvec_kernel<G, U8>, dim3((unsigned)blocks), kThreads, smem, c.stream,
+                    a, C, c.err);
+}
+
+template <int G>
+cudaError_t launch_g(const LaunchCtx& c, const MatvecArgs& a) {
+  return a.sf_type == MOE_WSF_UE8M0 ? launch_t<G, true>(c, a) : launch_t<G, false>(c, a);
 }
 
 }  // namespace
 
 cudaError_t launch_expert_matvec_fp4(const LaunchCtx& c, const MatvecArgs& a) {
-  const int per_cta = kWarps * kOutPerWarp;
-  // runs of rows: at most one per row, and at most one short run per expert
-  int64_t items = a.offsets ? a.E + a.R / kRows : (a.R + kRows - 1) / kRows;
-  if (items > a.R) items = a.R;
-  if (items > 65535) return cudaErrorInvalidConfiguration;
-  return launch_pdl(expert_matvec_kernel,
-                    dim3((unsigned)((a.N + per_cta - 1) / per_cta), (unsigned)items), kThreads, 0,
-                    c.stream, a, c.err);
+  switch (a.group) {
+    case 16: return launch_g<16>(c, a);
+    case 32: return launch_g<32>(c, a);
+    case 64: return launch_g<64>(c, a);
+    default: return launch_g<128>(c, a);
+  }
 }
 
 }  // namespace moe

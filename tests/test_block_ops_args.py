@@ -124,6 +124,7 @@ def test_expert_matvec_refusals(L):
     for name in "x w sf out".split():
         assert f(**{name: None}) == INVALID, name
     assert f(x=FAKE + 8) == INVALID and f(w=FAKE + 8) == INVALID and f(sf=FAKE + 2) == INVALID
+    assert f(st=1, sf=FAKE + 2) == INVALID
     assert f(out=FAKE + 1) == INVALID and f(od=1, out=FAKE + 2) == INVALID
 
 
