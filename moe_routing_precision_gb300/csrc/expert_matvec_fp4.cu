@@ -42,24 +42,38 @@ constexpr int kMaxRows = 8;   // columns of one mma
 constexpr int kBlockK = 128;  // channels per ring stage
 constexpr int kStages = 4;
 
-// Bytes of scales of one stage: f32 [16][128 / G], or the aligned 32-bit words
-// that hold 128 / G bytes at any offset, [16][words].
-template <int G, bool U8>
+// What one stage holds: 16 rows of 64 code bytes, the 16-byte units of a row
+// permuted by (row / 2) % 4 so that the fragment reads meet no bank twice, and
+// the rows' scales of the block.  ALIGNED (K a multiple of 128 and 16-byte
+// aligned scales: every row's scales of a block start on their own size): one
+// copy per row, f32 [16][128 / G], or bytes in one or two words per row.
+// Otherwise 4-byte copies: f32 as above, or the aligned words that hold 128 / G
+// bytes at any offset.
+template <int G, bool U8, bool ALIGNED>
 struct Stage {
   static constexpr int kGroups = kBlockK / G;
-  static constexpr int kWords = U8 ? (kGroups + 3 + 3) / 4 : kGroups;
+  static constexpr int kWords = !U8 ? kGroups : ALIGNED ? (kGroups + 3) / 4 : (kGroups + 6) / 4;
   static constexpr int kCodeBytes = 16 * 64;
   static constexpr int kBytes = kCodeBytes + 16 * kWords * 4;
 };
 
-// The two E2M1 codes of byte `i` of w as f16x2, element 0 (the low nibble) in
+// The two E2M1 codes of byte I of w as f16x2, element 0 (the low nibble) in
 // the low half: the hardware conversion, exact.
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w, int i) {
+template <int I>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w) {
   uint32_t r;
-  asm("{\n .reg .b8 b0, b1, b2, b3;\n .reg .b8 t;\n mov.b32 {b0, b1, b2, b3}, %1;\n"
-      " cvt.rn.f16x2.e2m1x2 %0, b0;\n}"
-      : "=r"(r)
-      : "r"(w >> (8 * i)));
+  if constexpr (I == 0)
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %1;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, b0;\n}" : "=r"(r) : "r"(w));
+  else if constexpr (I == 1)
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %1;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, b1;\n}" : "=r"(r) : "r"(w));
+  else if constexpr (I == 2)
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %1;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, b2;\n}" : "=r"(r) : "r"(w));
+  else
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %1;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, b3;\n}" : "=r"(r) : "r"(w));
   return r;
 }
 
@@ -74,11 +88,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         "f"(c[2]), "f"(c[3]));
 }
 
-// Asynchronous copies of 16 or 4 bytes into shared memory; only the first
+// Asynchronous copies of 16, 8 or 4 bytes into shared memory; only the first
 // `bytes` are read, the rest is zero.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -117,9 +134,11 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// 2^(b - 127): the exponent field itself, and 2^-127 as the denormal it is.
-__device__ __forceinline__ float ue8m0(uint32_t b) {
-  return __uint_as_float(b ? b << 23 : 0x00400000u);
+// 2^(b - 127) for byte j of w: the exponent field itself, and 2^-127 (byte 0)
+// as the denormal it is.
+__device__ __forceinline__ float ue8m0(uint32_t w, int j) {
+  const uint32_t f = (j == 3 ? w >> 1 : w << (23 - 8 * j)) & 0x7F800000u;
+  return __uint_as_float(max(f, 0x00400000u));
 }
 
 // Shared memory: the warps' rings, the x rows (f16, row stride 2 Kp + 64 bytes
@@ -156,11 +175,11 @@ __device__ __forceinline__ int64_t source_row(const MatvecArgs& a, int r, unsign
   return s;
 }
 
-template <int G, bool U8>
+template <int G, bool U8, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_matvec_kernel(const MatvecArgs a, const int C, unsigned* err) {
   pdl_enter();
-  using St = Stage<G, U8>;
+  using St = Stage<G, U8, ALIGNED>;
   extern __shared__ __align__(128) uint8_t smem[];
   const Smem L = smem_layout(St::kBytes, a.K, a.E, C);
   const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
@@ -176,35 +195,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t xrow_bytes = x_stride(a.K);
   const int64_t sf_row = a.K / G;  // scales of one weight row
 
-  // first[e]: items of the experts before e
-  if (warp == 0) {
-    int before = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      int runs = 0;
-      if (e < a.E) {
-        int64_t lo = 0, hi = a.R;
-        if (a.offsets != nullptr) {
-          lo = __ldg(a.offsets + e);
-          hi = __ldg(a.offsets + e + 1);
-          if (lo < 0 || hi > a.R) flag_error(err, MOE_DEVERR_POS_RANGE);
-          if (lo < 0) lo = 0;
-          if (hi > a.R) hi = a.R;
-        }
-        runs = hi > lo ? (int)((hi - lo + C - 1) / C) : 0;
-      }
-      int sum = runs;
+  // first[e]: items of the experts before e; each thread counts two experts
+  {
+    static_assert(2 * kThreads >= MOE_MAX_EXPERTS, "two experts per thread");
+    int* totals = reinterpret_cast<int*>(red);
+    int runs[2] = {0, 0};
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += v;
+    for (int i = 0; i < 2; ++i) {
+      const int e = 2 * tid + i;
+      if (e >= a.E) continue;
+      int64_t lo = 0, hi = a.R;
+      if (a.offsets != nullptr) {
+        lo = __ldg(a.offsets + e);
+        hi = __ldg(a.offsets + e + 1);
+        if (lo < 0 || hi > a.R) flag_error(err, MOE_DEVERR_POS_RANGE);
+        if (lo < 0) lo = 0;
+        if (hi > a.R) hi = a.R;
       }
-      if (e < a.E) first[e] = before + sum - runs;
-      before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      runs[i] = hi > lo ? (int)((hi - lo + C - 1) / C) : 0;
     }
-    if (lane == 0) first[a.E] = before;
+    int sum = runs[0] + runs[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) totals[warp] = sum;
+    __syncthreads();
+    int before = sum - runs[0] - runs[1];
+    for (int w = 0; w < warp; ++w) before += totals[w];
+    if (2 * tid <= a.E) first[2 * tid] = before;
+    if (2 * tid + 1 <= a.E) first[2 * tid + 1] = before + runs[0];
+    if (tid == kThreads - 1 && a.E == 2 * kThreads) first[a.E] = before + runs[0] + runs[1];
+    __syncthreads();
   }
-  __syncthreads();
   const int64_t units = (int64_t)first[a.E] * tiles;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
 
@@ -226,6 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int mine = b_hi - b_lo;  // blocks of each tile this warp sums
 
   const uint32_t ring = sbase + L.ring + (uint32_t)(warp * kStages * St::kBytes);
+  const uint32_t ring_end = ring + kStages * St::kBytes;
+  // this lane's 16 bytes of rows g and g + 8 in a stage ((g + 8) / 2 % 4 = g / 2 % 4)
+  const uint32_t code_dst = (uint32_t)(g * 64 + ((q ^ ((g >> 1) & 3)) << 4));
+  // whether its channels of the last block exist
+  const bool tail_ok = (nblk - 1) * 64 + q * 16 < a.K / 2;
   int parity = 0;
 
   int64_t u = u0;
@@ -241,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         hi = mid;
     }
     const int tile0 = (int)(u - (int64_t)item * tiles);
-    int64_t left = u1 - u;
+    const int64_t left = u1 - u;
     const int ntiles = (int)(left < tiles - tile0 ? left : tiles - tile0);
     u += ntiles;
     int64_t lo = 0, hi = a.R;
@@ -258,39 +287,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_tiles = ntiles > team ? (ntiles - team + teams - 1) / teams : 0;
     const int steps = my_tiles * mine;
     const int64_t m_base = (int64_t)e * M;
-    // weight row of tile row i (0..15), or -1
+    // weight row of row i of a tile; past the last output the last one, whose
+    // products are not stored
     auto weight_row = [&](int tile, int i) -> int64_t {
-      int nn;
       if (a.swiglu) {
-        nn = tile * 8 + (i & 7);
-        if (nn >= a.N) return -1;
-        return m_base + nn + (i >> 3) * a.N;
+        const int nn = tile * 8 + (i & 7);
+        return m_base + (nn < a.N ? nn : a.N - 1) + (i >> 3) * a.N;
       }
-      nn = tile * 16 + i;
-      return nn < a.N ? m_base + nn : -1;
+      const int nn = tile * 16 + i;
+      return m_base + (nn < a.N ? nn : a.N - 1);
     };
-    int ld_tile = tile0 + team, ld_blk = b_lo;
-    auto issue = [&](int step) {
-      if (step < steps) {
-        const uint32_t st = ring + (uint32_t)((step % kStages) * St::kBytes);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = g + 8 * i;
-          const int64_t m = weight_row(ld_tile, row);
-          const int c = ld_blk * 64 + q * 16;
-          const bool ok = m >= 0 && c < a.K / 2;
-          cp_async16(st + row * 64 + ((q ^ ((row >> 1) & 3)) << 4),
-                     a.w + (ok ? m * (a.K / 2) + c : 0), ok ? 16 : 0);
-        }
-        const uint32_t sst = st + St::kCodeBytes;
-        if (U8) {
+
+    // the stream of stages: where the next one comes from and goes to
+    int ld_tile = tile0 + team, ld_blk = b_lo, to_issue = steps;
+    uint32_t ld_st = ring;
+    const uint8_t *code_lo = nullptr, *code_hi = nullptr;
+    int64_t sf_at = 0;  // ALIGNED: element of this lane's scales in block ld_blk
+    auto open_tile = [&]() {
+      code_lo = a.w + weight_row(ld_tile, g) * (a.K / 2) + ld_blk * 64 + q * 16;
+      code_hi = a.w + weight_row(ld_tile, g + 8) * (a.K / 2) + ld_blk * 64 + q * 16;
+      if (ALIGNED) {
+        const bool half = !U8 && G == 16;  // two copies per row
+        const int row = half ? lane >> 1 : lane & 15;
+        sf_at = weight_row(ld_tile, row) * sf_row + ld_blk * St::kGroups + (half ? (lane & 1) * 4 : 0);
+      }
+    };
+    if (steps > 0) open_tile();
+    auto issue = [&]() {
+      if (to_issue > 0) {
+        --to_issue;
+        const int bytes = ld_blk + 1 < nblk || tail_ok ? 16 : 0;
+        // (a block past K still points inside its row: nothing of it is read)
+        cp_async16(ld_st + code_dst, bytes ? code_lo : a.w, bytes);
+        cp_async16(ld_st + code_dst + 512, bytes ? code_hi : a.w, bytes);
+        code_lo += 64;
+        code_hi += 64;
+        const uint32_t sst = ld_st + St::kCodeBytes;
+        if (ALIGNED) {
+          if (!U8) {
+            const float* p = static_cast<const float*>(a.sf) + sf_at;
+            if (G == 16)
+              cp_async16(sst + lane * 16, p, 16);
+            else if (lane < 16) {
+              if (G == 32) cp_async16(sst + lane * 16, p, 16);
+              if (G == 64) cp_async8(sst + lane * 8, p);
+              if (G == 128) cp_async4(sst + lane * 4, p, 4);
+            }
+          } else if (lane < 16) {
+            const uint8_t* p = static_cast<const uint8_t*>(a.sf);
+            if (G == 16) cp_async8(sst + lane * 8, p + sf_at);
+            if (G == 32) cp_async4(sst + lane * 4, p + sf_at, 4);
+            if (G >= 64) {  // the aligned word that holds the bytes
+              const int64_t at = sf_at & ~(int64_t)3, end = (int64_t)a.E * M * sf_row;
+              cp_async4(sst + lane * 4, p + at, end - at < 4 ? (int)(end - at) : 4);
+            }
+          }
+          sf_at += St::kGroups;
+        } else if (U8) {
           const uint8_t* sf = static_cast<const uint8_t*>(a.sf);
           const int64_t end = (int64_t)a.E * M * sf_row;
           for (int p = lane; p < 16 * St::kWords; p += 32) {
             const int row = p / St::kWords, wi = p % St::kWords;
             const int64_t m = weight_row(ld_tile, row);
             const int64_t at = ((m * sf_row + ld_blk * St::kGroups) & ~(int64_t)3) + 4 * wi;
-            int64_t bytes = m >= 0 ? end - at : 0;
+            int64_t bytes = end - at;
             bytes = bytes < 0 ? 0 : bytes > 4 ? 4 : bytes;
             cp_async4(sst + p * 4, sf + (bytes > 0 ? at : 0), (int)bytes);
           }
@@ -300,18 +360,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = p / St::kGroups, j = p % St::kGroups;
             const int64_t m = weight_row(ld_tile, row);
             const int gi = ld_blk * St::kGroups + j;
-            const bool ok = m >= 0 && gi < sf_row;
+            const bool ok = gi < sf_row;
             cp_async4(sst + p * 4, sf + (ok ? m * sf_row + gi : 0), ok ? 4 : 0);
           }
         }
+        ld_st += St::kBytes;
+        if (ld_st == ring_end) ld_st = ring;
         if (++ld_blk == b_hi) {
           ld_blk = b_lo;
           ld_tile += teams;
+          if (to_issue > 0) open_tile();
         }
       }
       cp_async_commit();
     };
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue();
 
     // x: each half warp converts one block of 128 channels of one row
     for (int t = tid >> 4; t < n * nblk; t += kThreads / 16) {
@@ -344,52 +408,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
 
-    const uint32_t xcol = sbase + L.x + g * xrow_bytes;
+    const uint32_t xcol = sbase + L.x + g * xrow_bytes + (G == 16 ? q * 8 : q * 16);
     const bool has_col = g < n;
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int tile = tile0 + team, blk = b_lo;
-    // a team whose warps have no block left still joins its tiles' sums
+    uint32_t st = ring;
+    // where a row's scales start in its first word (U8, not whole words)
+    constexpr bool kShift = U8 && (!ALIGNED || G >= 64);
+    int sf_off[2] = {0, 0};
+    auto tile_offsets = [&]() {
+      if (kShift) {
+        sf_off[0] = (int)((weight_row(tile, g) * sf_row) & 3);
+        sf_off[1] = (int)((weight_row(tile, g + 8) * sf_row) & 3);
+      }
+    };
+    tile_offsets();
+    // a warp without a block of its own still joins its team's sums
     const int loop = mine > 0 ? steps : my_tiles;
     for (int step = 0; step < loop; ++step) {
       if (mine > 0) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
-        issue(step + kStages - 1);
-        const uint32_t st = ring + (uint32_t)((step % kStages) * St::kBytes);
+        issue();
         const uint32_t sst = st + St::kCodeBytes;
         const float2 xc = *reinterpret_cast<const float2*>(xs + blk * kMaxRows + 2 * q);
         // scales of rows g and g + 8
         float s[2][St::kGroups];
-        if (U8) {
+        uint32_t sw[2][St::kWords];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int row = g + 8 * i;
-            const int64_t m = weight_row(tile, row);
-            const int sh = 8 * (int)((m * sf_row + blk * St::kGroups) & 3);
-            uint32_t w[St::kWords];
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t at = sst + (g + 8 * i) * (St::kWords * 4);
+          if constexpr (St::kWords % 4 == 0) {
 #pragma unroll
-            for (int j = 0; j < St::kWords; ++j) w[j] = lds32(sst + (row * St::kWords + j) * 4);
+            for (int j = 0; j < St::kWords; j += 4) {
+              const uint4 v = lds128(at + j * 4);
+              sw[i][j] = v.x, sw[i][j + 1] = v.y, sw[i][j + 2] = v.z, sw[i][j + 3] = v.w;
+            }
+          } else if constexpr (St::kWords == 2) {
+            const uint2 v = lds64(at);
+            sw[i][0] = v.x, sw[i][1] = v.y;
+          } else {
 #pragma unroll
-            for (int j = 0; j < St::kGroups; ++j) {
+            for (int j = 0; j < St::kWords; ++j) sw[i][j] = lds32(at + j * 4);
+          }
+#pragma unroll
+          for (int j = 0; j < St::kGroups; ++j) {
+            if constexpr (!U8) {
+              s[i][j] = __uint_as_float(sw[i][j]);
+            } else {
               const int wi = j >> 2;
-              const uint32_t word =
-                  wi + 1 < St::kWords ? __funnelshift_r(w[wi], w[wi + 1], sh) : w[wi] >> sh;
-              s[i][j] = ue8m0((word >> (8 * (j & 3))) & 0xFFu);
+              uint32_t word = sw[i][wi];
+              if constexpr (kShift) {
+                const int sh = 8 * ((sf_off[i] + blk * St::kGroups) & 3);
+                if constexpr (ALIGNED)
+                  word >>= sh;
+                else
+                  word = __funnelshift_r(word, wi + 1 < St::kWords ? sw[i][wi + 1] : 0u, sh);
+              }
+              s[i][j] = ue8m0(word, j & 3);
             }
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < St::kGroups; ++j)
-              s[i][j] = __uint_as_float(lds32(sst + ((g + 8 * i) * St::kGroups + j) * 4));
         }
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f}, blk_acc[4];
         auto flush = [&](int gi) {  // a group is complete: scale its sums
-          acc[0] = __fmaf_rn(s[0][gi] * xc.x, part[0], acc[0]);
-          acc[1] = __fmaf_rn(s[0][gi] * xc.y, part[1], acc[1]);
-          acc[2] = __fmaf_rn(s[1][gi] * xc.x, part[2], acc[2]);
-          acc[3] = __fmaf_rn(s[1][gi] * xc.y, part[3], acc[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            blk_acc[i] = gi == 0 ? s[i >> 1][gi] * part[i]
+                                 : __fmaf_rn(s[i >> 1][gi], part[i], blk_acc[i]);
         };
         const uint32_t xb = xcol + (uint32_t)blk * 256;
 #pragma unroll
@@ -398,35 +483,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t lo_row = st + g * 64 + unit, hi_row = lo_row + 8 * 64;
           uint32_t a0[4], a1[4];
           uint4 x = make_uint4(0, 0, 0, 0);
-          if (G == 16) {
+          if constexpr (G == 16) {
             // the 16 channels of a group: 2 bytes of codes per lane
             const uint32_t w0 = lds16(lo_row + 2 * q), w1 = lds16(lo_row + 8 + 2 * q);
             const uint32_t w2 = lds16(hi_row + 2 * q), w3 = lds16(hi_row + 8 + 2 * q);
-            a0[0] = e2m1x2_to_f16x2(w0, 0), a0[2] = e2m1x2_to_f16x2(w0, 1);
-            a0[1] = e2m1x2_to_f16x2(w2, 0), a0[3] = e2m1x2_to_f16x2(w2, 1);
-            a1[0] = e2m1x2_to_f16x2(w1, 0), a1[2] = e2m1x2_to_f16x2(w1, 1);
-            a1[1] = e2m1x2_to_f16x2(w3, 0), a1[3] = e2m1x2_to_f16x2(w3, 1);
+            a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
+            a0[1] = e2m1x2_to_f16x2<0>(w2), a0[3] = e2m1x2_to_f16x2<1>(w2);
+            a1[0] = e2m1x2_to_f16x2<0>(w1), a1[2] = e2m1x2_to_f16x2<1>(w1);
+            a1[1] = e2m1x2_to_f16x2<0>(w3), a1[3] = e2m1x2_to_f16x2<1>(w3);
             if (has_col) {
-              const uint2 p = lds64(xb + j * 64 + q * 8), r = lds64(xb + j * 64 + 32 + q * 8);
+              const uint2 p = lds64(xb + j * 64), r = lds64(xb + j * 64 + 32);
               x = make_uint4(p.x, p.y, r.x, r.y);
             }
           } else {
             const uint32_t w0 = lds32(lo_row + 4 * q), w1 = lds32(hi_row + 4 * q);
-            a0[0] = e2m1x2_to_f16x2(w0, 0), a0[2] = e2m1x2_to_f16x2(w0, 1);
-            a0[1] = e2m1x2_to_f16x2(w1, 0), a0[3] = e2m1x2_to_f16x2(w1, 1);
-            a1[0] = e2m1x2_to_f16x2(w0, 2), a1[2] = e2m1x2_to_f16x2(w0, 3);
-            a1[1] = e2m1x2_to_f16x2(w1, 2), a1[3] = e2m1x2_to_f16x2(w1, 3);
-            if (has_col) x = lds128(xb + j * 64 + q * 16);
+            a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
+            a0[1] = e2m1x2_to_f16x2<0>(w1), a0[3] = e2m1x2_to_f16x2<1>(w1);
+            a1[0] = e2m1x2_to_f16x2<2>(w0), a1[2] = e2m1x2_to_f16x2<3>(w0);
+            a1[1] = e2m1x2_to_f16x2<2>(w1), a1[3] = e2m1x2_to_f16x2<3>(w1);
+            if (has_col) x = lds128(xb + j * 64);
           }
-          const bool start = G <= 32 || (j * 32) % G == 0;
-          mma_16816(part, a0, x.x, x.y, start);
-          if (G == 16) flush(2 * j);
+          mma_16816(part, a0, x.x, x.y, G <= 32 || (j * 32) % G == 0);
+          if constexpr (G == 16) flush(2 * j);
           mma_16816(part, a1, x.z, x.w, G == 16);
-          if (G == 16)
+          if constexpr (G == 16)
             flush(2 * j + 1);
           else if ((j * 32 + 32) % G == 0)
             flush((j * 32) / G);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = __fmaf_rn(i & 1 ? xc.y : xc.x, blk_acc[i], acc[i]);
+        st += St::kBytes;
+        if (st == ring_end) st = ring;
         if (++blk < b_hi) continue;
         blk = b_lo;
       }
@@ -468,32 +556,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
       tile += teams;
+      tile_offsets();
     }
     cp_async_wait<0>();
     __syncthreads();  // x and the rings are free for the next item
   }
 }
 
-template <int G, bool U8>
+template <int G, bool U8, bool ALIGNED>
 cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
+  constexpr int kStageBytes = Stage<G, U8, ALIGNED>::kBytes;
   // rows per item: 8 columns of the mma, fewer where a long x would not fit
   int C = kMaxRows;
-  while (C > 1 && smem_layout(Stage<G, U8>::kBytes, a.K, a.E, C).total > 220 * 1024) C >>= 1;
-  const size_t smem = smem_layout(Stage<G, U8>::kBytes, a.K, a.E, C).total;
-  cudaError_t e = allow_max_dynamic_smem(expert_matvec_kernel<G, U8>);
+  while (C > 1 && smem_layout(kStageBytes, a.K, a.E, C).total > 220 * 1024) C >>= 1;
+  const size_t smem = smem_layout(kStageBytes, a.K, a.E, C).total;
+  auto* kernel = expert_matvec_kernel<G, U8, ALIGNED>;
+  cudaError_t e = allow_max_dynamic_smem(kernel);
   if (e != cudaSuccess) return e;
   int64_t items = (a.offsets ? a.E : 1) + a.R / C;
   if (items > a.R) items = a.R;
   const int per_tile = a.swiglu ? 8 : 16;
   const int64_t units = items * ((a.N + per_tile - 1) / per_tile);
   const int64_t blocks = units < c.num_sms ? units : c.num_sms;
-  return launch_pdl(expert_matvec_kernel<G, U8>, dim3((unsigned)blocks), kThreads, smem, c.stream,
-                    a, C, c.err);
+  return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, smem, c.stream, a, C, c.err);
 }
 
 template <int G>
 cudaError_t launch_g(const LaunchCtx& c, const MatvecArgs& a) {
-  return a.sf_type == MOE_WSF_UE8M0 ? launch_t<G, true>(c, a) : launch_t<G, false>(c, a);
+  const bool al = a.K % kBlockK == 0 && (reinterpret_cast<uintptr_t>(a.sf) & 15u) == 0;
+  if (a.sf_type == MOE_WSF_UE8M0)
+    return al ? launch_t<G, true, true>(c, a) : launch_t<G, true, false>(c, a);
+  return al ? launch_t<G, false, true>(c, a) : launch_t<G, false, false>(c, a);
 }
 
 }  // namespace
