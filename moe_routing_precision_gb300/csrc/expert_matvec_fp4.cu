@@ -12,7 +12,7 @@
 // hardware conversion E2M1 -> f16, which is exact.  (tcgen05.mma takes 4-bit
 // weights only beside activations of 8 bits or fewer, which would round x.)
 //
-// x is bf16, which f16 cannot hold in range, so each block of 128 channels of
+// x is bf16, which f16 cannot hold in range, so each block of 256 channels of
 // a row is scaled by the power of two that brings its largest magnitude to
 // [2^14, 2^15).  bf16's 8 significant bits fit f16's 11: a channel is exact
 // unless it is below 2^-31 of its block's largest, and then off by less than
@@ -25,7 +25,7 @@
 // a tile's channels (s chosen so that the units fill the warps; their sums are
 // added through shared memory in a fixed order).  Each warp streams its codes
 // and scales through a ring of its own in shared memory with cp.async, several
-// blocks of 128 channels ahead, so no barrier stands in the stream.
+// blocks of 256 channels ahead, so no barrier stands in the stream.
 //
 // With SwiGLU a tile is 8 gate outputs and the 8 up outputs of the same
 // channels, which the fragment layout leaves in one lane.
@@ -39,21 +39,24 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 8;   // columns of one mma
-constexpr int kBlockK = 128;  // channels per ring stage
-constexpr int kStages = 4;
+constexpr int kBlockK = 256;  // channels per ring stage
+constexpr int kStages = 3;
+constexpr int kRowBytes = kBlockK / 2 + 16;  // codes of a row in a stage, padded
 
-// What one stage holds: 16 rows of 64 code bytes, the 16-byte units of a row
-// permuted by (row / 2) % 4 so that the fragment reads meet no bank twice, and
-// the rows' scales of the block.  ALIGNED (K a multiple of 128 and 16-byte
-// aligned scales: every row's scales of a block start on their own size): one
-// copy per row, f32 [16][128 / G], or bytes in one or two words per row.
-// Otherwise 4-byte copies: f32 as above, or the aligned words that hold 128 / G
-// bytes at any offset.
+// What one stage holds: 16 rows of 128 code bytes, 144 bytes apart so that the
+// 8 rows x 4 lanes of a fragment read meet 32 banks, and the rows' scales of the
+// block.  ALIGNED (K a multiple of 128 and 16-byte aligned scales): a row's
+// scales of half a block start on a multiple of their own size, and each lane
+// copies those of one half row.  Otherwise, and for bytes of G >= 64, 4-byte
+// copies: f32 as above, or the aligned words that hold 256 / G bytes at any
+// offset.
 template <int G, bool U8, bool ALIGNED>
 struct Stage {
   static constexpr int kGroups = kBlockK / G;
-  static constexpr int kWords = !U8 ? kGroups : ALIGNED ? (kGroups + 3) / 4 : (kGroups + 6) / 4;
-  static constexpr int kCodeBytes = 16 * 64;
+  static constexpr bool kHalves = ALIGNED && (!U8 || G <= 32);
+  static constexpr int kWords = !U8 ? kGroups : kHalves ? kGroups / 4 : (kGroups + 6) / 4;
+  static constexpr int kCodeBytes = 16 * kRowBytes;
+  // a whole number of 16 bytes
   static constexpr int kBytes = kCodeBytes + 16 * kWords * 4;
 };
 
@@ -94,8 +97,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -134,16 +141,20 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// 2^(b - 127) for byte j of w: the exponent field itself, and 2^-127 (byte 0)
-// as the denormal it is.
-__device__ __forceinline__ float ue8m0(uint32_t w, int j) {
-  const uint32_t f = (j == 3 ? w >> 1 : w << (23 - 8 * j)) & 0x7F800000u;
-  return __uint_as_float(max(f, 0x00400000u));
+// 2^(b - 127) of the four bytes of w: the hardware conversion to bf16, exact
+// (2^-127 is a denormal there too).
+__device__ __forceinline__ void ue8m0x4(uint32_t w, float (&s)[4]) {
+  uint32_t lo, hi;
+  asm("{\n .reg .b16 h0, h1;\n mov.b32 {h0, h1}, %2;\n cvt.rn.bf16x2.ue8m0x2 %0, h0;\n"
+      " cvt.rn.bf16x2.ue8m0x2 %1, h1;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  s[0] = bf16_lo(lo), s[1] = bf16_hi(lo), s[2] = bf16_lo(hi), s[3] = bf16_hi(hi);
 }
 
 // Shared memory: the warps' rings, the x rows (f16, row stride 2 Kp + 64 bytes
 // so that neighbouring rows fall into different halves of the banks), the
-// powers of two [Kp / 128][8], two buffers of partial sums, the items' prefix.
+// powers of two [Kp / 256][8], two buffers of partial sums, the items' prefix.
 struct Smem {
   uint32_t ring, x, xs, red, first, total;
 };
@@ -251,10 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const uint32_t ring = sbase + L.ring + (uint32_t)(warp * kStages * St::kBytes);
   const uint32_t ring_end = ring + kStages * St::kBytes;
-  // this lane's 16 bytes of rows g and g + 8 in a stage ((g + 8) / 2 % 4 = g / 2 % 4)
-  const uint32_t code_dst = (uint32_t)(g * 64 + ((q ^ ((g >> 1) & 3)) << 4));
-  // whether its channels of the last block exist
-  const bool tail_ok = (nblk - 1) * 64 + q * 16 < a.K / 2;
+  // this lane's 16 bytes of the first half of row g in a stage
+  const uint32_t code_dst = (uint32_t)(g * kRowBytes + q * 16);
+  // which of its four copies of codes exist in the last block
+  const bool tail0 = (nblk - 1) * 128 + q * 16 < a.K / 2;
+  const bool tail1 = (nblk - 1) * 128 + 64 + q * 16 < a.K / 2;
+  const int halves = a.K / 128;  // ALIGNED: half blocks
   int parity = 0;
 
   int64_t u = u0;
@@ -302,50 +315,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ld_tile = tile0 + team, ld_blk = b_lo, to_issue = steps;
     uint32_t ld_st = ring;
     const uint8_t *code_lo = nullptr, *code_hi = nullptr;
-    int64_t sf_at = 0;  // ALIGNED: element of this lane's scales in block ld_blk
+    int64_t sf_at = 0;  // kHalves: this lane's first scale of block ld_blk
     auto open_tile = [&]() {
-      code_lo = a.w + weight_row(ld_tile, g) * (a.K / 2) + ld_blk * 64 + q * 16;
-      code_hi = a.w + weight_row(ld_tile, g + 8) * (a.K / 2) + ld_blk * 64 + q * 16;
-      if (ALIGNED) {
-        const bool half = !U8 && G == 16;  // two copies per row
-        const int row = half ? lane >> 1 : lane & 15;
-        sf_at = weight_row(ld_tile, row) * sf_row + ld_blk * St::kGroups + (half ? (lane & 1) * 4 : 0);
-      }
+      code_lo = a.w + weight_row(ld_tile, g) * (a.K / 2) + ld_blk * 128 + q * 16;
+      code_hi = a.w + weight_row(ld_tile, g + 8) * (a.K / 2) + ld_blk * 128 + q * 16;
+      if (St::kHalves)
+        sf_at = weight_row(ld_tile, lane >> 1) * sf_row + ld_blk * St::kGroups +
+                (lane & 1) * (St::kGroups / 2);
     };
     if (steps > 0) open_tile();
     auto issue = [&]() {
       if (to_issue > 0) {
         --to_issue;
-        const int bytes = ld_blk + 1 < nblk || tail_ok ? 16 : 0;
-        // (a block past K still points inside its row: nothing of it is read)
-        cp_async16(ld_st + code_dst, bytes ? code_lo : a.w, bytes);
-        cp_async16(ld_st + code_dst + 512, bytes ? code_hi : a.w, bytes);
-        code_lo += 64;
-        code_hi += 64;
+        const uint32_t dst = ld_st + code_dst;
+        if (ld_blk + 1 < nblk) {
+          cp_async16(dst, code_lo);
+          cp_async16(dst + 64, code_lo + 64);
+          cp_async16(dst + 8 * kRowBytes, code_hi);
+          cp_async16(dst + 8 * kRowBytes + 64, code_hi + 64);
+        } else {  // channels past K are zero, and nothing of them is read
+          cp_async16(dst, tail0 ? code_lo : a.w, tail0 ? 16 : 0);
+          cp_async16(dst + 64, tail1 ? code_lo + 64 : a.w, tail1 ? 16 : 0);
+          cp_async16(dst + 8 * kRowBytes, tail0 ? code_hi : a.w, tail0 ? 16 : 0);
+          cp_async16(dst + 8 * kRowBytes + 64, tail1 ? code_hi + 64 : a.w, tail1 ? 16 : 0);
+        }
+        code_lo += 128;
+        code_hi += 128;
         const uint32_t sst = ld_st + St::kCodeBytes;
-        if (ALIGNED) {
+        if (St::kHalves) {
+          const bool ok = ld_blk * 2 + (lane & 1) < halves;
           if (!U8) {
-            const float* p = static_cast<const float*>(a.sf) + sf_at;
-            if (G == 16)
-              cp_async16(sst + lane * 16, p, 16);
-            else if (lane < 16) {
-              if (G == 32) cp_async16(sst + lane * 16, p, 16);
-              if (G == 64) cp_async8(sst + lane * 8, p);
-              if (G == 128) cp_async4(sst + lane * 4, p, 4);
+            const float* p = static_cast<const float*>(a.sf) + (ok ? sf_at : 0);
+            if (G == 16) {
+              cp_async16(sst + lane * 32, p, ok ? 16 : 0);
+              cp_async16(sst + lane * 32 + 16, ok ? p + 4 : p, ok ? 16 : 0);
             }
-          } else if (lane < 16) {
-            const uint8_t* p = static_cast<const uint8_t*>(a.sf);
-            if (G == 16) cp_async8(sst + lane * 8, p + sf_at);
-            if (G == 32) cp_async4(sst + lane * 4, p + sf_at, 4);
-            if (G >= 64) {  // the aligned word that holds the bytes
-              const int64_t at = sf_at & ~(int64_t)3, end = (int64_t)a.E * M * sf_row;
-              cp_async4(sst + lane * 4, p + at, end - at < 4 ? (int)(end - at) : 4);
-            }
+            if (G == 32) cp_async16(sst + lane * 16, p, ok ? 16 : 0);
+            if (G == 64) cp_async8(sst + lane * 8, p, ok ? 8 : 0);
+            if (G == 128) cp_async4(sst + lane * 4, p, ok ? 4 : 0);
+          } else {
+            const uint8_t* p = static_cast<const uint8_t*>(a.sf) + (ok ? sf_at : 0);
+            if (G == 16) cp_async8(sst + lane * 8, p, ok ? 8 : 0);
+            if (G == 32) cp_async4(sst + lane * 4, p, ok ? 4 : 0);
           }
           sf_at += St::kGroups;
         } else if (U8) {
           const uint8_t* sf = static_cast<const uint8_t*>(a.sf);
           const int64_t end = (int64_t)a.E * M * sf_row;
+#pragma unroll
           for (int p = lane; p < 16 * St::kWords; p += 32) {
             const int row = p / St::kWords, wi = p % St::kWords;
             const int64_t m = weight_row(ld_tile, row);
@@ -356,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           const float* sf = static_cast<const float*>(a.sf);
+#pragma unroll
           for (int p = lane; p < 16 * St::kGroups; p += 32) {
             const int row = p / St::kGroups, j = p % St::kGroups;
             const int64_t m = weight_row(ld_tile, row);
@@ -377,12 +395,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue();
 
-    // x: each half warp converts one block of 128 channels of one row
-    for (int t = tid >> 4; t < n * nblk; t += kThreads / 16) {
-      const int col = t / nblk, b = t - col * nblk, l16 = tid & 15;
-      const unsigned half = 0xFFFFu << (lane & 16);
+    // x: each warp converts one block of one row
+    for (int t = warp; t < n * nblk; t += kWarps) {
+      const int col = t / nblk, b = t - col * nblk;
       const int64_t sr = source_row(a, r0 + col, err);
-      const int c = b * kBlockK + l16 * 8;
+      const int c = b * kBlockK + lane * 8;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (sr >= 0 && c < a.K) v = ld_v4(static_cast<const uint16_t*>(a.x) + sr * a.K + c);
       float f[8];
@@ -390,10 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(half, m, o));
       // 2^ex brings m's exponent to 14; kept to 126 so that 2^-ex is normal
-      int ex = 14 + 127 - (int)(__float_as_uint(m) >> 23);
+      int ex = (int)(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m)) >> 23);
+      ex = 14 + 127 - ex;
       ex = ex > 126 ? 126 : ex;
       const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
       uint4 h;
@@ -404,17 +420,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         hw[i] = *reinterpret_cast<const uint32_t*>(&p);
       }
       *reinterpret_cast<uint4*>(smem + L.x + col * xrow_bytes + c * 2) = h;
-      if (l16 == 0) xs[b * kMaxRows + col] = __uint_as_float((uint32_t)(127 - ex) << 23);
+      if (lane == 0) xs[b * kMaxRows + col] = __uint_as_float((uint32_t)(127 - ex) << 23);
     }
     __syncthreads();
 
-    const uint32_t xcol = sbase + L.x + g * xrow_bytes + (G == 16 ? q * 8 : q * 16);
-    const bool has_col = g < n;
+    // lanes of columns past the run read the last one's: their sums are not stored
+    const uint32_t xcol =
+        sbase + L.x + (g < n ? g : n - 1) * xrow_bytes + (G == 16 ? q * 8 : q * 16);
+    const uint32_t frag = (uint32_t)(g * kRowBytes + (G == 16 ? q * 2 : q * 4));
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int tile = tile0 + team, blk = b_lo;
     uint32_t st = ring;
-    // where a row's scales start in its first word (U8, not whole words)
-    constexpr bool kShift = U8 && (!ALIGNED || G >= 64);
+    // where a row's scales start in its first word
+    constexpr bool kShift = U8 && !St::kHalves;
     int sf_off[2] = {0, 0};
     auto tile_offsets = [&]() {
       if (kShift) {
@@ -430,42 +448,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async_wait<kStages - 2>();
         __syncwarp();
         issue();
-        const uint32_t sst = st + St::kCodeBytes;
+        const uint32_t sst = st + St::kCodeBytes + g * (St::kWords * 4);
         const float2 xc = *reinterpret_cast<const float2*>(xs + blk * kMaxRows + 2 * q);
         // scales of rows g and g + 8
-        float s[2][St::kGroups];
-        uint32_t sw[2][St::kWords];
+        float s[2][St::kGroups < 4 ? 4 : St::kGroups];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t at = sst + (g + 8 * i) * (St::kWords * 4);
+          uint32_t sw[St::kWords + 1];
+          const uint32_t at = sst + 8 * i * (St::kWords * 4);
           if constexpr (St::kWords % 4 == 0) {
 #pragma unroll
             for (int j = 0; j < St::kWords; j += 4) {
               const uint4 v = lds128(at + j * 4);
-              sw[i][j] = v.x, sw[i][j + 1] = v.y, sw[i][j + 2] = v.z, sw[i][j + 3] = v.w;
+              sw[j] = v.x, sw[j + 1] = v.y, sw[j + 2] = v.z, sw[j + 3] = v.w;
             }
           } else if constexpr (St::kWords == 2) {
             const uint2 v = lds64(at);
-            sw[i][0] = v.x, sw[i][1] = v.y;
+            sw[0] = v.x, sw[1] = v.y;
           } else {
 #pragma unroll
-            for (int j = 0; j < St::kWords; ++j) sw[i][j] = lds32(at + j * 4);
+            for (int j = 0; j < St::kWords; ++j) sw[j] = lds32(at + j * 4);
           }
+          sw[St::kWords] = 0;
+          if constexpr (!U8) {
 #pragma unroll
-          for (int j = 0; j < St::kGroups; ++j) {
-            if constexpr (!U8) {
-              s[i][j] = __uint_as_float(sw[i][j]);
-            } else {
-              const int wi = j >> 2;
-              uint32_t word = sw[i][wi];
-              if constexpr (kShift) {
-                const int sh = 8 * ((sf_off[i] + blk * St::kGroups) & 3);
-                if constexpr (ALIGNED)
-                  word >>= sh;
-                else
-                  word = __funnelshift_r(word, wi + 1 < St::kWords ? sw[i][wi + 1] : 0u, sh);
-              }
-              s[i][j] = ue8m0(word, j & 3);
+            for (int j = 0; j < St::kGroups; ++j) s[i][j] = __uint_as_float(sw[j]);
+          } else {
+            const int sh = 8 * ((sf_off[i] + blk * St::kGroups) & 3);
+#pragma unroll
+            for (int j = 0; j < St::kGroups; j += 4) {
+              uint32_t w = sw[j / 4];
+              if constexpr (kShift) w = __funnelshift_r(w, sw[j / 4 + 1], sh);
+              float v[4];
+              ue8m0x4(w, v);
+#pragma unroll
+              for (int b = 0; b < 4; ++b) s[i][j + b] = v[b];
             }
           }
         }
@@ -476,32 +493,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             blk_acc[i] = gi == 0 ? s[i >> 1][gi] * part[i]
                                  : __fmaf_rn(s[i >> 1][gi], part[i], blk_acc[i]);
         };
-        const uint32_t xb = xcol + (uint32_t)blk * 256;
+        const uint32_t xb = xcol + (uint32_t)blk * (2 * kBlockK);
+        const uint32_t lo_row = st + frag, hi_row = lo_row + 8 * kRowBytes;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t unit = (uint32_t)((j ^ (g >> 1)) << 4);  // rows g and g + 8 alike
-          const uint32_t lo_row = st + g * 64 + unit, hi_row = lo_row + 8 * 64;
+        for (int j = 0; j < kBlockK / 32; ++j) {
           uint32_t a0[4], a1[4];
-          uint4 x = make_uint4(0, 0, 0, 0);
+          uint4 x;
           if constexpr (G == 16) {
             // the 16 channels of a group: 2 bytes of codes per lane
-            const uint32_t w0 = lds16(lo_row + 2 * q), w1 = lds16(lo_row + 8 + 2 * q);
-            const uint32_t w2 = lds16(hi_row + 2 * q), w3 = lds16(hi_row + 8 + 2 * q);
+            const uint32_t w0 = lds16(lo_row + 16 * j), w1 = lds16(lo_row + 16 * j + 8);
+            const uint32_t w2 = lds16(hi_row + 16 * j), w3 = lds16(hi_row + 16 * j + 8);
             a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
             a0[1] = e2m1x2_to_f16x2<0>(w2), a0[3] = e2m1x2_to_f16x2<1>(w2);
             a1[0] = e2m1x2_to_f16x2<0>(w1), a1[2] = e2m1x2_to_f16x2<1>(w1);
             a1[1] = e2m1x2_to_f16x2<0>(w3), a1[3] = e2m1x2_to_f16x2<1>(w3);
-            if (has_col) {
-              const uint2 p = lds64(xb + j * 64), r = lds64(xb + j * 64 + 32);
-              x = make_uint4(p.x, p.y, r.x, r.y);
-            }
+            const uint2 p = lds64(xb + j * 64), r = lds64(xb + j * 64 + 32);
+            x = make_uint4(p.x, p.y, r.x, r.y);
           } else {
-            const uint32_t w0 = lds32(lo_row + 4 * q), w1 = lds32(hi_row + 4 * q);
+            const uint32_t w0 = lds32(lo_row + 16 * j), w1 = lds32(hi_row + 16 * j);
             a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
             a0[1] = e2m1x2_to_f16x2<0>(w1), a0[3] = e2m1x2_to_f16x2<1>(w1);
             a1[0] = e2m1x2_to_f16x2<2>(w0), a1[2] = e2m1x2_to_f16x2<3>(w0);
             a1[1] = e2m1x2_to_f16x2<2>(w1), a1[3] = e2m1x2_to_f16x2<3>(w1);
-            if (has_col) x = lds128(xb + j * 64);
+            x = lds128(xb + j * 64);
           }
           mma_16816(part, a0, x.x, x.y, G <= 32 || (j * 32) % G == 0);
           if constexpr (G == 16) flush(2 * j);
@@ -566,8 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int G, bool U8, bool ALIGNED>
 cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
   constexpr int kStageBytes = Stage<G, U8, ALIGNED>::kBytes;
-  // rows per item: 8 columns of the mma, fewer where a long x would not fit
+  // rows per item: the 8 columns of the mma, but no more than an expert can get
+  // (a token's experts are distinct: one row per token; more would only take
+  // more items), and fewer where a long x would not fit
   int C = kMaxRows;
+  while (C > 1 && C / 2 >= (a.R + a.k - 1) / a.k) C >>= 1;
   while (C > 1 && smem_layout(kStageBytes, a.K, a.E, C).total > 220 * 1024) C >>= 1;
   const size_t smem = smem_layout(kStageBytes, a.K, a.E, C).total;
   auto* kernel = expert_matvec_kernel<G, U8, ALIGNED>;
@@ -583,7 +600,7 @@ cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
 
 template <int G>
 cudaError_t launch_g(const LaunchCtx& c, const MatvecArgs& a) {
-  const bool al = a.K % kBlockK == 0 && (reinterpret_cast<uintptr_t>(a.sf) & 15u) == 0;
+  const bool al = a.K % 128 == 0 && (reinterpret_cast<uintptr_t>(a.sf) & 15u) == 0;
   if (a.sf_type == MOE_WSF_UE8M0)
     return al ? launch_t<G, true, true>(c, a) : launch_t<G, true, false>(c, a);
   return al ? launch_t<G, false, true>(c, a) : launch_t<G, false, false>(c, a);
