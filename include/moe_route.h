@@ -676,7 +676,7 @@ moe_status_t moe_combine_backward(const void *grad_out, int32_t grad_dtype, cons
  *   maps return it: src(r) = sorted_src[r] / num_topk, and a negative entry gives
  *   a row of zeros
  *   out [num_rows, N] in out_dtype (MOE_OUT_*)
- * group is 16, 32, 64 or 128; K % 32 == 0, K % group == 0, K <= 65536, N <= 2^24,
+ * group is 16, 32, 64 or 128; K % 32 == 0, K % group == 0, K <= 65536, M * K < 2^32,
  * num_rows <= MOE_MATVEC_MAX_ROWS.  offsets
  * beyond num_rows or a src outside [0, num_x) set MOE_DEVERR_POS_RANGE; such rows
  * are not written, or are zero.

@@ -33,6 +33,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -40,12 +42,12 @@ constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 8;   // columns of one mma
 constexpr int kBlockK = 256;  // channels per ring stage
-constexpr int kStages = 3;
+constexpr int kMinStages = 3, kMaxStages = 4;
 constexpr int kRowBytes = kBlockK / 2 + 16;  // codes of a row in a stage, padded
 
 // What one stage holds: 16 rows of 128 code bytes, 144 bytes apart so that the
 // 8 rows x 4 lanes of a fragment read meet 32 banks, and the rows' scales of the
-// block.  ALIGNED (K a multiple of 128 and 16-byte aligned scales): a row's
+// block.  ALIGNED (K a multiple of 256 and 16-byte aligned scales): a row's
 // scales of half a block start on a multiple of their own size, and each lane
 // copies those of one half row.  Otherwise, and for bytes of G >= 64, 4-byte
 // copies: f32 as above, or the aligned words that hold 256 / G bytes at any
@@ -55,6 +57,7 @@ struct Stage {
   static constexpr int kGroups = kBlockK / G;
   static constexpr bool kHalves = ALIGNED && (!U8 || G <= 32);
   static constexpr int kWords = !U8 ? kGroups : kHalves ? kGroups / 4 : (kGroups + 6) / 4;
+  static_assert(kGroups >= 1, "a block holds whole groups");
   static constexpr int kCodeBytes = 16 * kRowBytes;
   // a whole number of 16 bytes
   static constexpr int kBytes = kCodeBytes + 16 * kWords * 4;
@@ -97,9 +100,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
@@ -115,27 +115,51 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Waits until at most n of this thread's groups are in flight.
+__device__ __forceinline__ void cp_async_wait_but(int n) {
+  static_assert(kMinStages == 3 && kMaxStages == 4, "one case per ring length");
+  if (n == 1)
+    cp_async_wait<1>();
+  else
+    cp_async_wait<2>();
+}
+// Shared-memory loads at a 32-bit address plus a constant.  Volatile: kept in
+// program order, between the products that use them (grouped ahead of a block's
+// products, as the compiler would have them, they fill the load queue: 16 warps
+// then wait on it, 364 -> 448 us for 32768 outputs of 8 experts, K = 7168).
+template <int OFF>
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF));
   return v;
 }
+template <int OFF>
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  asm volatile("ld.shared.u16 %0, [%1+%2];" : "=h"(v) : "r"(a), "n"(OFF));
   return v;
 }
+template <int OFF>
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2+%3];" : "=r"(v.x), "=r"(v.y) : "r"(a), "n"(OFF));
   return v;
 }
+template <int OFF>
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4+%5];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
+               : "r"(a), "n"(OFF));
   return v;
+}
+// f(0), ..., f(N - 1), the arguments compile-time constants.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    unrolled<N, I + 1>(static_cast<F&&>(f));
+  }
 }
 __device__ __forceinline__ void group_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -160,10 +184,11 @@ struct Smem {
 };
 __host__ __device__ inline int padded_k(int K) { return (K + kBlockK - 1) / kBlockK * kBlockK; }
 __host__ __device__ inline uint32_t x_stride(int K) { return (uint32_t)padded_k(K) * 2 + 64; }
-__host__ __device__ inline Smem smem_layout(int stage_bytes, int K, int E, int C) {
+__host__ __device__ inline Smem smem_layout(int stage_bytes, int stages, int K, int E,
+                                              int C) {
   Smem s;
   s.ring = 0;
-  s.x = (uint32_t)(kWarps * kStages * stage_bytes);
+  s.x = (uint32_t)(kWarps * stages * stage_bytes);
   s.xs = s.x + (uint32_t)C * x_stride(K);
   s.red = s.xs + (uint32_t)(padded_k(K) / kBlockK) * kMaxRows * 4;
   s.first = s.red + 2 * kWarps * 512;
@@ -188,11 +213,11 @@ __device__ __forceinline__ int64_t source_row(const MatvecArgs& a, int r, unsign
 
 template <int G, bool U8, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1)
-    expert_matvec_kernel(const MatvecArgs a, const int C, unsigned* err) {
+    expert_matvec_kernel(const MatvecArgs a, const int C, const int stages, unsigned* err) {
   pdl_enter();
   using St = Stage<G, U8, ALIGNED>;
   extern __shared__ __align__(128) uint8_t smem[];
-  const Smem L = smem_layout(St::kBytes, a.K, a.E, C);
+  const Smem L = smem_layout(St::kBytes, stages, a.K, a.E, C);
   const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
   int* first = reinterpret_cast<int*>(smem + L.first);
   float* xs = reinterpret_cast<float*>(smem + L.xs);
@@ -202,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int M = a.swiglu ? 2 * a.N : a.N;
   const int per_tile = a.swiglu ? 8 : 16;  // outputs of one tile
   const int tiles = (a.N + per_tile - 1) / per_tile;
-  const int nblk = padded_k(a.K) / kBlockK;
+  const int nblk = (a.K + kBlockK - 1) / kBlockK;
   const uint32_t xrow_bytes = x_stride(a.K);
   const int64_t sf_row = a.K / G;  // scales of one weight row
 
@@ -260,14 +285,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b_hi = b_lo + bpw < nblk ? b_lo + bpw : nblk;
   const int mine = b_hi - b_lo;  // blocks of each tile this warp sums
 
-  const uint32_t ring = sbase + L.ring + (uint32_t)(warp * kStages * St::kBytes);
-  const uint32_t ring_end = ring + kStages * St::kBytes;
+  const uint32_t ring = sbase + L.ring + (uint32_t)(warp * stages * St::kBytes);
+  const uint32_t ring_end = ring + (uint32_t)(stages * St::kBytes);
   // this lane's 16 bytes of the first half of row g in a stage
   const uint32_t code_dst = (uint32_t)(g * kRowBytes + q * 16);
   // which of its four copies of codes exist in the last block
-  const bool tail0 = (nblk - 1) * 128 + q * 16 < a.K / 2;
-  const bool tail1 = (nblk - 1) * 128 + 64 + q * 16 < a.K / 2;
-  const int halves = a.K / 128;  // ALIGNED: half blocks
+  bool tail[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    tail[i] = (nblk - 1) * (kBlockK / 2) + 64 * i + q * 16 < a.K / 2;
   int parity = 0;
 
   int64_t u = u0;
@@ -299,87 +325,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this team's tiles: tile0 + team, + teams, ...; its steps are (tile, block)
     const int my_tiles = ntiles > team ? (ntiles - team + teams - 1) / teams : 0;
     const int steps = my_tiles * mine;
-    const int64_t m_base = (int64_t)e * M;
-    // weight row of row i of a tile; past the last output the last one, whose
-    // products are not stored
-    auto weight_row = [&](int tile, int i) -> int64_t {
-      if (a.swiglu) {
-        const int nn = tile * 8 + (i & 7);
-        return m_base + (nn < a.N ? nn : a.N - 1) + (i >> 3) * a.N;
-      }
-      const int nn = tile * 16 + i;
-      return m_base + (nn < a.N ? nn : a.N - 1);
+    const uint8_t* w_e = a.w + (int64_t)e * M * (a.K / 2);
+    const int64_t sf_e = (int64_t)e * M * sf_row;
+    // weight row, within the expert, of row i of a tile; past the last output
+    // the last one, whose products are not stored
+    auto weight_row = [&](int tile, int i) -> uint32_t {
+      const int nn = tile * per_tile + (a.swiglu ? i & 7 : i);
+      return (uint32_t)((nn < a.N ? nn : a.N - 1) + (a.swiglu ? (i >> 3) * a.N : 0));
     };
 
     // the stream of stages: where the next one comes from and goes to
     int ld_tile = tile0 + team, ld_blk = b_lo, to_issue = steps;
     uint32_t ld_st = ring;
     const uint8_t *code_lo = nullptr, *code_hi = nullptr;
-    int64_t sf_at = 0;  // kHalves: this lane's first scale of block ld_blk
+    const char* sf_at = nullptr;  // kHalves: this lane's first scale of block ld_blk
     auto open_tile = [&]() {
-      code_lo = a.w + weight_row(ld_tile, g) * (a.K / 2) + ld_blk * 128 + q * 16;
-      code_hi = a.w + weight_row(ld_tile, g + 8) * (a.K / 2) + ld_blk * 128 + q * 16;
-      if (St::kHalves)
-        sf_at = weight_row(ld_tile, lane >> 1) * sf_row + ld_blk * St::kGroups +
-                (lane & 1) * (St::kGroups / 2);
+      const uint32_t row_bytes = (uint32_t)a.K / 2, c = (uint32_t)(ld_blk * (kBlockK / 2) + q * 16);
+      code_lo = w_e + weight_row(ld_tile, g) * row_bytes + c;
+      code_hi = w_e + weight_row(ld_tile, g + 8) * row_bytes + c;
+      if (St::kHalves) {
+        const int64_t at = sf_e + weight_row(ld_tile, lane >> 1) * (uint32_t)sf_row +
+                           (uint32_t)(ld_blk * St::kGroups + (lane & 1) * (St::kGroups / 2));
+        sf_at = static_cast<const char*>(a.sf) + at * (U8 ? 1 : 4);
+      }
     };
     if (steps > 0) open_tile();
     auto issue = [&]() {
       if (to_issue > 0) {
         --to_issue;
         const uint32_t dst = ld_st + code_dst;
-        if (ld_blk + 1 < nblk) {
-          cp_async16(dst, code_lo);
-          cp_async16(dst + 64, code_lo + 64);
-          cp_async16(dst + 8 * kRowBytes, code_hi);
-          cp_async16(dst + 8 * kRowBytes + 64, code_hi + 64);
-        } else {  // channels past K are zero, and nothing of them is read
-          cp_async16(dst, tail0 ? code_lo : a.w, tail0 ? 16 : 0);
-          cp_async16(dst + 64, tail1 ? code_lo + 64 : a.w, tail1 ? 16 : 0);
-          cp_async16(dst + 8 * kRowBytes, tail0 ? code_hi : a.w, tail0 ? 16 : 0);
-          cp_async16(dst + 8 * kRowBytes + 64, tail1 ? code_hi + 64 : a.w, tail1 ? 16 : 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // channels past K: zero, nothing of them is read
+          const bool ok = ALIGNED || ld_blk + 1 < nblk || tail[i];
+          cp_async16(dst + 64 * i, ok ? code_lo + 64 * i : a.w, ok ? 16 : 0);
+          cp_async16(dst + 8 * kRowBytes + 64 * i, ok ? code_hi + 64 * i : a.w, ok ? 16 : 0);
         }
-        code_lo += 128;
-        code_hi += 128;
+        code_lo += kBlockK / 2;
+        code_hi += kBlockK / 2;
         const uint32_t sst = ld_st + St::kCodeBytes;
         if (St::kHalves) {
-          const bool ok = ld_blk * 2 + (lane & 1) < halves;
-          if (!U8) {
-            const float* p = static_cast<const float*>(a.sf) + (ok ? sf_at : 0);
-            if (G == 16) {
-              cp_async16(sst + lane * 32, p, ok ? 16 : 0);
-              cp_async16(sst + lane * 32 + 16, ok ? p + 4 : p, ok ? 16 : 0);
-            }
-            if (G == 32) cp_async16(sst + lane * 16, p, ok ? 16 : 0);
-            if (G == 64) cp_async8(sst + lane * 8, p, ok ? 8 : 0);
-            if (G == 128) cp_async4(sst + lane * 4, p, ok ? 4 : 0);
+          constexpr int kBytes = St::kGroups / 2 * (U8 ? 1 : 4);  // of half a row
+          if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < kBytes; i += 16) cp_async16(sst + lane * kBytes + i, sf_at + i, 16);
+          } else if constexpr (kBytes == 8) {
+            cp_async8(sst + lane * 8, sf_at, 8);
           } else {
-            const uint8_t* p = static_cast<const uint8_t*>(a.sf) + (ok ? sf_at : 0);
-            if (G == 16) cp_async8(sst + lane * 8, p, ok ? 8 : 0);
-            if (G == 32) cp_async4(sst + lane * 4, p, ok ? 4 : 0);
+            cp_async4(sst + lane * 4, sf_at, 4);
           }
-          sf_at += St::kGroups;
+          sf_at += 2 * kBytes;
         } else if (U8) {
           const uint8_t* sf = static_cast<const uint8_t*>(a.sf);
           const int64_t end = (int64_t)a.E * M * sf_row;
 #pragma unroll
-          for (int p = lane; p < 16 * St::kWords; p += 32) {
-            const int row = p / St::kWords, wi = p % St::kWords;
-            const int64_t m = weight_row(ld_tile, row);
-            const int64_t at = ((m * sf_row + ld_blk * St::kGroups) & ~(int64_t)3) + 4 * wi;
-            int64_t bytes = end - at;
-            bytes = bytes < 0 ? 0 : bytes > 4 ? 4 : bytes;
-            cp_async4(sst + p * 4, sf + (bytes > 0 ? at : 0), (int)bytes);
+          for (int i = 0; i < (St::kWords + 1) / 2; ++i) {
+            const int p = lane + 32 * i, row = p / St::kWords, wi = p % St::kWords;
+            if (St::kWords % 2 != 0 && p >= 16 * St::kWords) break;
+            const int64_t at = ((sf_e + weight_row(ld_tile, row) * (uint32_t)sf_row +
+                                 (uint32_t)(ld_blk * St::kGroups)) & ~(int64_t)3) + 4 * wi;
+            const int64_t left = end - at;
+            const int bytes = left < 0 ? 0 : left > 4 ? 4 : (int)left;
+            cp_async4(sst + p * 4, sf + (bytes > 0 ? at : 0), bytes);
           }
         } else {
-          const float* sf = static_cast<const float*>(a.sf);
+          const float* sf = static_cast<const float*>(a.sf) + sf_e;
 #pragma unroll
-          for (int p = lane; p < 16 * St::kGroups; p += 32) {
-            const int row = p / St::kGroups, j = p % St::kGroups;
-            const int64_t m = weight_row(ld_tile, row);
-            const int gi = ld_blk * St::kGroups + j;
-            const bool ok = gi < sf_row;
-            cp_async4(sst + p * 4, sf + (ok ? m * sf_row + gi : 0), ok ? 4 : 0);
+          for (int i = 0; i < (16 * St::kGroups + 31) / 32; ++i) {
+            const int p = lane + 32 * i, row = p / St::kGroups;
+            const uint32_t gi = (uint32_t)(ld_blk * St::kGroups + p % St::kGroups);
+            const bool ok = gi < (uint32_t)sf_row;
+            cp_async4(sst + p * 4, sf + (ok ? weight_row(ld_tile, row) * (uint32_t)sf_row + gi : 0),
+                      ok ? 4 : 0);
           }
         }
         ld_st += St::kBytes;
@@ -392,12 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue();
+    for (int i = 0; i < stages - 1; ++i) issue();
 
     // x: each warp converts one block of one row
-    for (int t = warp; t < n * nblk; t += kWarps) {
-      const int col = t / nblk, b = t - col * nblk;
+    const int xblk = padded_k(a.K) / kBlockK;
+    for (int t = warp; t < n * xblk; t += kWarps) {
+      const int col = t / xblk, b = t - col * xblk;
       const int64_t sr = source_row(a, r0 + col, err);
       const int c = b * kBlockK + lane * 8;
       uint4 v = make_uint4(0, 0, 0, 0);
@@ -436,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int sf_off[2] = {0, 0};
     auto tile_offsets = [&]() {
       if (kShift) {
-        sf_off[0] = (int)((weight_row(tile, g) * sf_row) & 3);
-        sf_off[1] = (int)((weight_row(tile, g + 8) * sf_row) & 3);
+        sf_off[0] = (int)((sf_e + weight_row(tile, g) * (uint32_t)sf_row) & 3);
+        sf_off[1] = (int)((sf_e + weight_row(tile, g + 8) * (uint32_t)sf_row) & 3);
       }
     };
     tile_offsets();
@@ -445,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int loop = mine > 0 ? steps : my_tiles;
     for (int step = 0; step < loop; ++step) {
       if (mine > 0) {
-        cp_async_wait<kStages - 2>();
+        cp_async_wait_but(stages - 2);
         __syncwarp();
         issue();
         const uint32_t sst = st + St::kCodeBytes + g * (St::kWords * 4);
@@ -457,17 +473,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t sw[St::kWords + 1];
           const uint32_t at = sst + 8 * i * (St::kWords * 4);
           if constexpr (St::kWords % 4 == 0) {
-#pragma unroll
-            for (int j = 0; j < St::kWords; j += 4) {
-              const uint4 v = lds128(at + j * 4);
-              sw[j] = v.x, sw[j + 1] = v.y, sw[j + 2] = v.z, sw[j + 3] = v.w;
-            }
+            unrolled<St::kWords / 4>([&](auto J) {
+              const uint4 v = lds128<J * 16>(at);
+              sw[J * 4] = v.x, sw[J * 4 + 1] = v.y, sw[J * 4 + 2] = v.z, sw[J * 4 + 3] = v.w;
+            });
           } else if constexpr (St::kWords == 2) {
-            const uint2 v = lds64(at);
+            const uint2 v = lds64<0>(at);
             sw[0] = v.x, sw[1] = v.y;
           } else {
-#pragma unroll
-            for (int j = 0; j < St::kWords; ++j) sw[j] = lds32(at + j * 4);
+            unrolled<St::kWords>([&](auto J) { sw[J] = lds32<J * 4>(at); });
           }
           sw[St::kWords] = 0;
           if constexpr (!U8) {
@@ -494,37 +508,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : __fmaf_rn(s[i >> 1][gi], part[i], blk_acc[i]);
         };
         const uint32_t xb = xcol + (uint32_t)blk * (2 * kBlockK);
-        const uint32_t lo_row = st + frag, hi_row = lo_row + 8 * kRowBytes;
-#pragma unroll
-        for (int j = 0; j < kBlockK / 32; ++j) {
+        const uint32_t row = st + frag;
+        constexpr int kHi = 8 * kRowBytes;  // from row g to row g + 8
+        unrolled<kBlockK / 32>([&](auto J) {
+          constexpr int j = J;
           uint32_t a0[4], a1[4];
           uint4 x;
           if constexpr (G == 16) {
             // the 16 channels of a group: 2 bytes of codes per lane
-            const uint32_t w0 = lds16(lo_row + 16 * j), w1 = lds16(lo_row + 16 * j + 8);
-            const uint32_t w2 = lds16(hi_row + 16 * j), w3 = lds16(hi_row + 16 * j + 8);
+            const uint32_t w0 = lds16<16 * j>(row), w1 = lds16<16 * j + 8>(row);
+            const uint32_t w2 = lds16<16 * j + kHi>(row), w3 = lds16<16 * j + 8 + kHi>(row);
             a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
             a0[1] = e2m1x2_to_f16x2<0>(w2), a0[3] = e2m1x2_to_f16x2<1>(w2);
             a1[0] = e2m1x2_to_f16x2<0>(w1), a1[2] = e2m1x2_to_f16x2<1>(w1);
             a1[1] = e2m1x2_to_f16x2<0>(w3), a1[3] = e2m1x2_to_f16x2<1>(w3);
-            const uint2 p = lds64(xb + j * 64), r = lds64(xb + j * 64 + 32);
+            const uint2 p = lds64<j * 64>(xb), r = lds64<j * 64 + 32>(xb);
             x = make_uint4(p.x, p.y, r.x, r.y);
           } else {
-            const uint32_t w0 = lds32(lo_row + 16 * j), w1 = lds32(hi_row + 16 * j);
+            const uint32_t w0 = lds32<16 * j>(row), w1 = lds32<16 * j + kHi>(row);
+            x = lds128<j * 64>(xb);
             a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
             a0[1] = e2m1x2_to_f16x2<0>(w1), a0[3] = e2m1x2_to_f16x2<1>(w1);
             a1[0] = e2m1x2_to_f16x2<2>(w0), a1[2] = e2m1x2_to_f16x2<3>(w0);
             a1[1] = e2m1x2_to_f16x2<2>(w1), a1[3] = e2m1x2_to_f16x2<3>(w1);
-            x = lds128(xb + j * 64);
           }
           mma_16816(part, a0, x.x, x.y, G <= 32 || (j * 32) % G == 0);
           if constexpr (G == 16) flush(2 * j);
           mma_16816(part, a1, x.z, x.w, G == 16);
           if constexpr (G == 16)
             flush(2 * j + 1);
-          else if ((j * 32 + 32) % G == 0)
+          else if constexpr ((j * 32 + 32) % G == 0)
             flush((j * 32) / G);
-        }
+        });
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = __fmaf_rn(i & 1 ? xc.y : xc.x, blk_acc[i], acc[i]);
         st += St::kBytes;
@@ -585,8 +600,12 @@ cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
   // more items), and fewer where a long x would not fit
   int C = kMaxRows;
   while (C > 1 && C / 2 >= (a.R + a.k - 1) / a.k) C >>= 1;
-  while (C > 1 && smem_layout(kStageBytes, a.K, a.E, C).total > 220 * 1024) C >>= 1;
-  const size_t smem = smem_layout(kStageBytes, a.K, a.E, C).total;
+  constexpr uint32_t kSmem = 226 * 1024;
+  while (C > 1 && smem_layout(kStageBytes, kMinStages, a.K, a.E, C).total > kSmem) C >>= 1;
+  int stages = kMinStages;
+  while (stages < kMaxStages && smem_layout(kStageBytes, stages + 1, a.K, a.E, C).total <= kSmem)
+    ++stages;
+  const size_t smem = smem_layout(kStageBytes, stages, a.K, a.E, C).total;
   auto* kernel = expert_matvec_kernel<G, U8, ALIGNED>;
   cudaError_t e = allow_max_dynamic_smem(kernel);
   if (e != cudaSuccess) return e;
@@ -595,12 +614,12 @@ cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
   const int per_tile = a.swiglu ? 8 : 16;
   const int64_t units = items * ((a.N + per_tile - 1) / per_tile);
   const int64_t blocks = units < c.num_sms ? units : c.num_sms;
-  return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, smem, c.stream, a, C, c.err);
+  return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, smem, c.stream, a, C, stages, c.err);
 }
 
 template <int G>
 cudaError_t launch_g(const LaunchCtx& c, const MatvecArgs& a) {
-  const bool al = a.K % 128 == 0 && (reinterpret_cast<uintptr_t>(a.sf) & 15u) == 0;
+  const bool al = a.K % kBlockK == 0 && (reinterpret_cast<uintptr_t>(a.sf) & 15u) == 0;
   if (a.sf_type == MOE_WSF_UE8M0)
     return al ? launch_t<G, true, true>(c, a) : launch_t<G, true, false>(c, a);
   return al ? launch_t<G, false, true>(c, a) : launch_t<G, false, false>(c, a);

@@ -114,7 +114,7 @@ def test_expert_matvec_refusals(L):
                                        od, None)
     assert f(R=0) == 0
     assert f(group=48) == UNSUPPORTED and f(K=65568) == UNSUPPORTED
-    assert f(R=(1 << 18) + 1) == UNSUPPORTED and f(N=(1 << 24) + 1) == UNSUPPORTED
+    assert f(R=(1 << 18) + 1) == UNSUPPORTED and f(N=1 << 26) == UNSUPPORTED
     assert f(st=2) == INVALID and f(od=2) == INVALID
     assert f(E=0) == INVALID and f(E=1025) == INVALID and f(k=0) == INVALID and f(k=33) == INVALID
     assert f(K=48) == INVALID and f(K=96, group=64) == INVALID and f(K=0) == INVALID
