@@ -676,10 +676,11 @@ moe_status_t moe_combine_backward(const void *grad_out, int32_t grad_dtype, cons
  *   maps return it: src(r) = sorted_src[r] / num_topk, and a negative entry gives
  *   a row of zeros
  *   out [num_rows, N] in out_dtype (MOE_OUT_*)
- * group is 16, 32, 64 or 128; K % 32 == 0, K % group == 0, K <= 65536, M * K < 2^32,
- * num_rows <= MOE_MATVEC_MAX_ROWS.  offsets
+ * group is 16, 32, 64 or 128; K % 32 == 0, K % group == 0, K <= 16384, M * K < 2^32,
+ * E * M < 2^31, num_rows <= MOE_MATVEC_MAX_ROWS.  offsets
  * beyond num_rows or a src outside [0, num_x) set MOE_DEVERR_POS_RANGE; such rows
- * are not written, or are zero.
+ * are not written, or are zero.  Every wait for a copy is bounded (1 s); one that
+ * runs out sets MOE_DEVERR_TIMEOUT.
  */
 moe_status_t moe_expert_matvec_fp4(const void *x, int64_t num_x, const uint8_t *w,
                                    const void *w_sf, int32_t sf_type, int32_t group,

@@ -309,8 +309,9 @@ moe_status_t moe_expert_matvec_fp4(const void* x, int64_t num_x, const uint8_t* 
     return MOE_ERR_INVALID_ARG;
   if (!offsets && num_experts != 1) return MOE_ERR_INVALID_ARG;
   if (!sorted_src && num_x < num_rows) return MOE_ERR_INVALID_ARG;
-  if (k_dim > 65536 || num_rows > MOE_MATVEC_MAX_ROWS ||
-      (int64_t)k_dim * n_dim * (swiglu ? 2 : 1) >= ((int64_t)1 << 32))
+  if (k_dim > 16384 || num_rows > MOE_MATVEC_MAX_ROWS ||
+      (int64_t)k_dim * n_dim * (swiglu ? 2 : 1) >= ((int64_t)1 << 32) ||
+      (int64_t)num_experts * n_dim * (swiglu ? 2 : 1) >= ((int64_t)1 << 31))
     return MOE_ERR_UNSUPPORTED;
   if (num_rows == 0) return MOE_OK;
   if ((num_x > 0 && !x) || !w || !w_sf || !out) return MOE_ERR_INVALID_ARG;

@@ -31,6 +31,7 @@
 // channels, which the fragment layout leaves in one lane.
 #include "block_ops.cuh"
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -38,29 +39,30 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 16;
+#ifndef MV_WARPS
+#define MV_WARPS 16
+#endif
+constexpr int kWarps = MV_WARPS;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 8;   // columns of one mma
 constexpr int kBlockK = 256;  // channels per ring stage
-constexpr int kMinStages = 3, kMaxStages = 4;
-constexpr int kRowBytes = kBlockK / 2 + 16;  // codes of a row in a stage, padded
+constexpr int kMinStages = 3, kMaxStages = 6;
+constexpr int kRowBytes = kBlockK / 2;  // codes of a row in a stage
+constexpr int kCodeBytes = 16 * kRowBytes;
 
-// What one stage holds: 16 rows of 128 code bytes, 144 bytes apart so that the
-// 8 rows x 4 lanes of a fragment read meet 32 banks, and the rows' scales of the
-// block.  ALIGNED (K a multiple of 256 and 16-byte aligned scales): a row's
-// scales of half a block start on a multiple of their own size, and each lane
-// copies those of one half row.  Otherwise, and for bytes of G >= 64, 4-byte
-// copies: f32 as above, or the aligned words that hold 256 / G bytes at any
-// offset.
+// A stage holds 16 rows of 128 code bytes (two TMA boxes of 8 rows, 128-byte
+// swizzle: the 16-byte unit u of row r lies at unit u ^ (r % 8), so the 8 rows x
+// 4 lanes of a fragment read meet 32 banks), and the rows' scales of the block.
+// ALIGNED (K a multiple of 256 and 16-byte aligned scales): a row's scales of
+// half a block start on a multiple of their own size, and each lane copies
+// those of one half row.  Otherwise, and for bytes of G >= 64, 4-byte copies:
+// f32 as above, or the aligned words that hold 256 / G bytes at any offset.
 template <int G, bool U8, bool ALIGNED>
 struct Stage {
   static constexpr int kGroups = kBlockK / G;
   static constexpr bool kHalves = ALIGNED && (!U8 || G <= 32);
   static constexpr int kWords = !U8 ? kGroups : kHalves ? kGroups / 4 : (kGroups + 6) / 4;
-  static_assert(kGroups >= 1, "a block holds whole groups");
-  static constexpr int kCodeBytes = 16 * kRowBytes;
-  // a whole number of 16 bytes
-  static constexpr int kBytes = kCodeBytes + 16 * kWords * 4;
+  static constexpr int kScaleBytes = 16 * kWords * 4;
 };
 
 // The two E2M1 codes of byte I of w as f16x2, element 0 (the low nibble) in
@@ -117,12 +119,56 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 // Waits until at most n of this thread's groups are in flight.
 __device__ __forceinline__ void cp_async_wait_but(int n) {
-  static_assert(kMinStages == 3 && kMaxStages == 4, "one case per ring length");
+  static_assert(kMinStages == 3 && kMaxStages == 6, "one case per ring length");
   if (n == 1)
     cp_async_wait<1>();
-  else
+  else if (n == 2)
     cp_async_wait<2>();
+  else if (n == 3)
+    cp_async_wait<3>();
+  else
+    cp_async_wait<4>();
 }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for the phase `parity` of the barrier; false if that took over a second.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  uint64_t begin = 0;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    const uint64_t t = now_ns();
+    if (begin == 0) begin = t;
+    if (t - begin > 1000000000ull) return false;
+  }
+}
+// A box of 8 rows of 128 bytes at byte column c and row r of the codes.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c, int r,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(c), "r"(r), "r"(bar)
+      : "memory");
+}
+
 // Shared-memory loads at a 32-bit address plus a constant.  Volatile: kept in
 // program order, between the products that use them (grouped ahead of a block's
 // products, as the compiler would have them, they fill the load queue: 16 warps
@@ -176,22 +222,24 @@ __device__ __forceinline__ void ue8m0x4(uint32_t w, float (&s)[4]) {
   s[0] = bf16_lo(lo), s[1] = bf16_hi(lo), s[2] = bf16_lo(hi), s[3] = bf16_hi(hi);
 }
 
-// Shared memory: the warps' rings, the x rows (f16, row stride 2 Kp + 64 bytes
-// so that neighbouring rows fall into different halves of the banks), the
-// powers of two [Kp / 256][8], two buffers of partial sums, the items' prefix.
+// Shared memory: the warps' rings of codes (1024-byte aligned for the swizzle)
+// and of scales, the x rows (f16, row stride 2 Kp + 64 bytes so that
+// neighbouring rows fall into different halves of the banks), the powers of two
+// [Kp / 256][8], two buffers of partial sums, the items' prefix, the barriers.
 struct Smem {
-  uint32_t ring, x, xs, red, first, total;
+  uint32_t codes, scales, x, xs, red, bars, first, total;
 };
 __host__ __device__ inline int padded_k(int K) { return (K + kBlockK - 1) / kBlockK * kBlockK; }
 __host__ __device__ inline uint32_t x_stride(int K) { return (uint32_t)padded_k(K) * 2 + 64; }
-__host__ __device__ inline Smem smem_layout(int stage_bytes, int stages, int K, int E,
-                                              int C) {
+__host__ __device__ inline Smem smem_layout(int scale_bytes, int stages, int K, int E, int C) {
   Smem s;
-  s.ring = 0;
-  s.x = (uint32_t)(kWarps * stages * stage_bytes);
+  s.codes = 0;
+  s.scales = (uint32_t)(kWarps * stages * kCodeBytes);
+  s.x = s.scales + (uint32_t)(kWarps * stages * scale_bytes);
   s.xs = s.x + (uint32_t)C * x_stride(K);
   s.red = s.xs + (uint32_t)(padded_k(K) / kBlockK) * kMaxRows * 4;
-  s.first = s.red + 2 * kWarps * 512;
+  s.bars = s.red + 2 * kWarps * 512;
+  s.first = s.bars + (uint32_t)(kWarps * stages * 8);
   s.total = s.first + (uint32_t)(E + 1) * 4;
   return s;
 }
@@ -213,11 +261,12 @@ __device__ __forceinline__ int64_t source_row(const MatvecArgs& a, int r, unsign
 
 template <int G, bool U8, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1)
-    expert_matvec_kernel(const MatvecArgs a, const int C, const int stages, unsigned* err) {
+    expert_matvec_kernel(const MatvecArgs a, const __grid_constant__ CUtensorMap map,
+                         const int C, const int stages, unsigned* err) {
   pdl_enter();
   using St = Stage<G, U8, ALIGNED>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const Smem L = smem_layout(St::kBytes, stages, a.K, a.E, C);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const Smem L = smem_layout(St::kScaleBytes, stages, a.K, a.E, C);
   const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
   int* first = reinterpret_cast<int*>(smem + L.first);
   float* xs = reinterpret_cast<float*>(smem + L.xs);
@@ -231,14 +280,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t xrow_bytes = x_stride(a.K);
   const int64_t sf_row = a.K / G;  // scales of one weight row
 
-  // first[e]: items of the experts before e; each thread counts two experts
+  const uint32_t bar = sbase + L.bars + (uint32_t)(warp * stages * 8);  // of this warp's stages
+  if (lane == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(bar + i * 8);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+
+  // first[e]: items of the experts before e; each thread counts kPer experts
   {
-    static_assert(2 * kThreads >= MOE_MAX_EXPERTS, "two experts per thread");
+    constexpr int kPer = (MOE_MAX_EXPERTS + kThreads - 1) / kThreads;
     int* totals = reinterpret_cast<int*>(red);
-    int runs[2] = {0, 0};
+    int runs[kPer] = {};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int e = 2 * tid + i;
+    for (int i = 0; i < kPer; ++i) {
+      const int e = kPer * tid + i;
       if (e >= a.E) continue;
       int64_t lo = 0, hi = a.R;
       if (a.offsets != nullptr) {
@@ -250,7 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       runs[i] = hi > lo ? (int)((hi - lo + C - 1) / C) : 0;
     }
-    int sum = runs[0] + runs[1];
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += runs[i];
+    const int own = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
@@ -258,11 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) totals[warp] = sum;
     __syncthreads();
-    int before = sum - runs[0] - runs[1];
+    int before = sum - own;
     for (int w = 0; w < warp; ++w) before += totals[w];
-    if (2 * tid <= a.E) first[2 * tid] = before;
-    if (2 * tid + 1 <= a.E) first[2 * tid + 1] = before + runs[0];
-    if (tid == kThreads - 1 && a.E == 2 * kThreads) first[a.E] = before + runs[0] + runs[1];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (kPer * tid + i <= a.E) first[kPer * tid + i] = before;
+      before += runs[i];
+    }
+    if (tid == kThreads - 1 && a.E == kPer * kThreads) first[a.E] = before;
     __syncthreads();
   }
   const int64_t units = (int64_t)first[a.E] * tiles;
@@ -285,15 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b_hi = b_lo + bpw < nblk ? b_lo + bpw : nblk;
   const int mine = b_hi - b_lo;  // blocks of each tile this warp sums
 
-  const uint32_t ring = sbase + L.ring + (uint32_t)(warp * stages * St::kBytes);
-  const uint32_t ring_end = ring + (uint32_t)(stages * St::kBytes);
-  // this lane's 16 bytes of the first half of row g in a stage
-  const uint32_t code_dst = (uint32_t)(g * kRowBytes + q * 16);
-  // which of its four copies of codes exist in the last block
-  bool tail[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    tail[i] = (nblk - 1) * (kBlockK / 2) + 64 * i + q * 16 < a.K / 2;
+  const uint32_t codes = sbase + L.codes + (uint32_t)(warp * stages * kCodeBytes);
+  const uint32_t scales = sbase + L.scales + (uint32_t)(warp * stages * St::kScaleBytes);
+  int ld_stage = 0, stage = 0;  // the next one to fill, to read
+  uint32_t phase = 0;           // bit i: the parity that stage i's barrier is at
+  int in_flight = 0;            // stages filled or being filled
+  bool ok = true;               // no wait ran out
   int parity = 0;
 
   int64_t u = u0;
@@ -325,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this team's tiles: tile0 + team, + teams, ...; its steps are (tile, block)
     const int my_tiles = ntiles > team ? (ntiles - team + teams - 1) / teams : 0;
     const int steps = my_tiles * mine;
-    const uint8_t* w_e = a.w + (int64_t)e * M * (a.K / 2);
-    const int64_t sf_e = (int64_t)e * M * sf_row;
+    const int m_e = e * M;
+    const int64_t sf_e = (int64_t)m_e * sf_row;
     // weight row, within the expert, of row i of a tile; past the last output
     // the last one, whose products are not stored
     auto weight_row = [&](int tile, int i) -> uint32_t {
@@ -336,13 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // the stream of stages: where the next one comes from and goes to
     int ld_tile = tile0 + team, ld_blk = b_lo, to_issue = steps;
-    uint32_t ld_st = ring;
-    const uint8_t *code_lo = nullptr, *code_hi = nullptr;
     const char* sf_at = nullptr;  // kHalves: this lane's first scale of block ld_blk
     auto open_tile = [&]() {
-      const uint32_t row_bytes = (uint32_t)a.K / 2, c = (uint32_t)(ld_blk * (kBlockK / 2) + q * 16);
-      code_lo = w_e + weight_row(ld_tile, g) * row_bytes + c;
-      code_hi = w_e + weight_row(ld_tile, g + 8) * row_bytes + c;
       if (St::kHalves) {
         const int64_t at = sf_e + weight_row(ld_tile, lane >> 1) * (uint32_t)sf_row +
                            (uint32_t)(ld_blk * St::kGroups + (lane & 1) * (St::kGroups / 2));
@@ -351,18 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (steps > 0) open_tile();
     auto issue = [&]() {
-      if (to_issue > 0) {
+      if (to_issue > 0 && ok) {
         --to_issue;
-        const uint32_t dst = ld_st + code_dst;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {  // channels past K: zero, nothing of them is read
-          const bool ok = ALIGNED || ld_blk + 1 < nblk || tail[i];
-          cp_async16(dst + 64 * i, ok ? code_lo + 64 * i : a.w, ok ? 16 : 0);
-          cp_async16(dst + 8 * kRowBytes + 64 * i, ok ? code_hi + 64 * i : a.w, ok ? 16 : 0);
+        ++in_flight;
+        if (lane == 0) {
+          // rows past the last output are another's, or past the tensor and zero
+          const uint32_t b = bar + ld_stage * 8, dst = codes + ld_stage * kCodeBytes;
+          const int r = m_e + ld_tile * per_tile;
+          mbar_expect(b, kCodeBytes);
+          tma_box(dst, &map, ld_blk * kRowBytes, r, b);
+          tma_box(dst + kCodeBytes / 2, &map, ld_blk * kRowBytes, r + (a.swiglu ? a.N : 8), b);
         }
-        code_lo += kBlockK / 2;
-        code_hi += kBlockK / 2;
-        const uint32_t sst = ld_st + St::kCodeBytes;
+        const uint32_t sst = scales + ld_stage * St::kScaleBytes;
         if (St::kHalves) {
           constexpr int kBytes = St::kGroups / 2 * (U8 ? 1 : 4);  // of half a row
           if constexpr (kBytes >= 16) {
@@ -398,8 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       ok ? 4 : 0);
           }
         }
-        ld_st += St::kBytes;
-        if (ld_st == ring_end) ld_st = ring;
+        if (++ld_stage == stages) ld_stage = 0;
         if (++ld_blk == b_hi) {
           ld_blk = b_lo;
           ld_tile += teams;
@@ -443,10 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // lanes of columns past the run read the last one's: their sums are not stored
     const uint32_t xcol =
         sbase + L.x + (g < n ? g : n - 1) * xrow_bytes + (G == 16 ? q * 8 : q * 16);
-    const uint32_t frag = (uint32_t)(g * kRowBytes + (G == 16 ? q * 2 : q * 4));
+    // unit j of row g (and of row g + 8, 1024 bytes on) in a stage
+    uint32_t frag[kBlockK / 32];
+#pragma unroll
+    for (int j = 0; j < kBlockK / 32; ++j)
+      frag[j] = codes + (uint32_t)(g * kRowBytes + ((j ^ g) << 4) + (G == 16 ? q * 2 : q * 4));
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int tile = tile0 + team, blk = b_lo;
-    uint32_t st = ring;
     // where a row's scales start in its first word
     constexpr bool kShift = U8 && !St::kHalves;
     int sf_off[2] = {0, 0};
@@ -462,9 +518,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int step = 0; step < loop; ++step) {
       if (mine > 0) {
         cp_async_wait_but(stages - 2);
+        if (in_flight > 0) {
+          --in_flight;
+          if (!mbar_wait(bar + stage * 8, (phase >> stage) & 1u)) {
+            ok = false;  // nothing more is fetched; what is on its way is waited for
+            flag_error(err, MOE_DEVERR_TIMEOUT);
+          }
+        }
+        phase ^= 1u << stage;
         __syncwarp();
         issue();
-        const uint32_t sst = st + St::kCodeBytes + g * (St::kWords * 4);
+        const uint32_t sst = scales + stage * St::kScaleBytes + g * (St::kWords * 4);
         const float2 xc = *reinterpret_cast<const float2*>(xs + blk * kMaxRows + 2 * q);
         // scales of rows g and g + 8
         float s[2][St::kGroups < 4 ? 4 : St::kGroups];
@@ -508,16 +572,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : __fmaf_rn(s[i >> 1][gi], part[i], blk_acc[i]);
         };
         const uint32_t xb = xcol + (uint32_t)blk * (2 * kBlockK);
-        const uint32_t row = st + frag;
+        const uint32_t st = (uint32_t)(stage * kCodeBytes);
         constexpr int kHi = 8 * kRowBytes;  // from row g to row g + 8
         unrolled<kBlockK / 32>([&](auto J) {
           constexpr int j = J;
+          const uint32_t row = frag[j] + st;
           uint32_t a0[4], a1[4];
           uint4 x;
           if constexpr (G == 16) {
             // the 16 channels of a group: 2 bytes of codes per lane
-            const uint32_t w0 = lds16<16 * j>(row), w1 = lds16<16 * j + 8>(row);
-            const uint32_t w2 = lds16<16 * j + kHi>(row), w3 = lds16<16 * j + 8 + kHi>(row);
+            const uint32_t w0 = lds16<0>(row), w1 = lds16<8>(row);
+            const uint32_t w2 = lds16<kHi>(row), w3 = lds16<kHi + 8>(row);
             a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
             a0[1] = e2m1x2_to_f16x2<0>(w2), a0[3] = e2m1x2_to_f16x2<1>(w2);
             a1[0] = e2m1x2_to_f16x2<0>(w1), a1[2] = e2m1x2_to_f16x2<1>(w1);
@@ -525,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint2 p = lds64<j * 64>(xb), r = lds64<j * 64 + 32>(xb);
             x = make_uint4(p.x, p.y, r.x, r.y);
           } else {
-            const uint32_t w0 = lds32<16 * j>(row), w1 = lds32<16 * j + kHi>(row);
+            const uint32_t w0 = lds32<0>(row), w1 = lds32<kHi>(row);
             x = lds128<j * 64>(xb);
             a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
             a0[1] = e2m1x2_to_f16x2<0>(w1), a0[3] = e2m1x2_to_f16x2<1>(w1);
@@ -542,8 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         });
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = __fmaf_rn(i & 1 ? xc.y : xc.x, blk_acc[i], acc[i]);
-        st += St::kBytes;
-        if (st == ring_end) st = ring;
+        if (++stage == stages) stage = 0;
         if (++blk < b_hi) continue;
         blk = b_lo;
       }
@@ -592,29 +656,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// The codes as a tensor of rows of K / 2 bytes, in boxes of 8 rows of 128 bytes.
+cudaError_t code_map(const MatvecArgs& a, CUtensorMap* map) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(fn)
+                                                                    : nullptr;
+  }();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.K / 2,
+                              (cuuint64_t)a.E * a.N * (a.swiglu ? 2 : 1)};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.K / 2};
+  const cuuint32_t box[2] = {kRowBytes, 8}, unit[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.w), dims,
+                            strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int G, bool U8, bool ALIGNED>
 cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
-  constexpr int kStageBytes = Stage<G, U8, ALIGNED>::kBytes;
+  constexpr int kScaleBytes = Stage<G, U8, ALIGNED>::kScaleBytes;
   // rows per item: the 8 columns of the mma, but no more than an expert can get
   // (a token's experts are distinct: one row per token; more would only take
   // more items), and fewer where a long x would not fit
   int C = kMaxRows;
   while (C > 1 && C / 2 >= (a.R + a.k - 1) / a.k) C >>= 1;
   constexpr uint32_t kSmem = 226 * 1024;
-  while (C > 1 && smem_layout(kStageBytes, kMinStages, a.K, a.E, C).total > kSmem) C >>= 1;
+  while (C > 1 && smem_layout(kScaleBytes, kMinStages, a.K, a.E, C).total > kSmem) C >>= 1;
   int stages = kMinStages;
-  while (stages < kMaxStages && smem_layout(kStageBytes, stages + 1, a.K, a.E, C).total <= kSmem)
+  while (stages < kMaxStages && smem_layout(kScaleBytes, stages + 1, a.K, a.E, C).total <= kSmem)
     ++stages;
-  const size_t smem = smem_layout(kStageBytes, stages, a.K, a.E, C).total;
+  const size_t smem = smem_layout(kScaleBytes, stages, a.K, a.E, C).total;
   auto* kernel = expert_matvec_kernel<G, U8, ALIGNED>;
   cudaError_t e = allow_max_dynamic_smem(kernel);
+  if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  e = code_map(a, &map);
   if (e != cudaSuccess) return e;
   int64_t items = (a.offsets ? a.E : 1) + a.R / C;
   if (items > a.R) items = a.R;
   const int per_tile = a.swiglu ? 8 : 16;
   const int64_t units = items * ((a.N + per_tile - 1) / per_tile);
   const int64_t blocks = units < c.num_sms ? units : c.num_sms;
-  return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, smem, c.stream, a, C, stages, c.err);
+  return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, smem, c.stream, a, map, C, stages, c.err);
 }
 
 template <int G>

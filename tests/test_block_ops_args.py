@@ -113,7 +113,7 @@ def test_expert_matvec_refusals(L):
         return L.moe_expert_matvec_fp4(x, nx, w, sf, st, group, off, src, E, k, R, K, N, sw, out,
                                        od, None)
     assert f(R=0) == 0
-    assert f(group=48) == UNSUPPORTED and f(K=65568) == UNSUPPORTED
+    assert f(group=48) == UNSUPPORTED and f(K=16416) == UNSUPPORTED
     assert f(R=(1 << 18) + 1) == UNSUPPORTED and f(N=1 << 26) == UNSUPPORTED
     assert f(st=2) == INVALID and f(od=2) == INVALID
     assert f(E=0) == INVALID and f(E=1025) == INVALID and f(k=0) == INVALID and f(k=33) == INVALID

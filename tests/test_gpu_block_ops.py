@@ -474,7 +474,8 @@ def test_matvec_one_expert(group, ue8m0, swiglu, K, N, R):
 @pytest.mark.parametrize("T,E,k,K,N,group", [(1, 16, 2, 256, 64, 32), (1, 256, 8, 512, 48, 32),
                                              (29, 16, 2, 1056, 101, 16), (64, 8, 4, 224, 33, 32),
                                              (40, 5, 5, 320, 7, 64), (3, 1024, 32, 128, 24, 128),
-                                             (16, 64, 8, 7168, 20, 128)])
+                                             (16, 64, 8, 7168, 20, 128), (9, 2, 1, 16384, 9, 16),
+                                             (3, 2, 1, 16352, 8, 32)])
 @pytest.mark.parametrize("gather", [False, True])
 def test_matvec_routed(T, E, k, K, N, group, gather):
     g = gen(T + E + K)
