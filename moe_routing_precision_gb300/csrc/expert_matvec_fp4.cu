@@ -39,14 +39,11 @@
 namespace moe {
 namespace {
 
-#ifndef MV_WARPS
-#define MV_WARPS 16
-#endif
-constexpr int kWarps = MV_WARPS;
+constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 8;   // columns of one mma
 constexpr int kBlockK = 256;  // channels per ring stage
-constexpr int kMinStages = 3, kMaxStages = 6;
+constexpr int kStages = 3;
 constexpr int kRowBytes = kBlockK / 2;  // codes of a row in a stage
 constexpr int kCodeBytes = 16 * kRowBytes;
 
@@ -116,18 +113,6 @@ __device__ __forceinline__ void cp_async_commit() {
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// Waits until at most n of this thread's groups are in flight.
-__device__ __forceinline__ void cp_async_wait_but(int n) {
-  static_assert(kMinStages == 3 && kMaxStages == 6, "one case per ring length");
-  if (n == 1)
-    cp_async_wait<1>();
-  else if (n == 2)
-    cp_async_wait<2>();
-  else if (n == 3)
-    cp_async_wait<3>();
-  else
-    cp_async_wait<4>();
 }
 
 __device__ __forceinline__ void mbar_init(uint32_t bar) {
@@ -231,15 +216,15 @@ struct Smem {
 };
 __host__ __device__ inline int padded_k(int K) { return (K + kBlockK - 1) / kBlockK * kBlockK; }
 __host__ __device__ inline uint32_t x_stride(int K) { return (uint32_t)padded_k(K) * 2 + 64; }
-__host__ __device__ inline Smem smem_layout(int scale_bytes, int stages, int K, int E, int C) {
+__host__ __device__ inline Smem smem_layout(int scale_bytes, int K, int E, int C) {
   Smem s;
   s.codes = 0;
-  s.scales = (uint32_t)(kWarps * stages * kCodeBytes);
-  s.x = s.scales + (uint32_t)(kWarps * stages * scale_bytes);
+  s.scales = (uint32_t)(kWarps * kStages * kCodeBytes);
+  s.x = s.scales + (uint32_t)(kWarps * kStages * scale_bytes);
   s.xs = s.x + (uint32_t)C * x_stride(K);
   s.red = s.xs + (uint32_t)(padded_k(K) / kBlockK) * kMaxRows * 4;
   s.bars = s.red + 2 * kWarps * 512;
-  s.first = s.bars + (uint32_t)(kWarps * stages * 8);
+  s.first = s.bars + (uint32_t)(kWarps * kStages * 8);
   s.total = s.first + (uint32_t)(E + 1) * 4;
   return s;
 }
@@ -262,16 +247,18 @@ __device__ __forceinline__ int64_t source_row(const MatvecArgs& a, int r, unsign
 template <int G, bool U8, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_matvec_kernel(const MatvecArgs a, const __grid_constant__ CUtensorMap map,
-                         const int C, const int stages, unsigned* err) {
+                         const int C, unsigned* err) {
   pdl_enter();
   using St = Stage<G, U8, ALIGNED>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const Smem L = smem_layout(St::kScaleBytes, stages, a.K, a.E, C);
+  const Smem L = smem_layout(St::kScaleBytes, a.K, a.E, C);
   const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
   int* first = reinterpret_cast<int*>(smem + L.first);
   float* xs = reinterpret_cast<float*>(smem + L.xs);
   float4* red = reinterpret_cast<float4*>(smem + L.red);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // broadcast, so that what derives from it is known to be one value per warp
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int g = lane >> 2, q = lane & 3;
   const int M = a.swiglu ? 2 * a.N : a.N;
   const int per_tile = a.swiglu ? 8 : 16;  // outputs of one tile
@@ -280,9 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t xrow_bytes = x_stride(a.K);
   const int64_t sf_row = a.K / G;  // scales of one weight row
 
-  const uint32_t bar = sbase + L.bars + (uint32_t)(warp * stages * 8);  // of this warp's stages
+  const uint32_t bar = sbase + L.bars + (uint32_t)(warp * kStages * 8);  // of this warp's stages
   if (lane == 0) {
-    for (int i = 0; i < stages; ++i) mbar_init(bar + i * 8);
+    for (int i = 0; i < kStages; ++i) mbar_init(bar + i * 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -347,12 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b_hi = b_lo + bpw < nblk ? b_lo + bpw : nblk;
   const int mine = b_hi - b_lo;  // blocks of each tile this warp sums
 
-  const uint32_t codes = sbase + L.codes + (uint32_t)(warp * stages * kCodeBytes);
-  const uint32_t scales = sbase + L.scales + (uint32_t)(warp * stages * St::kScaleBytes);
-  int ld_stage = 0, stage = 0;  // the next one to fill, to read
-  uint32_t phase = 0;           // bit i: the parity that stage i's barrier is at
-  int in_flight = 0;            // stages filled or being filled
-  bool ok = true;               // no wait ran out
+  const uint32_t codes = sbase + L.codes + (uint32_t)(warp * kStages * kCodeBytes);
+  const uint32_t scales = sbase + L.scales + (uint32_t)(warp * kStages * St::kScaleBytes);
+  uint32_t phase = 0;  // bit i: the parity that stage i's barrier is at
+  bool ok = true;      // no wait ran out
   int parity = 0;
 
   int64_t u = u0;
@@ -394,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // the stream of stages: where the next one comes from and goes to
-    int ld_tile = tile0 + team, ld_blk = b_lo, to_issue = steps;
+    int ld_tile = tile0 + team, ld_blk = b_lo, to_issue = ok ? steps : 0;
     const char* sf_at = nullptr;  // kHalves: this lane's first scale of block ld_blk
     auto open_tile = [&]() {
       if (St::kHalves) {
@@ -404,10 +389,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     if (steps > 0) open_tile();
-    auto issue = [&]() {
-      if (to_issue > 0 && ok) {
+    // fills stage I with the next block
+    auto issue = [&](auto I) {
+      constexpr int ld_stage = I;
+      if (to_issue > 0) {
         --to_issue;
-        ++in_flight;
         if (lane == 0) {
           // rows past the last output are another's, or past the tensor and zero
           const uint32_t b = bar + ld_stage * 8, dst = codes + ld_stage * kCodeBytes;
@@ -452,7 +438,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                       ok ? 4 : 0);
           }
         }
-        if (++ld_stage == stages) ld_stage = 0;
         if (++ld_blk == b_hi) {
           ld_blk = b_lo;
           ld_tile += teams;
@@ -461,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       cp_async_commit();
     };
-    for (int i = 0; i < stages - 1; ++i) issue();
+    unrolled<kStages - 1>(issue);
 
     // x: each warp converts one block of one row
     const int xblk = padded_k(a.K) / kBlockK;
@@ -513,21 +498,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     tile_offsets();
-    // a warp without a block of its own still joins its team's sums
-    const int loop = mine > 0 ? steps : my_tiles;
-    for (int step = 0; step < loop; ++step) {
-      if (mine > 0) {
-        cp_async_wait_but(stages - 2);
-        if (in_flight > 0) {
-          --in_flight;
-          if (!mbar_wait(bar + stage * 8, (phase >> stage) & 1u)) {
-            ok = false;  // nothing more is fetched; what is on its way is waited for
-            flag_error(err, MOE_DEVERR_TIMEOUT);
-          }
+    // one block of this warp's tiles, from stage I
+    auto block = [&](auto I) {
+        constexpr int stage = I;
+        cp_async_wait<kStages - 2>();
+        if (ok && !mbar_wait(bar + stage * 8, (phase >> stage) & 1u)) {
+          // reported; nothing more is fetched, and what may be on its way to the
+          // other stages is waited for (bounded again)
+          ok = false;
+          to_issue = 0;
+          flag_error(err, MOE_DEVERR_TIMEOUT);
+          for (int i = 0; i < kStages; ++i)
+            if (i != stage) (void)mbar_wait(bar + i * 8, (phase >> i) & 1u);
         }
         phase ^= 1u << stage;
         __syncwarp();
-        issue();
+        issue(std::integral_constant<int, (stage + kStages - 1) % kStages>());
         const uint32_t sst = scales + stage * St::kScaleBytes + g * (St::kWords * 4);
         const float2 xc = *reinterpret_cast<const float2*>(xs + blk * kMaxRows + 2 * q);
         // scales of rows g and g + 8
@@ -552,11 +538,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < St::kGroups; ++j) s[i][j] = __uint_as_float(sw[j]);
           } else {
-            const int sh = 8 * ((sf_off[i] + blk * St::kGroups) & 3);
 #pragma unroll
             for (int j = 0; j < St::kGroups; j += 4) {
               uint32_t w = sw[j / 4];
-              if constexpr (kShift) w = __funnelshift_r(w, sw[j / 4 + 1], sh);
+              if constexpr (kShift)
+                w = __funnelshift_r(w, sw[j / 4 + 1], 8 * ((sf_off[i] + blk * St::kGroups) & 3));
               float v[4];
               ue8m0x4(w, v);
 #pragma unroll
@@ -572,16 +558,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : __fmaf_rn(s[i >> 1][gi], part[i], blk_acc[i]);
         };
         const uint32_t xb = xcol + (uint32_t)blk * (2 * kBlockK);
-        const uint32_t st = (uint32_t)(stage * kCodeBytes);
-        constexpr int kHi = 8 * kRowBytes;  // from row g to row g + 8
+        constexpr int kSt = stage * kCodeBytes, kHi = kSt + 8 * kRowBytes;  // from row g to row g + 8
         unrolled<kBlockK / 32>([&](auto J) {
           constexpr int j = J;
-          const uint32_t row = frag[j] + st;
+          const uint32_t row = frag[j];
           uint32_t a0[4], a1[4];
           uint4 x;
           if constexpr (G == 16) {
             // the 16 channels of a group: 2 bytes of codes per lane
-            const uint32_t w0 = lds16<0>(row), w1 = lds16<8>(row);
+            const uint32_t w0 = lds16<kSt>(row), w1 = lds16<kSt + 8>(row);
             const uint32_t w2 = lds16<kHi>(row), w3 = lds16<kHi + 8>(row);
             a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
             a0[1] = e2m1x2_to_f16x2<0>(w2), a0[3] = e2m1x2_to_f16x2<1>(w2);
@@ -590,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint2 p = lds64<j * 64>(xb), r = lds64<j * 64 + 32>(xb);
             x = make_uint4(p.x, p.y, r.x, r.y);
           } else {
-            const uint32_t w0 = lds32<0>(row), w1 = lds32<kHi>(row);
+            const uint32_t w0 = lds32<kSt>(row), w1 = lds32<kHi>(row);
             x = lds128<j * 64>(xb);
             a0[0] = e2m1x2_to_f16x2<0>(w0), a0[2] = e2m1x2_to_f16x2<1>(w0);
             a0[1] = e2m1x2_to_f16x2<0>(w1), a0[3] = e2m1x2_to_f16x2<1>(w1);
@@ -607,11 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         });
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = __fmaf_rn(i & 1 ? xc.y : xc.x, blk_acc[i], acc[i]);
-        if (++stage == stages) stage = 0;
-        if (++blk < b_hi) continue;
-        blk = b_lo;
-      }
-      // the tile is complete for this warp
+        ++blk;
+    };
+    auto finish = [&]() {  // the tile is complete for this warp
+      blk = b_lo;
       bool writer = true;
       if (split > 1) {
         float4* buf = red + parity * kWarps * 32;
@@ -650,6 +634,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
       tile += teams;
       tile_offsets();
+    };
+    if (mine > 0) {
+      // whole turns of the ring, so that every stage address is a constant; the
+      // next item starts at stage 0 again
+      for (int step = 0; step < steps; step += kStages)
+        unrolled<kStages>([&](auto I) {
+          if (step + I < steps) {
+            block(I);
+            if (blk == b_hi) finish();
+          }
+        });
+    } else {
+      // a warp without a block of its own still joins its team's sums
+      for (int i = 0; i < my_tiles; ++i) finish();
     }
     cp_async_wait<0>();
     __syncthreads();  // x and the rings are free for the next item
@@ -687,12 +685,8 @@ cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
   // more items), and fewer where a long x would not fit
   int C = kMaxRows;
   while (C > 1 && C / 2 >= (a.R + a.k - 1) / a.k) C >>= 1;
-  constexpr uint32_t kSmem = 226 * 1024;
-  while (C > 1 && smem_layout(kScaleBytes, kMinStages, a.K, a.E, C).total > kSmem) C >>= 1;
-  int stages = kMinStages;
-  while (stages < kMaxStages && smem_layout(kScaleBytes, stages + 1, a.K, a.E, C).total <= kSmem)
-    ++stages;
-  const size_t smem = smem_layout(kScaleBytes, stages, a.K, a.E, C).total;
+  while (C > 1 && smem_layout(kScaleBytes, a.K, a.E, C).total > 226 * 1024) C >>= 1;
+  const size_t smem = smem_layout(kScaleBytes, a.K, a.E, C).total;
   auto* kernel = expert_matvec_kernel<G, U8, ALIGNED>;
   cudaError_t e = allow_max_dynamic_smem(kernel);
   if (e != cudaSuccess) return e;
@@ -704,7 +698,7 @@ cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
   const int per_tile = a.swiglu ? 8 : 16;
   const int64_t units = items * ((a.N + per_tile - 1) / per_tile);
   const int64_t blocks = units < c.num_sms ? units : c.num_sms;
-  return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, smem, c.stream, a, map, C, stages, c.err);
+  return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, smem, c.stream, a, map, C, c.err);
 }
 
 template <int G>
