@@ -53,8 +53,37 @@ __device__ __forceinline__ void gate_values(const NormArgs& a, float (&g)[VEC]) 
   }
 }
 
-template <class RT, class YT, int VEC, int NPT>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int tpr) {
+// Accesses a thread holds as loaded (a row waits in registers for its norm).
+template <class T, int VEC>
+struct Raw {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void zero() { v = T(); }
+  __device__ __forceinline__ void get(float (&f)[VEC]) const { load_elems<1>(&v, f); }
+};
+template <>
+struct Raw<Bf16, 8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const Bf16* p) { v = ld_once_v4(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(v, f); }
+};
+template <>
+struct Raw<float, 8> {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p) { load_elems<8>(p, v); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = v[i];
+  }
+};
+
+template <class RT, class YT, int VEC, int NPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_norm_kernel(const NormArgs a, int tpr) {
   pdl_enter();
   __shared__ float red[2][32];
   const int row_in_block = threadIdx.x / tpr, tid = threadIdx.x - row_in_block * tpr;
@@ -64,26 +93,41 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
   const int64_t base = t * a.H;
   const bool has_y = a.y != nullptr;
 
-  float h[NPT][VEC], y[NPT][VEC];
+  float h[NPT][VEC];
+  Raw<RT, VEC> r_raw[NPT];
+  Raw<YT, VEC> y_raw[NPT];
 #pragma unroll
   for (int i = 0; i < NPT; ++i) {
     const int c = (i * tpr + tid) * VEC;
-    if (live && c < a.H) {
-      load_elems<VEC>(static_cast<const RT*>(a.residual) + base + c, h[i]);
-      if (has_y) load_elems<VEC>(static_cast<const YT*>(a.y) + base + c, y[i]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) h[i][q] = y[i][q] = 0.0f;
+    if (has_y) {
+      if (live && c < a.H)
+        y_raw[i].load(static_cast<const YT*>(a.y) + base + c);
+      else
+        y_raw[i].zero();
     }
   }
-  if (has_y) {
+#pragma unroll
+  for (int i = 0; i < NPT; ++i) {
+    const int c = (i * tpr + tid) * VEC;
+    if (live && c < a.H)
+      r_raw[i].load(static_cast<const RT*>(a.residual) + base + c);
+    else
+      r_raw[i].zero();
+  }
+  if (!has_y) {
+#pragma unroll
+    for (int i = 0; i < NPT; ++i) r_raw[i].get(h[i]);
+  } else {
     float rho = 1.0f;
     if (a.post_w) {
       float ss[1] = {0.0f};
 #pragma unroll
-      for (int i = 0; i < NPT; ++i)
+      for (int i = 0; i < NPT; ++i) {
+        float y[VEC];
+        y_raw[i].get(y);
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) ss[0] = __fmaf_rn(y[i][q], y[i][q], ss[0]);
+        for (int q = 0; q < VEC; ++q) ss[0] = __fmaf_rn(y[q], y[q], ss[0]);
+      }
       row_sum<1>(ss, red[0], wpr, row_in_block);
       rho = 1.0f / sqrtf(ss[0] / (float)a.H + a.eps);
       if (live && tid == 0 && a.rstd_post) a.rstd_post[t] = rho;
@@ -96,10 +140,16 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a, int 
 #pragma unroll
     for (int i = 0; i < NPT; ++i) {
       const int c = (i * tpr + tid) * VEC;
-      if (!live || c >= a.H) continue;
-      float z[VEC], g[VEC];
+      if (!live || c >= a.H) {
 #pragma unroll
-      for (int q = 0; q < VEC; ++q) z[q] = y[i][q] * rho;
+        for (int q = 0; q < VEC; ++q) h[i][q] = 0.0f;
+        continue;
+      }
+      float z[VEC], g[VEC];
+      y_raw[i].get(z);
+      r_raw[i].get(h[i]);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) z[q] *= rho;
       if (a.post_w) {
         load_shared_f32<VEC>(a.post_w + c, g);
 #pragma unroll
@@ -353,13 +403,13 @@ Shape row_shape(int units, int npt) {
   return s;
 }
 
-template <class RT, class YT, int VEC, int NPT>
+template <class RT, class YT, int VEC, int NPT, int MAXT>
 cudaError_t fwd_t(const LaunchCtx& c, const NormArgs& a) {
   const Shape s = row_shape((a.H + VEC - 1) / VEC, NPT);
   const int64_t blocks = (a.T + s.rows - 1) / s.rows;
   if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-  return launch_pdl(block_norm_kernel<RT, YT, VEC, NPT>, dim3((unsigned)blocks), s.tpr * s.rows, 0,
-                    c.stream, a, s.tpr);
+  return launch_pdl(block_norm_kernel<RT, YT, VEC, NPT, MAXT>, dim3((unsigned)blocks),
+                    s.tpr * s.rows, 0, c.stream, a, s.tpr);
 }
 
 template <class RT, class YT, int VEC, int NPT>
@@ -387,13 +437,14 @@ template <class RT, class YT>
 cudaError_t fwd_types(const LaunchCtx& c, const NormArgs& a) {
   if (vec_ok(a)) {
     const int units = a.H / 8;
-    if (units <= 256) return fwd_t<RT, YT, 8, 1>(c, a);
-    if (units <= 512) return fwd_t<RT, YT, 8, 2>(c, a);
-    return fwd_t<RT, YT, 8, 4>(c, a);
+    if (units <= 256) return fwd_t<RT, YT, 8, 1, 256>(c, a);
+    if (units <= 512) return fwd_t<RT, YT, 8, 2, 256>(c, a);
+    if (units <= 1024) return fwd_t<RT, YT, 8, 4, 256>(c, a);
+    return fwd_t<RT, YT, 8, 4, 512>(c, a);
   }
-  if (a.H <= 256) return fwd_t<RT, YT, 1, 1>(c, a);
-  if (a.H <= 1024) return fwd_t<RT, YT, 1, 4>(c, a);
-  return fwd_t<RT, YT, 1, 16>(c, a);
+  if (a.H <= 1024) return fwd_t<RT, YT, 1, 4, 256>(c, a);
+  if (a.H <= 4096) return fwd_t<RT, YT, 1, 4, 1024>(c, a);
+  return fwd_t<RT, YT, 1, 16, 1024>(c, a);
 }
 
 template <class RT, class YT>
