@@ -87,8 +87,8 @@ moe_status_t moe_block_norm(const void* residual, int32_t stream_dtype, const vo
 
 size_t moe_block_norm_backward_workspace_bytes(int64_t num_tokens, int32_t hidden) {
   if (num_tokens <= 0 || hidden < 1 || hidden > MOE_NORM_MAX_HIDDEN) return 0;
-  const int64_t blocks = num_tokens < kNormMaxPartials ? num_tokens : kNormMaxPartials;
-  return ((size_t)blocks * 3 * (size_t)hidden * 4 + 255) / 256 * 256;
+  const int64_t blocks = norm_partial_blocks(num_tokens, hidden);
+  return ((size_t)blocks * 2 * (size_t)hidden * 4 + 255) / 256 * 256;
 }
 
 moe_status_t moe_block_norm_backward(

@@ -13,10 +13,11 @@ struct Bf16 {
   uint16_t bits;
 };
 
+// Two f32 values rounded to nearest even bf16, `lo` in the low half: one paired
+// conversion (the single one runs at a quarter of its rate).
 __device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
-  const uint32_t l = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
-  const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
-  return l | (h << 16);
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
 __device__ __forceinline__ void unpack8(const uint4& a, float (&v)[8]) {
@@ -105,7 +106,67 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + expf(-x)); }
+// g = 1 / (1 + e^-x) and g' = g (1 - g), both to a few ulp for every x: with
+// e = e^-|x| the larger of g and 1 - g is 1 / (1 + e), the smaller e / (1 + e).
+__device__ __forceinline__ float sigmoid_f32(float x, float* deriv = nullptr) {
+  const float e = expf(-fabsf(x));
+  const float big = __fdividef(1.0f, 1.0f + e), small = e * big;
+  if (deriv) *deriv = big * small;
+  return x < 0.0f ? small : big;
+}
+
+// 1 / sqrt(x) for x > 0: the hardware estimate and one Newton step.
+__device__ __forceinline__ float rsqrt_f32(float x) {
+  const float y = rsqrtf(x);
+  return __fmaf_rn(0.5f * y, __fmaf_rn(-x * y, y, 1.0f), y);
+}
+
+// ------------------------------------------------ barriers of bulk copies
+
+__device__ __forceinline__ void mbar_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for the phase `parity` of the barrier; false if that took over a second.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  uint64_t begin = 0;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    const uint64_t t = now_ns();
+    if (begin == 0) begin = t;
+    if (t - begin > 1000000000ull) return false;
+  }
+}
+// Copies `bytes` (a multiple of 16) from global to shared memory, both 16-byte
+// aligned, and counts them at the barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// Makes barriers that this thread initialised known to the copy engine.
+__device__ __forceinline__ void mbar_init_done() {
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 
 // ------------------------------------------------------------- launchers
 
@@ -135,15 +196,21 @@ struct NormArgs {
   void* grad_gate = nullptr;
   float* grad_post_w = nullptr;
   float* grad_pre_w = nullptr;
-  float* partials = nullptr;  // workspace: [3][blocks][H] sums over a block's tokens
+  float* partials = nullptr;  // workspace: [2][blocks][H] sums over a block's tokens
 };
 cudaError_t launch_block_norm(const LaunchCtx& c, const NormArgs& a, bool stream_f32,
                               bool block_f32);
 cudaError_t launch_block_norm_backward(const LaunchCtx& c, const NormArgs& a, bool stream_f32,
                                        bool block_f32);
 // Blocks of the backward that leave partial sums over tokens: at most this
-// many, and at most one per token.
-constexpr int kNormMaxPartials = 320;
+// many, and at most one per token.  (160 SMs at most, each with as many blocks
+// of H / 16 threads as make 512, at most 16.)
+inline int64_t norm_partial_blocks(int64_t T, int H) {
+  const int threads = (H + 511) / 512 * 32;
+  const int per_sm = threads >= 512 ? 1 : 512 / threads;
+  const int64_t cap = (int64_t)160 * (per_sm > 16 ? 16 : per_sm);
+  return T < cap ? T : cap;
+}
 
 // moe_balance_loss (balance_loss.cu).
 struct BalanceArgs {

@@ -115,35 +115,6 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void mbar_init(uint32_t bar) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// Waits for the phase `parity` of the barrier; false if that took over a second.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  uint64_t begin = 0;
-  for (;;) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    const uint64_t t = now_ns();
-    if (begin == 0) begin = t;
-    if (t - begin > 1000000000ull) return false;
-  }
-}
 // A box of 8 rows of 128 bytes at byte column c and row r of the codes.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c, int r,
                                         uint32_t bar) {
@@ -270,8 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar = sbase + L.bars + (uint32_t)(warp * kStages * 8);  // of this warp's stages
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(bar + i * 8);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    mbar_init_done();
   }
 
   // first[e]: items of the experts before e; each thread counts kPer experts

@@ -556,3 +556,31 @@ def test_matvec_past_32_bit_offsets():
         want, mag, _ = ref.expert_matvec(x[r:r + 1], w[e:e + 1], sf[e:e + 1], 32, None, None, 1,
                                          False, 1)
         ref.check(got[r:r + 1], want, mag, f"expert {e}")
+
+
+@pytest.mark.parametrize("T,H", [(512, 8), (700, 40), (5000, 264), (1300, 512), (900, 1024), (601, 4096),
+                                 (640, 7168), (513, 8192)])
+@pytest.mark.parametrize("sd,bd", [(BF, BF), (F32, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("gate", ["channel", "element"])
+def test_norm_many_tokens(T, H, sd, bd, gate):
+    """Enough rows that every block of the ring takes several."""
+    s = norm_inputs(T, H, sd, bd, gate, T * 31 + H)
+    check_norm(s, "sigmoid", run_norm(s, "sigmoid"))
+    run_check_backward(s, "sigmoid", H)
+
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "element"])
+@pytest.mark.parametrize("post,pre,y", [(True, True, True), (True, False, True), (False, True, True),
+                                        (False, False, True), (False, True, False)])
+@pytest.mark.parametrize("H", [256, 1032])
+def test_norm_many_tokens_options(gate, post, pre, y, H):
+    s = norm_inputs(1500, H, F32, BF, gate, 5, post=post, pre=pre, y=y)
+    act = "sigmoid" if s["gate"] is not None else "none"
+    check_norm(s, act, run_norm(s, act, scale=0.75), scale=0.75)
+    run_check_backward(s, act, 6, scale=0.75)
+    run_check_backward(s, act, 7, gh_none=True, scale=0.75)
+    a = run_norm(s, act)
+    n = None if a[1] is None else torch.empty_like(a[1])
+    if y:
+        b = run_norm(s, act, out=(s["residual"], n))          # in place
+        assert torch.equal(a[0], b[0]) and (n is None or torch.equal(a[1], n))
