@@ -594,6 +594,7 @@ size_t moe_block_norm_backward_workspace_bytes(int64_t num_tokens, int32_t hidde
  *   of all T tokens (num_seqs 1);  token_mask [T] u8, may be NULL
  *   balance, z [S] f32; counts [S, E] i32; probs [S, E] f32; tokens [S] i32 (n_i)
  *   workspace: moe_balance_loss_workspace_bytes(T, E, S) bytes, 16-byte aligned
+ *   (0 for small problems: it may then be NULL)
  * An index outside [0, E) is not counted and sets MOE_DEVERR_EXPERT_RANGE.
  * The same inputs give the same bits.  Requires the E and k limits of
  * moe_topk_gate, 1 <= num_seqs <= 65535 and 0 <= T < 2^31.

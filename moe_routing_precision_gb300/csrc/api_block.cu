@@ -194,10 +194,10 @@ moe_status_t moe_balance_loss(const float* scores, const int32_t* topk_idx, int6
     if (e == cudaSuccess) e = zero(probs, SE * 4, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e);
   }
-  if (!scores || !topk_idx || !workspace || !aligned(scores, 4) || !aligned(topk_idx, 4) ||
-      !aligned(workspace, 16))
+  if (!scores || !topk_idx || !aligned(scores, 4) || !aligned(topk_idx, 4))
     return MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < moe_balance_loss_workspace_bytes(num_tokens, num_experts, num_seqs))
+  const size_t need = moe_balance_loss_workspace_bytes(num_tokens, num_experts, num_seqs);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return MOE_ERR_INVALID_ARG;
   LaunchCtx c;
   moe_status_t s = context(stream, &c);

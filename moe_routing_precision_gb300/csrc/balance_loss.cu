@@ -9,19 +9,28 @@
 // second launch adds each sequence's rows in ascending order.  No float is
 // added atomically: the same inputs give the same bits.
 //
+// A small problem (see kOneBlockScores) is one block and one launch, without
+// the table.
+//
 // A group of L lanes holds one token's scores in registers (W consecutive
-// experts per access); the row's maximum, exponentials and sums come from
-// those registers, so the scores are read once, which bounds both passes.
+// experts per access), and loads the next token's while it works; the
+// exponentials and sums come from those registers, so the scores are read once,
+// which bounds both passes.  Rows whose largest score lies in [-20, 80] (any
+// router's, whatever its masked scores) need no maximum taken off: e^x, its sums
+// and the sigmoids e^x / (1 + e^x) stay in f32's range, and what underflows is
+// below 1e-29 of the row.  Other rows take the shifted form.
 #include "block_ops.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;  // forward
 constexpr int kWarps = kThreads / 32;
+constexpr int kBwdThreads = 256;
+constexpr int kBwdWarps = kBwdThreads / 32;
 
-// Chunks of consecutive tokens: about kBalanceChunks of them, each a multiple
-// of kWarps tokens.
+// Chunks of consecutive tokens: about kBalanceChunks of them (two blocks per
+// SM), each a multiple of kWarps tokens.
 constexpr int64_t kBalanceChunks = 304;
 __host__ __device__ inline int64_t chunk_tokens(int64_t T) {
   const int64_t c = (T + kBalanceChunks - 1) / kBalanceChunks;
@@ -31,6 +40,12 @@ inline int64_t num_chunks(int64_t T) {
   if (T <= 0) return 0;
   const int64_t c = chunk_tokens(T);
   return (T + c - 1) / c;
+}
+// One block up to this many scores.
+constexpr int64_t kOneBlockScores = 32768;
+constexpr int kOneBlockSeqs = 64;
+inline bool one_block(int64_t T, int E, int S) {
+  return T * E <= kOneBlockScores && S <= kOneBlockSeqs;
 }
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -125,53 +140,78 @@ struct Row {
   }
 };
 
-// From a row's scores x: the maximum m (-inf: the token does not count), the
-// log of the summed exponentials, and p in place of nothing else than `p`.
-// SIG: p = sigmoid(x) / sum sigmoid.  sigmoid(x) = e^min(x,0) / (1 + e^-|x|);
-// the numerators are taken relative to e^min(m,0), so a row of very negative
-// scores keeps its proportions instead of underflowing.
-template <int L, int N, bool SIG>
+// 1 / x for normal x, to an ulp: the hardware estimate and one Newton step.
+__device__ __forceinline__ float rcp_f32(float x) {
+  const float y = __fdividef(1.0f, x);
+  return __fmaf_rn(y, __fmaf_rn(-x, y, 1.0f), y);
+}
+
+// From a row's scores x (a group of L lanes, N values per lane): p, lse, whether
+// the token counts (any score above -inf), and what only the backward wants:
+// q = softmax(x) and, for SIG, n = 1 - sigmoid(x).
+template <int L, int N, bool SIG, bool BWD>
 __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], float (&q)[N],
-                                          float* lse, bool* counts) {
-  float m = kNegInf;
+                                          float (&n)[N], float* lse, bool* counts) {
+  float top = kNegInf;
 #pragma unroll
-  for (int i = 0; i < N; ++i) m = fmaxf(m, x[i]);
-  m = group_max<L>(m);
-  const bool ok = m > kNegInf;
-  const float mm = ok ? m : 0.0f;
-  float tot = 0.0f;
+  for (int i = 0; i < N; ++i) top = fmaxf(top, x[i]);
+  float tot = 0.0f, stot = 0.0f;
+  // groups whose maximum is finite but below -20, one bit each
+  unsigned some = __ballot_sync(0xFFFFFFFFu, top > kNegInf);
+  unsigned near = __ballot_sync(0xFFFFFFFFu, top >= -20.0f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = expf(x[i] - mm);
-    tot += q[i];
-  }
-  tot = group_sum<L>(tot);
-  const float inv = ok ? 1.0f / tot : 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) q[i] *= inv;
-  *lse = ok ? mm + logf(tot) : 0.0f;
-  *counts = ok;
-  if (SIG) {
-    const float m0 = fminf(mm, 0.0f);
-    tot = 0.0f;
+  for (int o = 1; o < L; o <<= 1) some |= some >> o, near |= near >> o;
+  constexpr unsigned kFirst = L == 4 ? 0x11111111u : L == 8 ? 0x01010101u : L == 16 ? 0x00010001u : 1u;
+  if ((some & ~near & kFirst) != 0 || __any_sync(0xFFFFFFFFu, top > 80.0f)) {
+    // scores far from zero: relative to the maximum, sigmoids to e^min(max, 0)
+    top = group_max<L>(top);
+    const bool ok = top > kNegInf;
+    const float m = ok ? top : 0.0f, m0 = fminf(m, 0.0f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      p[i] = expf(fminf(x[i], 0.0f) - m0) / (1.0f + expf(-fabsf(x[i])));
-      tot += p[i];
+      q[i] = expf(x[i] - m);
+      tot += q[i];
+      if (SIG) {
+        const float e = expf(-fabsf(x[i])), r = rcp_f32(1.0f + e);
+        p[i] = expf(fminf(x[i], 0.0f) - m0) * r;
+        n[i] = x[i] < 0.0f ? r : e * r;
+        stot += p[i];
+      }
     }
     tot = group_sum<L>(tot);
-    const float pin = ok ? 1.0f / tot : 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] *= pin;
+    if (SIG) stot = group_sum<L>(stot);
+    *lse = ok ? m + logf(tot) : 0.0f;
+    *counts = ok;
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = q[i];
+    for (int i = 0; i < N; ++i) {
+      q[i] = expf(x[i]);
+      tot += q[i];
+      if (SIG) {
+        n[i] = rcp_f32(1.0f + q[i]);
+        p[i] = q[i] * n[i];
+        stot += p[i];
+      }
+    }
+    tot = group_sum<L>(tot);
+    if (SIG) stot = group_sum<L>(stot);
+    *counts = tot > 0.0f;
+    *lse = *counts ? logf(tot) : 0.0f;
+  }
+  const float inv = *counts ? 1.0f / tot : 0.0f;
+  const float sinv = SIG && *counts ? 1.0f / stot : 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (!SIG || BWD) q[i] *= inv;
+    p[i] = SIG ? p[i] * sinv : q[i];
   }
 }
 
+// one: a single block, which writes the results itself.
 template <int L, int W, int NV, bool SIG>
-__global__ void __launch_bounds__(kThreads)
-    balance_chunk_kernel(const BalanceArgs a, const Work ws, int64_t chunk, unsigned* err) {
+__global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
+    balance_chunk_kernel(const BalanceArgs a, const Work ws, int64_t chunk, bool one,
+                         unsigned* err) {
   pdl_enter();
   extern __shared__ float smem[];  // [kWarps][E] sums of p, [E] counts, then per-warp n and z
   constexpr int N = NV * W, TPW = 32 / L;
@@ -181,8 +221,9 @@ __global__ void __launch_bounds__(kThreads)
   int* cnt = reinterpret_cast<int*>(smem + kWarps * E);
   float* wz = reinterpret_cast<float*>(cnt + E);
   int* wn = reinterpret_cast<int*>(wz + kWarps);
+  float* wf = reinterpret_cast<float*>(wn + kWarps);
 
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0 && !one)
     for (int i = threadIdx.x; i < a.S; i += kThreads) ws.arrived[i] = 0u;
   for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = 0;
   __syncthreads();
@@ -190,25 +231,42 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t b0 = (int64_t)blockIdx.x * chunk;
   const int64_t b1 = b0 + chunk < a.T ? b0 + chunk : a.T;
   bool bad = false;
-  for (int s = first_seq(a, b0); s < a.S; ++s) {
+  for (int s = one ? 0 : first_seq(a, b0); s < a.S; ++s) {
     const int64_t s0 = seq_at(a, s), s1 = seq_at(a, s + 1);
-    if (s0 >= b1) break;
+    if (s0 >= b1 && !one) break;
     const int64_t lo = s0 > b0 ? s0 : b0, hi = s1 < b1 ? s1 : b1;
-    if (lo >= hi) continue;
+    if (lo >= hi) {
+      if (one) {
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+          a.probs[(int64_t)s * E + e] = 0.0f;
+          a.counts[(int64_t)s * E + e] = 0;
+        }
+        if (threadIdx.x == 0) a.balance[s] = 0.0f, a.z[s] = 0.0f, a.tokens[s] = 0;
+      }
+      continue;
+    }
     float acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     float zsum = 0.0f;
     int n = 0;
+    Row<L, W, NV> next;
+    int32_t next_e = -1;  // this lane's first index of the next token
+    auto fetch = [&](int64_t t) {
+      const bool want = t < hi && (a.mask == nullptr || __ldg(a.mask + t) != 0);
+      next.load(a.scores, t, E, sub, want);
+      next_e = want && sub < a.k ? __ldg(a.idx + t * a.k + sub) : 0;
+    };
+    fetch(lo + warp * TPW + grp);
     for (int64_t t0 = lo + warp * TPW; t0 < hi; t0 += kWarps * TPW) {
       const int64_t t = t0 + grp;
-      const bool want = t < hi && (a.mask == nullptr || __ldg(a.mask + t) != 0);
-      Row<L, W, NV> row;
-      row.load(a.scores, t, E, sub, want);
-      float p[N], q[N], lse;
+      const Row<L, W, NV> row = next;
+      const int32_t e0 = next_e;
+      fetch(t + kWarps * TPW);
+      float p[N], q[N], unused[N], lse;
       bool counts;
-      row_probs<L, N, SIG>(row.x, p, q, &lse, &counts);
-      if (!counts) continue;  // uniform in the group; no shuffle follows
+      row_probs<L, N, SIG, false>(row.x, p, q, unused, &lse, &counts);
+      if (!counts) continue;  // uniform in the group; the next shuffle waits for all groups
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i] += p[i];
       if (sub == 0) {
@@ -216,13 +274,14 @@ __global__ void __launch_bounds__(kThreads)
         n += 1;
       }
       for (int j = sub; j < a.k; j += L) {
-        const int e = __ldg(a.idx + t * a.k + j);
+        const int e = j == sub ? e0 : __ldg(a.idx + t * a.k + j);
         if (e >= 0 && e < E)
           atomicAdd(cnt + e, 1);
         else
           bad = true;
       }
     }
+    __syncwarp();
     // the warp's groups, then the block's warps, in a fixed order
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -244,22 +303,44 @@ __global__ void __launch_bounds__(kThreads)
       wn[warp] = n;
     }
     __syncthreads();
+    float z = 0.0f;
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) z += wz[w], n += wn[w];
     const int64_t slot = (int64_t)blockIdx.x + s;
+    float f = 0.0f;
     for (int e = threadIdx.x; e < E; e += kThreads) {
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) v += psum[w * E + e];
-      ws.p[slot * E + e] = v;
-      ws.cnt[slot * E + e] = cnt[e];
+      const int c = cnt[e];
       cnt[e] = 0;
+      if (one) {
+        v = n > 0 ? v / (float)n : 0.0f;
+        a.probs[(int64_t)s * E + e] = v;
+        a.counts[(int64_t)s * E + e] = c;
+        f = __fmaf_rn((float)c, v, f);
+      } else {
+        ws.p[slot * E + e] = v;
+        ws.cnt[slot * E + e] = c;
+      }
     }
-    if (threadIdx.x == 0) {
-      float v = 0.0f;
-      int m = 0;
+    if (one) {
+      f = warp_sum(f);
+      if (lane == 0) wf[warp] = f;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        f = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += wz[w], m += wn[w];
-      ws.z[slot] = v;
-      ws.n[slot] = m;
+        for (int w = 0; w < kWarps; ++w) f += wf[w];
+        const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
+        a.balance[s] = f * inv * ((float)E / (float)a.k);
+        a.z[s] = z * inv;
+        a.tokens[s] = n;
+      }
+    } else if (threadIdx.x == 0) {
+      ws.z[slot] = z;
+      ws.n[slot] = n;
     }
     __syncthreads();
   }
@@ -344,10 +425,10 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 }
 
 template <int L, int W, int NV, bool SIG>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
     balance_backward_kernel(const BalanceArgs a, int64_t chunk, unsigned* err) {
   pdl_enter();
-  extern __shared__ float smem[];  // per group: [E] gradients of the selected scores
+  extern __shared__ __align__(16) float smem[];  // per group: [E] gradients of the selected scores
   constexpr int N = NV * W, TPW = 32 / L;
   const int E = a.E, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % L, grp = lane / L;
@@ -372,6 +453,20 @@ __global__ void __launch_bounds__(kThreads)
       if (hi > b1) hi = b1;
       if (hi <= lo) continue;
       done = hi;
+      // the next token's scores, and this lane's first selection of it
+      Row<L, W, NV> next;
+      int32_t next_e = 0;
+      float next_w = 0.0f, next_g = 0.0f;
+      auto fetch = [&](int64_t t) {
+        const bool want = in_seq && t < hi && (a.mask == nullptr || __ldg(a.mask + t) != 0);
+        next.load(a.scores, t, E, sub, want);
+        if (sel && want && sub < a.k) {
+          next_e = __ldg(a.idx + t * a.k + sub);
+          next_w = __ldg(a.w + t * a.k + sub);
+          next_g = __ldg(a.grad_w + t * a.k + sub);
+        }
+      };
+      fetch(lo + warp * TPW + grp);
       float coef[N], zc = 0.0f;
 #pragma unroll
       for (int i = 0; i < N; ++i) coef[i] = 0.0f;
@@ -381,8 +476,7 @@ __global__ void __launch_bounds__(kThreads)
           const float inv = 1.0f / (float)n;
           if (a.grad_z) zc = 2.0f * __ldg(a.grad_z + s) * inv;
           if (a.grad_balance) {
-            const float gb =
-                __ldg(a.grad_balance + s) * inv * inv * ((float)E / (float)a.k);
+            const float gb = __ldg(a.grad_balance + s) * inv * inv * ((float)E / (float)a.k);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -393,69 +487,77 @@ __global__ void __launch_bounds__(kThreads)
           }
         }
       }
-      for (int64_t t0 = lo + warp * TPW; t0 < hi; t0 += kWarps * TPW) {
+      for (int64_t t0 = lo + warp * TPW; t0 < hi; t0 += kBwdWarps * TPW) {
         const int64_t t = t0 + grp;
-        const bool mine_t = t < hi;
-        const bool want = in_seq && mine_t && (a.mask == nullptr || __ldg(a.mask + t) != 0);
-        Row<L, W, NV> row;
-        row.load(a.scores, t, E, sub, want);
-        float p[N], q[N], lse;
+        const Row<L, W, NV> row = next;
+        const int32_t e0 = next_e;
+        const float w0 = next_w, g0 = next_g;
+        fetch(t + kBwdWarps * TPW);
+        float p[N], q[N], om[N], lse;
         bool counts;
-        row_probs<L, N, SIG>(row.x, p, q, &lse, &counts);
-        float dot = 0.0f;
+        row_probs<L, N, SIG, true>(row.x, p, q, om, &lse, &counts);
+        float dot = 0.0f, wg = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) dot = __fmaf_rn(p[i], coef[i], dot);
+        if (sel && counts) {
+          for (int j = sub; j < a.k; j += L) {
+            const float w = j == sub ? w0 : __ldg(a.w + t * a.k + j);
+            const float g = j == sub ? g0 : __ldg(a.grad_w + t * a.k + j);
+            wg = __fmaf_rn(w, g, wg);
+          }
+        }
         dot = group_sum<L>(dot);
+        if (sel) {
+          wg = group_sum<L>(wg);
+          if (counts) {
+            for (int j = sub; j < a.k; j += L) {
+              const int e = j == sub ? e0 : __ldg(a.idx + t * a.k + j);
+              const float w = j == sub ? w0 : __ldg(a.w + t * a.k + j);
+              const float g = j == sub ? g0 : __ldg(a.grad_w + t * a.k + j);
+              if (e >= 0 && e < E)
+                mine[e] = w * (g - wg);
+              else
+                bad = true;
+            }
+          }
+          __syncwarp();
+        }
         float d[N];
         const float zl = zc * lse;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           float v = p[i] * (coef[i] - dot);
-          if (SIG) v *= 1.0f / (1.0f + expf(row.x[i]));
+          if (SIG) v *= om[i];
           d[i] = counts ? __fmaf_rn(zl, q[i], v) : 0.0f;
         }
-        if (sel) {
-          float wg = 0.0f;
-          for (int j = sub; j < a.k; j += L)
-            if (counts) wg = __fmaf_rn(__ldg(a.w + t * a.k + j), __ldg(a.grad_w + t * a.k + j), wg);
-          wg = group_sum<L>(wg);
-          for (int j = sub; j < a.k; j += L) {
-            if (!counts) break;
-            const int e = __ldg(a.idx + t * a.k + j);
-            if (e >= 0 && e < E)
-              mine[e] = __ldg(a.w + t * a.k + j) * (__ldg(a.grad_w + t * a.k + j) - wg);
-            else
-              bad = true;
-          }
-          __syncwarp();
 #pragma unroll
-          for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-              const int e = Row<L, W, NV>::expert(sub, v) + i;
-              if (e < E) d[v * W + i] += mine[e];
+        for (int v = 0; v < NV; ++v) {
+          const int e = Row<L, W, NV>::expert(sub, v);
+          if (e >= E) continue;
+          if constexpr (W == 4) {
+            if (sel) {
+              const float4 m = *reinterpret_cast<const float4*>(mine + e);
+              d[4 * v] += m.x, d[4 * v + 1] += m.y, d[4 * v + 2] += m.z, d[4 * v + 3] += m.w;
             }
-          __syncwarp();
-          for (int j = sub; j < a.k; j += L) {
-            if (!counts) break;
-            const int e = __ldg(a.idx + t * a.k + j);
-            if (e >= 0 && e < E) mine[e] = 0.0f;
-          }
-          __syncwarp();
-        }
-        if (mine_t) {
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const int e = Row<L, W, NV>::expert(sub, v);
-            if (e >= E) continue;
-            if constexpr (W == 4)
+            if (t < hi)
               st_stream_v4(a.grad_scores + t * E + e,
                            make_uint4(__float_as_uint(d[4 * v]), __float_as_uint(d[4 * v + 1]),
                                       __float_as_uint(d[4 * v + 2]),
                                       __float_as_uint(d[4 * v + 3])));
-            else
-              st_stream_f32(a.grad_scores + t * E + e, d[v]);
+          } else {
+            if (sel) d[v] += mine[e];
+            if (t < hi) st_stream_f32(a.grad_scores + t * E + e, d[v]);
           }
+        }
+        if (sel) {
+          __syncwarp();
+          if (counts) {
+            for (int j = sub; j < a.k; j += L) {
+              const int e = j == sub ? e0 : __ldg(a.idx + t * a.k + j);
+              if (e >= 0 && e < E) mine[e] = 0.0f;
+            }
+          }
+          __syncwarp();
         }
       }
     }
@@ -465,22 +567,30 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int L, int W, int NV, bool SIG>
 cudaError_t forward_t(const LaunchCtx& c, const BalanceArgs& a) {
-  const int64_t chunk = chunk_tokens(a.T), chunks = num_chunks(a.T);
+  const bool one = one_block(a.T, a.E, a.S);
+  const int64_t chunk = one ? a.T : chunk_tokens(a.T), chunks = one ? 1 : num_chunks(a.T);
   const Work ws = work_layout(a.ws, a.T, a.E, a.S);
-  const size_t smem = (size_t)(kWarps + 1) * a.E * 4 + kWarps * 8;
-  cudaError_t e = launch_pdl(balance_chunk_kernel<L, W, NV, SIG>, dim3((unsigned)chunks), kThreads,
-                             smem, c.stream, a, ws, chunk, c.err);
+  const size_t smem = (size_t)(kWarps + 1) * a.E * 4 + kWarps * 12;
+  auto* kernel = balance_chunk_kernel<L, W, NV, SIG>;
+  cudaError_t e = smem > 48 * 1024 ? allow_max_dynamic_smem(kernel) : cudaSuccess;
   if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3((unsigned)chunks), kThreads, smem, c.stream, a, ws, chunk, one,
+                 c.err);
+  if (e != cudaSuccess || one) return e;
   return launch_pdl(balance_sum_kernel, dim3((unsigned)((a.E + kTile - 1) / kTile), (unsigned)a.S),
                     32 * kSumWarps, 0, c.stream, a, ws, chunk);
 }
 
 template <int L, int W, int NV, bool SIG>
 cudaError_t backward_t(const LaunchCtx& c, const BalanceArgs& a) {
-  const int64_t chunk = chunk_tokens(a.T), chunks = num_chunks(a.T);
-  const size_t smem = a.grad_w ? (size_t)kWarps * (32 / L) * a.E * 4 : 0;
-  return launch_pdl(balance_backward_kernel<L, W, NV, SIG>, dim3((unsigned)chunks), kThreads, smem,
-                    c.stream, a, chunk, c.err);
+  // eight blocks' worth of tokens per SM, at least one pass of a block's warps
+  constexpr int kPass = kBwdWarps * (32 / L);
+  int64_t chunk = (a.T + 8 * c.num_sms - 1) / (8 * c.num_sms);
+  chunk = (chunk + kPass - 1) / kPass * kPass;
+  const int64_t chunks = (a.T + chunk - 1) / chunk;
+  const size_t smem = a.grad_w ? (size_t)kPass * a.E * 4 : 0;
+  return launch_pdl(balance_backward_kernel<L, W, NV, SIG>, dim3((unsigned)chunks), kBwdThreads,
+                    smem, c.stream, a, chunk, c.err);
 }
 
 template <int L, int W, int NV>
@@ -515,6 +625,7 @@ cudaError_t dispatch(const LaunchCtx& c, const BalanceArgs& a, bool backward) {
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t T, int E, int S) {
+  if (one_block(T, E, S)) return 0;
   return work_layout(nullptr, T, E, S).bytes;
 }
 

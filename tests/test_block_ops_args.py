@@ -66,11 +66,12 @@ def test_block_norm_backward_refusals(L):
 
 
 def test_balance_loss_refusals(L):
-    need = L.moe_balance_loss_workspace_bytes(100, 16, 3)
-    assert need > 0 and L.moe_balance_loss_workspace_bytes(0, 16, 1) == 0
+    need = L.moe_balance_loss_workspace_bytes(10000, 16, 3)
+    assert need > 0 and L.moe_balance_loss_workspace_bytes(100, 16, 3) == 0
+    assert L.moe_balance_loss_workspace_bytes(0, 16, 1) == 0
     assert L.moe_balance_loss_workspace_bytes(100, 2000, 1) == 0
 
-    def f(s=FAKE, i=FAKE, T=100, E=16, k=2, func=0, seq=FAKE, S=3, mask=None, b=FAKE, z=FAKE,
+    def f(s=FAKE, i=FAKE, T=10000, E=16, k=2, func=0, seq=FAKE, S=3, mask=None, b=FAKE, z=FAKE,
           c=FAKE, p=FAKE, t=FAKE, ws=FAKE, wsb=need):
         return L.moe_balance_loss(s, i, T, E, k, func, seq, S, mask, b, z, c, p, t, ws, wsb, None)
     assert f(T=-1) == INVALID and f(T=1 << 31) == INVALID
