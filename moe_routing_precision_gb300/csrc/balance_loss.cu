@@ -159,8 +159,12 @@ __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], fl
   // groups whose maximum is finite but below -20, one bit each
   unsigned some = __ballot_sync(0xFFFFFFFFu, top > kNegInf);
   unsigned near = __ballot_sync(0xFFFFFFFFu, top >= -20.0f);
+  if (L == 32) {
+    some = some != 0, near = near != 0;
+  } else {
 #pragma unroll
-  for (int o = 1; o < L; o <<= 1) some |= some >> o, near |= near >> o;
+    for (int o = 1; o < L; o <<= 1) some |= some >> o, near |= near >> o;
+  }
   constexpr unsigned kFirst = L == 4 ? 0x11111111u : L == 8 ? 0x01010101u : L == 16 ? 0x00010001u : 1u;
   if ((some & ~near & kFirst) != 0 || __any_sync(0xFFFFFFFFu, top > 80.0f)) {
     // scores far from zero: relative to the maximum, sigmoids to e^min(max, 0)
@@ -572,7 +576,8 @@ cudaError_t forward_t(const LaunchCtx& c, const BalanceArgs& a) {
   const Work ws = work_layout(a.ws, a.T, a.E, a.S);
   const size_t smem = (size_t)(kWarps + 1) * a.E * 4 + kWarps * 12;
   auto* kernel = balance_chunk_kernel<L, W, NV, SIG>;
-  cudaError_t e = smem > 48 * 1024 ? allow_max_dynamic_smem(kernel) : cudaSuccess;
+  static SmemOptIn opt_in;
+  cudaError_t e = smem > 48 * 1024 ? opt_in.once(c, kernel) : cudaSuccess;
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3((unsigned)chunks), kThreads, smem, c.stream, a, ws, chunk, one,
                  c.err);

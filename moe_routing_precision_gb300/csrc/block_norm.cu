@@ -804,11 +804,16 @@ cudaError_t bwd_t(const LaunchCtx& c, const NormArgs& a) {
   const Shape s = row_shape((a.H + VEC - 1) / VEC, NPT);
   const size_t smem = 192 * sizeof(float) + (s.rows > 1 ? (size_t)s.rows * a.H * sizeof(float) : 0);
   auto* kernel = block_norm_backward_kernel<RT, YT, VEC, NPT>;
-  cudaError_t e = allow_max_dynamic_smem(kernel);
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.once(c, kernel);
   if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, s.tpr * s.rows, smem);
-  if (e != cudaSuccess) return e;
+  // blocks per SM, looked up when the shape changes (1 us a call)
+  thread_local int known = -1, per_sm = 0;
+  if (known != a.H) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, s.tpr * s.rows, smem);
+    if (e != cudaSuccess) return e;
+    known = a.H;
+  }
   int64_t blocks = (a.T + s.rows - 1) / s.rows;
   const int64_t cap = (int64_t)c.num_sms * (per_sm > 0 ? per_sm : 1);
   if (blocks > cap) blocks = cap;
@@ -825,8 +830,8 @@ bool ring_ok(const NormArgs& a) {
   return a.H <= kRingMaxHidden && a.T >= 512 && vec_ok(a, 32);
 }
 
-template <class KernelPtr>
-cudaError_t ring_launch(const LaunchCtx& c, const NormArgs& a, KernelPtr kernel, int rows,
+template <auto* kernel>
+cudaError_t ring_launch(const LaunchCtx& c, const NormArgs& a, int rows,
                         const uint32_t (&row_bytes)[5], int64_t max_blocks, int* blocks_out) {
   Ring ring;
   for (int i = 0; i < 5; ++i) {
@@ -842,7 +847,8 @@ cudaError_t ring_launch(const LaunchCtx& c, const NormArgs& a, KernelPtr kernel,
   }
   if (ring.stages > kRingMaxStages) ring.stages = kRingMaxStages;
   const size_t smem = kRingHeader + (size_t)ring.stages * ring.stage_bytes;
-  cudaError_t e = allow_max_dynamic_smem(kernel);
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.once(c, kernel);
   if (e != cudaSuccess) return e;
   int64_t blocks = (int64_t)c.num_sms * per_sm;
   if (blocks > max_blocks) blocks = max_blocks;
@@ -867,11 +873,11 @@ cudaError_t fwd_types(const LaunchCtx& c, const NormArgs& a) {
     int blocks = 0;
     if (ring_fits<RT, YT>(a, 2, 1, y_rows)) {
       const int64_t room = (a.T + 1) / 2;
-      return gel ? ring_launch(c, a, norm_ring_kernel<RT, YT, true, 2>, 2, bytes, room, &blocks)
-                 : ring_launch(c, a, norm_ring_kernel<RT, YT, false, 2>, 2, bytes, room, &blocks);
+      return gel ? ring_launch<norm_ring_kernel<RT, YT, true, 2>>(c, a, 2, bytes, room, &blocks)
+                 : ring_launch<norm_ring_kernel<RT, YT, false, 2>>(c, a, 2, bytes, room, &blocks);
     }
-    return gel ? ring_launch(c, a, norm_ring_kernel<RT, YT, true, 1>, 1, bytes, a.T, &blocks)
-               : ring_launch(c, a, norm_ring_kernel<RT, YT, false, 1>, 1, bytes, a.T, &blocks);
+    return gel ? ring_launch<norm_ring_kernel<RT, YT, true, 1>>(c, a, 1, bytes, a.T, &blocks)
+               : ring_launch<norm_ring_kernel<RT, YT, false, 1>>(c, a, 1, bytes, a.T, &blocks);
   }
   if (vec_ok(a)) {
     const int units = a.H / 8;
@@ -896,8 +902,8 @@ cudaError_t bwd_types(const LaunchCtx& c, const NormArgs& a) {
     int blocks = 0;
     const int64_t room = norm_partial_blocks(a.T, a.H);
     const cudaError_t e =
-        gel ? ring_launch(c, a, norm_backward_ring_kernel<RT, YT, true>, 1, bytes, room, &blocks)
-            : ring_launch(c, a, norm_backward_ring_kernel<RT, YT, false>, 1, bytes, room, &blocks);
+        gel ? ring_launch<norm_backward_ring_kernel<RT, YT, true>>(c, a, 1, bytes, room, &blocks)
+            : ring_launch<norm_backward_ring_kernel<RT, YT, false>>(c, a, 1, bytes, room, &blocks);
     return e == cudaSuccess ? launch_partials(c, a, blocks) : e;
   }
   if (vec_ok(a)) {

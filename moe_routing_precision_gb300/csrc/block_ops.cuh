@@ -170,6 +170,24 @@ __device__ __forceinline__ void mbar_init_done() {
 
 // ------------------------------------------------------------- launchers
 
+// allow_max_dynamic_smem, called once per device for each kernel: a launch that
+// needs more than the default must not pay the call every time (0.6 us each on
+// a Grace host).  One object per kernel instance.
+class SmemOptIn {
+ public:
+  template <typename... KArgs>
+  cudaError_t once(const LaunchCtx& c, void (*kernel)(KArgs...)) {
+    const uint64_t bit = 1ull << c.device;  // context() admits 64 devices
+    if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = allow_max_dynamic_smem(kernel);
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
+
 // moe_block_norm and its backward (block_norm.cu); the fields are the
 // arguments of the C calls, checked by the caller.
 struct NormArgs {

@@ -658,7 +658,8 @@ cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
   while (C > 1 && smem_layout(kScaleBytes, a.K, a.E, C).total > 226 * 1024) C >>= 1;
   const size_t smem = smem_layout(kScaleBytes, a.K, a.E, C).total;
   auto* kernel = expert_matvec_kernel<G, U8, ALIGNED>;
-  cudaError_t e = allow_max_dynamic_smem(kernel);
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.once(c, kernel);
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   e = code_map(a, &map);

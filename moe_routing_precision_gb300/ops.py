@@ -10,6 +10,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -102,6 +103,8 @@ def lib() -> ctypes.CDLL:
     environment variable MOE_DEBUG_BOUNDS is 1 at the first call (raises if
     it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = lib_path()
@@ -129,8 +132,16 @@ def _check(rc: int, what: str):
         raise MoeError(rc, what)
 
 
+# The current stream's handle without building a Stream object around it (2.9
+# against 0.1 us per call on a Grace host), where this PyTorch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cuda_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and _cuda_device is not None:
+            return _raw_stream(_cuda_device()) or None
         return torch.cuda.current_stream().cuda_stream or None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream or None
@@ -138,6 +149,9 @@ def _stream(stream) -> int | None:
 
 
 def _dev(t: torch.Tensor, name: str, dtype, shape=None):
+    if (type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -580,10 +594,11 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
         raise ValueError("post_weight and gate need y")
     elif pre_weight is None:
         raise ValueError("nothing to do: neither y nor pre_weight given")
-    for name, wt in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if wt is not None:
-            _dev(wt, name, torch.float32, (H,))
-    kind = _gate_kind(gate, T, H, block_dtype)
+    if post_weight is not None:
+        _dev(post_weight, "post_weight", torch.float32, (H,))
+    if pre_weight is not None:
+        _dev(pre_weight, "pre_weight", torch.float32, (H,))
+    kind = GATE_NONE if gate is None else _gate_kind(gate, T, H, block_dtype)
     h, n = out if out is not None else (None, None)
     if y is None:
         h = residual
@@ -594,11 +609,15 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
     if pre_weight is None:
         n = None
     elif n is None:
-        n = _empty((T, H), block_dtype, residual)
+        n = torch.empty_like(y) if y is not None else _empty((T, H), block_dtype, residual)
     else:
         _dev(n, "out[1]", block_dtype, (T, H))
-    rp = _empty((T,), torch.float32, residual) if post_weight is not None else None
-    rn = _empty((T,), torch.float32, residual) if pre_weight is not None else None
+    dev = residual.device
+    rp = rn = None
+    if post_weight is not None:
+        rp = torch.empty((T,), dtype=torch.float32, device=dev)
+    if pre_weight is not None:
+        rn = torch.empty((T,), dtype=torch.float32, device=dev)
     rc = lib().moe_block_norm(_ptr(residual), sd, _ptr(y),
                               DT_F32 if block_dtype == torch.float32 else DT_BF16, T, H,
                               _ptr(post_weight), _ptr(gate), kind,
@@ -608,6 +627,7 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
     return h, n, rp, rn
 
 
+@functools.lru_cache(maxsize=256)
 def block_norm_backward_workspace_bytes(T: int, H: int) -> int:
     return int(lib().moe_block_norm_backward_workspace_bytes(T, H))
 
@@ -676,6 +696,7 @@ def _sequences(seq_offsets, token_mask, T: int) -> int:
     return 1 if seq_offsets is None else seq_offsets.numel() - 1
 
 
+@functools.lru_cache(maxsize=256)
 def balance_loss_workspace_bytes(T: int, E: int, S: int = 1) -> int:
     return int(lib().moe_balance_loss_workspace_bytes(T, E, S))
 
@@ -693,21 +714,24 @@ def balance_loss(scores: torch.Tensor, topk_idx: torch.Tensor, *, score_func: st
     -> (balance [S], z [S], counts [S, E] int32, probs [S, E], tokens [S] int32)."""
     _dev(scores, "scores", torch.float32)
     T, E = scores.shape
-    _dev(topk_idx, "topk_idx", torch.int32)
     k = topk_idx.shape[1]
     _dev(topk_idx, "topk_idx", torch.int32, (T, k))
     S = _sequences(seq_offsets, token_mask, T)
-    bal, z = _empty((S,), torch.float32, scores), _empty((S,), torch.float32, scores)
-    counts = _empty((S, E), torch.int32, scores)
-    probs = _empty((S, E), torch.float32, scores)
-    tokens = _empty((S,), torch.int32, scores)
-    if workspace is None:
-        workspace = _empty((balance_loss_workspace_bytes(T, E, S),), torch.uint8, scores)
-    _dev(workspace, "workspace", torch.uint8)
+    dev = scores.device
+    bal = torch.empty((S,), dtype=torch.float32, device=dev)
+    z = torch.empty_like(bal)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    probs = torch.empty((S, E), dtype=torch.float32, device=dev)
+    tokens = torch.empty((S,), dtype=torch.int32, device=dev)
+    ws_bytes = balance_loss_workspace_bytes(T, E, S)
+    if workspace is None and ws_bytes:
+        workspace = _empty((ws_bytes,), torch.uint8, scores)
+    if workspace is not None:
+        ws_bytes = _dev(workspace, "workspace", torch.uint8).numel()
     rc = lib().moe_balance_loss(_ptr(scores), _ptr(topk_idx), T, E, k,
                                 _choice(score_func, _SCORE_FUNC, "score_func"), _ptr(seq_offsets),
                                 S, _ptr(token_mask), _ptr(bal), _ptr(z), _ptr(counts),
-                                _ptr(probs), _ptr(tokens), _ptr(workspace), workspace.numel(),
+                                _ptr(probs), _ptr(tokens), _ptr(workspace), ws_bytes,
                                 _stream(stream))
     _check(rc, "moe_balance_loss")
     return bal, z, counts, probs, tokens
@@ -766,18 +790,18 @@ def combine_backward(grad_out: torch.Tensor, y: torch.Tensor, topk_weights: torc
     gd = _dt(grad_out, "grad_out")
     _dev(grad_out, "grad_out", grad_out.dtype)
     T, H = grad_out.shape
-    _dev(y, "y", torch.bfloat16)
-    R = y.shape[0]
+    R, k = y.shape[0], topk_weights.shape[1]
     _dev(y, "y", torch.bfloat16, (R, H))
-    _dev(topk_weights, "topk_weights", torch.float32)
-    k = topk_weights.shape[1]
     _dev(topk_weights, "topk_weights", torch.float32, (T, k))
     _dev(pos, "pos", torch.int32, (T, k))
     if sorted_src is not None:
         _dev(sorted_src, "sorted_src", torch.int32, (R,))
-    gy, gw = out if out is not None else (torch.empty_like(y), torch.empty_like(topk_weights))
-    _dev(gy, "out[0]", torch.bfloat16, (R, H))
-    _dev(gw, "out[1]", torch.float32, (T, k))
+    if out is None:
+        gy, gw = torch.empty_like(y), torch.empty_like(topk_weights)
+    else:
+        gy, gw = out
+        _dev(gy, "out[0]", torch.bfloat16, (R, H))
+        _dev(gw, "out[1]", torch.float32, (T, k))
     rc = lib().moe_combine_backward(_ptr(grad_out), gd, _ptr(y), _ptr(topk_weights), _ptr(pos),
                                     _ptr(sorted_src), T, H, k, R, _ptr(gy), _ptr(gw),
                                     _stream(stream))
@@ -799,7 +823,6 @@ def expert_matvec_fp4(x: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, offs
     swiglu: M = 2N, the gate's outputs first; out = silu(gate) * up.
     -> out [R, N] bfloat16 or float32 (rows past offsets[E] not written)."""
     _dev(x, "x", torch.bfloat16)
-    _dev(w, "w", torch.uint8)
     if x.dim() != 2 or w.dim() != 3:
         raise ValueError("x must be [rows, K] and w [E, M, K/2]")
     K = x.shape[1]
@@ -822,8 +845,10 @@ def expert_matvec_fp4(x: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, offs
     else:
         R = x.shape[0]
     N = M // 2 if swiglu else M
-    o = out if out is not None else _empty((R, N), out_dtype, x)
-    _dev(o, "out", out_dtype, (R, N))
+    if out is None:
+        o = torch.empty((R, N), dtype=out_dtype, device=x.device)
+    else:
+        o = _dev(out, "out", out_dtype, (R, N))
     rc = lib().moe_expert_matvec_fp4(_ptr(x), x.shape[0], _ptr(w), _ptr(w_sf),
                                      WSF_UE8M0 if w_sf.dtype == torch.uint8 else WSF_F32, group,
                                      _ptr(offsets), _ptr(sorted_src), E, k, R, K, N, int(swiglu),
