@@ -623,6 +623,7 @@ cudaError_t dispatch(const LaunchCtx& c, const BalanceArgs& a, bool backward) {
   if (E <= 8) return dispatch_func<8, 1, 1>(c, a, backward);
   if (E <= 32) return dispatch_func<32, 1, 1>(c, a, backward);
   if (E <= 128) return dispatch_func<32, 1, 4>(c, a, backward);
+  if (E <= 256) return dispatch_func<32, 1, 8>(c, a, backward);
   if (E <= 512) return dispatch_func<32, 1, 16>(c, a, backward);
   return dispatch_func<32, 1, 32>(c, a, backward);
 }

@@ -221,13 +221,14 @@ cudaError_t launch_block_norm(const LaunchCtx& c, const NormArgs& a, bool stream
 cudaError_t launch_block_norm_backward(const LaunchCtx& c, const NormArgs& a, bool stream_f32,
                                        bool block_f32);
 // Blocks of the backward that leave partial sums over tokens: at most this
-// many, and at most one per token.  (160 SMs at most, each with as many blocks
-// of H / 16 threads as make 512, at most 16.)
+// many (160 SMs at most, each with as many blocks as its 8192 channels in
+// registers make rows, at most kNormMaxBlocksPerSm), and at most one per token.
+constexpr int kNormMaxBlocksPerSm = 24;
 inline int64_t norm_partial_blocks(int64_t T, int H) {
-  const int threads = (H + 511) / 512 * 32;
-  const int per_sm = threads >= 512 ? 1 : 512 / threads;
-  const int64_t cap = (int64_t)160 * (per_sm > 16 ? 16 : per_sm);
-  return T < cap ? T : cap;
+  int64_t per_sm = (8192 + H - 1) / H;
+  if (per_sm > kNormMaxBlocksPerSm) per_sm = kNormMaxBlocksPerSm;
+  if (per_sm < 1) per_sm = 1;
+  return T < 160 * per_sm ? T : 160 * per_sm;
 }
 
 // moe_balance_loss (balance_loss.cu).

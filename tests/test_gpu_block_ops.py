@@ -584,3 +584,21 @@ def test_norm_many_tokens_options(gate, post, pre, y, H):
     if y:
         b = run_norm(s, act, out=(s["residual"], n))          # in place
         assert torch.equal(a[0], b[0]) and (n is None or torch.equal(a[1], n))
+
+
+@pytest.mark.parametrize("T,H", [(513, 1), (700, 3), (1001, 33), (515, 250), (900, 1155), (640, 2050), (517, 4099),
+                                 (514, 7161), (530, 8191)])
+@pytest.mark.parametrize("sd,bd", [(BF, BF), (F32, BF), (BF, F32), (F32, F32)])
+def test_norm_many_tokens_of_odd_widths(T, H, sd, bd):
+    """Rows that start and end inside 16-byte pieces, the last one included."""
+    for gate in ("token", "element"):
+        s = norm_inputs(T, H, sd, bd, gate, T * 31 + H)
+        check_norm(s, "sigmoid", run_norm(s, "sigmoid"))
+        run_check_backward(s, "sigmoid", H)
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 151, 153, 305, 511])
+@pytest.mark.parametrize("H", [1024, 1027])
+def test_norm_backward_of_few_tokens(T, H):
+    s = norm_inputs(T, H, F32, BF, "channel", T)
+    run_check_backward(s, "sigmoid", T)
