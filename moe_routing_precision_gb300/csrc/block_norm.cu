@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(MAXT) block_norm_kernel(const NormArgs a, int 
 
 // Forward: R consecutive rows per turn of a block, whose sums are reduced
 // together.
-template <class RT, class YT, bool GEL, int R, int V, int U>
-__global__ void __launch_bounds__(ring_max_threads(V, U), ring_min_blocks(V, U))
+template <class RT, class YT, bool GEL, int R, int V, int U, int NT>
+__global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U, NT))
     norm_ring_kernel(const NormArgs a, const Ring ring, unsigned* err) {
   pdl_enter();
   extern __shared__ __align__(128) uint8_t ring_smem[];
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(ring_max_threads(V, U), ring_min_blocks(V, U))
   RingState rs;
   rs.bars = sbase + kRingHeader - 64;
   rs.stages_at = sbase + kRingHeader;
-  const int tid = threadIdx.x, nt = blockDim.x, wpr = nt >> 5;
+  const int tid = threadIdx.x, nt = NT ? NT : blockDim.x, wpr = nt >> 5;
   const bool has_y = a.y != nullptr, post = a.post_w != nullptr, pre = a.pre_w != nullptr;
   const bool gtok = a.gate_kind == MOE_GATE_TOKEN;
   const void* const src[5] = {a.residual, a.y, GEL ? a.gate : nullptr, nullptr, nullptr};
@@ -298,20 +298,20 @@ cudaError_t fwd_t(const LaunchCtx& c, const NormArgs& a) {
 constexpr int64_t kFwdRingTokens = 512;
 
 // The forward through the ring; false if it does not fit.
-template <class RT, class YT, bool GEL, int V, int U>
+template <class RT, class YT, bool GEL, int V, int U, int NT>
 bool fwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
   const uint32_t rb = (uint32_t)(a.H * sizeof(RT)), yb = (uint32_t)(a.H * sizeof(YT));
   const uint32_t bytes[5] = {rb, a.y ? yb : 0u, GEL ? yb : 0u, 0u, 0u};
   int blocks = 0;
-  const RingShape two = ring_shape<V, U>(a.H, 2, bytes);
+  const RingShape two = ring_shape<V, U, NT>(a.H, 2, bytes);
   if (two.ring.stages) {
-    *e = ring_launch<norm_ring_kernel<RT, YT, GEL, 2, V, U>>(c, a, two, (a.T + 1) / 2, &blocks);
+    *e = ring_launch<norm_ring_kernel<RT, YT, GEL, 2, V, U, NT>>(c, a, two, (a.T + 1) / 2, &blocks);
     return true;
   }
   if constexpr (V * U == 16) {
-    const RingShape one = ring_shape<V, U>(a.H, 1, bytes);
+    const RingShape one = ring_shape<V, U, NT>(a.H, 1, bytes);
     if (one.ring.stages) {
-      *e = ring_launch<norm_ring_kernel<RT, YT, GEL, 1, V, U>>(c, a, one, a.T, &blocks);
+      *e = ring_launch<norm_ring_kernel<RT, YT, GEL, 1, V, U, NT>>(c, a, one, a.T, &blocks);
       return true;
     }
   }
@@ -320,8 +320,13 @@ bool fwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
 template <class RT, class YT, bool GEL>
 bool fwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e) {
   if (vec == 8)
-    return a.H <= 2048 ? fwd_ring<RT, YT, GEL, 8, 1>(c, a, e) : fwd_ring<RT, YT, GEL, 8, 2>(c, a, e);
-  return a.H <= 4096 ? fwd_ring<RT, YT, GEL, 1, 4>(c, a, e) : fwd_ring<RT, YT, GEL, 1, 16>(c, a, e);
+    return a.H <= 2048 ? fwd_ring<RT, YT, GEL, 8, 1, 0>(c, a, e)
+                       : fwd_ring<RT, YT, GEL, 8, 2, 0>(c, a, e);
+  if (a.H <= 256) return fwd_ring<RT, YT, GEL, 1, 4, 64>(c, a, e);
+  if (a.H <= 1024) return fwd_ring<RT, YT, GEL, 1, 8, 128>(c, a, e);
+  if (a.H <= 2048) return fwd_ring<RT, YT, GEL, 1, 8, 256>(c, a, e);
+  if (a.H <= 4096) return fwd_ring<RT, YT, GEL, 1, 8, 512>(c, a, e);
+  return fwd_ring<RT, YT, GEL, 1, 16, 512>(c, a, e);
 }
 
 template <class RT, class YT>

@@ -64,12 +64,19 @@ __device__ __forceinline__ void gate_values(const NormArgs& a, float (&g)[VEC], 
 //
 // Wide rows take 16 channels per thread, one block of at most 512 threads per SM
 // or more of fewer threads; narrower ones fewer channels, and as many blocks per
-// SM as their registers allow.
+// SM as their registers allow.  With V = 1 the number of threads is NT, fixed at
+// compile time: the offsets between a thread's 4 to 16 channels are then
+// constants (computed, they were half of all instructions).
 constexpr int kRingMaxHidden = 8192;
 constexpr int kRingMaxStages = 4;
 constexpr int kRingHeader = 1152;  // sums and barriers in front of the stages
-constexpr int ring_max_threads(int V, int U) { return V == 8 ? (U == 1 ? 256 : 512) : (U == 4 ? 1024 : 512); }
-constexpr int ring_min_blocks(int V, int U) { return V == 8 && U == 1 ? 3 : 1; }
+constexpr int ring_max_threads(int U, int NT) { return NT ? NT : U == 1 ? 256 : 512; }
+// Blocks per SM of that size: 512 threads of 128 registers, 640 of 102, 768 of
+// 85 or 1024 of 64.
+constexpr int ring_min_blocks(int V, int U, int NT) {
+  const int n = (V * U == 16 ? 512 : V == 8 ? 768 : U == 8 ? 640 : 1024) / ring_max_threads(U, NT);
+  return n > 0 ? n : 1;
+}
 
 struct Ring {
   int stages = 0;
@@ -227,7 +234,7 @@ struct RingShape {
   Ring ring;
   int threads = 0, per_sm = 0;
 };
-template <int V, int U>
+template <int V, int U, int NT>
 RingShape ring_shape(int H, int rows, const uint32_t (&row_bytes)[5]) {
   RingShape s;
   for (int i = 0; i < 5; ++i) {
@@ -235,8 +242,8 @@ RingShape ring_shape(int H, int rows, const uint32_t (&row_bytes)[5]) {
     // (up to 15 bytes before the rows and 15 behind them)
     if (row_bytes[i]) s.ring.stage_bytes += (rows * row_bytes[i] + 32 + 127) / 128 * 128;
   }
-  s.threads = (H + 32 * V * U - 1) / (32 * V * U) * 32;
-  s.per_sm = ring_max_threads(V, U) * ring_min_blocks(V, U) / s.threads;
+  s.threads = NT ? NT : (H + 32 * V * U - 1) / (32 * V * U) * 32;
+  s.per_sm = ring_max_threads(U, NT) * ring_min_blocks(V, U, NT) / s.threads;
   if (s.per_sm > kNormMaxBlocksPerSm) s.per_sm = kNormMaxBlocksPerSm;
   for (; s.per_sm > 0; --s.per_sm) {  // (1 KB of each block's shared memory is the system's)
     const uint32_t room = 226u * 1024 / s.per_sm - 1024 - kRingHeader;

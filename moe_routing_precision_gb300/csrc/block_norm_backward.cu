@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(32 * kSumWarps)
   if (a.grad_post_w) a.grad_post_w[c] = v * g;
 }
 
-template <class RT, class YT, bool GEL, int V, int U>
-__global__ void __launch_bounds__(ring_max_threads(V, U), ring_min_blocks(V, U))
+template <class RT, class YT, bool GEL, int V, int U, int NT>
+__global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U, NT))
     norm_backward_ring_kernel(const NormArgs a, const Ring ring, unsigned* err) {
   pdl_enter();
   extern __shared__ __align__(128) uint8_t ring_smem[];
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(ring_max_threads(V, U), ring_min_blocks(V, U))
   RingState rs;
   rs.bars = sbase + kRingHeader - 64;
   rs.stages_at = sbase + kRingHeader;
-  const int tid = threadIdx.x, nt = blockDim.x, wpr = nt >> 5;
+  const int tid = threadIdx.x, nt = NT ? NT : blockDim.x, wpr = nt >> 5;
   const bool has_y = a.y != nullptr, post = a.post_w != nullptr, pre = a.pre_w != nullptr;
   const bool gtok = a.gate_kind == MOE_GATE_TOKEN;
   const void* const src[5] = {a.grad_h, pre ? a.h : nullptr, pre ? a.grad_n : nullptr, a.y,
@@ -381,16 +381,16 @@ cudaError_t bwd_t(const LaunchCtx& c, const NormArgs& a) {
 }
 
 // The backward through the ring; false if it does not fit.
-template <class RT, class YT, bool GEL, int V, int U>
+template <class RT, class YT, bool GEL, int V, int U, int NT>
 bool bwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
   const bool pre = a.pre_w != nullptr;
   const uint32_t rb = (uint32_t)(a.H * sizeof(RT)), yb = (uint32_t)(a.H * sizeof(YT));
   const uint32_t bytes[5] = {a.grad_h ? rb : 0u, pre ? rb : 0u, pre ? yb : 0u, a.y ? yb : 0u,
                              GEL ? yb : 0u};
-  const RingShape s = ring_shape<V, U>(a.H, 1, bytes);
+  const RingShape s = ring_shape<V, U, NT>(a.H, 1, bytes);
   if (!s.ring.stages) return false;
   int blocks = 0;
-  *e = ring_launch<norm_backward_ring_kernel<RT, YT, GEL, V, U>>(
+  *e = ring_launch<norm_backward_ring_kernel<RT, YT, GEL, V, U, NT>>(
       c, a, s, norm_partial_blocks(a.T, a.H), &blocks);
   if (*e == cudaSuccess) *e = launch_partials(c, a, blocks);
   return true;
@@ -398,8 +398,13 @@ bool bwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
 template <class RT, class YT, bool GEL>
 bool bwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e) {
   if (vec == 8)
-    return a.H <= 2048 ? bwd_ring<RT, YT, GEL, 8, 1>(c, a, e) : bwd_ring<RT, YT, GEL, 8, 2>(c, a, e);
-  return a.H <= 4096 ? bwd_ring<RT, YT, GEL, 1, 4>(c, a, e) : bwd_ring<RT, YT, GEL, 1, 16>(c, a, e);
+    return a.H <= 2048 ? bwd_ring<RT, YT, GEL, 8, 1, 0>(c, a, e)
+                       : bwd_ring<RT, YT, GEL, 8, 2, 0>(c, a, e);
+  if (a.H <= 256) return bwd_ring<RT, YT, GEL, 1, 4, 64>(c, a, e);
+  if (a.H <= 1024) return bwd_ring<RT, YT, GEL, 1, 8, 128>(c, a, e);
+  if (a.H <= 2048) return bwd_ring<RT, YT, GEL, 1, 8, 256>(c, a, e);
+  if (a.H <= 4096) return bwd_ring<RT, YT, GEL, 1, 8, 512>(c, a, e);
+  return bwd_ring<RT, YT, GEL, 1, 16, 512>(c, a, e);
 }
 
 template <class RT, class YT>
