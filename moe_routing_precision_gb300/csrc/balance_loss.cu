@@ -121,42 +121,66 @@ template <int L, int W, int NV>
 struct Row {
   float x[NV * W];
   __device__ __forceinline__ static int expert(int sub, int v) { return (v * L + sub) * W; }
-  // Scores of token t; -inf past E and for a token that is not wanted.
-  __device__ __forceinline__ void load(const float* scores, int64_t t, int E, int sub, bool want) {
+  // A token's scores, p its first one of this lane; -inf past E and for a token
+  // that is not wanted.
+  __device__ __forceinline__ void load(const float* p, int E, int sub, bool want) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = expert(sub, v);
+      const bool in = want && expert(sub, v) < E;
       if constexpr (W == 4) {
         uint4 q = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-        if (want && e < E) q = ld_stream_v4(scores + t * E + e);
+        if (in) q = ld_stream_v4(p + v * L * W);
         x[4 * v] = __uint_as_float(q.x);
         x[4 * v + 1] = __uint_as_float(q.y);
         x[4 * v + 2] = __uint_as_float(q.z);
         x[4 * v + 3] = __uint_as_float(q.w);
       } else {
-        x[v] = want && e < E ? __ldg(scores + t * E + e) : kNegInf;
+        x[v] = in ? __ldg(p + v * L) : kNegInf;
       }
     }
   }
 };
 
-// 1 / x for normal x, to an ulp: the hardware estimate and one Newton step.
+// The tokens first, first + stride, ... below hi of one group of lanes, by
+// offsets that move along (index products in 64 bits cost a fifth of the
+// instructions).
+template <int L, int W, int NV>
+struct Walk {
+  int64_t e_at, k_at;  // this lane's first score, and its first of the k selections
+  const uint8_t* mask;
+  int left;  // tokens from the current one to hi
+  __device__ __forceinline__ Walk(const BalanceArgs& a, int64_t first, int64_t hi, int sub)
+      : e_at(first * a.E + sub * W),
+        k_at(first * a.k + sub),
+        mask(a.mask == nullptr ? nullptr : a.mask + first),
+        left(hi > first ? (int)(hi - first) : 0) {}
+  __device__ __forceinline__ bool want() const {
+    return left > 0 && (mask == nullptr || __ldg(mask) != 0);
+  }
+  __device__ __forceinline__ void step(const BalanceArgs& a, int stride) {
+    e_at += (int64_t)stride * a.E;
+    k_at += stride * a.k;
+    if (mask != nullptr) mask += stride;
+    left -= stride;
+  }
+};
+
+// 1 / x for 2^-126 <= x < 2^126, to an ulp: the hardware estimate and one Newton step.
 __device__ __forceinline__ float rcp_f32(float x) {
-  const float y = __fdividef(1.0f, x);
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return __fmaf_rn(y, __fmaf_rn(-x, y, 1.0f), y);
 }
 
-// From a row's scores x (a group of L lanes, N values per lane): p, lse, whether
-// the token counts (any score above -inf), and what only the backward wants:
-// q = softmax(x) and, for SIG, n = 1 - sigmoid(x).
-template <int L, int N, bool SIG, bool BWD>
-__device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], float (&q)[N],
-                                          float (&n)[N], float* lse, bool* counts) {
+// Whether any group of this warp (L lanes a row, N values per lane) needs the
+// shifted form: its largest score is above 80, or finite and below -20.
+template <int L, int N>
+__device__ __forceinline__ bool far_row(const float (&x)[N], float* top_out) {
   float top = kNegInf;
 #pragma unroll
   for (int i = 0; i < N; ++i) top = fmaxf(top, x[i]);
-  float tot = 0.0f, stot = 0.0f;
-  // groups whose maximum is finite but below -20, one bit each
+  *top_out = top;
+  // groups with a finite score, and with one that is at least -20, one bit each
   unsigned some = __ballot_sync(0xFFFFFFFFu, top > kNegInf);
   unsigned near = __ballot_sync(0xFFFFFFFFu, top >= -20.0f);
   if (L == 32) {
@@ -166,48 +190,120 @@ __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], fl
     for (int o = 1; o < L; o <<= 1) some |= some >> o, near |= near >> o;
   }
   constexpr unsigned kFirst = L == 4 ? 0x11111111u : L == 8 ? 0x01010101u : L == 16 ? 0x00010001u : 1u;
-  if ((some & ~near & kFirst) != 0 || __any_sync(0xFFFFFFFFu, top > 80.0f)) {
-    // scores far from zero: relative to the maximum, sigmoids to e^min(max, 0)
-    top = group_max<L>(top);
-    const bool ok = top > kNegInf;
-    const float m = ok ? top : 0.0f, m0 = fminf(m, 0.0f);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      q[i] = expf(x[i] - m);
-      tot += q[i];
-      if (SIG) {
-        const float e = expf(-fabsf(x[i])), r = rcp_f32(1.0f + e);
-        p[i] = expf(fminf(x[i], 0.0f) - m0) * r;
-        n[i] = x[i] < 0.0f ? r : e * r;
-        stot += p[i];
-      }
-    }
-    tot = group_sum<L>(tot);
-    if (SIG) stot = group_sum<L>(stot);
-    *lse = ok ? m + logf(tot) : 0.0f;
-    *counts = ok;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      q[i] = expf(x[i]);
-      tot += q[i];
-      if (SIG) {
-        n[i] = rcp_f32(1.0f + q[i]);
-        p[i] = q[i] * n[i];
-        stot += p[i];
-      }
-    }
-    tot = group_sum<L>(tot);
-    if (SIG) stot = group_sum<L>(stot);
-    *counts = tot > 0.0f;
-    *lse = *counts ? logf(tot) : 0.0f;
-  }
-  const float inv = *counts ? 1.0f / tot : 0.0f;
-  const float sinv = SIG && *counts ? 1.0f / stot : 0.0f;
+  return (some & ~near & kFirst) != 0 || __any_sync(0xFFFFFFFFu, top > 80.0f);
+}
+
+// The shifted form: e^(x - max), and sigmoids relative to e^min(max, 0) with
+// n = 1 - sigmoid(x); the sums over the row.
+template <int L, int N, bool SIG>
+__device__ __forceinline__ void far_sums(const float (&x)[N], float top, float (&p)[N],
+                                         float (&q)[N], float (&n)[N], float* m_out, float* tot,
+                                         float* stot) {
+  top = group_max<L>(top);
+  const float m = top > kNegInf ? top : 0.0f, m0 = fminf(m, 0.0f);
+  *m_out = top;
+  float t = 0.0f, st = 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    if (!SIG || BWD) q[i] *= inv;
-    p[i] = SIG ? p[i] * sinv : q[i];
+    q[i] = expf(x[i] - m);
+    t += q[i];
+    if (SIG) {
+      const float e = expf(-fabsf(x[i])), r = rcp_f32(1.0f + e);
+      p[i] = expf(fminf(x[i], 0.0f) - m0) * r;
+      n[i] = x[i] < 0.0f ? r : e * r;
+      st += p[i];
+    }
+  }
+  *tot = group_sum<L>(t);
+  *stot = SIG ? group_sum<L>(st) : 0.0f;
+}
+
+// A row's probabilities, the log of its summed exponentials, and whether the
+// token counts (any score above -inf).
+template <int L, int N, bool SIG>
+__device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], float* lse,
+                                          bool* counts) {
+  float top, tot = 0.0f, stot = 0.0f;
+  if (far_row<L, N>(x, &top)) {
+    float q[N], n[N], m;
+    far_sums<L, N, SIG>(x, top, p, q, n, &m, &tot, &stot);
+    *counts = m > kNegInf;
+    *lse = *counts ? m + logf(tot) : 0.0f;
+    const float inv = *counts ? 1.0f / (SIG ? stot : tot) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = (SIG ? p[i] : q[i]) * inv;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    p[i] = expf(x[i]);
+    tot += p[i];
+    if (SIG) {
+      p[i] *= rcp_f32(1.0f + p[i]);
+      stot += p[i];
+    }
+  }
+  tot = group_sum<L>(tot);
+  if (SIG) stot = group_sum<L>(stot);
+  // (e^-20 <= tot < 2^126; the fast logarithm's error is absolute, 2^-22)
+  *counts = tot > 0.0f;
+  *lse = *counts ? __logf(tot) : 0.0f;
+  const float inv = *counts ? rcp_f32(SIG ? stot : tot) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] *= inv;
+}
+
+// A row's score gradient p (a - sum p a) [(1 - sigmoid)] + zc lse q, zero for a
+// token that does not count.  Near rows keep e^x and 1 - sigmoid alone: with
+// u = e^x, p = u / sum u or u n / sum (u n).
+template <int L, int N, bool SIG>
+__device__ __forceinline__ void row_grad(const float (&x)[N], const float (&a)[N], float zc,
+                                         float (&d)[N], bool* counts) {
+  float top, tot = 0.0f, stot = 0.0f, dot = 0.0f, n[N];
+  if (far_row<L, N>(x, &top)) {
+    float p[N], m;
+    far_sums<L, N, SIG>(x, top, p, d, n, &m, &tot, &stot);
+    *counts = m > kNegInf;
+    const float inv = *counts ? 1.0f / tot : 0.0f, sinv = SIG && *counts ? 1.0f / stot : 0.0f;
+    const float z = *counts ? zc * (m + logf(tot)) * inv : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      p[i] = SIG ? p[i] * sinv : d[i] * inv;
+      dot = __fmaf_rn(p[i], a[i], dot);
+    }
+    dot = group_sum<L>(dot);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float v = p[i] * (a[i] - dot);
+      d[i] = __fmaf_rn(z, d[i], SIG ? v * n[i] : v);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    d[i] = expf(x[i]);
+    tot += d[i];
+    float s = d[i];
+    if (SIG) {
+      n[i] = rcp_f32(1.0f + d[i]);
+      s *= n[i];
+      stot += s;
+    }
+    dot = __fmaf_rn(s, a[i], dot);
+  }
+  tot = group_sum<L>(tot);
+  if (SIG) stot = group_sum<L>(stot);
+  dot = group_sum<L>(dot);
+  *counts = tot > 0.0f;
+  const float inv = *counts ? rcp_f32(tot) : 0.0f;
+  const float pinv = SIG ? (*counts ? rcp_f32(stot) : 0.0f) : inv;
+  const float z = *counts ? zc * __logf(tot) * inv : 0.0f;
+  dot *= pinv;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float v = pinv * (a[i] - dot);
+    if (SIG) v *= n[i] * n[i];
+    d[i] *= v + z;
   }
 }
 
@@ -255,21 +351,25 @@ __global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
     float zsum = 0.0f;
     int n = 0;
     Row<L, W, NV> next;
-    int32_t next_e = -1;  // this lane's first index of the next token
-    auto fetch = [&](int64_t t) {
-      const bool want = t < hi && (a.mask == nullptr || __ldg(a.mask + t) != 0);
-      next.load(a.scores, t, E, sub, want);
-      next_e = want && sub < a.k ? __ldg(a.idx + t * a.k + sub) : 0;
+    int32_t next_e = 0;  // this lane's first index of the next token
+    constexpr int kStride = kWarps * TPW;
+    Walk<L, W, NV> walk(a, lo + warp * TPW + grp, hi, sub);
+    auto fetch = [&]() {
+      const bool want = walk.want();
+      next.load(a.scores + walk.e_at, E, sub, want);
+      if (want && sub < a.k) next_e = __ldg(a.idx + walk.k_at);
     };
-    fetch(lo + warp * TPW + grp);
-    for (int64_t t0 = lo + warp * TPW; t0 < hi; t0 += kWarps * TPW) {
-      const int64_t t = t0 + grp;
+    fetch();
+    const int64_t mine = hi - lo - warp * TPW;
+    for (int64_t done = 0; done < mine; done += kStride) {
       const Row<L, W, NV> row = next;
       const int32_t e0 = next_e;
-      fetch(t + kWarps * TPW);
-      float p[N], q[N], unused[N], lse;
+      const int64_t k_at = walk.k_at;
+      walk.step(a, kStride);
+      fetch();
+      float p[N], lse;
       bool counts;
-      row_probs<L, N, SIG, false>(row.x, p, q, unused, &lse, &counts);
+      row_probs<L, N, SIG>(row.x, p, &lse, &counts);
       if (!counts) continue;  // uniform in the group; the next shuffle waits for all groups
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i] += p[i];
@@ -278,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
         n += 1;
       }
       for (int j = sub; j < a.k; j += L) {
-        const int e = j == sub ? e0 : __ldg(a.idx + t * a.k + j);
+        const int e = j == sub ? e0 : __ldg(a.idx + k_at + j - sub);
         if (e >= 0 && e < E)
           atomicAdd(cnt + e, 1);
         else
@@ -461,16 +561,19 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
       Row<L, W, NV> next;
       int32_t next_e = 0;
       float next_w = 0.0f, next_g = 0.0f;
-      auto fetch = [&](int64_t t) {
-        const bool want = in_seq && t < hi && (a.mask == nullptr || __ldg(a.mask + t) != 0);
-        next.load(a.scores, t, E, sub, want);
+      constexpr int kStride = kBwdWarps * TPW;
+      const int64_t first = lo + warp * TPW + grp;
+      Walk<L, W, NV> walk(a, first, hi, sub);
+      auto fetch = [&]() {
+        const bool want = in_seq && walk.want();
+        next.load(a.scores + walk.e_at, E, sub, want);
         if (sel && want && sub < a.k) {
-          next_e = __ldg(a.idx + t * a.k + sub);
-          next_w = __ldg(a.w + t * a.k + sub);
-          next_g = __ldg(a.grad_w + t * a.k + sub);
+          next_e = __ldg(a.idx + walk.k_at);
+          next_w = __ldg(a.w + walk.k_at);
+          next_g = __ldg(a.grad_w + walk.k_at);
         }
       };
-      fetch(lo + warp * TPW + grp);
+      fetch();
       float coef[N], zc = 0.0f;
 #pragma unroll
       for (int i = 0; i < N; ++i) coef[i] = 0.0f;
@@ -491,48 +594,43 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
           }
         }
       }
-      for (int64_t t0 = lo + warp * TPW; t0 < hi; t0 += kBwdWarps * TPW) {
-        const int64_t t = t0 + grp;
+      const int64_t mine_n = hi - lo - warp * TPW;
+      for (int64_t at = 0; at < mine_n; at += kStride) {
+        const bool live = walk.left > 0;
         const Row<L, W, NV> row = next;
         const int32_t e0 = next_e;
         const float w0 = next_w, g0 = next_g;
-        fetch(t + kBwdWarps * TPW);
-        float p[N], q[N], om[N], lse;
+        const int64_t k_at = walk.k_at;
+        float* out = a.grad_scores + walk.e_at;
+        walk.step(a, kStride);
+        fetch();
+        float d[N];
         bool counts;
-        row_probs<L, N, SIG, true>(row.x, p, q, om, &lse, &counts);
-        float dot = 0.0f, wg = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) dot = __fmaf_rn(p[i], coef[i], dot);
-        if (sel && counts) {
-          for (int j = sub; j < a.k; j += L) {
-            const float w = j == sub ? w0 : __ldg(a.w + t * a.k + j);
-            const float g = j == sub ? g0 : __ldg(a.grad_w + t * a.k + j);
-            wg = __fmaf_rn(w, g, wg);
-          }
-        }
-        dot = group_sum<L>(dot);
+        row_grad<L, N, SIG>(row.x, coef, zc, d, &counts);
         if (sel) {
+          // this lane's selections sub, sub + L, ...: the first is at hand
+          float wg = counts && sub < a.k ? w0 * g0 : 0.0f;
+          if (a.k > L && counts)
+            for (int j = sub + L; j < a.k; j += L)
+              wg = __fmaf_rn(__ldg(a.w + k_at + j - sub), __ldg(a.grad_w + k_at + j - sub), wg);
           wg = group_sum<L>(wg);
           if (counts) {
-            for (int j = sub; j < a.k; j += L) {
-              const int e = j == sub ? e0 : __ldg(a.idx + t * a.k + j);
-              const float w = j == sub ? w0 : __ldg(a.w + t * a.k + j);
-              const float g = j == sub ? g0 : __ldg(a.grad_w + t * a.k + j);
-              if (e >= 0 && e < E)
-                mine[e] = w * (g - wg);
+            if (sub < a.k) {
+              if (e0 >= 0 && e0 < E)
+                mine[e0] = w0 * (g0 - wg);
               else
                 bad = true;
             }
+            if (a.k > L)
+              for (int j = sub + L; j < a.k; j += L) {
+                const int e = __ldg(a.idx + k_at + j - sub);
+                if (e >= 0 && e < E)
+                  mine[e] = __ldg(a.w + k_at + j - sub) * (__ldg(a.grad_w + k_at + j - sub) - wg);
+                else
+                  bad = true;
+              }
           }
           __syncwarp();
-        }
-        float d[N];
-        const float zl = zc * lse;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          float v = p[i] * (coef[i] - dot);
-          if (SIG) v *= om[i];
-          d[i] = counts ? __fmaf_rn(zl, q[i], v) : 0.0f;
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -543,23 +641,25 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
               const float4 m = *reinterpret_cast<const float4*>(mine + e);
               d[4 * v] += m.x, d[4 * v + 1] += m.y, d[4 * v + 2] += m.z, d[4 * v + 3] += m.w;
             }
-            if (t < hi)
-              st_stream_v4(a.grad_scores + t * E + e,
+            if (live)
+              st_stream_v4(out + v * L * W,
                            make_uint4(__float_as_uint(d[4 * v]), __float_as_uint(d[4 * v + 1]),
                                       __float_as_uint(d[4 * v + 2]),
                                       __float_as_uint(d[4 * v + 3])));
           } else {
             if (sel) d[v] += mine[e];
-            if (t < hi) st_stream_f32(a.grad_scores + t * E + e, d[v]);
+            if (live) st_stream_f32(out + v * L, d[v]);
           }
         }
         if (sel) {
           __syncwarp();
           if (counts) {
-            for (int j = sub; j < a.k; j += L) {
-              const int e = j == sub ? e0 : __ldg(a.idx + t * a.k + j);
-              if (e >= 0 && e < E) mine[e] = 0.0f;
-            }
+            if (sub < a.k && e0 >= 0 && e0 < E) mine[e0] = 0.0f;
+            if (a.k > L)
+              for (int j = sub + L; j < a.k; j += L) {
+                const int e = __ldg(a.idx + k_at + j - sub);
+                if (e >= 0 && e < E) mine[e] = 0.0f;
+              }
           }
           __syncwarp();
         }
