@@ -21,9 +21,9 @@
 // One CTA per SM.  Each computes, from the offsets, the list of (expert, run
 // of up to C rows) items, and takes an equal share of all (item, tile of 16
 // outputs) units.  For each item the CTA converts the run's rows of x into
-// shared memory once; then its 16 warps work through tiles, s warps splitting
-// a tile's channels (s chosen so that the units fill the warps; their sums are
-// added through shared memory in a fixed order).  Each warp streams its codes
+// shared memory once; then its 16 warps share the item's blocks of (tile, 256
+// channels) in equal consecutive runs.  A tile that falls into several warps'
+// runs is added up in warp order through shared memory.  Each warp streams its codes
 // and scales through a ring of its own in shared memory with cp.async, several
 // blocks of 256 channels ahead, so no barrier stands in the stream.
 //
@@ -163,10 +163,6 @@ __device__ __forceinline__ void unrolled(F&& f) {
     unrolled<N, I + 1>(static_cast<F&&>(f));
   }
 }
-__device__ __forceinline__ void group_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // 2^(b - 127) of the four bytes of w: the hardware conversion to bf16, exact
 // (2^-127 is a denormal there too).
 __device__ __forceinline__ void ue8m0x4(uint32_t w, float (&s)[4]) {
@@ -181,9 +177,10 @@ __device__ __forceinline__ void ue8m0x4(uint32_t w, float (&s)[4]) {
 // Shared memory: the warps' rings of codes (1024-byte aligned for the swizzle)
 // and of scales, the x rows (f16, row stride 2 Kp + 64 bytes so that
 // neighbouring rows fall into different halves of the banks), the powers of two
-// [Kp / 256][8], two buffers of partial sums, the items' prefix, the barriers.
+// [Kp / 256][8], the warps' partial sums, the barriers, and per expert the items
+// before it, its first row and the end of its rows.
 struct Smem {
-  uint32_t codes, scales, x, xs, red, bars, first, total;
+  uint32_t codes, scales, x, xs, red, bars, first, rows, total;
 };
 __host__ __device__ inline int padded_k(int K) { return (K + kBlockK - 1) / kBlockK * kBlockK; }
 __host__ __device__ inline uint32_t x_stride(int K) { return (uint32_t)padded_k(K) * 2 + 64; }
@@ -194,9 +191,10 @@ __host__ __device__ inline Smem smem_layout(int scale_bytes, int K, int E, int C
   s.x = s.scales + (uint32_t)(kWarps * kStages * scale_bytes);
   s.xs = s.x + (uint32_t)C * x_stride(K);
   s.red = s.xs + (uint32_t)(padded_k(K) / kBlockK) * kMaxRows * 4;
-  s.bars = s.red + 2 * kWarps * 512;
+  s.bars = s.red + kWarps * 512;
   s.first = s.bars + (uint32_t)(kWarps * kStages * 8);
-  s.total = s.first + (uint32_t)(E + 1) * 4;
+  s.rows = s.first + (uint32_t)(E + 2) / 2 * 8;
+  s.total = s.rows + (uint32_t)E * 8;
   return s;
 }
 
@@ -225,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Smem L = smem_layout(St::kScaleBytes, a.K, a.E, C);
   const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
   int* first = reinterpret_cast<int*>(smem + L.first);
+  int2* rows_of = reinterpret_cast<int2*>(smem + L.rows);
   float* xs = reinterpret_cast<float*>(smem + L.xs);
   float4* red = reinterpret_cast<float4*>(smem + L.red);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -261,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lo < 0) lo = 0;
         if (hi > a.R) hi = a.R;
       }
+      rows_of[e] = make_int2((int)lo, (int)hi);
       runs[i] = hi > lo ? (int)((hi - lo + C - 1) / C) : 0;
     }
     int sum = 0;
@@ -287,28 +287,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t units = (int64_t)first[a.E] * tiles;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
 
-  // warps per tile: the split with the fewest block steps for this share
-  int split = 1;
-  {
-    const int64_t share = u1 - u0;
-    int64_t best = INT64_MAX;
-    for (int s = 1; s <= kWarps; s <<= 1) {
-      const int64_t rounds = (share * s + kWarps - 1) / kWarps;
-      const int64_t cost = rounds * ((nblk + s - 1) / s + (s > 1 ? 1 : 0));
-      if (cost < best) best = cost, split = s;
-    }
-  }
-  const int sub = warp % split, team = warp / split, teams = kWarps / split;
-  const int bpw = (nblk + split - 1) / split;
-  const int b_lo = sub * bpw < nblk ? sub * bpw : nblk;
-  const int b_hi = b_lo + bpw < nblk ? b_lo + bpw : nblk;
-  const int mine = b_hi - b_lo;  // blocks of each tile this warp sums
-
   const uint32_t codes = sbase + L.codes + (uint32_t)(warp * kStages * kCodeBytes);
   const uint32_t scales = sbase + L.scales + (uint32_t)(warp * kStages * St::kScaleBytes);
   uint32_t phase = 0;  // bit i: the parity that stage i's barrier is at
   bool ok = true;      // no wait ran out
-  int parity = 0;
 
   int64_t u = u0;
   while (u < u1) {
@@ -326,19 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t left = u1 - u;
     const int ntiles = (int)(left < tiles - tile0 ? left : tiles - tile0);
     u += ntiles;
-    int64_t lo = 0, hi = a.R;
-    if (a.offsets != nullptr) {
-      lo = __ldg(a.offsets + e);
-      hi = __ldg(a.offsets + e + 1);
-      if (lo < 0) lo = 0;
-      if (hi > a.R) hi = a.R;
-    }
-    const int r0 = (int)lo + (item - first[e]) * C;
-    const int n = hi - r0 < C ? (int)(hi - r0) : C;
+    const int2 rows = rows_of[e];
+    const int r0 = rows.x + (item - first[e]) * C;
+    const int n = rows.y - r0 < C ? rows.y - r0 : C;
 
-    // this team's tiles: tile0 + team, + teams, ...; its steps are (tile, block)
-    const int my_tiles = ntiles > team ? (ntiles - team + teams - 1) / teams : 0;
-    const int steps = my_tiles * mine;
+    // this warp's run of the item's (tile, block) steps
+    const int all = ntiles * nblk;
+    auto run_begin = [&](int w) { return (int)((int64_t)all * w / kWarps); };
+    const int run0 = run_begin(warp), steps = run_begin(warp + 1) - run0;
     const int m_e = e * M;
     const int64_t sf_e = (int64_t)m_e * sf_row;
     // weight row, within the expert, of row i of a tile; past the last output
@@ -349,7 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // the stream of stages: where the next one comes from and goes to
-    int ld_tile = tile0 + team, ld_blk = b_lo, to_issue = ok ? steps : 0;
+    int ld_tile = tile0 + run0 / nblk, ld_blk = run0 % nblk, to_issue = ok ? steps : 0;
+    int tile = ld_tile, blk = ld_blk;
+    bool head = blk != 0;  // the current tile began in an earlier warp's run
     const char* sf_at = nullptr;  // kHalves: this lane's first scale of block ld_blk
     auto open_tile = [&]() {
       if (St::kHalves) {
@@ -408,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                       ok ? 4 : 0);
           }
         }
-        if (++ld_blk == b_hi) {
-          ld_blk = b_lo;
-          ld_tile += teams;
+        if (++ld_blk == nblk) {
+          ld_blk = 0;
+          ++ld_tile;
           if (to_issue > 0) open_tile();
         }
       }
@@ -418,14 +397,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     unrolled<kStages - 1>(issue);
 
-    // x: each warp converts one block of one row
-    const int xblk = padded_k(a.K) / kBlockK;
-    for (int t = warp; t < n * xblk; t += kWarps) {
-      const int col = t / xblk, b = t - col * xblk;
-      const int64_t sr = source_row(a, r0 + col, err);
-      const int c = b * kBlockK + lane * 8;
+    // x: each warp converts blocks of 256 channels of a row, two loads ahead
+    const int64_t my_src = lane < n ? source_row(a, r0 + lane, err) : -1;
+    auto fetch_x = [&](int t) {
+      const int col = t / nblk, c = (t - col * nblk) * kBlockK + lane * 8;
+      const int64_t sr = __shfl_sync(0xFFFFFFFFu, my_src, col & 7);
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (sr >= 0 && c < a.K) v = ld_v4(static_cast<const uint16_t*>(a.x) + sr * a.K + c);
+      if (t < n * nblk && sr >= 0 && c < a.K)
+        v = ld_v4(static_cast<const uint16_t*>(a.x) + sr * a.K + c);
+      return v;
+    };
+    uint4 v0 = fetch_x(warp), v1 = fetch_x(warp + kWarps);
+    for (int t = warp; t < n * nblk; t += kWarps) {
+      const uint4 v = v0;
+      v0 = v1;
+      v1 = fetch_x(t + 2 * kWarps);
+      const int col = t / nblk, b = t - col * nblk, c = b * kBlockK + lane * 8;
       float f[8];
       unpack8(v, f);
       float m = 0.0f;
@@ -457,7 +444,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < kBlockK / 32; ++j)
       frag[j] = codes + (uint32_t)(g * kRowBytes + ((j ^ g) << 4) + (G == 16 ? q * 2 : q * 4));
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int tile = tile0 + team, blk = b_lo;
     // where a row's scales start in its first word
     constexpr bool kShift = U8 && !St::kHalves;
     int sf_off[2] = {0, 0};
@@ -564,63 +550,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) acc[i] = __fmaf_rn(i & 1 ? xc.y : xc.x, blk_acc[i], acc[i]);
         ++blk;
     };
-    auto finish = [&]() {  // the tile is complete for this warp
-      blk = b_lo;
-      bool writer = true;
-      if (split > 1) {
-        float4* buf = red + parity * kWarps * 32;
-        buf[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        group_barrier(1 + team, split * 32);
-        writer = sub == 0;
-        if (writer) {
-          for (int w = 1; w < split; ++w) {
-            const float4 v = buf[(warp + w) * 32 + lane];
-            acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
-          }
-        }
-        parity ^= 1;
-      }
-      if (writer) {
+    auto write_out = [&]() {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = 2 * q + (i & 1);
-          float o = acc[i];
-          int nn;
-          if (a.swiglu) {
-            if (i >= 2) break;
-            o = o / (1.0f + expf(-o)) * acc[i + 2];
-            nn = tile * 8 + g;
-          } else {
-            nn = tile * 16 + g + (i >> 1) * 8;
-          }
-          if (col >= n || nn >= a.N) continue;
-          const int64_t at = (int64_t)(r0 + col) * a.N + nn;
-          if (a.out_f32)
-            static_cast<float*>(a.out)[at] = o;
-          else
-            static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+      for (int i = 0; i < 4; ++i) {
+        const int col = 2 * q + (i & 1);
+        float o = acc[i];
+        int nn;
+        if (a.swiglu) {
+          if (i >= 2) break;
+          o = o / (1.0f + expf(-o)) * acc[i + 2];
+          nn = tile * 8 + g;
+        } else {
+          nn = tile * 16 + g + (i >> 1) * 8;
         }
+        if (col >= n || nn >= a.N) continue;
+        const int64_t at = (int64_t)(r0 + col) * a.N + nn;
+        if (a.out_f32)
+          static_cast<float*>(a.out)[at] = o;
+        else
+          static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
       }
-      acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-      tile += teams;
-      tile_offsets();
     };
-    if (mine > 0) {
-      // whole turns of the ring, so that every stage address is a constant; the
-      // next item starts at stage 0 again
-      for (int step = 0; step < steps; step += kStages)
-        unrolled<kStages>([&](auto I) {
-          if (step + I < steps) {
-            block(I);
-            if (blk == b_hi) finish();
-          }
-        });
-    } else {
-      // a warp without a block of its own still joins its team's sums
-      for (int i = 0; i < my_tiles; ++i) finish();
+    auto leave = [&]() { red[warp * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]); };
+    // whole turns of the ring, so that every stage address is a constant; the
+    // next item starts at stage 0 again
+    for (int step = 0; step < steps; step += kStages)
+      unrolled<kStages>([&](auto I) {
+        if (step + I >= steps) return;
+        block(I);
+        if (blk < nblk) return;
+        // the tile ends here
+        if (head)
+          leave();
+        else
+          write_out();
+        head = false;
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+        blk = 0;
+        ++tile;
+        tile_offsets();
+      });
+    // a tile that goes on in the next run: its first warp adds the others' sums
+    const bool open = steps > 0 && blk > 0;
+    if (open && head) leave();
+    __syncthreads();
+    if (open && !head) {
+      const int end = (tile - tile0 + 1) * nblk;
+      for (int w = warp + 1; w < kWarps && run_begin(w) < end; ++w) {
+        if (run_begin(w) == run_begin(w + 1)) continue;
+        const float4 v = red[w * 32 + lane];
+        acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
+      }
+      write_out();
     }
     cp_async_wait<0>();
-    __syncthreads();  // x and the rings are free for the next item
+    __syncthreads();  // x and the sums are free for the next item
   }
 }
 
