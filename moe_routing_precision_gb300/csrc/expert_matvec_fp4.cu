@@ -217,6 +217,9 @@ template <int G, bool U8, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_matvec_kernel(const MatvecArgs a, const __grid_constant__ CUtensorMap map,
                          const int C, unsigned* err) {
+  // the map is a launch parameter: its fetch need not wait for earlier kernels
+  if (threadIdx.x == 0)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
   pdl_enter();
   using St = Stage<G, U8, ALIGNED>;
   extern __shared__ __align__(1024) uint8_t smem[];
