@@ -744,7 +744,7 @@ uint64_t moe_kernel_launch_count(void);
  * defined give libmoe_route_debug.so (the Python binding loads it when the
  * environment variable MOE_DEBUG_BOUNDS is 1).  Its kernels check, before the
  * access each guards, invariants that the normal build takes from the kernels'
- * construction: the alignment, size and shared-memory source of every TMA bulk
+ * construction: the alignment, size and place in shared memory of every TMA
  * copy, the alignment of wide scale stores, the shared-memory extent of the
  * staging slots, and the sorted_src row of every copy the decode kernels
  * place.  A failed check skips that access and sets MOE_DEVERR_BOUNDS; no

@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
   const uint32_t bytes[5] = {rb, yb, yb, 0u, 0u};
   const int64_t step = (int64_t)gridDim.x * R, first = (int64_t)blockIdx.x * R;
   auto fill = [&](int stage, int64_t t) {
-    ring_fill<V>(rs, ring, ring_smem, stage, src, bytes, t, a.T - t < R ? (int)(a.T - t) : R, a.T);
+    ring_fill<V>(rs, ring, ring_smem, stage, src, bytes, t, a.T - t < R ? (int)(a.T - t) : R, a.T,
+                 err);
   };
   if (tid == 0) {
     for (int i = 0; i < ring.stages; ++i) mbar_init(rs.bars + i * 8);

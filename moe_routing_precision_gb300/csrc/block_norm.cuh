@@ -144,7 +144,7 @@ template <int V>
 __device__ __forceinline__ void ring_fill(const RingState& r, const Ring& ring, uint8_t* smem,
                                           int stage, const void* const (&src)[5],
                                           const uint32_t (&row_bytes)[5], int64_t t, int rows,
-                                          int64_t T) {
+                                          int64_t T, unsigned* err) {
   const uint32_t bar = r.bars + stage * 8;
   const uint32_t dst = r.stages_at + stage * ring.stage_bytes;
   int64_t from[5];
@@ -170,6 +170,12 @@ __device__ __forceinline__ void ring_fill(const RingState& r, const Ring& ring, 
       }
     }
     bytes[i] = to > from[i] ? (uint32_t)(to - from[i]) : 0u;
+    if (!MOE_DBG_OK(((reinterpret_cast<uintptr_t>(src[i]) | (uintptr_t)from[i] | bytes[i] |
+                      (dst + ring.at[i])) & 15u) == 0 &&
+                        ring.at[i] + bytes[i] <= ring.stage_bytes &&
+                        kRingHeader + (stage + 1) * ring.stage_bytes <= dynamic_smem_bytes(),
+                    err))
+      bytes[i] = 0;
     total += bytes[i];
   }
   mbar_expect(bar, total);

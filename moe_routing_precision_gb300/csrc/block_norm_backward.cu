@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
     mbar_init_done();
     for (int i = 0; i < ring.stages; ++i) {
       const int64_t t = blockIdx.x + i * step;
-      if (t < a.T) ring_fill<V>(rs, ring, ring_smem, i, src, bytes, t, 1, a.T);
+      if (t < a.T) ring_fill<V>(rs, ring, ring_smem, i, src, bytes, t, 1, a.T, err);
     }
   }
   __syncthreads();
@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
     // every thread holds its part of the row: the stage is free
     if (wpr == 1) __syncwarp();
     if (tid == 0 && rs.ok && t + ring.stages * step < a.T)
-      ring_fill<V>(rs, ring, ring_smem, rs.stage, src, bytes, t + ring.stages * step, 1, a.T);
+      ring_fill<V>(rs, ring, ring_smem, rs.stage, src, bytes, t + ring.stages * step, 1, a.T,
+                   err);
     rs.next(ring.stages);
     const float m = rho * rho * rho * sums[0] * inv_h;
     const float dot = a.scale * (sums[1] - m * sums[2]);

@@ -350,9 +350,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           // rows past the last output are another's, or past the tensor and zero
           const uint32_t b = bar + ld_stage * 8, dst = codes + ld_stage * kCodeBytes;
           const int r = m_e + ld_tile * per_tile;
-          mbar_expect(b, kCodeBytes);
-          tma_box(dst, &map, ld_blk * kRowBytes, r, b);
-          tma_box(dst + kCodeBytes / 2, &map, ld_blk * kRowBytes, r + (a.swiglu ? a.N : 8), b);
+          // the boxes' columns are whole 16 bytes; each fills 1024 bytes of the ring
+          const bool box_ok =
+              MOE_DBG_OK(dst % (kCodeBytes / 2) == 0 && dst + kCodeBytes <= sbase + L.scales &&
+                             (ld_blk * kRowBytes) % 16 == 0 && ld_blk < nblk,
+                         err);
+          mbar_expect(b, box_ok ? kCodeBytes : 0);
+          if (box_ok) {
+            tma_box(dst, &map, ld_blk * kRowBytes, r, b);
+            tma_box(dst + kCodeBytes / 2, &map, ld_blk * kRowBytes, r + (a.swiglu ? a.N : 8), b);
+          }
         }
         const uint32_t sst = scales + ld_stage * St::kScaleBytes;
         if (St::kHalves) {
@@ -642,7 +649,7 @@ cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
   // more items), and fewer where a long x would not fit
   int C = kMaxRows;
   while (C > 1 && C / 2 >= (a.R + a.k - 1) / a.k) C >>= 1;
-  while (C > 1 && smem_layout(kScaleBytes, a.K, a.E, C).total > 226 * 1024) C >>= 1;
+  while (C > 1 && smem_layout(kScaleBytes, a.K, a.E, C).total > 227 * 1024) C >>= 1;
   const size_t smem = smem_layout(kScaleBytes, a.K, a.E, C).total;
   auto* kernel = expert_matvec_kernel<G, U8, ALIGNED>;
   static SmemOptIn opt_in;
