@@ -41,8 +41,11 @@ inline int64_t num_chunks(int64_t T) {
   const int64_t c = chunk_tokens(T);
   return (T + c - 1) / c;
 }
-// One block up to this many scores.
-constexpr int64_t kOneBlockScores = 32768;
+// One block up to this many scores: eight passes of its warps.  One block against
+// the table and its second launch, in us: E = 16: 4.8 : 8.2 at T = 512, 6.8 : 7.9
+// at 1024, 10.6 : 9.1 at 2048; E = 64: 4.9 : 7.7 at 128, 7.2 : 7.0 at 256; E = 256:
+// 5.6 : 7.9 at 64, 8.2 : 8.0 at 128.
+constexpr int64_t kOneBlockScores = 16384;
 constexpr int kOneBlockSeqs = 64;
 inline bool one_block(int64_t T, int E, int S) {
   return T * E <= kOneBlockScores && S <= kOneBlockSeqs;

@@ -294,9 +294,14 @@ cudaError_t fwd_t(const LaunchCtx& c, const NormArgs& a) {
                     s.tpr * s.rows, 0, c.stream, a, s.tpr);
 }
 
-// Rows enough that the forward's ring turns over; below, one block per row has
-// the lower latency.
-constexpr int64_t kFwdRingTokens = 512;
+// Elements from which the forward goes through the ring; below, one block per
+// row has the lower latency.  Ring against rows, us: H = 7168: 4.5 : 4.6 at
+// T = 152, 7.2 : 9.3 at 512, 39.9 : 46.8 at 4096; H = 2048: 3.6 : 3.4 at 512,
+// 5.5 : 5.6 at 1024, 7.7 : 8.6 at 2048; H = 512: 5.3 : 5.5 at 4096, 13.3 : 18.5 at
+// 16384; H = 256: 4.0 : 3.1 at 4096, 7.4 : 7.5 at 16384, 25 : 29 at 65536.  Widths
+// that are no multiple of 8, whose rows go element by element: H = 1155: 3.8 : 3.9
+// at 256, 4.1 : 4.3 at 512, 6.3 : 7.8 at 1024.
+constexpr int64_t kFwdRingElems = (int64_t)1 << 21, kFwdRingOddElems = (int64_t)1 << 19;
 
 // The forward through the ring; false if it does not fit.
 template <class RT, class YT, bool GEL, int V, int U, int NT>
@@ -320,9 +325,14 @@ bool fwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
 }
 template <class RT, class YT, bool GEL>
 bool fwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e) {
+  // one or two units of 8 channels per thread, us at 16384 tokens: H = 64: 7.3 :
+  // 8.3, 256: 7.3 : 8.4, 512: 13.3 : 10.3, 1024: 27.4 : 23.4, 2048: 49.4 : 46.8
   if (vec == 8)
-    return a.H <= 2048 ? fwd_ring<RT, YT, GEL, 8, 1, 0>(c, a, e)
-                       : fwd_ring<RT, YT, GEL, 8, 2, 0>(c, a, e);
+    return a.H <= 256 ? fwd_ring<RT, YT, GEL, 8, 1, 0>(c, a, e)
+                      : fwd_ring<RT, YT, GEL, 8, 2, 0>(c, a, e);
+  // the smallest block that holds the row; the next larger one, us at 8192 tokens:
+  // H = 250: 8.5 : 31, 1001: 16 : 32, 2047: 36 : 61 (a block's threads past the
+  // row are idle, and fewer blocks fit an SM)
   if (a.H <= 256) return fwd_ring<RT, YT, GEL, 1, 4, 64>(c, a, e);
   if (a.H <= 1024) return fwd_ring<RT, YT, GEL, 1, 8, 128>(c, a, e);
   if (a.H <= 2048) return fwd_ring<RT, YT, GEL, 1, 8, 256>(c, a, e);
@@ -332,7 +342,8 @@ bool fwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e
 
 template <class RT, class YT>
 cudaError_t fwd_types(const LaunchCtx& c, const NormArgs& a) {
-  const int vec = a.T >= kFwdRingTokens ? ring_vec(a) : 0;
+  int vec = ring_vec(a);
+  if (a.T * a.H < (vec == 8 ? kFwdRingElems : kFwdRingOddElems)) vec = 0;
   if (vec) {
     cudaError_t e;
     if (a.gate_kind == MOE_GATE_ELEMENT ? fwd_ring_vec<RT, YT, true>(c, a, vec, &e)

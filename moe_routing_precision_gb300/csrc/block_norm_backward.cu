@@ -11,6 +11,10 @@
 // element, so this cancels no more than d does.)
 #include "block_norm.cuh"
 
+#include <cooperative_groups.h>
+
+namespace cg = cooperative_groups;
+
 namespace moe {
 namespace {
 
@@ -173,28 +177,47 @@ __global__ void __launch_bounds__(1024) block_norm_backward_kernel(const NormArg
 }
 
 // The channels' sums over the blocks' partials, 32 columns per CTA: warp w adds
-// the blocks w, w + 8, ...; then the warps' sums are added in order.
-constexpr int kSumWarps = 8;
+// the blocks w, w + 32, ... of the CTA's part; then the warps' sums are added in
+// order.  Narrow rows leave up to 24 partials per SM and few columns: there a
+// cluster of SPLIT CTAs shares the blocks, and its first CTA adds the others'
+// sums in order through distributed shared memory.  (H = 256, 16384 tokens, the
+// whole backward: 36 us with one CTA of 8 warps per 32 columns.)
+constexpr int kSumWarps = 32, kSumSplit = 8;
+template <int SPLIT>
 __global__ void __launch_bounds__(32 * kSumWarps)
     norm_partials_kernel(const NormArgs a, int blocks) {
   pdl_enter();
   __shared__ float part[kSumWarps][33];
+  __shared__ float whole[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int o = blockIdx.y, c = blockIdx.x * 32 + lane;
+  const int o = blockIdx.y, c = blockIdx.x * 32 + lane, rank = blockIdx.z;
   const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
-  if (o == kPartPost ? !a.grad_post_w && !channel : !a.grad_pre_w) return;
+  if (o == kPartPost ? !a.grad_post_w && !channel : !a.grad_pre_w) return;  // the whole cluster
   float v = 0.0f;
   if (c < a.H) {
+    const int b0 = blocks * rank / SPLIT, b1 = blocks * (rank + 1) / SPLIT;
     const float* src = a.partials + (int64_t)o * blocks * a.H + c;
 #pragma unroll 8
-    for (int b = warp; b < blocks; b += kSumWarps) v += src[(int64_t)b * a.H];
+    for (int b = b0 + warp; b < b1; b += kSumWarps) v += src[(int64_t)b * a.H];
   }
   part[warp][lane] = v;
   __syncthreads();
-  if (warp != 0 || c >= a.H) return;
-  v = 0.0f;
+  if (warp == 0) {
+    v = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kSumWarps; ++i) v += part[i][lane];
+    for (int i = 0; i < kSumWarps; ++i) v += part[i][lane];
+    if (SPLIT > 1) whole[lane] = v;
+  }
+  if (SPLIT > 1) {
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    if (rank == 0 && warp == 0) {
+#pragma unroll
+      for (int i = 1; i < SPLIT; ++i) v += *cluster.map_shared_rank(&whole[lane], i);
+    }
+    cluster.sync();  // no CTA leaves while its sums are read
+  }
+  if (rank != 0 || warp != 0 || c >= a.H) return;
   if (o == kPartPre) {
     a.grad_pre_w[c] = v;
     return;
@@ -352,8 +375,26 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
 
 cudaError_t launch_partials(const LaunchCtx& c, const NormArgs& a, int blocks) {
   if (!a.grad_post_w && !a.grad_pre_w && a.gate_kind != MOE_GATE_CHANNEL) return cudaSuccess;
-  return launch_pdl(norm_partials_kernel, dim3((unsigned)((a.H + 31) / 32), 2), 32 * kSumWarps, 0,
-                    c.stream, a, blocks);
+  const unsigned cols = (unsigned)((a.H + 31) / 32);
+  // a cluster where one CTA's warps would add more than 16 partials each
+  if (blocks <= 16 * kSumWarps)
+    return launch_pdl(norm_partials_kernel<1>, dim3(cols, 2, 1), 32 * kSumWarps, 0, c.stream, a,
+                      blocks);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cols, 2, kSumSplit);
+  cfg.blockDim = 32 * kSumWarps;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = kSumSplit;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, norm_partials_kernel<kSumSplit>, a, blocks);
 }
 
 template <class RT, class YT, int VEC, int NPT>
@@ -398,9 +439,13 @@ bool bwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
 }
 template <class RT, class YT, bool GEL>
 bool bwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e) {
+  // one or two units of 8 channels per thread, us at 16384 tokens: H = 64: 15.3 :
+  // 17.2, 256: 18.0 : 19.6, 512: 32.9 : 32.9, 1024: 55.8 : 58.2, 2048: 95 : 107
   if (vec == 8)
     return a.H <= 2048 ? bwd_ring<RT, YT, GEL, 8, 1, 0>(c, a, e)
                        : bwd_ring<RT, YT, GEL, 8, 2, 0>(c, a, e);
+  // the smallest block that holds the row; the next larger one, us at 8192 tokens:
+  // H = 250: 32 : 48, 1001: 47 : 58, 2047: 72 : 107
   if (a.H <= 256) return bwd_ring<RT, YT, GEL, 1, 4, 64>(c, a, e);
   if (a.H <= 1024) return bwd_ring<RT, YT, GEL, 1, 8, 128>(c, a, e);
   if (a.H <= 2048) return bwd_ring<RT, YT, GEL, 1, 8, 256>(c, a, e);

@@ -18,6 +18,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 8;
+constexpr int kZeroRows = 8;  // rows a warp looks at
 
 template <class GT>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(
@@ -28,10 +29,11 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x;
   if (t >= T) {
-    // the CTAs past the tokens zero the rows no copy lands on, 32 per warp
-    const int64_t r0 = ((t - T) * kWarps + warp) * 32;
+    // the CTAs past the tokens zero the rows no copy lands on (whole runs at the
+    // ends of the experts' segments: few rows per warp spread a run)
+    const int64_t r0 = ((t - T) * kWarps + warp) * kZeroRows;
     const int64_t r = r0 + lane;
-    unsigned m = __ballot_sync(0xFFFFFFFFu, r < R && __ldg(src + r) < 0);
+    unsigned m = __ballot_sync(0xFFFFFFFFu, lane < kZeroRows && r < R && __ldg(src + r) < 0);
     while (m) {
       const int i = __ffs(m) - 1;
       m &= m - 1;
@@ -102,7 +104,7 @@ template <class GT>
 cudaError_t launch_t(const LaunchCtx& c, const void* go, const void* y, const float* w,
                      const int32_t* pos, const int32_t* src, int64_t T, int H, int k, int64_t R,
                      void* gy, float* gw) {
-  const int64_t zero = src ? (R + 32 * kWarps - 1) / (32 * kWarps) : 0;
+  const int64_t zero = src ? (R + kZeroRows * kWarps - 1) / (kZeroRows * kWarps) : 0;
   const int64_t blocks = T + zero;
   if (blocks == 0) return cudaSuccess;
   if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
