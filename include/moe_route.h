@@ -667,10 +667,13 @@ moe_status_t moe_combine_backward(const void *grad_out, int32_t grad_dtype, cons
  *   out[r, n] = o[r, n] / (1 + exp(-o[r, n])) * o[r, N + n]    (swiglu: M = 2N)
  * for the rows offsets[e] <= r < offsets[e+1] of every expert e, in f32, rounded
  * once to out_dtype.  Rows at or past offsets[E] are not written.
+ * x enters the products scaled by a power of two per 256 channels and rounded to
+ * f16: a channel is exact unless it is below 2^-31 of the largest of its 256, and
+ * then off by less than 2^-39 of that.
  *   x [num_x, K] bf16, finite, 16-byte aligned
  *   w [E, M, K/2] u8, two E2M1 codes per byte, element 2i in the low nibble (the
- *   layout moe_expand_cast_fp4 writes), 16-byte aligned; w_sf as MOE_WSF_*, 4-byte
- *   aligned
+ *   layout moe_expand_cast_fp4 writes), 16-byte aligned; w_sf as MOE_WSF_*, below
+ *   2^100, 4-byte aligned
  *   offsets [E+1] i32, non-decreasing, within [0, num_rows], as the route maps
  *   return it; NULL (E == 1 only): all num_rows rows
  *   sorted_src: NULL: src(r) = r (num_x >= num_rows); or [num_rows] i32 as the route

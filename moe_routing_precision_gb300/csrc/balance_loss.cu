@@ -19,6 +19,12 @@
 // router's, whatever its masked scores) need no maximum taken off: e^x, its sums
 // and the sigmoids e^x / (1 + e^x) stay in f32's range, and what underflows is
 // below 1e-29 of the row.  Other rows take the shifted form.
+//
+// At 65536 tokens of 256 experts (67 MB of scores) the exponentials and the
+// rows' index work bound both passes, not HBM: about 280 warp instructions per
+// token forward (26 us, 2.6 TB/s) and 500 for the sigmoid gradient (39 us, 3.6
+// TB/s).  The rows' next scores are in flight meanwhile; without them the
+// forward waited on its loads (43 us).
 #include "block_ops.cuh"
 
 namespace moe {
@@ -64,6 +70,10 @@ struct Work {
   size_t bytes;
 };
 constexpr int kTile = 32;  // experts per CTA of the second launch
+// Below so many table rows per sequence the second launch takes 4 warps per CTA
+// instead of 16, us at 65536 tokens, 256 experts: 1000 sequences 48 : 74, 256:
+// 31 : 39, 64 (five rows each): 28.4 : 27.9, 8: 32 : 26.
+constexpr int64_t kFewRows = 4;
 __host__ inline Work work_layout(void* ws, int64_t T, int E, int S) {
   const size_t slots = (size_t)num_chunks(T) + S;
   const size_t tiles = (size_t)(E + kTile - 1) / kTile;
@@ -91,15 +101,18 @@ __device__ __forceinline__ int64_t seq_at(const BalanceArgs& a, int i) {
   const int64_t v = __ldg(a.seq + i);
   return v < 0 ? 0 : (v > a.T ? a.T : v);
 }
-// The first sequence that ends after token t (S if none).
+// The first sequence that ends after token t (S if none).  A whole warp calls
+// it: 32 boundaries are looked at per step (one load deep instead of five).
 __device__ __forceinline__ int first_seq(const BalanceArgs& a, int64_t t) {
-  int lo = 0, hi = a.S;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = a.S;  // the answer lies in [lo, hi]
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_at(a, mid + 1) <= t)
-      lo = mid + 1;
-    else
-      hi = mid;
+    const int step = (hi - lo + 31) / 32, p = lo + lane * step;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, p < hi && seq_at(a, p + 1) <= t));
+    if (n == 0) return lo;
+    const int last = lo + (n - 1) * step;  // the last probe that ends by t
+    if (last + step < hi) hi = last + step;
+    lo = last + 1;
   }
   return lo;
 }
@@ -167,13 +180,6 @@ struct Walk {
     left -= stride;
   }
 };
-
-// 1 / x for 2^-126 <= x < 2^126, to an ulp: the hardware estimate and one Newton step.
-__device__ __forceinline__ float rcp_f32(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return __fmaf_rn(y, __fmaf_rn(-x, y, 1.0f), y);
-}
 
 // Whether any group of this warp (L lanes a row, N values per lane) needs the
 // shifted form: its largest score is above 80, or finite and below -20.
@@ -454,17 +460,17 @@ __global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
   if (bad) flag_error(err, MOE_DEVERR_EXPERT_RANGE);
 }
 
-// One CTA per (sequence, 32 experts): warp w adds the sequence's table rows w,
-// w + kSumWarps, ...; the CTA that arrives last at a sequence adds the tiles'
+// One CTA per (sequence, 32 experts): warp w of SW adds the sequence's table rows
+// w, w + SW, ...; the CTA that arrives last at a sequence adds the tiles'
 // losses in order.
-constexpr int kSumWarps = 16;
-__global__ void __launch_bounds__(32 * kSumWarps)
+template <int SW>
+__global__ void __launch_bounds__(32 * SW)
     balance_sum_kernel(const BalanceArgs a, const Work ws, int64_t chunk) {
   pdl_enter();
-  __shared__ float sp[kSumWarps][33];
-  __shared__ int sc[kSumWarps][33];
-  __shared__ float sz[kSumWarps];
-  __shared__ int sn[kSumWarps];
+  __shared__ float sp[SW][33];
+  __shared__ int sc[SW][33];
+  __shared__ float sz[SW];
+  __shared__ int sn[SW];
   __shared__ int last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int s = blockIdx.y, tile = blockIdx.x, e = tile * kTile + lane;
@@ -474,13 +480,13 @@ __global__ void __launch_bounds__(32 * kSumWarps)
   if (s0 < s1) {
     const int64_t r0 = s0 / chunk + s, r1 = (s1 - 1) / chunk + s;
 #pragma unroll 4
-    for (int64_t r = r0 + warp; r <= r1; r += kSumWarps) {
+    for (int64_t r = r0 + warp; r <= r1; r += SW) {
       if (e < a.E) {
         p += ws.p[r * a.E + e];
         c += ws.cnt[r * a.E + e];
       }
     }
-    for (int64_t r = r0 + threadIdx.x; r <= r1; r += 32 * kSumWarps) {
+    for (int64_t r = r0 + threadIdx.x; r <= r1; r += 32 * SW) {
       z += ws.z[r];
       n += ws.n[r];
     }
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(32 * kSumWarps)
   if (warp != 0) return;
   p = 0.0f, c = 0, z = 0.0f, n = 0;
 #pragma unroll
-  for (int w = 0; w < kSumWarps; ++w) {
+  for (int w = 0; w < SW; ++w) {
     p += sp[w][lane];
     c += sc[w][lane];
     z += sz[w];
@@ -685,8 +691,10 @@ cudaError_t forward_t(const LaunchCtx& c, const BalanceArgs& a) {
   e = launch_pdl(kernel, dim3((unsigned)chunks), kThreads, smem, c.stream, a, ws, chunk, one,
                  c.err);
   if (e != cudaSuccess || one) return e;
-  return launch_pdl(balance_sum_kernel, dim3((unsigned)((a.E + kTile - 1) / kTile), (unsigned)a.S),
-                    32 * kSumWarps, 0, c.stream, a, ws, chunk);
+  const dim3 grid((unsigned)((a.E + kTile - 1) / kTile), (unsigned)a.S);
+  if (chunks / a.S < kFewRows)
+    return launch_pdl(balance_sum_kernel<4>, grid, 128, 0, c.stream, a, ws, chunk);
+  return launch_pdl(balance_sum_kernel<16>, grid, 512, 0, c.stream, a, ws, chunk);
 }
 
 template <int L, int W, int NV, bool SIG>

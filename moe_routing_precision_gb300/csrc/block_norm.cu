@@ -6,6 +6,12 @@
 //   n = h * rsqrt(mean(h^2) + eps) * pre_w
 // A row stays in registers from its load to its stores, so HBM sees r, y (and
 // an elementwise gate) once and h, n once; that traffic bounds it.
+//
+// Measured: 16384 tokens, H = 7168, bf16, gated per token (940 MB): 140 us, 6.7
+// TB/s, 98 % of a plain copy, through the ring with two rows per turn (176 us
+// with one block per row, whose loads stop while a row is summed; 206 us with
+// the ring but one row per turn and single bf16 conversions).  One token, H =
+// 4096: 3.1 us.
 #include "block_norm.cuh"
 
 namespace moe {

@@ -106,11 +106,18 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// 1 / x for 2^-126 <= x < 2^126, to an ulp: the hardware estimate and one Newton step.
+__device__ __forceinline__ float rcp_f32(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return __fmaf_rn(y, __fmaf_rn(-x, y, 1.0f), y);
+}
+
 // g = 1 / (1 + e^-x) and g' = g (1 - g), both to a few ulp for every x: with
 // e = e^-|x| the larger of g and 1 - g is 1 / (1 + e), the smaller e / (1 + e).
 __device__ __forceinline__ float sigmoid_f32(float x, float* deriv = nullptr) {
   const float e = expf(-fabsf(x));
-  const float big = __fdividef(1.0f, 1.0f + e), small = e * big;
+  const float big = rcp_f32(1.0f + e), small = e * big;
   if (deriv) *deriv = big * small;
   return x < 0.0f ? small : big;
 }

@@ -27,6 +27,16 @@
 // and scales through a ring of its own in shared memory with cp.async, several
 // blocks of 256 channels ahead, so no barrier stands in the stream.
 //
+// Measured: 64 tokens, top 8 of 256 experts, K = 2048, N = 7168, f32 scales per 128
+// (1.74 GB): 244 us, 7.1 TB/s, above a plain copy's rate (reads alone run faster).
+// One token, K = 7168, SwiGLU of 2 x 2048, UE8M0 scales per 32 (125 MB): 27 us, of
+// which 8 us do not depend on N (launch, offsets, x, filling the rings); the
+// slope is 6.4 TB/s.  At that rate a scheduler issues two thirds of its slots;
+// what the warps execute per weight bounds it next: 64 conversions and 16 products
+// per 4096 weights among about 290 instructions.  A stage of 128 channels doubled
+// the rest (42 us); cp.async for the codes filled the load queue ahead of the
+// shared-memory reads (batch 292 us); 8 warps could not hide the latencies (51 us).
+//
 // With SwiGLU a tile is 8 gate outputs and the 8 up outputs of the same
 // channels, which the fragment layout leaves in one lane.
 #include "block_ops.cuh"
