@@ -12,6 +12,11 @@ declared in ``include/moe_route.h``:
 * ``swiglu_cast_fp8``  silu(gate) * up in fp32, then the same FP8 cast;
 * ``combine``          the weighted sum of each token's expert outputs.
 
+Around them, the operators of an MoE block in training and decoding:
+``block_norm`` (the norms before and after the block, with its gate and
+residual scale), ``balance_loss``, ``combine_backward`` and the backward
+passes, and ``expert_matvec_fp4`` (products with 4-bit expert weights).
+
 ``ops`` is the thin Python binding (argument marshalling only); it loads the
 in-tree shared library and raises if it is missing.  ``workloads`` draws the
 seeded synthetic inputs.

@@ -46,7 +46,8 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    headers = glob.glob(os.path.join(CSRC, "**", "*.cuh"), recursive=True)
+    return _sources() + headers + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def debug_bounds_requested() -> bool:

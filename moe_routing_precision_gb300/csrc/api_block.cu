@@ -3,7 +3,7 @@
 // A rejected call launches nothing.
 #include <cmath>
 
-#include "block_ops.cuh"
+#include "block/block_ops.cuh"
 
 namespace moe {
 namespace {

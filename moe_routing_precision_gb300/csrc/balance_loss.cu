@@ -25,7 +25,7 @@
 // token forward (26 us, 2.6 TB/s) and 500 for the sigmoid gradient (39 us, 3.6
 // TB/s).  The rows' next scores are in flight meanwhile; without them the
 // forward waited on its loads (43 us).
-#include "block_ops.cuh"
+#include "block/block_ops.cuh"
 
 namespace moe {
 namespace {
@@ -686,7 +686,7 @@ cudaError_t forward_t(const LaunchCtx& c, const BalanceArgs& a) {
   const size_t smem = (size_t)(kWarps + 1) * a.E * 4 + kWarps * 12;
   auto* kernel = balance_chunk_kernel<L, W, NV, SIG>;
   static SmemOptIn opt_in;
-  cudaError_t e = smem > 48 * 1024 ? opt_in.once(c, kernel) : cudaSuccess;
+  cudaError_t e = smem > 48 * 1024 ? opt_in.once(kernel) : cudaSuccess;
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3((unsigned)chunks), kThreads, smem, c.stream, a, ws, chunk, one,
                  c.err);

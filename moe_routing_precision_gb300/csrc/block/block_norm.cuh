@@ -2,7 +2,7 @@
 // sums, the gate, and the ring of staged rows.
 #pragma once
 
-#include "block_ops.cuh"
+#include "block/block_ops.cuh"
 
 namespace moe {
 namespace {
@@ -265,7 +265,7 @@ template <auto* kernel>
 cudaError_t ring_launch(const LaunchCtx& c, const NormArgs& a, const RingShape& s,
                         int64_t max_blocks, int* blocks_out) {
   static SmemOptIn opt_in;
-  cudaError_t e = opt_in.once(c, kernel);
+  cudaError_t e = opt_in.once(kernel);
   if (e != cudaSuccess) return e;
   int64_t blocks = (int64_t)c.num_sms * s.per_sm;
   if (blocks > max_blocks) blocks = max_blocks;

@@ -183,10 +183,13 @@ __device__ __forceinline__ void mbar_init_done() {
 class SmemOptIn {
  public:
   template <typename... KArgs>
-  cudaError_t once(const LaunchCtx& c, void (*kernel)(KArgs...)) {
-    const uint64_t bit = 1ull << c.device;  // context() admits 64 devices
+  cudaError_t once(void (*kernel)(KArgs...)) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (device & 63);  // context() admits 64 devices
     if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    const cudaError_t e = allow_max_dynamic_smem(kernel);
+    e = allow_max_dynamic_smem(kernel);
     if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
     return e;
   }

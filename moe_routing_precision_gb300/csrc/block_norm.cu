@@ -12,7 +12,7 @@
 // with one block per row, whose loads stop while a row is summed; 206 us with
 // the ring but one row per turn and single bf16 conversions).  One token, H =
 // 4096: 3.1 us.
-#include "block_norm.cuh"
+#include "block/block_norm.cuh"
 
 namespace moe {
 namespace {

@@ -13,7 +13,7 @@
 // Measured: 8192 tokens, H = 7168, f32 stream, bf16 block, gate per channel (1.06
 // GB): 172 us, 6.1 TB/s, 91 % of a plain copy (two rows of 86 KB in flight per
 // SM); 321 us with one block per row and no ring.
-#include "block_norm.cuh"
+#include "block/block_norm.cuh"
 
 #include <cooperative_groups.h>
 
@@ -407,7 +407,7 @@ cudaError_t bwd_t(const LaunchCtx& c, const NormArgs& a) {
   const size_t smem = 192 * sizeof(float) + (s.rows > 1 ? (size_t)s.rows * a.H * sizeof(float) : 0);
   auto* kernel = block_norm_backward_kernel<RT, YT, VEC, NPT>;
   static SmemOptIn opt_in;
-  cudaError_t e = opt_in.once(c, kernel);
+  cudaError_t e = opt_in.once(kernel);
   if (e != cudaSuccess) return e;
   // blocks per SM, looked up when the shape changes (1 us a call)
   thread_local int known = -1, per_sm = 0;

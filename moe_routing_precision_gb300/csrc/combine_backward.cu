@@ -11,7 +11,7 @@
 // 8 routed rows before it uses any, so 8 gathers of 16 bytes are in flight per
 // thread.  The k dot products stay in registers until the row is done; one
 // shuffle and shared-memory reduction in a fixed order then writes them.
-#include "block_ops.cuh"
+#include "block/block_ops.cuh"
 
 namespace moe {
 namespace {

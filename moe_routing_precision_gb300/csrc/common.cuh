@@ -352,7 +352,6 @@ struct LaunchCtx {
   cudaStream_t stream;
   int num_sms;
   unsigned* err;  // device error word
-  int device;     // ordinal
 };
 
 // The device conversions on arbitrary f32 values, for tests (debug_cvt.cu).

@@ -39,7 +39,7 @@
 //
 // With SwiGLU a tile is 8 gate outputs and the 8 up outputs of the same
 // channels, which the fragment layout leaves in one lane.
-#include "block_ops.cuh"
+#include "block/block_ops.cuh"
 
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -663,7 +663,7 @@ cudaError_t launch_t(const LaunchCtx& c, const MatvecArgs& a) {
   const size_t smem = smem_layout(kScaleBytes, a.K, a.E, C).total;
   auto* kernel = expert_matvec_kernel<G, U8, ALIGNED>;
   static SmemOptIn opt_in;
-  cudaError_t e = opt_in.once(c, kernel);
+  cudaError_t e = opt_in.once(kernel);
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   e = code_map(a, &map);
