@@ -21,8 +21,8 @@
 // below 1e-29 of the row.  Other rows take the shifted form.
 //
 // At 65536 tokens of 256 experts (67 MB of scores) the exponentials and the
-// rows' index work bound both passes, not HBM: about 280 warp instructions per
-// token forward (26 us, 2.6 TB/s) and 500 for the sigmoid gradient (39 us, 3.6
+// rows' index work bound both passes, not HBM: about 250 warp instructions per
+// token forward (26 us, 2.7 TB/s) and 470 for the sigmoid gradient (37 us, 3.8
 // TB/s).  The rows' next scores are in flight meanwhile; without them the
 // forward waited on its loads (43 us).
 #include "block/block_ops.cuh"
@@ -132,8 +132,9 @@ __device__ __forceinline__ float group_sum(float v) {
 
 constexpr float kNegInf = -INFINITY;
 
-// Lane layout: value (v, i) of a lane is expert (v L + lane) W + i.
-template <int L, int W, int NV>
+// Lane layout: value (v, i) of a lane is expert (v L + lane) W + i.  FULL: E = L W NV,
+// so every lane's experts exist.
+template <int L, int W, int NV, bool FULL>
 struct Row {
   float x[NV * W];
   __device__ __forceinline__ static int expert(int sub, int v) { return (v * L + sub) * W; }
@@ -142,7 +143,7 @@ struct Row {
   __device__ __forceinline__ void load(const float* p, int E, int sub, bool want) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const bool in = want && expert(sub, v) < E;
+      const bool in = want && (FULL || expert(sub, v) < E);
       if constexpr (W == 4) {
         uint4 q = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
         if (in) q = ld_stream_v4(p + v * L * W);
@@ -160,13 +161,12 @@ struct Row {
 // The tokens first, first + stride, ... below hi of one group of lanes, by
 // offsets that move along (index products in 64 bits cost a fifth of the
 // instructions).
-template <int L, int W, int NV>
 struct Walk {
   int64_t e_at, k_at;  // this lane's first score, and its first of the k selections
   const uint8_t* mask;
   int left;  // tokens from the current one to hi
-  __device__ __forceinline__ Walk(const BalanceArgs& a, int64_t first, int64_t hi, int sub)
-      : e_at(first * a.E + sub * W),
+  __device__ __forceinline__ Walk(const BalanceArgs& a, int64_t first, int64_t hi, int sub, int w)
+      : e_at(first * a.E + sub * w),
         k_at(first * a.k + sub),
         mask(a.mask == nullptr ? nullptr : a.mask + first),
         left(hi > first ? (int)(hi - first) : 0) {}
@@ -317,7 +317,7 @@ __device__ __forceinline__ void row_grad(const float (&x)[N], const float (&a)[N
 }
 
 // one: a single block, which writes the results itself.
-template <int L, int W, int NV, bool SIG>
+template <int L, int W, int NV, bool SIG, bool FULL>
 __global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
     balance_chunk_kernel(const BalanceArgs a, const Work ws, int64_t chunk, bool one,
                          unsigned* err) {
@@ -359,23 +359,26 @@ __global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     float zsum = 0.0f;
     int n = 0;
-    Row<L, W, NV> next;
+    Row<L, W, NV, FULL> next;
     int32_t next_e = 0;  // this lane's first index of the next token
     constexpr int kStride = kWarps * TPW;
-    Walk<L, W, NV> walk(a, lo + warp * TPW + grp, hi, sub);
+    Walk walk(a, lo + warp * TPW + grp, hi, sub, W);
+    bool now = false;  // whether the next token is wanted
     auto fetch = [&]() {
-      const bool want = walk.want();
-      next.load(a.scores + walk.e_at, E, sub, want);
-      if (want && sub < a.k) next_e = __ldg(a.idx + walk.k_at);
+      now = walk.want();
+      next.load(a.scores + walk.e_at, E, sub, now);
+      if (now && sub < a.k) next_e = __ldg(a.idx + walk.k_at);
     };
     fetch();
     const int64_t mine = hi - lo - warp * TPW;
     for (int64_t done = 0; done < mine; done += kStride) {
-      const Row<L, W, NV> row = next;
+      const Row<L, W, NV, FULL> row = next;
       const int32_t e0 = next_e;
       const int64_t k_at = walk.k_at;
+      const bool want = now;
       walk.step(a, kStride);
       fetch();
+      if (L == 32 && !want) continue;  // the warp's only row
       float p[N], lse;
       bool counts;
       row_probs<L, N, SIG>(row.x, p, &lse, &counts);
@@ -407,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const int e = Row<L, W, NV>::expert(sub, v) + i;
-          if (e < E) psum[warp * E + e] = acc[v * W + i];
+          const int e = Row<L, W, NV, FULL>::expert(sub, v) + i;
+          if (FULL || e < E) psum[warp * E + e] = acc[v * W + i];
         }
     }
     if (lane == 0) {
@@ -537,7 +540,7 @@ __global__ void __launch_bounds__(32 * SW)
   }
 }
 
-template <int L, int W, int NV, bool SIG>
+template <int L, int W, int NV, bool SIG, bool FULL>
 __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
     balance_backward_kernel(const BalanceArgs a, int64_t chunk, unsigned* err) {
   pdl_enter();
@@ -567,12 +570,12 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
       if (hi <= lo) continue;
       done = hi;
       // the next token's scores, and this lane's first selection of it
-      Row<L, W, NV> next;
+      Row<L, W, NV, FULL> next;
       int32_t next_e = 0;
       float next_w = 0.0f, next_g = 0.0f;
       constexpr int kStride = kBwdWarps * TPW;
       const int64_t first = lo + warp * TPW + grp;
-      Walk<L, W, NV> walk(a, first, hi, sub);
+      Walk walk(a, first, hi, sub, W);
       auto fetch = [&]() {
         const bool want = in_seq && walk.want();
         next.load(a.scores + walk.e_at, E, sub, want);
@@ -597,8 +600,8 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
             for (int v = 0; v < NV; ++v)
 #pragma unroll
               for (int i = 0; i < W; ++i) {
-                const int e = Row<L, W, NV>::expert(sub, v) + i;
-                if (e < E) coef[v * W + i] = gb * (float)__ldg(a.counts + (int64_t)s * E + e);
+                const int e = Row<L, W, NV, FULL>::expert(sub, v) + i;
+                if (FULL || e < E) coef[v * W + i] = gb * (float)__ldg(a.counts + (int64_t)s * E + e);
               }
           }
         }
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
       const int64_t mine_n = hi - lo - warp * TPW;
       for (int64_t at = 0; at < mine_n; at += kStride) {
         const bool live = walk.left > 0;
-        const Row<L, W, NV> row = next;
+        const Row<L, W, NV, FULL> row = next;
         const int32_t e0 = next_e;
         const float w0 = next_w, g0 = next_g;
         const int64_t k_at = walk.k_at;
@@ -643,8 +646,8 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          const int e = Row<L, W, NV>::expert(sub, v);
-          if (e >= E) continue;
+          const int e = Row<L, W, NV, FULL>::expert(sub, v);
+          if (!FULL && e >= E) continue;
           if constexpr (W == 4) {
             if (sel) {
               const float4 m = *reinterpret_cast<const float4*>(mine + e);
@@ -678,13 +681,13 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
   if (bad) flag_error(err, MOE_DEVERR_EXPERT_RANGE);
 }
 
-template <int L, int W, int NV, bool SIG>
+template <int L, int W, int NV, bool SIG, bool FULL>
 cudaError_t forward_t(const LaunchCtx& c, const BalanceArgs& a) {
   const bool one = one_block(a.T, a.E, a.S);
   const int64_t chunk = one ? a.T : chunk_tokens(a.T), chunks = one ? 1 : num_chunks(a.T);
   const Work ws = work_layout(a.ws, a.T, a.E, a.S);
   const size_t smem = (size_t)(kWarps + 1) * a.E * 4 + kWarps * 12;
-  auto* kernel = balance_chunk_kernel<L, W, NV, SIG>;
+  auto* kernel = balance_chunk_kernel<L, W, NV, SIG, FULL>;
   static SmemOptIn opt_in;
   cudaError_t e = smem > 48 * 1024 ? opt_in.once(kernel) : cudaSuccess;
   if (e != cudaSuccess) return e;
@@ -697,7 +700,7 @@ cudaError_t forward_t(const LaunchCtx& c, const BalanceArgs& a) {
   return launch_pdl(balance_sum_kernel<16>, grid, 512, 0, c.stream, a, ws, chunk);
 }
 
-template <int L, int W, int NV, bool SIG>
+template <int L, int W, int NV, bool SIG, bool FULL>
 cudaError_t backward_t(const LaunchCtx& c, const BalanceArgs& a) {
   // eight blocks' worth of tokens per SM, at least one pass of a block's warps
   constexpr int kPass = kBwdWarps * (32 / L);
@@ -705,15 +708,22 @@ cudaError_t backward_t(const LaunchCtx& c, const BalanceArgs& a) {
   chunk = (chunk + kPass - 1) / kPass * kPass;
   const int64_t chunks = (a.T + chunk - 1) / chunk;
   const size_t smem = a.grad_w ? (size_t)kPass * a.E * 4 : 0;
-  return launch_pdl(balance_backward_kernel<L, W, NV, SIG>, dim3((unsigned)chunks), kBwdThreads,
+  return launch_pdl(balance_backward_kernel<L, W, NV, SIG, FULL>, dim3((unsigned)chunks), kBwdThreads,
                     smem, c.stream, a, chunk, c.err);
 }
 
-template <int L, int W, int NV>
+template <int L, int W, int NV, bool FULL>
 cudaError_t dispatch_func(const LaunchCtx& c, const BalanceArgs& a, bool backward) {
   if (a.func == MOE_SCORE_SIGMOID)
-    return backward ? backward_t<L, W, NV, true>(c, a) : forward_t<L, W, NV, true>(c, a);
-  return backward ? backward_t<L, W, NV, false>(c, a) : forward_t<L, W, NV, false>(c, a);
+    return backward ? backward_t<L, W, NV, true, FULL>(c, a)
+                    : forward_t<L, W, NV, true, FULL>(c, a);
+  return backward ? backward_t<L, W, NV, false, FULL>(c, a)
+                  : forward_t<L, W, NV, false, FULL>(c, a);
+}
+template <int L, int W, int NV>
+cudaError_t dispatch_full(const LaunchCtx& c, const BalanceArgs& a, bool backward) {
+  return a.E == L * W * NV ? dispatch_func<L, W, NV, true>(c, a, backward)
+                           : dispatch_func<L, W, NV, false>(c, a, backward);
 }
 
 // Lanes per token and accesses per lane from E: 16-byte accesses where the
@@ -723,20 +733,20 @@ cudaError_t dispatch(const LaunchCtx& c, const BalanceArgs& a, bool backward) {
       reinterpret_cast<uintptr_t>(a.scores) | reinterpret_cast<uintptr_t>(a.grad_scores);
   const int E = a.E;
   if (E % 4 == 0 && (bits & 15u) == 0) {
-    if (E <= 16) return dispatch_func<4, 4, 1>(c, a, backward);
-    if (E <= 32) return dispatch_func<8, 4, 1>(c, a, backward);
-    if (E <= 64) return dispatch_func<16, 4, 1>(c, a, backward);
-    if (E <= 128) return dispatch_func<32, 4, 1>(c, a, backward);
-    if (E <= 256) return dispatch_func<32, 4, 2>(c, a, backward);
-    if (E <= 512) return dispatch_func<32, 4, 4>(c, a, backward);
-    return dispatch_func<32, 4, 8>(c, a, backward);
+    if (E <= 16) return dispatch_full<4, 4, 1>(c, a, backward);
+    if (E <= 32) return dispatch_full<8, 4, 1>(c, a, backward);
+    if (E <= 64) return dispatch_full<16, 4, 1>(c, a, backward);
+    if (E <= 128) return dispatch_full<32, 4, 1>(c, a, backward);
+    if (E <= 256) return dispatch_full<32, 4, 2>(c, a, backward);
+    if (E <= 512) return dispatch_full<32, 4, 4>(c, a, backward);
+    return dispatch_full<32, 4, 8>(c, a, backward);
   }
-  if (E <= 8) return dispatch_func<8, 1, 1>(c, a, backward);
-  if (E <= 32) return dispatch_func<32, 1, 1>(c, a, backward);
-  if (E <= 128) return dispatch_func<32, 1, 4>(c, a, backward);
-  if (E <= 256) return dispatch_func<32, 1, 8>(c, a, backward);
-  if (E <= 512) return dispatch_func<32, 1, 16>(c, a, backward);
-  return dispatch_func<32, 1, 32>(c, a, backward);
+  if (E <= 8) return dispatch_func<8, 1, 1, false>(c, a, backward);
+  if (E <= 32) return dispatch_func<32, 1, 1, false>(c, a, backward);
+  if (E <= 128) return dispatch_func<32, 1, 4, false>(c, a, backward);
+  if (E <= 256) return dispatch_func<32, 1, 8, false>(c, a, backward);
+  if (E <= 512) return dispatch_func<32, 1, 16, false>(c, a, backward);
+  return dispatch_func<32, 1, 32, false>(c, a, backward);
 }
 
 }  // namespace

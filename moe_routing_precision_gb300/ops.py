@@ -582,8 +582,7 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
     out: None or (h, n), where h may be residual itself.
     -> (h, n, rstd_post, rstd_pre), None for what there is not."""
     sd = _dt(residual, "residual")
-    _dev(residual, "residual", residual.dtype)
-    T, H = residual.shape
+    T, H = _dev(residual, "residual", residual.dtype).shape
     if block_dtype is None:
         block_dtype = torch.bfloat16 if y is None else y.dtype
     if block_dtype not in (torch.bfloat16, torch.float32):
@@ -640,8 +639,7 @@ def block_norm_backward(grad_h, grad_n, h: torch.Tensor, *, y=None, post_weight=
     -> (grad_residual, grad_y, grad_post_weight, grad_gate, grad_pre_weight),
     None for what there is not; each in its tensor's type and shape."""
     sd = _dt(h, "h")
-    _dev(h, "h", h.dtype)
-    T, H = h.shape
+    T, H = _dev(h, "h", h.dtype).shape
     if grad_h is not None:
         _dev(grad_h, "grad_h", h.dtype, (T, H))
     if (pre_weight is None) != (grad_n is None) or (pre_weight is None) != (rstd_pre is None):
@@ -658,26 +656,28 @@ def block_norm_backward(grad_h, grad_n, h: torch.Tensor, *, y=None, post_weight=
         raise ValueError("post_weight and gate need y")
     if grad_n is not None:
         _dev(grad_n, "grad_n", block.dtype, (T, H))
-    for name, wt in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if wt is not None:
-            _dev(wt, name, torch.float32, (H,))
-    for name, r in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
-        if r is not None:
-            _dev(r, name, torch.float32, (T,))
-    kind = _gate_kind(gate, T, H, block.dtype)
+    if post_weight is not None:
+        _dev(post_weight, "post_weight", torch.float32, (H,))
+        _dev(rstd_post, "rstd_post", torch.float32, (T,))
+    if pre_weight is not None:
+        _dev(pre_weight, "pre_weight", torch.float32, (H,))
+        _dev(rstd_pre, "rstd_pre", torch.float32, (T,))
+    kind = GATE_NONE if gate is None else _gate_kind(gate, T, H, block.dtype)
     gr = torch.empty_like(h)
     gy = None if y is None else torch.empty_like(y)
     gpw = None if post_weight is None else torch.empty_like(post_weight)
     gg = None if gate is None else torch.empty_like(gate)
     gnw = None if pre_weight is None else torch.empty_like(pre_weight)
+    ws_bytes = block_norm_backward_workspace_bytes(T, H)
     if workspace is None:
-        workspace = _empty((block_norm_backward_workspace_bytes(T, H),), torch.uint8, h)
-    _dev(workspace, "workspace", torch.uint8)
+        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=h.device)
+    else:
+        ws_bytes = _dev(workspace, "workspace", torch.uint8).numel()
     rc = lib().moe_block_norm_backward(
         _ptr(grad_h), _ptr(grad_n), _ptr(h), sd, _ptr(y), bd, T, H, _ptr(post_weight), _ptr(gate),
         kind, _choice(gate_act, _GATE_ACT, "gate_act"), scale, _ptr(pre_weight), _ptr(rstd_post),
         _ptr(rstd_pre), _ptr(gr), _ptr(gy), _ptr(gpw), _ptr(gg), _ptr(gnw), _ptr(workspace),
-        workspace.numel(), _stream(stream))
+        ws_bytes, _stream(stream))
     _check(rc, "moe_block_norm_backward")
     return gr, gy, gpw, gg, gnw
 
