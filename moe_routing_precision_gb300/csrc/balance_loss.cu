@@ -9,8 +9,10 @@
 // second launch adds each sequence's rows in ascending order.  No float is
 // added atomically: the same inputs give the same bits.
 //
-// A small problem (see kOneBlockScores) is one block and one launch, without
-// the table.
+// A small problem (see kBlockScores) is one launch of a block per sequence,
+// without the table (162 tokens of 64 experts in 52 sequences: 3.4 us; 89 us with
+// one block for all sequences).  The gradient's warps have a run of tokens each
+// (244 tokens of 16 experts in 63 sequences: 13.7 us; 26 us with a run per block).
 //
 // A group of L lanes holds one token's scores in registers (W consecutive
 // experts per access), and loads the next token's while it works; the
@@ -22,7 +24,7 @@
 //
 // At 65536 tokens of 256 experts (67 MB of scores) the exponentials and the
 // rows' index work bound both passes, not HBM: about 250 warp instructions per
-// token forward (26 us, 2.7 TB/s) and 470 for the sigmoid gradient (37 us, 3.8
+// token forward (26 us, 2.7 TB/s) and 470 for the sigmoid gradient (36 us, 3.9
 // TB/s).  The rows' next scores are in flight meanwhile; without them the
 // forward waited on its loads (43 us).
 #include "block/block_ops.cuh"
@@ -47,15 +49,13 @@ inline int64_t num_chunks(int64_t T) {
   const int64_t c = chunk_tokens(T);
   return (T + c - 1) / c;
 }
-// One block up to this many scores: eight passes of its warps.  One block against
-// the table and its second launch, in us: E = 16: 4.8 : 8.2 at T = 512, 6.8 : 7.9
-// at 1024, 10.6 : 9.1 at 2048; E = 64: 4.9 : 7.7 at 128, 7.2 : 7.0 at 256; E = 256:
-// 5.6 : 7.9 at 64, 8.2 : 8.0 at 128.
-constexpr int64_t kOneBlockScores = 16384;
-constexpr int kOneBlockSeqs = 64;
-inline bool one_block(int64_t T, int E, int S) {
-  return T * E <= kOneBlockScores && S <= kOneBlockSeqs;
-}
+// A block per sequence up to this many scores: eight passes of its warps, if
+// one sequence has them all.  That against the table and its second launch, in us,
+// one sequence: E = 16: 4.8 : 8.2 at T = 512, 6.8 : 7.9 at 1024, 10.6 : 9.1 at
+// 2048; E = 64: 4.9 : 7.7 at 128, 7.2 : 7.0 at 256; E = 256: 5.6 : 7.9 at 64,
+// 8.2 : 8.0 at 128.
+constexpr int64_t kBlockScores = 16384;
+inline bool block_per_seq(int64_t T, int E) { return T * E <= kBlockScores; }
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Workspace: [slots][E] f32 sums of p, [slots][E] i32 counts, [slots] f32 sums
@@ -316,7 +316,7 @@ __device__ __forceinline__ void row_grad(const float (&x)[N], const float (&a)[N
   }
 }
 
-// one: a single block, which writes the results itself.
+// one: a block is a sequence, and writes its results itself.
 template <int L, int W, int NV, bool SIG, bool FULL>
 __global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
     balance_chunk_kernel(const BalanceArgs a, const Work ws, int64_t chunk, bool one,
@@ -337,10 +337,11 @@ __global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
   for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = 0;
   __syncthreads();
 
-  const int64_t b0 = (int64_t)blockIdx.x * chunk;
+  const int64_t b0 = one ? 0 : (int64_t)blockIdx.x * chunk;
   const int64_t b1 = b0 + chunk < a.T ? b0 + chunk : a.T;
+  const int s_end = one ? blockIdx.x + 1 : a.S;
   bool bad = false;
-  for (int s = one ? 0 : first_seq(a, b0); s < a.S; ++s) {
+  for (int s = one ? (int)blockIdx.x : first_seq(a, b0); s < s_end; ++s) {
     const int64_t s0 = seq_at(a, s), s1 = seq_at(a, s + 1);
     if (s0 >= b1 && !one) break;
     const int64_t lo = s0 > b0 ? s0 : b0, hi = s1 < b1 ? s1 : b1;
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(32 * SW)
 
 template <int L, int W, int NV, bool SIG, bool FULL>
 __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
-    balance_backward_kernel(const BalanceArgs a, int64_t chunk, unsigned* err) {
+    balance_backward_kernel(const BalanceArgs a, int64_t run, unsigned* err) {
   pdl_enter();
   extern __shared__ __align__(16) float smem[];  // per group: [E] gradients of the selected scores
   constexpr int N = NV * W, TPW = 32 / L;
@@ -554,8 +555,10 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
     for (int e = sub; e < E; e += L) mine[e] = 0.0f;
   __syncwarp();
 
-  const int64_t b0 = (int64_t)blockIdx.x * chunk;
-  const int64_t b1 = b0 + chunk < a.T ? b0 + chunk : a.T;
+  // each warp has its own run of tokens, so that it meets few short sequences
+  const int64_t b0 = ((int64_t)blockIdx.x * kBwdWarps + warp) * run;
+  const int64_t b1 = b0 + run < a.T ? b0 + run : a.T;
+  if (b0 >= b1) return;
   bool bad = false;
   int64_t done = b0;  // tokens below it are written
   for (int s = first_seq(a, b0); done < b1; ++s) {
@@ -573,9 +576,7 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
       Row<L, W, NV, FULL> next;
       int32_t next_e = 0;
       float next_w = 0.0f, next_g = 0.0f;
-      constexpr int kStride = kBwdWarps * TPW;
-      const int64_t first = lo + warp * TPW + grp;
-      Walk walk(a, first, hi, sub, W);
+      Walk walk(a, lo + grp, hi, sub, W);
       auto fetch = [&]() {
         const bool want = in_seq && walk.want();
         next.load(a.scores + walk.e_at, E, sub, want);
@@ -606,15 +607,14 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
           }
         }
       }
-      const int64_t mine_n = hi - lo - warp * TPW;
-      for (int64_t at = 0; at < mine_n; at += kStride) {
+      for (int64_t at = lo; at < hi; at += TPW) {
         const bool live = walk.left > 0;
         const Row<L, W, NV, FULL> row = next;
         const int32_t e0 = next_e;
         const float w0 = next_w, g0 = next_g;
         const int64_t k_at = walk.k_at;
         float* out = a.grad_scores + walk.e_at;
-        walk.step(a, kStride);
+        walk.step(a, TPW);
         fetch();
         float d[N];
         bool counts;
@@ -683,8 +683,8 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
 
 template <int L, int W, int NV, bool SIG, bool FULL>
 cudaError_t forward_t(const LaunchCtx& c, const BalanceArgs& a) {
-  const bool one = one_block(a.T, a.E, a.S);
-  const int64_t chunk = one ? a.T : chunk_tokens(a.T), chunks = one ? 1 : num_chunks(a.T);
+  const bool one = block_per_seq(a.T, a.E);
+  const int64_t chunk = one ? a.T : chunk_tokens(a.T), chunks = one ? a.S : num_chunks(a.T);
   const Work ws = work_layout(a.ws, a.T, a.E, a.S);
   const size_t smem = (size_t)(kWarps + 1) * a.E * 4 + kWarps * 12;
   auto* kernel = balance_chunk_kernel<L, W, NV, SIG, FULL>;
@@ -709,7 +709,7 @@ cudaError_t backward_t(const LaunchCtx& c, const BalanceArgs& a) {
   const int64_t chunks = (a.T + chunk - 1) / chunk;
   const size_t smem = a.grad_w ? (size_t)kPass * a.E * 4 : 0;
   return launch_pdl(balance_backward_kernel<L, W, NV, SIG, FULL>, dim3((unsigned)chunks), kBwdThreads,
-                    smem, c.stream, a, chunk, c.err);
+                    smem, c.stream, a, chunk / kBwdWarps, c.err);
 }
 
 template <int L, int W, int NV, bool FULL>
@@ -752,7 +752,7 @@ cudaError_t dispatch(const LaunchCtx& c, const BalanceArgs& a, bool backward) {
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t T, int E, int S) {
-  if (one_block(T, E, S)) return 0;
+  if (block_per_seq(T, E)) return 0;
   return work_layout(nullptr, T, E, S).bytes;
 }
 

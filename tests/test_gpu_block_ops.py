@@ -332,6 +332,18 @@ def test_balance_scores_far_from_zero(func, shift):
     check_balance_grad(x, idx, func, seq, m, c, t, 1)
 
 
+@pytest.mark.parametrize("T,E,S", [(162, 64, 52), (15, 309, 40), (40, 16, 300), (1, 8, 70),
+                                   (2048, 8, 130), (2049, 8, 130), (700, 16, 63)])
+def test_balance_more_sequences_than_warps(T, E, S):
+    x, idx, _, m = balance_inputs(T, E, 3, 1, T + S, mask=True)
+    cuts = torch.randint(0, T + 1, (S + 1,), generator=torch.Generator().manual_seed(T))
+    cuts, _ = torch.sort(cuts)  # gaps at both ends, empty sequences
+    seq = cuts.to(torch.int32).to(DEV)
+    for func in ("softmax", "sigmoid"):
+        c, t = check_balance(x, idx, func, seq, m)
+        check_balance_grad(x, idx, func, seq, m, c, t, S)
+
+
 def test_balance_determinism_errors_and_views():
     x, idx, seq, m = balance_inputs(3000, 256, 8, 7, 11, mask=False)
     a = ops.balance_loss(x, idx, seq_offsets=seq)
