@@ -130,6 +130,13 @@ struct RingState {
       flag_error(err, MOE_DEVERR_TIMEOUT);
     }
   }
+  // The copying thread, before it leaves: after a wait that ran out, copies may
+  // still be on their way.  A stage's barrier is in a phase of either parity;
+  // waiting for the other one returns at once.
+  __device__ __forceinline__ void drain(int stages) {
+    if (ok || threadIdx.x != 0) return;
+    for (int i = 0; i < 2 * stages; ++i) (void)mbar_wait(bars + i / 2 * 8, i & 1);
+  }
   __device__ __forceinline__ void next(int stages) {
     if (++stage == stages) {
       stage = 0;
@@ -235,13 +242,13 @@ int ring_vec(const NormArgs& a) {
   return a.H % 8 == 0 && (bits & 31u) == 0 ? 8 : 1;
 }
 
-// The ring's shape; at least two stages, or none.
+// The ring's shape; at least `least` stages, or none.
 struct RingShape {
   Ring ring;
   int threads = 0, per_sm = 0;
 };
 template <int V, int U, int NT>
-RingShape ring_shape(int H, int rows, const uint32_t (&row_bytes)[5]) {
+RingShape ring_shape(int H, int rows, const uint32_t (&row_bytes)[5], int least = 2) {
   RingShape s;
   for (int i = 0; i < 5; ++i) {
     s.ring.at[i] = s.ring.stage_bytes;
@@ -254,7 +261,7 @@ RingShape ring_shape(int H, int rows, const uint32_t (&row_bytes)[5]) {
   for (; s.per_sm > 0; --s.per_sm) {  // (1 KB of each block's shared memory is the system's)
     const uint32_t room = 226u * 1024 / s.per_sm - 1024 - kRingHeader;
     s.ring.stages = (int)(room / s.ring.stage_bytes);
-    if (s.ring.stages >= 2) break;
+    if (s.ring.stages >= least) break;
     s.ring.stages = 0;
   }
   if (s.ring.stages > kRingMaxStages) s.ring.stages = kRingMaxStages;

@@ -287,8 +287,7 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
       }
     }
   }
-  if (!rs.ok && tid == 0)
-    for (int i = 0; i < ring.stages; ++i) (void)mbar_wait(rs.bars + i * 8, rs.parity);
+  rs.drain(ring.stages);
 }
 
 template <class RT, class YT, int VEC, int NPT, int MAXT>

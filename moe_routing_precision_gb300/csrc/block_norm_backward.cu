@@ -235,7 +235,42 @@ __global__ void __launch_bounds__(32 * kSumWarps)
   if (a.grad_post_w) a.grad_post_w[c] = v * g;
 }
 
-template <class RT, class YT, bool GEL, int V, int U, int NT>
+// Starts the copies of channels [c0, c1) of row t of every stream into a stage
+// (sizes: bytes per element).
+__device__ __forceinline__ void ring_fill_piece(const RingState& r, const Ring& ring, int stage,
+                                                const void* const (&src)[5],
+                                                const uint32_t (&sizes)[5], int64_t t, int H,
+                                                int c0, int c1, unsigned* err) {
+  const uint32_t bar = r.bars + stage * 8;
+  const uint32_t dst = r.stages_at + stage * ring.stage_bytes;
+  uint32_t bytes[5], total = 0;
+  int64_t from[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    bytes[i] = 0;
+    if (src[i] == nullptr) continue;
+    from[i] = (t * H + c0) * sizes[i];
+    bytes[i] = (uint32_t)(c1 - c0) * sizes[i];
+    if (!MOE_DBG_OK(((reinterpret_cast<uintptr_t>(src[i]) | (uintptr_t)from[i] | bytes[i] |
+                      (dst + ring.at[i])) & 15u) == 0 &&
+                        ring.at[i] + bytes[i] <= ring.stage_bytes &&
+                        kRingHeader + (stage + 1) * ring.stage_bytes <= dynamic_smem_bytes(),
+                    err))
+      bytes[i] = 0;
+    total += bytes[i];
+  }
+  mbar_expect(bar, total);
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    if (bytes[i] > 0)
+      bulk_load(dst + ring.at[i], static_cast<const uint8_t*>(src[i]) + from[i], bytes[i], bar);
+}
+
+// P: stages per row.  Two (U = 2, V = 8, one unit of every thread each) where two
+// whole rows do not fit: H = 7168, all f32, element gate, 4096 tokens 173 us; 251
+// without the ring.  Whole rows where they fit (half rows take two turns of the
+// copying thread: bf16, 8192 tokens 148 : 177 us).
+template <class RT, class YT, bool GEL, int V, int U, int NT, int P>
 __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U, NT))
     norm_backward_ring_kernel(const NormArgs a, const Ring ring, unsigned* err) {
   pdl_enter();
@@ -253,12 +288,24 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
   const uint32_t rb = (uint32_t)(a.H * sizeof(RT)), yb = (uint32_t)(a.H * sizeof(YT));
   const uint32_t bytes[5] = {rb, rb, yb, yb, yb};
   const int64_t step = gridDim.x;
+  // piece n of this block's rows (P each) into a stage
+  auto fill_piece = [&](int stage, int n) {
+    const int64_t t = blockIdx.x + n / P * step;
+    const int half = nt * V, c0 = n % P ? half : 0, c1 = n % P ? a.H : half;
+    if (t < a.T)
+      ring_fill_piece(rs, ring, stage, src,
+                      {sizeof(RT), sizeof(RT), sizeof(YT), sizeof(YT), sizeof(YT)}, t, a.H, c0, c1,
+                      err);
+  };
   if (tid == 0) {
     for (int i = 0; i < ring.stages; ++i) mbar_init(rs.bars + i * 8);
     mbar_init_done();
     for (int i = 0; i < ring.stages; ++i) {
       const int64_t t = blockIdx.x + i * step;
-      if (t < a.T) ring_fill<V>(rs, ring, ring_smem, i, src, bytes, t, 1, a.T, err);
+      if (P > 1)
+        fill_piece(i, i);
+      else if (t < a.T)
+        ring_fill<V>(rs, ring, ring_smem, i, src, bytes, t, 1, a.T, err);
     }
   }
   __syncthreads();
@@ -278,14 +325,15 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
     if (gtok) next_gt = __ldg(static_cast<const float*>(a.gate) + t);
   };
   if (blockIdx.x < a.T) scalars(blockIdx.x);
-  int buf = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += step, buf ^= 1) {
+  int buf = 0, piece = 0;  // piece: this row's first
+  for (int64_t t = blockIdx.x; t < a.T; t += step, buf ^= 1, piece += P) {
     const float rho = next_rho, rho_y = next_rho_y;
     float gt[1] = {next_gt}, gt1[1] = {1.0f};
     if (t + step < a.T) scalars(t + step);
     if (gtok) gate_values<1>(a, gt, gt1);
     rs.wait(err);
     const uint8_t* st = ring_smem + kRingHeader + rs.stage * ring.stage_bytes;
+    const int stage0 = rs.stage;
     const uint32_t r_off = V == 1 ? (uint32_t)(t * rb) & 15u : 0u;
     const uint32_t y_off = V == 1 ? (uint32_t)(t * yb) & 15u : 0u;
     float d[U][V], h[U][V], y[U][V], g[U][V];
@@ -295,13 +343,19 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
       const int c = (i * nt + tid) * V;
 #pragma unroll
       for (int q = 0; q < V; ++q) d[i][q] = h[i][q] = y[i][q] = 0.0f, g[i][q] = 1.0f;
+      if (P > 1 && i > 0) {
+        rs.next(ring.stages);
+        rs.wait(err);
+        st = ring_smem + kRingHeader + rs.stage * ring.stage_bytes;
+      }
+      const int at_c = P > 1 ? tid * V : c;  // a piece's channels lie at its stage's start
       if (c >= a.H) continue;
       if (a.grad_h)
-        stage_elems<V>(st + ring.at[0] + r_off, c, static_cast<const RT*>(nullptr), d[i]);
+        stage_elems<V>(st + ring.at[0] + r_off, at_c, static_cast<const RT*>(nullptr), d[i]);
       if (pre) {
         float gn[V];
-        stage_elems<V>(st + ring.at[1] + r_off, c, static_cast<const RT*>(nullptr), h[i]);
-        stage_elems<V>(st + ring.at[2] + y_off, c, static_cast<const YT*>(nullptr), gn);
+        stage_elems<V>(st + ring.at[1] + r_off, at_c, static_cast<const RT*>(nullptr), h[i]);
+        stage_elems<V>(st + ring.at[2] + y_off, at_c, static_cast<const YT*>(nullptr), gn);
 #pragma unroll
         for (int q = 0; q < V; ++q) {
           const float v = gn[q] * pw[i][q];
@@ -311,8 +365,8 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
         }
       }
       if (has_y) {
-        stage_elems<V>(st + ring.at[3] + y_off, c, static_cast<const YT*>(nullptr), y[i]);
-        if (GEL) stage_elems<V>(st + ring.at[4] + y_off, c, static_cast<const YT*>(nullptr), g[i]);
+        stage_elems<V>(st + ring.at[3] + y_off, at_c, static_cast<const YT*>(nullptr), y[i]);
+        if (GEL) stage_elems<V>(st + ring.at[4] + y_off, at_c, static_cast<const YT*>(nullptr), g[i]);
         float gv[V];
 #pragma unroll
         for (int q = 0; q < V; ++q) gv[q] = g[i][q];
@@ -328,7 +382,12 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
     row_sum<3>(sums, red + buf * 96, wpr, 0);
     // every thread holds its part of the row: the stage is free
     if (wpr == 1) __syncwarp();
-    if (tid == 0 && rs.ok && t + ring.stages * step < a.T)
+    if (P > 1) {
+      if (tid == 0 && rs.ok) {
+#pragma unroll 1
+        for (int i = 0; i < P; ++i) fill_piece(i ? rs.stage : stage0, piece + i + ring.stages);
+      }
+    } else if (tid == 0 && rs.ok && t + ring.stages * step < a.T)
       ring_fill<V>(rs, ring, ring_smem, rs.stage, src, bytes, t + ring.stages * step, 1, a.T,
                    err);
     rs.next(ring.stages);
@@ -373,8 +432,7 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
     if (post || a.gate_kind == MOE_GATE_CHANNEL) store_elems<V>(p, s_post[i]);
     if (pre) store_elems<V>(p + plane, s_pre[i]);
   }
-  if (!rs.ok && tid == 0)
-    for (int i = 0; i < ring.stages; ++i) (void)mbar_wait(rs.bars + i * 8, rs.parity);
+  rs.drain(ring.stages);
 }
 
 cudaError_t launch_partials(const LaunchCtx& c, const NormArgs& a, int blocks) {
@@ -427,16 +485,19 @@ cudaError_t bwd_t(const LaunchCtx& c, const NormArgs& a) {
 }
 
 // The backward through the ring; false if it does not fit.
-template <class RT, class YT, bool GEL, int V, int U, int NT>
+template <class RT, class YT, bool GEL, int V, int U, int NT, int P = 1>
 bool bwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
   const bool pre = a.pre_w != nullptr;
   const uint32_t rb = (uint32_t)(a.H * sizeof(RT)), yb = (uint32_t)(a.H * sizeof(YT));
   const uint32_t bytes[5] = {a.grad_h ? rb : 0u, pre ? rb : 0u, pre ? yb : 0u, a.y ? yb : 0u,
                              GEL ? yb : 0u};
-  const RingShape s = ring_shape<V, U, NT>(a.H, 1, bytes);
+  uint32_t part[5];  // of a stage: the first piece is the largest
+  const int first = P > 1 ? (a.H + 32 * V * U - 1) / (32 * V * U) * 32 * V : a.H;
+  for (int i = 0; i < 5; ++i) part[i] = bytes[i] / a.H * first;
+  const RingShape s = ring_shape<V, U, NT>(a.H, 1, part, P + 1);
   if (!s.ring.stages) return false;
   int blocks = 0;
-  *e = ring_launch<norm_backward_ring_kernel<RT, YT, GEL, V, U, NT>>(
+  *e = ring_launch<norm_backward_ring_kernel<RT, YT, GEL, V, U, NT, P>>(
       c, a, s, norm_partial_blocks(a.T, a.H), &blocks);
   if (*e == cudaSuccess) *e = launch_partials(c, a, blocks);
   return true;
@@ -445,9 +506,13 @@ template <class RT, class YT, bool GEL>
 bool bwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e) {
   // one or two units of 8 channels per thread, us at 16384 tokens: H = 64: 15.3 :
   // 17.2, 256: 18.0 : 19.6, 512: 32.9 : 32.9, 1024: 55.8 : 58.2, 2048: 95 : 107
-  if (vec == 8)
-    return a.H <= 2048 ? bwd_ring<RT, YT, GEL, 8, 1, 0>(c, a, e)
-                       : bwd_ring<RT, YT, GEL, 8, 2, 0>(c, a, e);
+  if (vec == 8) {
+    if (a.H <= 2048) return bwd_ring<RT, YT, GEL, 8, 1, 0>(c, a, e);
+    if (bwd_ring<RT, YT, GEL, 8, 2, 0>(c, a, e)) return true;
+    // (two rows of bf16 fit at any width)
+    if constexpr (sizeof(RT) + sizeof(YT) > 4) return bwd_ring<RT, YT, GEL, 8, 2, 0, 2>(c, a, e);
+    return false;
+  }
   // the smallest block that holds the row; the next larger one, us at 8192 tokens:
   // H = 250: 32 : 48, 1001: 47 : 58, 2047: 72 : 107
   if (a.H <= 256) return bwd_ring<RT, YT, GEL, 1, 4, 64>(c, a, e);
