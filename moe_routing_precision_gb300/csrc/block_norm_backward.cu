@@ -11,8 +11,9 @@
 // element, so this cancels no more than d does.)
 //
 // Measured: 8192 tokens, H = 7168, f32 stream, bf16 block, gate per channel (1.06
-// GB): 172 us, 6.1 TB/s, 91 % of a plain copy (two rows of 86 KB in flight per
-// SM); 321 us with one block per row and no ring.
+// GB): 161 us, 6.5 TB/s, 97 % of a plain copy (two rows of 86 KB in flight per
+// SM); 321 us with one block per row and no ring.  What bounds the other types is the
+// chain of a row (its sums) and the instructions: all bf16 125 us, 83 %.
 #include "block/block_norm.cuh"
 
 #include <cooperative_groups.h>
@@ -266,11 +267,13 @@ __device__ __forceinline__ void ring_fill_piece(const RingState& r, const Ring& 
       bulk_load(dst + ring.at[i], static_cast<const uint8_t*>(src[i]) + from[i], bytes[i], bar);
 }
 
+// ALL: rows that fill the threads, with every input: no conditions between the
+// loads (H = 7168, 8192 tokens, bf16: 137 us; 147 with them).
 // P: stages per row.  Two (U = 2, V = 8, one unit of every thread each) where two
-// whole rows do not fit: H = 7168, all f32, element gate, 4096 tokens 173 us; 251
+// whole rows do not fit: H = 7168, all f32, element gate, 4096 tokens 162 us; 251
 // without the ring.  Whole rows where they fit (half rows take two turns of the
 // copying thread: bf16, 8192 tokens 148 : 177 us).
-template <class RT, class YT, bool GEL, int V, int U, int NT, int P>
+template <class RT, class YT, bool GEL, int V, int U, int NT, int P, bool ALL>
 __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U, NT))
     norm_backward_ring_kernel(const NormArgs a, const Ring ring, unsigned* err) {
   pdl_enter();
@@ -280,13 +283,17 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
   RingState rs;
   rs.bars = sbase + kRingHeader - 64;
   rs.stages_at = sbase + kRingHeader;
-  const int tid = threadIdx.x, nt = NT ? NT : blockDim.x, wpr = nt >> 5;
-  const bool has_y = a.y != nullptr, post = a.post_w != nullptr, pre = a.pre_w != nullptr;
+  const int tid = threadIdx.x, nt = NT && V == 1 ? NT : blockDim.x, wpr = nt >> 5;
+  const bool has_y = ALL || a.y != nullptr, pre = ALL || a.pre_w != nullptr;
+  const bool post = a.post_w != nullptr, has_gh = ALL || a.grad_h != nullptr;
   const bool gtok = a.gate_kind == MOE_GATE_TOKEN;
   const void* const src[5] = {a.grad_h, pre ? a.h : nullptr, pre ? a.grad_n : nullptr, a.y,
                               GEL ? a.gate : nullptr};
   const uint32_t rb = (uint32_t)(a.H * sizeof(RT)), yb = (uint32_t)(a.H * sizeof(YT));
   const uint32_t bytes[5] = {rb, rb, yb, yb, yb};
+  // (with an element gate and two units the pairs of registers cost spills: 4096
+  // tokens, H = 7168, f32: 162 us, in pairs 170)
+  constexpr bool kPairs = !(GEL && U == 2);
   const int64_t step = gridDim.x;
   // piece n of this block's rows (P each) into a stage
   auto fill_piece = [&](int stage, int n) {
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
     const uint32_t r_off = V == 1 ? (uint32_t)(t * rb) & 15u : 0u;
     const uint32_t y_off = V == 1 ? (uint32_t)(t * yb) & 15u : 0u;
     float d[U][V], h[U][V], y[U][V], g[U][V];
-    float sums[3] = {0.0f, 0.0f, 0.0f};
+    float sum2[3][2] = {};
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int c = (i * nt + tid) * V;
@@ -349,36 +356,39 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
         st = ring_smem + kRingHeader + rs.stage * ring.stage_bytes;
       }
       const int at_c = P > 1 ? tid * V : c;  // a piece's channels lie at its stage's start
-      if (c >= a.H) continue;
-      if (a.grad_h)
+      if (!ALL && c >= a.H) continue;
+      if (has_gh)
         stage_elems<V>(st + ring.at[0] + r_off, at_c, static_cast<const RT*>(nullptr), d[i]);
       if (pre) {
         float gn[V];
         stage_elems<V>(st + ring.at[1] + r_off, at_c, static_cast<const RT*>(nullptr), h[i]);
         stage_elems<V>(st + ring.at[2] + y_off, at_c, static_cast<const YT*>(nullptr), gn);
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-          const float v = gn[q] * pw[i][q];
-          sums[0] = __fmaf_rn(v, h[i][q], sums[0]);
-          d[i][q] = __fmaf_rn(rho, v, d[i][q]);
-          s_pre[i][q] = __fmaf_rn(gn[q] * rho, h[i][q], s_pre[i][q]);
-        }
+        float v[V];
+        mul_v<kPairs>(v, gn, pw[i]);
+        dot_v<kPairs>(sum2[0], v, h[i]);
+        fma_v<kPairs>(d[i], rho, v);
+        mul_v<kPairs>(gn, rho, gn);
+        fma_v<kPairs>(s_pre[i], gn, h[i]);
       }
       if (has_y) {
         stage_elems<V>(st + ring.at[3] + y_off, at_c, static_cast<const YT*>(nullptr), y[i]);
         if (GEL) stage_elems<V>(st + ring.at[4] + y_off, at_c, static_cast<const YT*>(nullptr), g[i]);
-        float gv[V];
+        float cy[V];
+        mul_v<kPairs>(cy, wg[i], y[i]);
+        if (GEL) {
+          float gv[V];
 #pragma unroll
-        for (int q = 0; q < V; ++q) gv[q] = g[i][q];
-        if (GEL) gate_values<V>(a, gv);
-#pragma unroll
-        for (int q = 0; q < V; ++q) {
-          const float cy = (GEL ? wg[i][q] * gv[q] : wg[i][q]) * y[i][q];
-          sums[1] = __fmaf_rn(cy, d[i][q], sums[1]);
-          sums[2] = __fmaf_rn(cy, h[i][q], sums[2]);
+          for (int q = 0; q < V; ++q) gv[q] = g[i][q];
+          gate_values<V>(a, gv);
+          mul_v<kPairs>(cy, cy, gv);
         }
+        dot_v<kPairs>(sum2[1], cy, d[i]);
+        dot_v<kPairs>(sum2[2], cy, h[i]);
       }
     }
+    float sums[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) sums[i] = sum2[i][0] + sum2[i][1];
     row_sum<3>(sums, red + buf * 96, wpr, 0);
     // every thread holds its part of the row: the stage is free
     if (wpr == 1) __syncwarp();
@@ -399,25 +409,28 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
     const int64_t at = t * a.H + tid * V;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const bool in = (i * nt + tid) * V < a.H;
+      const bool in = ALL || (i * nt + tid) * V < a.H;
       const int64_t ci = at + i * nt * V;
-#pragma unroll
-      for (int q = 0; q < V; ++q) d[i][q] = __fmaf_rn(-h[i][q], m, d[i][q]);
+      fma_v<kPairs>(d[i], -m, h[i]);
       if (in) store_row<V>(static_cast<RT*>(a.grad_residual) + ci, d[i]);
       if (!has_y) continue;
-      float gg[V], gy[V], g1[V];
+      float gg[V], gy[V], g1[V], yn[V], b[V];
       if (GEL) gate_values<V>(a, g[i], g1);
-#pragma unroll
-      for (int q = 0; q < V; ++q) {
-        const float yn = y[i][q] * rho_y;
-        if (GEL) {
-          const float dg = a.scale * d[i][q] * wg[i][q] * yn;  // scale d z
-          gg[q] = dg * g1[q];
-        }
-        const float b = cs * (GEL ? g[i][q] * d[i][q] : d[i][q]);
-        s_post[i][q] = __fmaf_rn(b, yn, s_post[i][q]);
-        gy[q] = __fmaf_rn(rho_y * b, wg[i][q], -y[i][q] * my);
+      mul_v<kPairs>(yn, rho_y, y[i]);
+      if (GEL) {
+        mul_v<kPairs>(gg, d[i], wg[i]);
+        mul_v<kPairs>(gg, gg, yn);
+        mul_v<kPairs>(gg, a.scale, gg);  // scale d z
+        mul_v<kPairs>(gg, gg, g1);
+        mul_v<kPairs>(b, g[i], d[i]);
+        mul_v<kPairs>(b, cs, b);
+      } else {
+        mul_v<kPairs>(b, cs, d[i]);
       }
+      fma_v<kPairs>(s_post[i], b, yn);
+      mul_v<kPairs>(b, rho_y, b);
+      mul_v<kPairs>(gy, -my, y[i]);
+      fma_v<kPairs>(gy, b, wg[i]);
       if (!in) continue;
       store_row<V>(static_cast<YT*>(a.grad_y) + ci, gy);
       if (GEL) store_row<V>(static_cast<YT*>(a.grad_gate) + ci, gg);
@@ -484,42 +497,83 @@ cudaError_t bwd_t(const LaunchCtx& c, const NormArgs& a) {
   return launch_partials(c, a, (int)blocks);
 }
 
-// The backward through the ring; false if it does not fit.
-template <class RT, class YT, bool GEL, int V, int U, int NT, int P = 1>
-bool bwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
-  const bool pre = a.pre_w != nullptr;
+template <class RT, class YT, bool GEL>
+void bwd_bytes(const NormArgs& a, uint32_t (&bytes)[5]) {
   const uint32_t rb = (uint32_t)(a.H * sizeof(RT)), yb = (uint32_t)(a.H * sizeof(YT));
-  const uint32_t bytes[5] = {a.grad_h ? rb : 0u, pre ? rb : 0u, pre ? yb : 0u, a.y ? yb : 0u,
-                             GEL ? yb : 0u};
-  uint32_t part[5];  // of a stage: the first piece is the largest
+  const uint32_t b[5] = {a.grad_h ? rb : 0u, a.pre_w ? rb : 0u, a.pre_w ? yb : 0u,
+                         a.y ? yb : 0u, GEL ? yb : 0u};
+  for (int i = 0; i < 5; ++i) bytes[i] = b[i];
+}
+
+// The backward through the ring; false if it does not fit.
+template <class RT, class YT, bool GEL, int V, int U, int NT, int P, bool ALL>
+bool bwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
+  uint32_t bytes[5];
+  bwd_bytes<RT, YT, GEL>(a, bytes);
+  // of a stage: the first piece is the largest
   const int first = P > 1 ? (a.H + 32 * V * U - 1) / (32 * V * U) * 32 * V : a.H;
-  for (int i = 0; i < 5; ++i) part[i] = bytes[i] / a.H * first;
-  const RingShape s = ring_shape<V, U, NT>(a.H, 1, part, P + 1);
+  for (int i = 0; i < 5; ++i) bytes[i] = bytes[i] / a.H * first;
+  const RingShape s = ring_shape<V, U, NT>(a.H, 1, bytes, P + 1);
   if (!s.ring.stages) return false;
   int blocks = 0;
-  *e = ring_launch<norm_backward_ring_kernel<RT, YT, GEL, V, U, NT, P>>(
+  *e = ring_launch<norm_backward_ring_kernel<RT, YT, GEL, V, U, NT, P, ALL>>(
       c, a, s, norm_partial_blocks(a.T, a.H), &blocks);
   if (*e == cudaSuccess) *e = launch_partials(c, a, blocks);
   return true;
 }
+
+// Units of 8 channels per thread and threads, us, f32 stream and bf16 block / all
+// bf16 / the former with an element gate, at 8192 tokens (the last: 4096):
+//   H = 256 (32768 tokens), 1024, 2048: one unit by a tenth over two
+//   H = 2304: one 63 / 56 / 40, two 58 / 48 / 47     3584: 85 / 68 / 55, 90 / 61 / 64
+//   4096: 95 / 74 / 62, 105 / 68 / 83                5120: 117 / 86 / 83, 128 / 108 / 100
+//   6144: 147 / 116 / 96, 141 / 114 / 113            7168: 161 / 126 / 113, 166 / 130 / 123
+// So one unit, except up to 4096 where an SM holds six rows that way, and around 6144 (768 threads of 80 registers) without an
+// element gate.  Only rows that fill the threads have the forms of one unit above
+// 2048.
+template <class RT, class YT, bool GEL>
+bool bwd_ring_8(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
+  const bool all = a.y && a.pre_w && a.grad_h;
+  const bool all1 = all && a.H % 256 == 0, all2 = all && a.H % 512 == 0;
+  if (a.H <= 2048)
+    return all1 ? bwd_ring<RT, YT, GEL, 8, 1, 0, 1, true>(c, a, e)
+                : bwd_ring<RT, YT, GEL, 8, 1, 0, 1, false>(c, a, e);
+  if (all1) {
+    if (a.H <= 4096) {
+      uint32_t bytes[5];
+      bwd_bytes<RT, YT, GEL>(a, bytes);
+      const RingShape two = ring_shape<8, 2, 0>(a.H, 1, bytes);
+      if ((GEL || two.per_sm * two.ring.stages < 6) &&
+          bwd_ring<RT, YT, GEL, 8, 1, 512, 1, true>(c, a, e))
+        return true;
+    } else if (a.H <= 5120) {
+      if (bwd_ring<RT, YT, GEL, 8, 1, 640, 1, true>(c, a, e)) return true;
+    } else if (a.H <= 6144) {
+      if constexpr (GEL)
+        if (bwd_ring<RT, YT, GEL, 8, 1, 768, 1, true>(c, a, e)) return true;
+    } else if (a.H <= 7168) {
+      if (bwd_ring<RT, YT, GEL, 8, 1, 896, 1, true>(c, a, e)) return true;
+    }
+  }
+  if (all2 ? bwd_ring<RT, YT, GEL, 8, 2, 0, 1, true>(c, a, e)
+           : bwd_ring<RT, YT, GEL, 8, 2, 0, 1, false>(c, a, e))
+    return true;
+  // (two rows of bf16 fit at any width)
+  if constexpr (sizeof(RT) + sizeof(YT) > 4)
+    return all2 ? bwd_ring<RT, YT, GEL, 8, 2, 0, 2, true>(c, a, e)
+                : bwd_ring<RT, YT, GEL, 8, 2, 0, 2, false>(c, a, e);
+  return false;
+}
 template <class RT, class YT, bool GEL>
 bool bwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e) {
-  // one or two units of 8 channels per thread, us at 16384 tokens: H = 64: 15.3 :
-  // 17.2, 256: 18.0 : 19.6, 512: 32.9 : 32.9, 1024: 55.8 : 58.2, 2048: 95 : 107
-  if (vec == 8) {
-    if (a.H <= 2048) return bwd_ring<RT, YT, GEL, 8, 1, 0>(c, a, e);
-    if (bwd_ring<RT, YT, GEL, 8, 2, 0>(c, a, e)) return true;
-    // (two rows of bf16 fit at any width)
-    if constexpr (sizeof(RT) + sizeof(YT) > 4) return bwd_ring<RT, YT, GEL, 8, 2, 0, 2>(c, a, e);
-    return false;
-  }
+  if (vec == 8) return bwd_ring_8<RT, YT, GEL>(c, a, e);
   // the smallest block that holds the row; the next larger one, us at 8192 tokens:
   // H = 250: 32 : 48, 1001: 47 : 58, 2047: 72 : 107
-  if (a.H <= 256) return bwd_ring<RT, YT, GEL, 1, 4, 64>(c, a, e);
-  if (a.H <= 1024) return bwd_ring<RT, YT, GEL, 1, 8, 128>(c, a, e);
-  if (a.H <= 2048) return bwd_ring<RT, YT, GEL, 1, 8, 256>(c, a, e);
-  if (a.H <= 4096) return bwd_ring<RT, YT, GEL, 1, 8, 512>(c, a, e);
-  return bwd_ring<RT, YT, GEL, 1, 16, 512>(c, a, e);
+  if (a.H <= 256) return bwd_ring<RT, YT, GEL, 1, 4, 64, 1, false>(c, a, e);
+  if (a.H <= 1024) return bwd_ring<RT, YT, GEL, 1, 8, 128, 1, false>(c, a, e);
+  if (a.H <= 2048) return bwd_ring<RT, YT, GEL, 1, 8, 256, 1, false>(c, a, e);
+  if (a.H <= 4096) return bwd_ring<RT, YT, GEL, 1, 8, 512, 1, false>(c, a, e);
+  return bwd_ring<RT, YT, GEL, 1, 16, 512, 1, false>(c, a, e);
 }
 
 template <class RT, class YT>

@@ -154,6 +154,18 @@ def test_norm_in_place_streams_and_unaligned_views(H):
     run_check_backward(v, "sigmoid", 4)
 
 
+@pytest.mark.parametrize("H", [256, 2048, 2304, 3584, 4096, 4608, 5120, 5632, 6144, 6656, 7168,
+                               7680, 8192, 2312, 5128, 7176])
+@pytest.mark.parametrize("gate", ["none", "element"])
+def test_norm_backward_wide_rows_several_per_block(H, gate):
+    for T, sd, bd in ((700, BF, BF), (467, F32, F32), (3, F32, BF), (463, BF, F32)):
+        s = norm_inputs(T, H, sd, bd, gate, H)
+        run_check_backward(s, "sigmoid" if gate != "none" else "none", T)
+    run_check_backward(s, "none", T, gh_none=True)
+    run_check_backward(norm_inputs(470, H, F32, BF, gate, H, pre=False), "none", 5)
+    run_check_backward(norm_inputs(470, H, F32, BF, gate, H, post=False), "none", 6)
+
+
 def test_norm_zero_rows_and_extremes():
     s = norm_inputs(6, 264, BF, BF, "none", 1)
     s["y"][0] = 0
