@@ -156,8 +156,9 @@ __global__ void __launch_bounds__(MAXT) block_norm_kernel(const NormArgs a, int 
 }
 
 // Forward: R consecutive rows per turn of a block, whose sums are reduced
-// together.
-template <class RT, class YT, bool GEL, int R, int V, int U, int NT>
+// together.  ALL: rows that fill the threads, with y and the pre-norm: no
+// conditions between the loads.
+template <class RT, class YT, bool GEL, int R, int V, int U, int NT, bool ALL>
 __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U, NT))
     norm_ring_kernel(const NormArgs a, const Ring ring, unsigned* err) {
   pdl_enter();
@@ -167,12 +168,15 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
   RingState rs;
   rs.bars = sbase + kRingHeader - 64;
   rs.stages_at = sbase + kRingHeader;
-  const int tid = threadIdx.x, nt = NT ? NT : blockDim.x, wpr = nt >> 5;
-  const bool has_y = a.y != nullptr, post = a.post_w != nullptr, pre = a.pre_w != nullptr;
+  const int tid = threadIdx.x, nt = NT && V == 1 ? NT : blockDim.x, wpr = nt >> 5;
+  const bool has_y = ALL || a.y != nullptr, pre = ALL || a.pre_w != nullptr;
+  const bool post = a.post_w != nullptr;
   const bool gtok = a.gate_kind == MOE_GATE_TOKEN;
   const void* const src[5] = {a.residual, a.y, GEL ? a.gate : nullptr, nullptr, nullptr};
   const uint32_t rb = (uint32_t)(a.H * sizeof(RT)), yb = (uint32_t)(a.H * sizeof(YT));
   const uint32_t bytes[5] = {rb, yb, yb, 0u, 0u};
+  // (pairs of registers do not pay at 72 of them: H = 7168 139.5 us, in pairs 142)
+  constexpr bool kPairs = ALL && NT < 896;
   const int64_t step = (int64_t)gridDim.x * R, first = (int64_t)blockIdx.x * R;
   auto fill = [&](int stage, int64_t t) {
     ring_fill<V>(rs, ring, ring_smem, stage, src, bytes, t, a.T - t < R ? (int)(a.T - t) : R, a.T,
@@ -210,34 +214,33 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
     const uint32_t y_off = V == 1 ? (uint32_t)(t * yb) & 15u : 0u;
     // (the second row of a last single one is what the stage held before: its
     // sums are its own and nothing of it is stored)
-    float h[R][U][V], z[R][U][V], ss[R];
+    float h[R][U][V], z[R][U][V], ss2[R][2] = {}, ss[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const uint8_t* r_row = st + ring.at[0] + r_off + r * rb;
       const uint8_t* y_row = st + ring.at[1] + y_off + r * yb;
       const uint8_t* g_row = st + ring.at[2] + y_off + r * yb;
-      ss[r] = 0.0f;
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int c = (i * nt + tid) * V;
 #pragma unroll
         for (int q = 0; q < V; ++q) h[r][i][q] = z[r][i][q] = 0.0f;
-        if (c >= a.H) continue;
+        if (!ALL && c >= a.H) continue;
         if (has_y) {
           stage_elems<V>(y_row, c, static_cast<const YT*>(nullptr), z[r][i]);
-#pragma unroll
-          for (int q = 0; q < V; ++q) ss[r] = __fmaf_rn(z[r][i][q], z[r][i][q], ss[r]);
+          dot_v<kPairs>(ss2[r], z[r][i], z[r][i]);
           if (GEL) {
             float g[V];
             stage_elems<V>(g_row, c, static_cast<const YT*>(nullptr), g);
             gate_values<V>(a, g);
-#pragma unroll
-            for (int q = 0; q < V; ++q) z[r][i][q] *= g[q];
+            mul_v<kPairs>(z[r][i], g, z[r][i]);
           }
         }
         stage_elems<V>(r_row, c, static_cast<const RT*>(nullptr), h[r][i]);
       }
     }
+#pragma unroll
+    for (int r = 0; r < R; ++r) ss[r] = ss2[r][0] + ss2[r][1];
     row_sum<R>(ss, red + buf * 32 * R, wpr, 0);
     // every thread holds its part of the rows: the stage is free
     if (wpr == 1) __syncwarp();
@@ -255,21 +258,19 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
         RT* out = static_cast<RT*>(a.h) + (t + r) * a.H + tid * V;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-#pragma unroll
-          for (int q = 0; q < V; ++q)
-            h[r][i][q] = __fmaf_rn(f * wg[i][q], z[r][i][q], h[r][i][q]);
-          if ((i * nt + tid) * V < a.H && t + r < a.T) store_row<V>(out + i * nt * V, h[r][i]);
+          mul_v<kPairs>(z[r][i], f, z[r][i]);
+          fma_v<kPairs>(h[r][i], wg[i], z[r][i]);
+          if ((ALL || (i * nt + tid) * V < a.H) && t + r < a.T) store_row<V>(out + i * nt * V, h[r][i]);
         }
       }
     }
     if (pre) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        ss[r] = 0.0f;
+        ss2[r][0] = ss2[r][1] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-          for (int q = 0; q < V; ++q) ss[r] = __fmaf_rn(h[r][i][q], h[r][i][q], ss[r]);
+        for (int i = 0; i < U; ++i) dot_v<kPairs>(ss2[r], h[r][i], h[r][i]);
+        ss[r] = ss2[r][0] + ss2[r][1];
       }
       row_sum<R>(ss, red + (2 + buf) * 32 * R, wpr, 0);
 #pragma unroll
@@ -280,9 +281,9 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
         YT* out = static_cast<YT*>(a.n) + (t + r) * a.H + tid * V;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-#pragma unroll
-          for (int q = 0; q < V; ++q) h[r][i][q] *= rho * pw[i][q];
-          if ((i * nt + tid) * V < a.H) store_row<V>(out + i * nt * V, h[r][i]);
+          mul_v<kPairs>(h[r][i], rho, h[r][i]);
+          mul_v<kPairs>(h[r][i], pw[i], h[r][i]);
+          if (ALL || (i * nt + tid) * V < a.H) store_row<V>(out + i * nt * V, h[r][i]);
         }
       }
     }
@@ -309,20 +310,23 @@ cudaError_t fwd_t(const LaunchCtx& c, const NormArgs& a) {
 constexpr int64_t kFwdRingElems = (int64_t)1 << 21, kFwdRingOddElems = (int64_t)1 << 19;
 
 // The forward through the ring; false if it does not fit.
-template <class RT, class YT, bool GEL, int V, int U, int NT>
+template <class RT, class YT, bool GEL, int V, int U, int NT, bool ALL>
 bool fwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
   const uint32_t rb = (uint32_t)(a.H * sizeof(RT)), yb = (uint32_t)(a.H * sizeof(YT));
   const uint32_t bytes[5] = {rb, a.y ? yb : 0u, GEL ? yb : 0u, 0u, 0u};
   int blocks = 0;
   const RingShape two = ring_shape<V, U, NT>(a.H, 2, bytes);
   if (two.ring.stages) {
-    *e = ring_launch<norm_ring_kernel<RT, YT, GEL, 2, V, U, NT>>(c, a, two, (a.T + 1) / 2, &blocks);
+    *e = ring_launch<norm_ring_kernel<RT, YT, GEL, 2, V, U, NT, ALL>>(c, a, two, (a.T + 1) / 2,
+                                                                      &blocks);
     return true;
   }
-  if constexpr (V * U == 16) {
+  // the widest rows of this form, where two stages of two rows may not fit
+  constexpr int kWidest = NT ? NT * 8 : U == 1 ? 256 : ALL ? 1024 : kRingMaxHidden;
+  if constexpr (V == 8 && 4 * kWidest * (sizeof(RT) + (GEL ? 2 : 1) * sizeof(YT)) > 220 * 1024) {
     const RingShape one = ring_shape<V, U, NT>(a.H, 1, bytes);
     if (one.ring.stages) {
-      *e = ring_launch<norm_ring_kernel<RT, YT, GEL, 1, V, U, NT>>(c, a, one, a.T, &blocks);
+      *e = ring_launch<norm_ring_kernel<RT, YT, GEL, 1, V, U, NT, ALL>>(c, a, one, a.T, &blocks);
       return true;
     }
   }
@@ -331,18 +335,35 @@ bool fwd_ring(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
 template <class RT, class YT, bool GEL>
 bool fwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e) {
   // one or two units of 8 channels per thread, us at 16384 tokens: H = 64: 7.3 :
-  // 8.3, 256: 7.3 : 8.4, 512: 13.3 : 10.3, 1024: 27.4 : 23.4, 2048: 49.4 : 46.8
-  if (vec == 8)
-    return a.H <= 256 ? fwd_ring<RT, YT, GEL, 8, 1, 0>(c, a, e)
-                      : fwd_ring<RT, YT, GEL, 8, 2, 0>(c, a, e);
+  // 8.3, 256: 7.3 : 8.4, 512: 13.3 : 10.3, 1024: 27.4 : 23.4, 2048: 49.4 : 46.8.  From
+  // 4096 on one unit and one block per SM (bf16, then with an element gate): 4096: 86
+  // : 95, 116 : 105; 5120: 102 : 118, 136 : 167; 6144: 120 : 121, 159 : 169; 7168: 140 :
+  // 143, 183 : 199; 8192: 160 : 180, 206 : 207; f32 rows alike within 2 %.  The form
+  // without conditions, two units: 512: 8.4 : 10.0, 1024: 22.3 : 23.0, element gate
+  // 2048: 59 : 54, 6144: 136 : 122, so it is taken up to 1024.
+  if (vec == 8) {
+    const bool all = a.y && a.pre_w;
+    if (a.H <= 256)
+      return all && a.H == 256 ? fwd_ring<RT, YT, GEL, 8, 1, 0, true>(c, a, e)
+                               : fwd_ring<RT, YT, GEL, 8, 1, 0, false>(c, a, e);
+    if (all && a.H % 256 == 0 && a.H > (GEL ? 4096 : 4095)) {
+      if (a.H <= 4096) return fwd_ring<RT, YT, GEL, 8, 1, 512, true>(c, a, e);
+      if (a.H <= 5120) return fwd_ring<RT, YT, GEL, 8, 1, 640, true>(c, a, e);
+      if (a.H <= 6144) return fwd_ring<RT, YT, GEL, 8, 1, 768, true>(c, a, e);
+      if (a.H <= 7168) return fwd_ring<RT, YT, GEL, 8, 1, 896, true>(c, a, e);
+      return fwd_ring<RT, YT, GEL, 8, 1, 1024, true>(c, a, e);
+    }
+    return all && (a.H == 512 || a.H == 1024) ? fwd_ring<RT, YT, GEL, 8, 2, 0, true>(c, a, e)
+                                              : fwd_ring<RT, YT, GEL, 8, 2, 0, false>(c, a, e);
+  }
   // the smallest block that holds the row; the next larger one, us at 8192 tokens:
   // H = 250: 8.5 : 31, 1001: 16 : 32, 2047: 36 : 61 (a block's threads past the
   // row are idle, and fewer blocks fit an SM)
-  if (a.H <= 256) return fwd_ring<RT, YT, GEL, 1, 4, 64>(c, a, e);
-  if (a.H <= 1024) return fwd_ring<RT, YT, GEL, 1, 8, 128>(c, a, e);
-  if (a.H <= 2048) return fwd_ring<RT, YT, GEL, 1, 8, 256>(c, a, e);
-  if (a.H <= 4096) return fwd_ring<RT, YT, GEL, 1, 8, 512>(c, a, e);
-  return fwd_ring<RT, YT, GEL, 1, 16, 512>(c, a, e);
+  if (a.H <= 256) return fwd_ring<RT, YT, GEL, 1, 4, 64, false>(c, a, e);
+  if (a.H <= 1024) return fwd_ring<RT, YT, GEL, 1, 8, 128, false>(c, a, e);
+  if (a.H <= 2048) return fwd_ring<RT, YT, GEL, 1, 8, 256, false>(c, a, e);
+  if (a.H <= 4096) return fwd_ring<RT, YT, GEL, 1, 8, 512, false>(c, a, e);
+  return fwd_ring<RT, YT, GEL, 1, 16, 512, false>(c, a, e);
 }
 
 template <class RT, class YT>

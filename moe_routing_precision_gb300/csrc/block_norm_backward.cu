@@ -558,8 +558,8 @@ bool bwd_ring_8(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
   if (all2 ? bwd_ring<RT, YT, GEL, 8, 2, 0, 1, true>(c, a, e)
            : bwd_ring<RT, YT, GEL, 8, 2, 0, 1, false>(c, a, e))
     return true;
-  // (two rows of bf16 fit at any width)
-  if constexpr (sizeof(RT) + sizeof(YT) > 4)
+  // (two rows of the other types fit at any width)
+  if constexpr (sizeof(RT) + sizeof(YT) > (GEL ? 4 : 6))
     return all2 ? bwd_ring<RT, YT, GEL, 8, 2, 0, 2, true>(c, a, e)
                 : bwd_ring<RT, YT, GEL, 8, 2, 0, 2, false>(c, a, e);
   return false;

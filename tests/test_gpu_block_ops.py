@@ -166,6 +166,18 @@ def test_norm_backward_wide_rows_several_per_block(H, gate):
     run_check_backward(norm_inputs(470, H, F32, BF, gate, H, post=False), "none", 6)
 
 
+@pytest.mark.parametrize("H", [256, 512, 1024, 2560, 4096, 4608, 5120, 6144, 6656, 7168, 7680, 8192])
+@pytest.mark.parametrize("gate", ["token", "element"])
+def test_norm_wide_rows_several_per_block(H, gate):
+    T = (2 << 20) // H + 701                   # an odd last row for two rows per turn
+    T += 1 - T % 2
+    for sd, bd in ((BF, BF), (F32, BF), (F32, F32)):
+        s = norm_inputs(T, H, sd, bd, gate, H)
+        check_norm(s, "sigmoid", run_norm(s, "sigmoid"))
+    s = norm_inputs(T, H, BF, BF, gate, H, post=False)
+    check_norm(s, "none", run_norm(s, "none"))
+
+
 def test_norm_zero_rows_and_extremes():
     s = norm_inputs(6, 264, BF, BF, "none", 1)
     s["y"][0] = 0
