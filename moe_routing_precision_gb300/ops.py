@@ -6,6 +6,10 @@ C ABI with raw device pointers and the current CUDA stream.  All computation
 happens in the CUDA kernels of ``libmoe_route.so``; there is no fallback: if
 the library is missing or the tensors are not on a CUDA device, the call
 raises.
+
+``stream`` (a torch.cuda.Stream or a raw handle; None: the current one) is where
+a call's kernels run.  What the call allocates belongs to that stream; tensors
+that the caller passes are the caller's to order and to keep.
 """
 from __future__ import annotations
 
@@ -169,8 +173,31 @@ def _ptr(t):
     return None if t is None else (t.data_ptr() or None)
 
 
-def _empty(shape, dtype, like):
-    return torch.empty(shape, dtype=dtype, device=like.device)
+def _empty(shape, dtype, like, stream=None, alloc=None):
+    """A tensor for a call whose kernels run on `stream` (None: the current one).
+
+    On another stream than the current one it is allocated as that stream's own:
+    taken from the current stream's memory, its last user there might still be
+    running, and a workspace or an output that the caller drops would go back
+    to the current stream while the kernels are yet to write it.  The current
+    stream is recorded on it, for the work the caller gives it there."""
+    alloc = alloc or torch.empty
+    if stream is None:
+        return alloc(shape, dtype=dtype, device=like.device)
+    here = torch.cuda.current_stream()
+    handle = _stream(stream) or 0
+    if handle == here.cuda_stream:
+        return alloc(shape, dtype=dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = alloc(shape, dtype=dtype, device=like.device)
+    t.record_stream(here)
+    return t
+
+
+def _like(t, stream=None):
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t, stream)
 
 
 # --------------------------------------------------------------------------
@@ -182,11 +209,11 @@ def topk_gate(scores: torch.Tensor, k: int, weights: bool = True, *, out_idx=Non
     scores [T, E] float32 -> (idx [T, k] int32, w [T, k] float32 or None)."""
     _dev(scores, "scores", torch.float32)
     T, E = scores.shape
-    idx = out_idx if out_idx is not None else _empty((T, k), torch.int32, scores)
+    idx = out_idx if out_idx is not None else _empty((T, k), torch.int32, scores, stream)
     _dev(idx, "out_idx", torch.int32, (T, k))
     w = None
     if weights:
-        w = out_w if out_w is not None else _empty((T, k), torch.float32, scores)
+        w = out_w if out_w is not None else _empty((T, k), torch.float32, scores, stream)
         _dev(w, "out_w", torch.float32, (T, k))
     rc = lib().moe_topk_gate(_ptr(scores), T, E, k, _ptr(idx), _ptr(w),
                              MOE_WEIGHTS_SOFTMAX_TOPK if weights else MOE_WEIGHTS_NONE,
@@ -209,10 +236,10 @@ def route_map(topk_idx: torch.Tensor, num_experts: int, *, workspace=None, out=N
     T, k = topk_idx.shape
     E = int(num_experts)
     if out is None:
-        counts = _empty((E,), torch.int32, topk_idx)
-        offsets = _empty((E + 1,), torch.int32, topk_idx)
-        pos = _empty((T, k), torch.int32, topk_idx)
-        src = _empty((T * k,), torch.int32, topk_idx)
+        counts = _empty((E,), torch.int32, topk_idx, stream)
+        offsets = _empty((E + 1,), torch.int32, topk_idx, stream)
+        pos = _empty((T, k), torch.int32, topk_idx, stream)
+        src = _empty((T * k,), torch.int32, topk_idx, stream)
     else:
         counts, offsets, pos, src = out
     _dev(counts, "counts", torch.int32, (E,))
@@ -221,7 +248,7 @@ def route_map(topk_idx: torch.Tensor, num_experts: int, *, workspace=None, out=N
     _dev(src, "sorted_src", torch.int32, (T * k,))
     need = route_map_workspace_bytes(T, E, k)
     if workspace is None:
-        workspace = _empty((max(need, 1),), torch.uint8, topk_idx)
+        workspace = _empty((max(need, 1),), torch.uint8, topk_idx, stream)
     _dev(workspace, "workspace", torch.uint8)
     rc = lib().moe_route_map(_ptr(topk_idx), T, E, k, _ptr(counts), _ptr(offsets), _ptr(pos),
                              _ptr(src), _ptr(workspace), workspace.numel(), _stream(stream))
@@ -239,13 +266,13 @@ def route_map_aligned(topk_idx: torch.Tensor, num_experts: int, align: int,
     T, k = topk_idx.shape
     E = int(num_experts)
     R = T * k + E * (align - 1) if num_rows is None else int(num_rows)
-    counts = _empty((E,), torch.int32, topk_idx)
-    offsets = _empty((E + 1,), torch.int32, topk_idx)
-    pos = _empty((T, k), torch.int32, topk_idx)
-    src = _empty((R,), torch.int32, topk_idx)
+    counts = _empty((E,), torch.int32, topk_idx, stream)
+    offsets = _empty((E + 1,), torch.int32, topk_idx, stream)
+    pos = _empty((T, k), torch.int32, topk_idx, stream)
+    src = _empty((R,), torch.int32, topk_idx, stream)
     need = route_map_workspace_bytes(T, E, k)
     if workspace is None:
-        workspace = _empty((max(need, 1),), torch.uint8, topk_idx)
+        workspace = _empty((max(need, 1),), torch.uint8, topk_idx, stream)
     _dev(workspace, "workspace", torch.uint8)
     rc = lib().moe_route_map_aligned(_ptr(topk_idx), T, E, k, int(align), R, _ptr(counts),
                                      _ptr(offsets), _ptr(pos), _ptr(src), _ptr(workspace),
@@ -264,8 +291,8 @@ def expand_cast_fp8_padded(x: torch.Tensor, pos: torch.Tensor, sorted_src: torch
     T, H = x.shape
     k = pos.shape[1]
     R = sorted_src.shape[0]
-    q = out if out is not None else _empty((R, H), torch.uint8, x)
-    sf = out_sf if out_sf is not None else _empty((R, H // GROUP), torch.float32, x)
+    q = out if out is not None else _empty((R, H), torch.uint8, x, stream)
+    sf = out_sf if out_sf is not None else _empty((R, H // GROUP), torch.float32, x, stream)
     _dev(q, "out", torch.uint8, (R, H))
     _dev(sf, "out_sf", torch.float32, (R, H // GROUP))
     rc = lib().moe_expand_cast_fp8_padded(_ptr(x), T, H, k, _ptr(pos), _ptr(sorted_src), R,
@@ -274,28 +301,29 @@ def expand_cast_fp8_padded(x: torch.Tensor, pos: torch.Tensor, sorted_src: torch
     return q, sf
 
 
-def sf_empty(rows: int, G: int, flags: int, ld: int | None, like: torch.Tensor):
+def sf_empty(rows: int, G: int, flags: int, ld: int | None, like: torch.Tensor, stream=None):
     """Scale buffer of the layout `flags` names: f32 [rows, G] or [G, ld];
     uint8 [rows, G]; or packed words as uint8 [ceil(G/4), ld, 4]."""
     ld = rows if ld is None else ld
     if flags & SF_UE8M0:
         if flags & SF_COLMAJOR:
-            return _empty(((G + 3) // 4, ld, 4), torch.uint8, like), ld
-        return _empty((rows, G), torch.uint8, like), ld
+            return _empty(((G + 3) // 4, ld, 4), torch.uint8, like, stream), ld
+        return _empty((rows, G), torch.uint8, like, stream), ld
     if flags & SF_COLMAJOR:
-        return _empty((G, ld), torch.float32, like), ld
-    return _empty((rows, G), torch.float32, like), ld
+        return _empty((G, ld), torch.float32, like, stream), ld
+    return _empty((rows, G), torch.float32, like, stream), ld
 
 
 PATH_AUTO, PATH_FUSED, PATH_SEPARATE, PATH_REPLICATED, PATH_CHAINED = 0, 1, 2, 3, 4
 DEBUG_WAIT_TIMEOUT_NS, DEBUG_SKIP_ROUTE_SIGNAL = 1, 2
 
 
-def route_expand_cast_workspace(T: int, E: int, k: int, like: torch.Tensor) -> torch.Tensor:
+def route_expand_cast_workspace(T: int, E: int, k: int, like: torch.Tensor,
+                                stream=None) -> torch.Tensor:
     """A zero-filled workspace for route_expand_cast_fp8 (its first 256 bytes
     are the fused path's control words, which must start at zero)."""
     n = int(lib().moe_route_expand_cast_fp8_workspace_bytes(T, E, k))
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=like.device)
+    return _empty((max(n, 256),), torch.uint8, like, stream, torch.zeros)
 
 
 def route_expand_cast_fp8(scores: torch.Tensor, x: torch.Tensor, k: int, *, mode: int = PATH_AUTO,
@@ -310,13 +338,15 @@ def route_expand_cast_fp8(scores: torch.Tensor, x: torch.Tensor, k: int, *, mode
     T, E = scores.shape
     H = x.shape[1]
     R = T * k
-    idx, w = _empty((T, k), torch.int32, x), _empty((T, k), torch.float32, x)
-    counts, offsets = _empty((E,), torch.int32, x), _empty((E + 1,), torch.int32, x)
-    pos, src = _empty((T, k), torch.int32, x), _empty((R,), torch.int32, x)
+    idx, w = _empty((T, k), torch.int32, x, stream), _empty((T, k), torch.float32, x, stream)
+    counts = _empty((E,), torch.int32, x, stream)
+    offsets = _empty((E + 1,), torch.int32, x, stream)
+    pos, src = _empty((T, k), torch.int32, x, stream), _empty((R,), torch.int32, x, stream)
     q, sf = (out if out is not None else
-             (_empty((R, H), torch.uint8, x), _empty((R, H // GROUP), torch.float32, x)))
+             (_empty((R, H), torch.uint8, x, stream),
+              _empty((R, H // GROUP), torch.float32, x, stream)))
     if workspace is None:
-        workspace = route_expand_cast_workspace(T, E, k, x)
+        workspace = route_expand_cast_workspace(T, E, k, x, stream)
     rc = lib().moe_route_expand_cast_fp8(_ptr(scores), T, E, k, _ptr(x), H, _ptr(idx), _ptr(w),
                                          _ptr(counts), _ptr(offsets), _ptr(pos), _ptr(src),
                                          _ptr(q), _ptr(sf), _ptr(workspace), workspace.numel(),
@@ -332,7 +362,7 @@ def debug_cvt(values: torch.Tensor, fmt: int, out=None, stream=None) -> torch.Te
     """The device's f32 -> E4M3 / E2M1 conversion of every value (one code
     per byte), as the cast kernels convert; for tests."""
     _dev(values, "values", torch.float32)
-    out = out if out is not None else _empty(values.shape, torch.uint8, values)
+    out = out if out is not None else _empty(values.shape, torch.uint8, values, stream)
     _check(lib().moe_debug_cvt(fmt, _ptr(values), _ptr(out), values.numel(), _stream(stream)),
            "moe_debug_cvt")
     return out
@@ -363,15 +393,15 @@ def expand_cast_fp8_ex(x: torch.Tensor, pos: torch.Tensor, num_rows: int | None 
     R = (T * k if sorted_src is None else sorted_src.shape[0]) if num_rows is None else int(num_rows)
     if sf_ld is None and (sf_flags & SF_COLMAJOR):
         sf_ld = (R + 3) // 4 * 4
-    q = out if out is not None else _empty((R, H), torch.uint8, x)
+    q = out if out is not None else _empty((R, H), torch.uint8, x, stream)
     _dev(q, "out", torch.uint8, (R, H))
     if out_sf is None:
-        out_sf, sf_ld = sf_empty(R, H // GROUP, sf_flags, sf_ld, x)
-    if out_sf.device.type != "cuda" or not out_sf.is_contiguous():
+        out_sf, sf_ld = sf_empty(R, H // GROUP, sf_flags, sf_ld, x, stream)
+    elif out_sf.device.type != "cuda" or not out_sf.is_contiguous():
         raise ValueError("out_sf must be a contiguous CUDA tensor")
     if workspace is True:
         n = expand_cast_fp8_ex_workspace_bytes(T, H, sf_flags)
-        workspace = _empty((n,), torch.uint8, x) if n > 0 else None
+        workspace = _empty((n,), torch.uint8, x, stream) if n > 0 else None
     ws_bytes = 0 if workspace is None else workspace.numel()
     rc = lib().moe_expand_cast_fp8_ex(_ptr(x), T, H, k, _ptr(pos), _ptr(sorted_src), R, _ptr(q),
                                       _ptr(out_sf), sf_flags, int(sf_ld or R), _ptr(workspace),
@@ -395,13 +425,13 @@ def expand_cast_fp4(x: torch.Tensor, pos: torch.Tensor, num_rows: int | None = N
     R = (T * k if sorted_src is None else sorted_src.shape[0]) if num_rows is None else int(num_rows)
     if sf_ld is None and (sf_flags & SF_COLMAJOR):
         sf_ld = (R + 3) // 4 * 4
-    q = out if out is not None else _empty((R, H // 2), torch.uint8, x)
+    q = out if out is not None else _empty((R, H // 2), torch.uint8, x, stream)
     _dev(q, "out", torch.uint8, (R, H // 2))
     if out_sf is None:
-        out_sf, sf_ld = sf_empty(R, H // group, sf_flags, sf_ld, x)
+        out_sf, sf_ld = sf_empty(R, H // group, sf_flags, sf_ld, x, stream)
     if workspace is True:
         n = int(lib().moe_expand_cast_fp4_workspace_bytes(T, H, group, sf_flags))
-        workspace = _empty((n,), torch.uint8, x) if n > 0 else None
+        workspace = _empty((n,), torch.uint8, x, stream) if n > 0 else None
     ws_bytes = 0 if workspace is None else workspace.numel()
     rc = lib().moe_expand_cast_fp4(_ptr(x), T, H, k, _ptr(pos), _ptr(sorted_src), R, _ptr(q),
                                    _ptr(out_sf), sf_flags, int(sf_ld or R), _ptr(workspace),
@@ -424,10 +454,10 @@ def swiglu_cast_fp4(x: torch.Tensor, *, group: int = 32, clamp: float | None = N
         _dev(clamp_count, "clamp_count", torch.int64, (1,))
     if sf_ld is None and (sf_flags & SF_COLMAJOR):
         sf_ld = (M + 3) // 4 * 4
-    q = out if out is not None else _empty((M, N // 2), torch.uint8, x)
+    q = out if out is not None else _empty((M, N // 2), torch.uint8, x, stream)
     _dev(q, "out", torch.uint8, (M, N // 2))
     if out_sf is None:
-        out_sf, sf_ld = sf_empty(M, N // group, sf_flags, sf_ld, x)
+        out_sf, sf_ld = sf_empty(M, N // group, sf_flags, sf_ld, x, stream)
     rc = lib().swiglu_cast_fp4(_ptr(x), M, N, _ptr(q), _ptr(out_sf), sf_flags, int(sf_ld or M),
                                int(clamp is not None), float(clamp or 0.0), _ptr(weights),
                                _ptr(clamp_count), group, _stream(stream))
@@ -449,10 +479,10 @@ def swiglu_cast_fp8_ex(x: torch.Tensor, *, clamp: float | None = None, weights=N
         _dev(clamp_count, "clamp_count", torch.int64, (1,))
     if sf_ld is None and (sf_flags & SF_COLMAJOR):
         sf_ld = (M + 3) // 4 * 4
-    q = out if out is not None else _empty((M, N), torch.uint8, x)
+    q = out if out is not None else _empty((M, N), torch.uint8, x, stream)
     _dev(q, "out", torch.uint8, (M, N))
     if out_sf is None:
-        out_sf, sf_ld = sf_empty(M, N // GROUP, sf_flags, sf_ld, x)
+        out_sf, sf_ld = sf_empty(M, N // GROUP, sf_flags, sf_ld, x, stream)
     rc = lib().swiglu_cast_fp8_ex(_ptr(x), M, N, _ptr(q), _ptr(out_sf), sf_flags, int(sf_ld or M),
                                   int(clamp is not None), float(clamp or 0.0), _ptr(weights),
                                   _ptr(clamp_count), GROUP, _stream(stream))
@@ -474,8 +504,8 @@ def expand_cast_fp8(x: torch.Tensor, pos: torch.Tensor, num_rows: int | None = N
     if pos.shape[0] != T:
         raise ValueError("pos must have one row per token")
     R = T * k if num_rows is None else int(num_rows)
-    q = out if out is not None else _empty((R, H), torch.uint8, x)
-    sf = out_sf if out_sf is not None else _empty((R, H // GROUP), torch.float32, x)
+    q = out if out is not None else _empty((R, H), torch.uint8, x, stream)
+    sf = out_sf if out_sf is not None else _empty((R, H // GROUP), torch.float32, x, stream)
     _dev(q, "out", torch.uint8, (R, H))
     _dev(sf, "out_sf", torch.float32, (R, H // GROUP))
     rc = lib().moe_expand_cast_fp8(_ptr(x), T, H, k, _ptr(pos), R, _ptr(q), _ptr(sf), GROUP,
@@ -491,8 +521,8 @@ def swiglu_cast_fp8(x: torch.Tensor, *, out=None, out_sf=None, stream=None):
     _dev(x, "x", torch.bfloat16)
     M, N2 = x.shape
     N = N2 // 2
-    q = out if out is not None else _empty((M, N), torch.uint8, x)
-    sf = out_sf if out_sf is not None else _empty((M, N // GROUP), torch.float32, x)
+    q = out if out is not None else _empty((M, N), torch.uint8, x, stream)
+    sf = out_sf if out_sf is not None else _empty((M, N // GROUP), torch.float32, x, stream)
     _dev(q, "out", torch.uint8, (M, N))
     _dev(sf, "out_sf", torch.float32, (M, N // GROUP))
     rc = lib().swiglu_cast_fp8(_ptr(x), M, N, _ptr(q), _ptr(sf), GROUP, _stream(stream))
@@ -513,7 +543,7 @@ def combine(y: torch.Tensor, topk_weights: torch.Tensor, pos: torch.Tensor,
     T, k = pos.shape
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be bfloat16 or float32")
-    o = out if out is not None else _empty((T, H), out_dtype, y)
+    o = out if out is not None else _empty((T, H), out_dtype, y, stream)
     _dev(o, "out", out_dtype, (T, H))
     rc = lib().moe_combine(_ptr(y), _ptr(topk_weights), _ptr(pos), T, H, k, R, _ptr(o),
                            MOE_OUT_F32 if out_dtype == torch.float32 else MOE_OUT_BF16,
@@ -602,21 +632,20 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
     if y is None:
         h = residual
     elif h is None:
-        h = torch.empty_like(residual)
+        h = _like(residual, stream)
     else:
         _dev(h, "out[0]", residual.dtype, (T, H))
     if pre_weight is None:
         n = None
     elif n is None:
-        n = torch.empty_like(y) if y is not None else _empty((T, H), block_dtype, residual)
+        n = _like(y, stream) if y is not None else _empty((T, H), block_dtype, residual, stream)
     else:
         _dev(n, "out[1]", block_dtype, (T, H))
-    dev = residual.device
     rp = rn = None
     if post_weight is not None:
-        rp = torch.empty((T,), dtype=torch.float32, device=dev)
+        rp = _empty((T,), torch.float32, residual, stream)
     if pre_weight is not None:
-        rn = torch.empty((T,), dtype=torch.float32, device=dev)
+        rn = _empty((T,), torch.float32, residual, stream)
     rc = lib().moe_block_norm(_ptr(residual), sd, _ptr(y),
                               DT_F32 if block_dtype == torch.float32 else DT_BF16, T, H,
                               _ptr(post_weight), _ptr(gate), kind,
@@ -663,14 +692,14 @@ def block_norm_backward(grad_h, grad_n, h: torch.Tensor, *, y=None, post_weight=
         _dev(pre_weight, "pre_weight", torch.float32, (H,))
         _dev(rstd_pre, "rstd_pre", torch.float32, (T,))
     kind = GATE_NONE if gate is None else _gate_kind(gate, T, H, block.dtype)
-    gr = torch.empty_like(h)
-    gy = None if y is None else torch.empty_like(y)
-    gpw = None if post_weight is None else torch.empty_like(post_weight)
-    gg = None if gate is None else torch.empty_like(gate)
-    gnw = None if pre_weight is None else torch.empty_like(pre_weight)
+    gr = _like(h, stream)
+    gy = None if y is None else _like(y, stream)
+    gpw = None if post_weight is None else _like(post_weight, stream)
+    gg = None if gate is None else _like(gate, stream)
+    gnw = None if pre_weight is None else _like(pre_weight, stream)
     ws_bytes = block_norm_backward_workspace_bytes(T, H)
     if workspace is None:
-        workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=h.device)
+        workspace = _empty((ws_bytes,), torch.uint8, h, stream)
     else:
         ws_bytes = _dev(workspace, "workspace", torch.uint8).numel()
     rc = lib().moe_block_norm_backward(
@@ -717,15 +746,14 @@ def balance_loss(scores: torch.Tensor, topk_idx: torch.Tensor, *, score_func: st
     k = topk_idx.shape[1]
     _dev(topk_idx, "topk_idx", torch.int32, (T, k))
     S = _sequences(seq_offsets, token_mask, T)
-    dev = scores.device
-    bal = torch.empty((S,), dtype=torch.float32, device=dev)
-    z = torch.empty_like(bal)
-    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-    probs = torch.empty((S, E), dtype=torch.float32, device=dev)
-    tokens = torch.empty((S,), dtype=torch.int32, device=dev)
+    bal = _empty((S,), torch.float32, scores, stream)
+    z = _empty((S,), torch.float32, scores, stream)
+    counts = _empty((S, E), torch.int32, scores, stream)
+    probs = _empty((S, E), torch.float32, scores, stream)
+    tokens = _empty((S,), torch.int32, scores, stream)
     ws_bytes = balance_loss_workspace_bytes(T, E, S)
     if workspace is None and ws_bytes:
-        workspace = _empty((ws_bytes,), torch.uint8, scores)
+        workspace = _empty((ws_bytes,), torch.uint8, scores, stream)
     if workspace is not None:
         ws_bytes = _dev(workspace, "workspace", torch.uint8).numel()
     rc = lib().moe_balance_loss(_ptr(scores), _ptr(topk_idx), T, E, k,
@@ -768,7 +796,7 @@ def balance_loss_backward(scores: torch.Tensor, counts: torch.Tensor, tokens: to
             raise ValueError("grad_topk_weights needs topk_idx and topk_weights")
         _dev(topk_weights, "topk_weights", torch.float32, (T, k))
         _dev(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k))
-    g = out if out is not None else torch.empty_like(scores)
+    g = out if out is not None else _like(scores, stream)
     _dev(g, "out", torch.float32, (T, E))
     rc = lib().moe_balance_loss_backward(
         _ptr(scores), T, E, k, _choice(score_func, _SCORE_FUNC, "score_func"), _ptr(seq_offsets),
@@ -797,7 +825,7 @@ def combine_backward(grad_out: torch.Tensor, y: torch.Tensor, topk_weights: torc
     if sorted_src is not None:
         _dev(sorted_src, "sorted_src", torch.int32, (R,))
     if out is None:
-        gy, gw = torch.empty_like(y), torch.empty_like(topk_weights)
+        gy, gw = _like(y, stream), _like(topk_weights, stream)
     else:
         gy, gw = out
         _dev(gy, "out[0]", torch.bfloat16, (R, H))
@@ -846,7 +874,7 @@ def expert_matvec_fp4(x: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, offs
         R = x.shape[0]
     N = M // 2 if swiglu else M
     if out is None:
-        o = torch.empty((R, N), dtype=out_dtype, device=x.device)
+        o = _empty((R, N), out_dtype, x, stream)
     else:
         o = _dev(out, "out", out_dtype, (R, N))
     rc = lib().moe_expert_matvec_fp4(_ptr(x), x.shape[0], _ptr(w), _ptr(w_sf),
