@@ -523,7 +523,8 @@ typedef enum moe_dtype {
  *   rstd_pre[t] = 1 / sqrt(mean_c h[t,c]^2 + eps)
  *   n[t,c] = h[t,c] * rstd_pre[t] * pre_weight[c]       (pre_weight NULL: no n)
  * h is rounded to the stream's type when stored, and n is computed from h
- * before that rounding; every sum and product is f32.
+ * before that rounding; every sum and product is f32.  A row whose squares sum
+ * beyond f32's range (elements near 2^64) has the inverse norm 0.
  *   residual, h      [T, H] in stream_dtype; h may be residual itself (in place)
  *   y, n             [T, H] in block_dtype; y may be NULL (h is then not written)
  *   gate             see MOE_GATE_*; NULL exactly when gate_kind is MOE_GATE_NONE

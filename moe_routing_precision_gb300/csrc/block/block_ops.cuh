@@ -122,10 +122,11 @@ __device__ __forceinline__ float sigmoid_f32(float x, float* deriv = nullptr) {
   return x < 0.0f ? small : big;
 }
 
-// 1 / sqrt(x) for x > 0: the hardware estimate and one Newton step.
+// 1 / sqrt(x) for x > 0: the hardware estimate and one Newton step; 0 for +inf,
+// where the step would be 0 * inf.
 __device__ __forceinline__ float rsqrt_f32(float x) {
   const float y = rsqrtf(x);
-  return __fmaf_rn(0.5f * y, __fmaf_rn(-x * y, y, 1.0f), y);
+  return x < INFINITY ? __fmaf_rn(0.5f * y, __fmaf_rn(-x * y, y, 1.0f), y) : y;
 }
 
 // ------------------------------------------------ barriers of bulk copies
