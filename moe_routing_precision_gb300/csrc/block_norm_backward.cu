@@ -32,6 +32,11 @@ namespace {
 // blocks in ascending order.
 enum { kPartPost = 0, kPartPre = 1 };
 
+// rho^3 x.  One factor at a time: the cube alone leaves f32's range for rows of
+// magnitude 2^42 and more, and for rows below eps where eps is below 2^-85; x has
+// the row's magnitude, so the products do not.
+__device__ __forceinline__ float cubed(float rho, float x) { return rho * x * rho * rho; }
+
 template <class RT, class YT, int VEC, int NPT>
 __global__ void __launch_bounds__(1024) block_norm_backward_kernel(const NormArgs a, int tpr) {
   pdl_enter();
@@ -111,13 +116,13 @@ __global__ void __launch_bounds__(1024) block_norm_backward_kernel(const NormArg
     }
     // two buffers: the next row's first writes cannot meet this row's reads
     row_sum<3>(sums, smem + parity * 96, wpr, row_in_block);
-    const float m = rho * rho * rho * sums[0] * inv_h;
+    const float m = cubed(rho, sums[0] * inv_h);
     const float dot = a.scale * (sums[1] - m * sums[2]);  // sum scale g_c d w y
     if (live && gtok && tid == 0) {
       static_cast<float*>(a.grad_gate)[t] = dot * rho_y * gt1[0];
     }
     const float cs = a.scale * gt[0];
-    const float my = post ? rho_y * rho_y * rho_y * dot * gt[0] * inv_h : 0.0f;
+    const float my = post ? cubed(rho_y, dot * gt[0] * inv_h) : 0.0f;
 #pragma unroll
     for (int i = 0; i < NPT; ++i) {
       const int c = (i * tpr + tid) * VEC;
@@ -401,11 +406,11 @@ __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U,
       ring_fill<V>(rs, ring, ring_smem, rs.stage, src, bytes, t + ring.stages * step, 1, a.T,
                    err);
     rs.next(ring.stages);
-    const float m = rho * rho * rho * sums[0] * inv_h;
+    const float m = cubed(rho, sums[0] * inv_h);
     const float dot = a.scale * (sums[1] - m * sums[2]);
     if (gtok && tid == 0) static_cast<float*>(a.grad_gate)[t] = dot * rho_y * gt1[0];
     const float cs = a.scale * gt[0];
-    const float my = post ? rho_y * rho_y * rho_y * dot * gt[0] * inv_h : 0.0f;
+    const float my = post ? cubed(rho_y, dot * gt[0] * inv_h) : 0.0f;
     const int64_t at = t * a.H + tid * V;
 #pragma unroll
     for (int i = 0; i < U; ++i) {

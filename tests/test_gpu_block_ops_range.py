@@ -68,3 +68,39 @@ def test_norm_of_rows_whose_squares_overflow(T, H, sd):
                                               pre_weight=w, rstd_post=rp, rstd_pre=rn)
     assert torch.equal(gr[1], r0[1])              # the norm of that row is constant: 0
     assert not gy[3].any()
+
+
+@pytest.mark.parametrize("T,H", [(8, 264), (7, 33), (5, 9000), (700, 4096), (600, 1155)])
+@pytest.mark.parametrize("bd", [BF, F32])
+@pytest.mark.parametrize("eps", [1e-6, 1e-30])
+def test_norm_backward_of_large_and_tiny_rows(T, H, bd, eps):
+    """Rows whose inverse norm cubed leaves f32's range, with no other gradient that
+    would hide the terms: rows of 2^45 to 2^60, and (eps = 1e-30) rows of zeros."""
+    g = gen(T + H)
+    r, y = randn((T, H), g), randn((T, H), g, bd)
+    for i, e in enumerate((45, 50, 60)):
+        r[i] *= 2.0 ** e
+    y[3] *= 2.0 ** 48
+    y[4] *= 2.0 ** 60
+    if eps < 1e-20:
+        r[2] = 0
+        y[2] = 0
+        y[0] = 0
+    w, v = 1 + randn((H,), g, std=0.2), 1 + randn((H,), g, std=0.2)
+    # the post-norm's rows are of order one: h is as large as r
+    h, n, rp, rn = ops.block_norm(r, y, post_weight=w, pre_weight=v, scale=0.5, eps=eps)
+    gn = randn((T, H), g, bd)
+    got = ops.block_norm_backward(None, gn, h, y=y, post_weight=w, scale=0.5, pre_weight=v,
+                                  rstd_post=rp, rstd_pre=rn)
+    want = ref.norm_backward(None, gn, h, y, w, None, "none", 0.5, v, rp, rn)
+    for name, t in zip(("grad_residual", "grad_y", "grad_post_weight"), got[:3]):
+        val, mag = want[name]
+        if t.dim() == 1:
+            ref.check(t, val, mag, name)
+            continue
+        # row by row, so that no row hides behind another's size; those below 1e-30 are
+        # compared times 2^60
+        s = torch.where(val.abs().max(1, keepdim=True).values < 1e-12, 2.0 ** 60, 1.0).double()
+        if t.dtype == BF:
+            s = torch.ones_like(s)
+        ref.check((t.double() * s.to(DEV)).to(F32 if t.dtype == F32 else BF), val * s, mag * s, name)
