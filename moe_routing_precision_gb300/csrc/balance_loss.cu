@@ -310,9 +310,9 @@ __device__ __forceinline__ void row_grad(const float (&x)[N], const float (&a)[N
   dot *= pinv;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float v = pinv * (a[i] - dot);
-    if (SIG) v *= n[i] * n[i];
-    d[i] *= v + z;
+    const float v = pinv * (a[i] - dot);
+    // (e^x n lies in [0, 1]; n^2 alone underflows from x = 44 on)
+    d[i] = SIG ? __fmaf_rn(d[i], z, d[i] * n[i] * n[i] * v) : d[i] * (v + z);
   }
 }
 

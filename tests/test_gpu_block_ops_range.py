@@ -45,6 +45,24 @@ def at_bytes(t, by):
     return v
 
 
+# ------------------------------------------------------------ score gradient
+
+@pytest.mark.parametrize("top", [46.0, 50.0, 52.0, 56.0, 60.0])
+@pytest.mark.parametrize("E", [16, 17, 256])
+def test_sigmoid_gradient_of_saturated_scores(top, E):
+    """The balance loss alone: p (a - sum p a) (1 - sigmoid), where 1 - sigmoid is e^-x."""
+    T, k = 40, 2
+    x = torch.randn(T, E, generator=gen(E))
+    x = (x - x.max(1, keepdim=True).values + top).to(DEV)
+    idx = x.topk(k, 1).indices.to(torch.int32)
+    _, _, counts, _, tokens = ops.balance_loss(x, idx, score_func="sigmoid")
+    gb = torch.full((1,), 100.0, device=DEV)
+    got = ops.balance_loss_backward(x, counts, tokens, gb, k=k, score_func="sigmoid")
+    d, mag = ref.balance_backward(x, counts, tokens, gb, None, "sigmoid", None, None, None, None,
+                                  None, k)
+    ref.check(got, d, 2 * mag, "grad_scores")
+
+
 # ---------------------------------------------------------- norms out of range
 
 @pytest.mark.parametrize("T,H", [(6, 264), (5, 33), (4, 9000), (1100, 4096), (2100, 1001)])
