@@ -19,8 +19,8 @@
 // exponentials and sums come from those registers, so the scores are read once,
 // which bounds both passes.  Rows whose largest score lies in [-20, 80] (any
 // router's, whatever its masked scores) need no maximum taken off: e^x, its sums
-// and the sigmoids e^x / (1 + e^x) stay in f32's range, and what underflows is
-// below 1e-29 of the row.  Other rows take the shifted form.
+// and their inverses, and the sigmoids e^x / (1 + e^x) stay in f32's range, and what
+// underflows is below 1e-29 of the row.  Other rows take the shifted form.
 //
 // At 65536 tokens of 256 experts (67 MB of scores) the exponentials and the
 // rows' index work bound both passes, not HBM: about 250 warp instructions per
@@ -263,8 +263,10 @@ __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], fl
 }
 
 // A row's score gradient p (a - sum p a) [(1 - sigmoid)] + zc lse q, zero for a
-// token that does not count.  Near rows keep e^x and 1 - sigmoid alone: with
-// u = e^x, p = u / sum u or u n / sum (u n).
+// token that does not count.  Near rows keep u = e^x and n = 1 - sigmoid alone:
+// p = u / sum u or u n / sum (u n).  u meets its sum before it meets a coefficient:
+// a may be anything finite (small losses over many tokens, a loss scale), and
+// a / sum u or u a would leave f32's range.
 template <int L, int N, bool SIG>
 __device__ __forceinline__ void row_grad(const float (&x)[N], const float (&a)[N], float zc,
                                          float (&d)[N], bool* counts) {
@@ -292,27 +294,34 @@ __device__ __forceinline__ void row_grad(const float (&x)[N], const float (&a)[N
   for (int i = 0; i < N; ++i) {
     d[i] = expf(x[i]);
     tot += d[i];
-    float s = d[i];
     if (SIG) {
       n[i] = rcp_f32(1.0f + d[i]);
-      s *= n[i];
-      stot += s;
+      stot = __fmaf_rn(d[i], n[i], stot);
     }
-    dot = __fmaf_rn(s, a[i], dot);
   }
   tot = group_sum<L>(tot);
   if (SIG) stot = group_sum<L>(stot);
-  dot = group_sum<L>(dot);
   *counts = tot > 0.0f;
   const float inv = *counts ? rcp_f32(tot) : 0.0f;
   const float pinv = SIG ? (*counts ? rcp_f32(stot) : 0.0f) : inv;
-  const float z = *counts ? zc * __logf(tot) * inv : 0.0f;
-  dot *= pinv;
+  const float z = *counts ? zc * __logf(tot) : 0.0f;
+  // (e^x n lies in [0, 1]; n^2 alone underflows from x = 44 on)
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float v = pinv * (a[i] - dot);
-    // (e^x n lies in [0, 1]; n^2 alone underflows from x = 44 on)
-    d[i] = SIG ? __fmaf_rn(d[i], z, d[i] * n[i] * n[i] * v) : d[i] * (v + z);
+    if (SIG) {
+      dot = __fmaf_rn(d[i] * n[i] * pinv, a[i], dot);
+    } else {
+      d[i] *= inv;
+      dot = __fmaf_rn(d[i], a[i], dot);
+    }
+  }
+  dot = group_sum<L>(dot);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (SIG)
+      d[i] = __fmaf_rn(d[i] * inv, z, d[i] * n[i] * pinv * (a[i] - dot) * n[i]);
+    else
+      d[i] *= a[i] + (z - dot);
   }
 }
 
@@ -596,13 +605,14 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
           const float inv = 1.0f / (float)n;
           if (a.grad_z) zc = 2.0f * __ldg(a.grad_z + s) * inv;
           if (a.grad_balance) {
-            const float gb = __ldg(a.grad_balance + s) * inv * inv * ((float)E / (float)a.k);
+            const float gb = __ldg(a.grad_balance + s) * inv * ((float)E / (float)a.k);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
               for (int i = 0; i < W; ++i) {
                 const int e = Row<L, W, NV, FULL>::expert(sub, v) + i;
-                if (FULL || e < E) coef[v * W + i] = gb * (float)__ldg(a.counts + (int64_t)s * E + e);
+                if (FULL || e < E)
+                  coef[v * W + i] = gb * ((float)__ldg(a.counts + (int64_t)s * E + e) * inv);
               }
           }
         }

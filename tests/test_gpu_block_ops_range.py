@@ -63,6 +63,25 @@ def test_sigmoid_gradient_of_saturated_scores(top, E):
     ref.check(got, d, 2 * mag, "grad_scores")
 
 
+@pytest.mark.parametrize("func", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(16, 2), (37, 3), (256, 8)])
+@pytest.mark.parametrize("top", [66.0, 70.0, 75.0, 79.0, 80.0])
+def test_score_gradient_of_large_scores(func, E, k, top):
+    """Coefficients from tiny (small losses over many tokens) to large (a loss scale)."""
+    T = 24
+    x = torch.randn(T, E, generator=gen(E))
+    x = (x - x.max(1, keepdim=True).values + top).to(DEV)
+    for n, scale in ((65536, 1e-8), (65536, 1e-4), (65536, 1.0), (1, 1.0), (1, 65536.0)):
+        counts = torch.randint(0, 2 * n * k // E + 2, (1, E), generator=gen(3)).to(torch.int32)
+        counts, tokens = counts.to(DEV), torch.full((1,), n, dtype=torch.int32, device=DEV)
+        g = torch.full((1,), scale, device=DEV)
+        for gb, gz in ((g, None), (None, g), (g, g)):
+            got = ops.balance_loss_backward(x, counts, tokens, gb, gz, k=k, score_func=func)
+            d, mag = ref.balance_backward(x, counts, tokens, gb, gz, func, None, None, None, None,
+                                          None, k)
+            ref.check(got, d, 2 * mag, f"grad_scores, n = {n}, upstream {scale}")
+
+
 # ---------------------------------------------------------- norms out of range
 
 @pytest.mark.parametrize("T,H", [(6, 264), (5, 33), (4, 9000), (1100, 4096), (2100, 1001)])
