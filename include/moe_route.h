@@ -582,8 +582,8 @@ size_t moe_block_norm_backward_workspace_bytes(int64_t num_tokens, int32_t hidde
  * moe_balance_loss -- per-expert counts and the router's auxiliary losses over
  * packed sequences.  Sequence i holds the tokens seq_offsets[i] <= t <
  * seq_offsets[i+1].  A token counts if it lies in a sequence, token_mask (if
- * given) is nonzero there, and its row has a score above -inf; n_i is the
- * number of such tokens of sequence i.  Scores of a token that does not count
+ * given) is nonzero there, and its row has a score above -inf and no NaN; n_i is
+ * the number of such tokens of sequence i.  Scores of a token that does not count
  * may hold anything.  Over the tokens that count:
  *   counts[i,e] = #{(t,j) : topk_idx[t,j] == e}
  *   probs[i,e]  = (1/n_i) sum_t p[t,e]

@@ -228,7 +228,8 @@ __device__ __forceinline__ void far_sums(const float (&x)[N], float top, float (
 }
 
 // A row's probabilities, the log of its summed exponentials, and whether the
-// token counts (any score above -inf).
+// token counts: a score above -inf and no NaN, for which either form's sum of
+// exponentials is above zero.
 template <int L, int N, bool SIG>
 __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], float* lse,
                                           bool* counts) {
@@ -236,7 +237,7 @@ __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], fl
   if (far_row<L, N>(x, &top)) {
     float q[N], n[N], m;
     far_sums<L, N, SIG>(x, top, p, q, n, &m, &tot, &stot);
-    *counts = m > kNegInf;
+    *counts = tot > 0.0f;
     *lse = *counts ? m + logf(tot) : 0.0f;
     const float inv = *counts ? 1.0f / (SIG ? stot : tot) : 0.0f;
 #pragma unroll
@@ -262,8 +263,8 @@ __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], fl
   for (int i = 0; i < N; ++i) p[i] *= inv;
 }
 
-// A row's score gradient p (a - sum p a) [(1 - sigmoid)] + zc lse q, zero for a
-// token that does not count.  Near rows keep u = e^x and n = 1 - sigmoid alone:
+// A row's score gradient p (a - sum p a) [(1 - sigmoid)] + zc lse q, of no meaning
+// for a token that does not count.  Near rows keep u = e^x and n = 1 - sigmoid alone:
 // p = u / sum u or u n / sum (u n).  u meets its sum before it meets a coefficient:
 // a may be anything finite (small losses over many tokens, a loss scale), and
 // a / sum u or u a would leave f32's range.
@@ -274,7 +275,7 @@ __device__ __forceinline__ void row_grad(const float (&x)[N], const float (&a)[N
   if (far_row<L, N>(x, &top)) {
     float p[N], m;
     far_sums<L, N, SIG>(x, top, p, d, n, &m, &tot, &stot);
-    *counts = m > kNegInf;
+    *counts = tot > 0.0f;
     const float inv = *counts ? 1.0f / tot : 0.0f, sinv = SIG && *counts ? 1.0f / stot : 0.0f;
     const float z = *counts ? zc * (m + logf(tot)) * inv : 0.0f;
 #pragma unroll
@@ -629,6 +630,10 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
         float d[N];
         bool counts;
         row_grad<L, N, SIG>(row.x, coef, zc, d, &counts);
+        if (!counts) {  // (a NaN is no zero times the row's inverse sum)
+#pragma unroll
+          for (int i = 0; i < N; ++i) d[i] = 0.0f;
+        }
         if (sel) {
           // this lane's selections sub, sub + L, ...: the first is at hand
           float wg = counts && sub < a.k ? w0 * g0 : 0.0f;

@@ -736,7 +736,8 @@ def balance_loss(scores: torch.Tensor, topk_idx: torch.Tensor, *, score_func: st
 
     scores [T, E] float32 (-inf allowed), topk_idx [T, k] int32; seq_offsets
     [S+1] int32 (None: one sequence of all T tokens); token_mask [T] bool or
-    uint8, zero where a token does not count.  With p = softmax(scores), or
+    uint8, zero where a token does not count (nor does one whose scores are all
+    -inf or hold a NaN).  With p = softmax(scores), or
     sigmoid(scores) over its row sum:
         balance[i] = sum_e E counts[i,e] / (k n_i) * probs[i,e],  probs = mean p
         z[i]       = mean of logsumexp(scores)^2

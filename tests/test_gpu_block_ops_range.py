@@ -82,6 +82,45 @@ def test_score_gradient_of_large_scores(func, E, k, top):
             ref.check(got, d, 2 * mag, f"grad_scores, n = {n}, upstream {scale}")
 
 
+# ------------------------------------------------------------------ NaN rows
+
+@pytest.mark.parametrize("func", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E", [(96, 16), (60, 24), (50, 64), (40, 256), (30, 300), (2500, 24)])
+@pytest.mark.parametrize("far", [False, True])
+def test_a_row_with_a_nan_does_not_count(func, T, E, far):
+    """Alone, beside -inf, beside ordinary scores, and beside rows far from zero; the
+    other rows are as without it."""
+    g, k = gen(T + E), 3
+    x = torch.randn(T, E, generator=g)
+    idx = x.topk(k, 1).indices.to(torch.int32).to(DEV)
+    if far:
+        x[::5] += 300.0
+    keep = torch.ones(T, dtype=torch.bool)
+    for i, t in enumerate(range(1, T, 7)):
+        keep[t] = False
+        if i % 3 == 0:
+            x[t] = math.nan
+        elif i % 3 == 1:
+            x[t, :] = -math.inf
+            x[t, i % E] = math.nan
+        else:
+            x[t, (5 * i) % E] = math.nan
+    x = x.to(DEV)
+    seq = torch.tensor([0, T // 3, T], dtype=torch.int32, device=DEV)
+    bal, z, counts, probs, tokens = ops.balance_loss(x, idx, score_func=func, seq_offsets=seq)
+    want, wc, wt = ref.balance_forward(x, idx, func, seq, keep)
+    assert torch.equal(counts.cpu(), wc) and torch.equal(tokens.cpu(), wt)
+    for name, t in (("balance", bal), ("z", z), ("probs", probs)):
+        ref.check(t, *want[name], name)
+    gb, gz = randn((2,), g), randn((2,), g)
+    w, gw = torch.softmax(randn((T, k), g), 1), randn((T, k), g)
+    got = ops.balance_loss_backward(x, counts, tokens, gb, gz, score_func=func, seq_offsets=seq,
+                                    topk_idx=idx, topk_weights=w, grad_topk_weights=gw)
+    d, mag = ref.balance_backward(x, counts, tokens, gb, gz, func, seq, keep, idx, w, gw, k)
+    ref.check(got, d, 2 * mag, "grad_scores")
+    assert not got[~keep.to(DEV)].any()
+
+
 # ---------------------------------------------------------- norms out of range
 
 @pytest.mark.parametrize("T,H", [(6, 264), (5, 33), (4, 9000), (1100, 4096), (2100, 1001)])
