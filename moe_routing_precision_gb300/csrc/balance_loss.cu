@@ -156,6 +156,11 @@ struct Row {
       }
     }
   }
+  // The same, value i alone.
+  __device__ __forceinline__ static float fetch(const float* p, int E, int sub, bool want, int i) {
+    const int v = i / W;
+    return want && (FULL || expert(sub, v) < E) ? __ldg(p + v * L * W + i % W) : kNegInf;
+  }
 };
 
 // The tokens first, first + stride, ... below hi of one group of lanes, by
@@ -227,12 +232,35 @@ __device__ __forceinline__ void far_sums(const float (&x)[N], float top, float (
   *stot = SIG ? group_sum<L>(st) : 0.0f;
 }
 
+// The log of a near row's summed exponentials `tot`.  Where tot lies near one its
+// own rounding is all of the log's digits (one open expert of score 1e-3: the log
+// is 1e-3, tot 1.001 to 2^-24), so there the lane's scores, score(0) to score(N - 1),
+// are fetched again (kept, they would cost the registers of every row) and the log
+// is taken as max + log sum e^(x - max), which is the score itself where one expert
+// is open.  Outside [0.5, 2] the fast logarithm is within 3 ulp.
+template <int L, int N, class Score>
+__device__ __forceinline__ float near_log(float tot, Score&& score) {
+  float lse = __logf(tot);
+  const bool one = tot >= 0.5f && tot <= 2.0f;
+  if (__any_sync(0xFFFFFFFFu, one)) {
+    float top = kNegInf, t = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) top = fmaxf(top, score(i));
+    top = group_max<L>(top);
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) t += expf(score(i) - top);
+    t = group_sum<L>(t);
+    if (one) lse = top + logf(t);
+  }
+  return lse;
+}
+
 // A row's probabilities, the log of its summed exponentials, and whether the
 // token counts: a score above -inf and no NaN, for which either form's sum of
 // exponentials is above zero.
-template <int L, int N, bool SIG>
+template <int L, int N, bool SIG, class Score>
 __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], float* lse,
-                                          bool* counts) {
+                                          bool* counts, Score&& score) {
   float top, tot = 0.0f, stot = 0.0f;
   if (far_row<L, N>(x, &top)) {
     float q[N], n[N], m;
@@ -255,9 +283,8 @@ __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], fl
   }
   tot = group_sum<L>(tot);
   if (SIG) stot = group_sum<L>(stot);
-  // (e^-20 <= tot < 2^126; the fast logarithm's error is absolute, 2^-22)
   *counts = tot > 0.0f;
-  *lse = *counts ? __logf(tot) : 0.0f;
+  *lse = near_log<L, N>(tot, score);
   const float inv = *counts ? rcp_f32(SIG ? stot : tot) : 0.0f;
 #pragma unroll
   for (int i = 0; i < N; ++i) p[i] *= inv;
@@ -268,9 +295,9 @@ __device__ __forceinline__ void row_probs(const float (&x)[N], float (&p)[N], fl
 // p = u / sum u or u n / sum (u n).  u meets its sum before it meets a coefficient:
 // a may be anything finite (small losses over many tokens, a loss scale), and
 // a / sum u or u a would leave f32's range.
-template <int L, int N, bool SIG>
+template <int L, int N, bool SIG, class Score>
 __device__ __forceinline__ void row_grad(const float (&x)[N], const float (&a)[N], float zc,
-                                         float (&d)[N], bool* counts) {
+                                         float (&d)[N], bool* counts, Score&& score) {
   float top, tot = 0.0f, stot = 0.0f, dot = 0.0f, n[N];
   if (far_row<L, N>(x, &top)) {
     float p[N], m;
@@ -305,7 +332,7 @@ __device__ __forceinline__ void row_grad(const float (&x)[N], const float (&a)[N
   *counts = tot > 0.0f;
   const float inv = *counts ? rcp_f32(tot) : 0.0f;
   const float pinv = SIG ? (*counts ? rcp_f32(stot) : 0.0f) : inv;
-  const float z = *counts ? zc * __logf(tot) : 0.0f;
+  const float z = zc * near_log<L, N>(tot, score);
   // (e^x n lies in [0, 1]; n^2 alone underflows from x = 44 on)
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -392,7 +419,9 @@ __global__ void __launch_bounds__(kThreads, NV * W <= 8 ? 2 : 1)
       if (L == 32 && !want) continue;  // the warp's only row
       float p[N], lse;
       bool counts;
-      row_probs<L, N, SIG>(row.x, p, &lse, &counts);
+      row_probs<L, N, SIG>(row.x, p, &lse, &counts, [&](int i) {
+        return row.fetch(a.scores + walk.e_at - (int64_t)kStride * E, E, sub, want, i);
+      });
       if (!counts) continue;  // uniform in the group; the next shuffle waits for all groups
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i] += p[i];
@@ -587,10 +616,11 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
       int32_t next_e = 0;
       float next_w = 0.0f, next_g = 0.0f;
       Walk walk(a, lo + grp, hi, sub, W);
+      bool now = false;  // whether the next token is wanted
       auto fetch = [&]() {
-        const bool want = in_seq && walk.want();
-        next.load(a.scores + walk.e_at, E, sub, want);
-        if (sel && want && sub < a.k) {
+        now = in_seq && walk.want();
+        next.load(a.scores + walk.e_at, E, sub, now);
+        if (sel && now && sub < a.k) {
           next_e = __ldg(a.idx + walk.k_at);
           next_w = __ldg(a.w + walk.k_at);
           next_g = __ldg(a.grad_w + walk.k_at);
@@ -619,7 +649,7 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
         }
       }
       for (int64_t at = lo; at < hi; at += TPW) {
-        const bool live = walk.left > 0;
+        const bool live = walk.left > 0, want = now;
         const Row<L, W, NV, FULL> row = next;
         const int32_t e0 = next_e;
         const float w0 = next_w, g0 = next_g;
@@ -629,7 +659,9 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
         fetch();
         float d[N];
         bool counts;
-        row_grad<L, N, SIG>(row.x, coef, zc, d, &counts);
+        row_grad<L, N, SIG>(row.x, coef, zc, d, &counts, [&](int i) {
+          return row.fetch(a.scores + (out - a.grad_scores), E, sub, want, i);
+        });
         if (!counts) {  // (a NaN is no zero times the row's inverse sum)
 #pragma unroll
           for (int i = 0; i < N; ++i) d[i] = 0.0f;

@@ -121,6 +121,33 @@ def test_a_row_with_a_nan_does_not_count(func, T, E, far):
     assert not got[~keep.to(DEV)].any()
 
 
+# ------------------------------------------------- log of sums that are near one
+
+@pytest.mark.parametrize("func", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [1, 16, 64, 256, 300])
+@pytest.mark.parametrize("many", [False, True])
+def test_z_of_rows_with_one_open_expert(func, E, many):
+    """log sum exp is that score exactly, however small: each output is off by no more
+    than the bound relative to itself."""
+    small = [1e-3, -2e-3, 0.1, -0.3, 1e-5, 0.6, -0.69, 3.0, 0.0, 7e-7]
+    T = len(small)
+    x = torch.full((T, E), -math.inf)
+    at = torch.arange(T) * 7 % E
+    x[torch.arange(T), at] = torch.tensor(small)
+    if many:                      # more scores than the form with a block per sequence takes
+        pad = torch.randn(40000 // E, E, generator=gen(1))
+        x = torch.cat([x, pad])
+    idx = torch.zeros((x.shape[0], 1), dtype=torch.int32, device=DEV)
+    seq = torch.arange(T + 1, dtype=torch.int32, device=DEV)       # a sequence per token
+    v = torch.tensor(small, dtype=F32).double()
+    x = x.to(DEV)
+    _, z, counts, _, tokens = ops.balance_loss(x, idx, score_func=func, seq_offsets=seq)
+    ref.check(z, v.square(), 2 * v.square(), "z")
+    got = ops.balance_loss_backward(x, counts, tokens, None, torch.ones(T, device=DEV), k=1,
+                                    score_func=func, seq_offsets=seq)
+    ref.check(got[torch.arange(T), at.to(DEV)], 2 * v, 2 * v.abs(), "grad_scores")
+
+
 # ---------------------------------------------------------- norms out of range
 
 @pytest.mark.parametrize("T,H", [(6, 264), (5, 33), (4, 9000), (1100, 4096), (2100, 1001)])
