@@ -30,68 +30,6 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* buf, int wpr, int 
   }
 }
 
-// y = a b, y += a b, s += a . b of V channels, a one value or V.  PAIRS: two
-// channels per instruction.
-__device__ __forceinline__ void mul2(float* y, const float* a, const float* b) {
-  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
-      " mul.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}"
-      : "=f"(y[0]), "=f"(y[1])
-      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
-}
-__device__ __forceinline__ void fma2(float* y, const float* a, const float* b) {
-  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
-      " mov.b64 r, {%0, %1};\n fma.rn.f32x2 r, p, q, r;\n mov.b64 {%0, %1}, r;\n}"
-      : "+f"(y[0]), "+f"(y[1])
-      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
-}
-template <bool PAIRS, int V>
-__device__ __forceinline__ void mul_v(float (&y)[V], const float (&a)[V], const float (&b)[V]) {
-  if constexpr (PAIRS && V % 2 == 0) {
-#pragma unroll
-    for (int q = 0; q < V; q += 2) mul2(y + q, a + q, b + q);
-  } else {
-#pragma unroll
-    for (int q = 0; q < V; ++q) y[q] = a[q] * b[q];
-  }
-}
-template <bool PAIRS, int V>
-__device__ __forceinline__ void fma_v(float (&y)[V], const float (&a)[V], const float (&b)[V]) {
-  if constexpr (PAIRS && V % 2 == 0) {
-#pragma unroll
-    for (int q = 0; q < V; q += 2) fma2(y + q, a + q, b + q);
-  } else {
-#pragma unroll
-    for (int q = 0; q < V; ++q) y[q] = __fmaf_rn(a[q], b[q], y[q]);
-  }
-}
-template <int V>
-__device__ __forceinline__ void fill_v(float (&y)[V], float a) {
-#pragma unroll
-  for (int q = 0; q < V; ++q) y[q] = a;
-}
-template <bool PAIRS, int V>
-__device__ __forceinline__ void mul_v(float (&y)[V], float a, const float (&b)[V]) {
-  float p[V];
-  fill_v(p, a);
-  mul_v<PAIRS>(y, p, b);
-}
-template <bool PAIRS, int V>
-__device__ __forceinline__ void fma_v(float (&y)[V], float a, const float (&b)[V]) {
-  float p[V];
-  fill_v(p, a);
-  fma_v<PAIRS>(y, p, b);
-}
-template <bool PAIRS, int V>
-__device__ __forceinline__ void dot_v(float (&s)[2], const float (&a)[V], const float (&b)[V]) {
-  if constexpr (PAIRS && V % 2 == 0) {
-#pragma unroll
-    for (int q = 0; q < V; q += 2) fma2(s, a + q, b + q);
-  } else {
-#pragma unroll
-    for (int q = 0; q < V; ++q) s[0] = __fmaf_rn(a[q], b[q], s[0]);
-  }
-}
-
 // The gate's values from what is stored, and for the backward their derivatives.
 template <int VEC>
 __device__ __forceinline__ void gate_values(const NormArgs& a, float (&g)[VEC]) {

@@ -129,6 +129,84 @@ __device__ __forceinline__ float rsqrt_f32(float x) {
   return x < INFINITY ? __fmaf_rn(0.5f * y, __fmaf_rn(-x * y, y, 1.0f), y) : y;
 }
 
+// ----------------------------------------------------------- pairs of f32
+
+// y = a b, y += a b, s += a . b, y = a + b of V values, a scalar operand taken V times.
+// PAIRS: two values per instruction.
+__device__ __forceinline__ void mul2(float* y, const float* a, const float* b) {
+  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+      " mul.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}"
+      : "=f"(y[0]), "=f"(y[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+__device__ __forceinline__ void fma2(float* y, const float* a, const float* b) {
+  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+      " mov.b64 r, {%0, %1};\n fma.rn.f32x2 r, p, q, r;\n mov.b64 {%0, %1}, r;\n}"
+      : "+f"(y[0]), "+f"(y[1])
+      : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+template <bool PAIRS, int V>
+__device__ __forceinline__ void mul_v(float (&y)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (PAIRS && V % 2 == 0) {
+#pragma unroll
+    for (int q = 0; q < V; q += 2) mul2(y + q, a + q, b + q);
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; ++q) y[q] = a[q] * b[q];
+  }
+}
+template <bool PAIRS, int V>
+__device__ __forceinline__ void fma_v(float (&y)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (PAIRS && V % 2 == 0) {
+#pragma unroll
+    for (int q = 0; q < V; q += 2) fma2(y + q, a + q, b + q);
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; ++q) y[q] = __fmaf_rn(a[q], b[q], y[q]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void fill_v(float (&y)[V], float a) {
+#pragma unroll
+  for (int q = 0; q < V; ++q) y[q] = a;
+}
+template <bool PAIRS, int V>
+__device__ __forceinline__ void mul_v(float (&y)[V], float a, const float (&b)[V]) {
+  float p[V];
+  fill_v(p, a);
+  mul_v<PAIRS>(y, p, b);
+}
+template <bool PAIRS, int V>
+__device__ __forceinline__ void fma_v(float (&y)[V], float a, const float (&b)[V]) {
+  float p[V];
+  fill_v(p, a);
+  fma_v<PAIRS>(y, p, b);
+}
+template <bool PAIRS, int V>
+__device__ __forceinline__ void dot_v(float (&s)[2], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (PAIRS && V % 2 == 0) {
+#pragma unroll
+    for (int q = 0; q < V; q += 2) fma2(s, a + q, b + q);
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; ++q) s[0] = __fmaf_rn(a[q], b[q], s[0]);
+  }
+}
+template <bool PAIRS, int V>
+__device__ __forceinline__ void add_v(float (&y)[V], const float (&a)[V], float b) {
+  if constexpr (PAIRS && V % 2 == 0) {
+#pragma unroll
+    for (int q = 0; q < V; q += 2)
+      asm("{\n .reg .b64 p, q;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %4};\n"
+          " add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}"
+          : "=f"(y[q]), "=f"(y[q + 1])
+          : "f"(a[q]), "f"(a[q + 1]), "f"(b));
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; ++q) y[q] = a[q] + b;
+  }
+}
+
 // ------------------------------------------------ barriers of bulk copies
 
 __device__ __forceinline__ void mbar_init(uint32_t bar) {
