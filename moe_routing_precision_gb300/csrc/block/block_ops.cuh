@@ -122,11 +122,12 @@ __device__ __forceinline__ float sigmoid_f32(float x, float* deriv = nullptr) {
   return x < 0.0f ? small : big;
 }
 
-// 1 / sqrt(x) for x > 0: the hardware estimate and one Newton step; 0 for +inf,
-// where the step would be 0 * inf.
+// 1 / sqrt(x) for x > 0: the hardware estimate and one Newton step, whose x is kept
+// finite: 0 for +inf, not 0 * inf.  (Beside the estimate; a choice after the step
+// stood in every row's chain: 16384 rows of 7168, bf16, 140.3 : 139.4 us.)
 __device__ __forceinline__ float rsqrt_f32(float x) {
-  const float y = rsqrtf(x);
-  return x < INFINITY ? __fmaf_rn(0.5f * y, __fmaf_rn(-x * y, y, 1.0f), y) : y;
+  const float y = rsqrtf(x), v = fminf(x, 3.402823466e38f);
+  return __fmaf_rn(0.5f * y, __fmaf_rn(-v * y, y, 1.0f), y);
 }
 
 // ----------------------------------------------------------- pairs of f32
