@@ -166,7 +166,10 @@ size_t moe_balance_loss_workspace_bytes(int64_t num_tokens, int32_t num_experts,
   if (num_tokens <= 0 || num_tokens >= ((int64_t)1 << 31) || num_experts < 1 ||
       num_experts > MOE_MAX_EXPERTS || num_seqs < 1 || num_seqs > 65535)
     return 0;
-  return balance_workspace_bytes(num_tokens, num_experts, num_seqs);
+  // whatever the scores' alignment will be
+  const size_t a = balance_workspace_bytes(num_tokens, num_experts, num_seqs, true);
+  const size_t b = balance_workspace_bytes(num_tokens, num_experts, num_seqs, false);
+  return a > b ? a : b;
 }
 
 moe_status_t moe_balance_loss(const float* scores, const int32_t* topk_idx, int64_t num_tokens,
@@ -196,7 +199,8 @@ moe_status_t moe_balance_loss(const float* scores, const int32_t* topk_idx, int6
   }
   if (!scores || !topk_idx || !aligned(scores, 4) || !aligned(topk_idx, 4))
     return MOE_ERR_INVALID_ARG;
-  const size_t need = moe_balance_loss_workspace_bytes(num_tokens, num_experts, num_seqs);
+  const size_t need =
+      balance_workspace_bytes(num_tokens, num_experts, num_seqs, aligned(scores, 16));
   if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
     return MOE_ERR_INVALID_ARG;
   LaunchCtx c;

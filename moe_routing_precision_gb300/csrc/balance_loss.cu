@@ -49,13 +49,28 @@ inline int64_t num_chunks(int64_t T) {
   const int64_t c = chunk_tokens(T);
   return (T + c - 1) / c;
 }
-// A block per sequence up to this many scores: eight passes of its warps, if
-// one sequence has them all.  That against the table and its second launch, in us,
-// one sequence: E = 16: 4.8 : 8.2 at T = 512, 6.8 : 7.9 at 1024, 10.6 : 9.1 at
-// 2048; E = 64: 4.9 : 7.7 at 128, 7.2 : 7.0 at 256; E = 256: 5.6 : 7.9 at 64,
-// 8.2 : 8.0 at 128.
-constexpr int64_t kBlockScores = 16384;
-inline bool block_per_seq(int64_t T, int E) { return T * E <= kBlockScores; }
+// Lanes that hold a token's scores: as many as they need, four scores each where
+// the rows are 16-byte aligned (vec), else one.
+inline int token_lanes(int E, bool vec) {
+  if (vec) return E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : 32;
+  return E <= 8 ? 8 : 32;
+}
+// A block per sequence up to this many scores, and up to eight passes of a block's
+// warps over all tokens for each of the first four sequences (the longest is not
+// known here).  That against the table and its second launch, us:
+//   one sequence, passes: E = 17, 33, 100: 4 (64 tokens) 4.0, 4.4, 4.5 : 6.4; 8 6.0,
+//   6.6, 6.7 : 6.4; 16 (256 tokens) 9.8, 11 : 6.4; 61 (E = 17, 963 tokens) 31 : 7.5
+//   E = 16, 12, 8: 4 4.3 : 6.6; 8 6.4 : 7.0      E = 4: 4 5.8 : 7.4; 8 9.9 : 7.9
+//   E = 1: 1 2.8 : 6.4, 4 4.9 : 6.4; 8 7.8 : 6.6; 256 173 : 11.5
+//   E = 256: 4 (64 tokens) 5.1 : 6.7             E = 1024: 1 (16 tokens) 5.5 : 9.4
+//   four sequences of equal length: E = 33: 31 passes 6.9 : 8.5; E = 4: 16 6.7 : 8.1, 32
+//   10.1 : 9.5; E = 17: 61 10.0 : 8.5; E = 3: 86 15.8 : 9.4
+constexpr int64_t kBlockScores = 16384, kBlockPasses = 8, kBlockSeqs = 4;
+inline bool block_per_seq(int64_t T, int E, int S, bool vec) {
+  const int64_t pass = kWarps * (32 / token_lanes(E, vec));
+  const int64_t most = kBlockPasses * (S < kBlockSeqs ? S : kBlockSeqs);
+  return T * E <= kBlockScores && (T + pass - 1) / pass <= most;
+}
 inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Workspace: [slots][E] f32 sums of p, [slots][E] i32 counts, [slots] f32 sums
@@ -730,9 +745,16 @@ __global__ void __launch_bounds__(kBwdThreads, NV * W <= 8 ? 3 : 1)
   if (bad) flag_error(err, MOE_DEVERR_EXPERT_RANGE);
 }
 
+// Whether the rows take 16-byte accesses.
+inline bool rows_vec(const BalanceArgs& a, bool backward) {
+  uintptr_t bits = reinterpret_cast<uintptr_t>(a.scores);
+  if (backward) bits |= reinterpret_cast<uintptr_t>(a.grad_scores);
+  return a.E % 4 == 0 && (bits & 15u) == 0;
+}
+
 template <int L, int W, int NV, bool SIG, bool FULL>
 cudaError_t forward_t(const LaunchCtx& c, const BalanceArgs& a) {
-  const bool one = block_per_seq(a.T, a.E);
+  const bool one = block_per_seq(a.T, a.E, a.S, rows_vec(a, false));
   const int64_t chunk = one ? a.T : chunk_tokens(a.T), chunks = one ? a.S : num_chunks(a.T);
   const Work ws = work_layout(a.ws, a.T, a.E, a.S);
   const size_t smem = (size_t)(kWarps + 1) * a.E * 4 + kWarps * 12;
@@ -775,13 +797,10 @@ cudaError_t dispatch_full(const LaunchCtx& c, const BalanceArgs& a, bool backwar
                            : dispatch_func<L, W, NV, false>(c, a, backward);
 }
 
-// Lanes per token and accesses per lane from E: 16-byte accesses where the
-// rows are 16-byte aligned; a token takes only as many lanes as its scores need.
+// Lanes per token (token_lanes) and accesses per lane.
 cudaError_t dispatch(const LaunchCtx& c, const BalanceArgs& a, bool backward) {
-  const uintptr_t bits =
-      reinterpret_cast<uintptr_t>(a.scores) | reinterpret_cast<uintptr_t>(a.grad_scores);
   const int E = a.E;
-  if (E % 4 == 0 && (bits & 15u) == 0) {
+  if (rows_vec(a, backward)) {
     if (E <= 16) return dispatch_full<4, 4, 1>(c, a, backward);
     if (E <= 32) return dispatch_full<8, 4, 1>(c, a, backward);
     if (E <= 64) return dispatch_full<16, 4, 1>(c, a, backward);
@@ -800,8 +819,8 @@ cudaError_t dispatch(const LaunchCtx& c, const BalanceArgs& a, bool backward) {
 
 }  // namespace
 
-size_t balance_workspace_bytes(int64_t T, int E, int S) {
-  if (block_per_seq(T, E)) return 0;
+size_t balance_workspace_bytes(int64_t T, int E, int S, bool aligned) {
+  if (block_per_seq(T, E, S, aligned && E % 4 == 0)) return 0;
   return work_layout(nullptr, T, E, S).bytes;
 }
 

@@ -342,7 +342,8 @@ struct BalanceArgs {
   const float* grad_w = nullptr;
   float* grad_scores = nullptr;
 };
-size_t balance_workspace_bytes(int64_t T, int E, int S);
+// aligned: whether scores are 16-byte aligned.
+size_t balance_workspace_bytes(int64_t T, int E, int S, bool aligned);
 cudaError_t launch_balance_loss(const LaunchCtx& c, const BalanceArgs& a);
 cudaError_t launch_balance_loss_backward(const LaunchCtx& c, const BalanceArgs& a);
 

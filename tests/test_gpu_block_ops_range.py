@@ -148,6 +148,31 @@ def test_z_of_rows_with_one_open_expert(func, E, many):
     ref.check(got[torch.arange(T), at.to(DEV)], 2 * v, 2 * v.abs(), "grad_scores")
 
 
+# --------------------------------------------------- forms chosen by the sizes
+
+@pytest.mark.parametrize("E,T", [(1, 16384), (1, 500), (3, 5461), (5, 700), (17, 963), (33, 496),
+                                 (16, 1024), (16, 1025), (64, 256), (24, 300)])
+@pytest.mark.parametrize("func", ["softmax", "sigmoid"])
+def test_balance_of_narrow_and_odd_rows(E, T, func):
+    """Sizes on both sides of the limits of one block per sequence, 16-byte aligned rows
+    and not, with as much workspace as the library names."""
+    g, k = gen(E + T), min(2, E)
+    x = randn((T, E), g)
+    idx = x.topk(k, 1).indices.to(torch.int32)
+    need = ops.balance_loss_workspace_bytes(T, E, 3)
+    seq = torch.tensor([0, T // 4, T // 4, T], dtype=torch.int32, device=DEV)
+    for xs in (x, at_bytes(x, 4)):
+        guard = torch.full((need + 512,), 77, dtype=torch.uint8, device=DEV)
+        bal, z, counts, probs, tokens = ops.balance_loss(xs, idx, score_func=func,
+                                                         seq_offsets=seq,
+                                                         workspace=guard[:need] if need else None)
+        assert bool((guard[need:] == 77).all())
+        want, wc, wt = ref.balance_forward(x, idx, func, seq, None)
+        assert torch.equal(counts.cpu(), wc) and torch.equal(tokens.cpu(), wt)
+        for name, t in (("balance", bal), ("z", z), ("probs", probs)):
+            ref.check(t, *want[name], name)
+
+
 # ---------------------------------------------------------- norms out of range
 
 @pytest.mark.parametrize("T,H", [(6, 264), (5, 33), (4, 9000), (1100, 4096), (2100, 1001)])
