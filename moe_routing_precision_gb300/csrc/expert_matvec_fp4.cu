@@ -405,15 +405,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           sf_at += 2 * kBytes;
         } else if (U8) {
+          // nothing past the row's own scales: beside the zero codes and channels past
+          // K another row's 255 (a NaN) would not vanish
           const uint8_t* sf = static_cast<const uint8_t*>(a.sf);
-          const int64_t end = (int64_t)a.E * M * sf_row;
 #pragma unroll
           for (int i = 0; i < (St::kWords + 1) / 2; ++i) {
             const int p = lane + 32 * i, row = p / St::kWords, wi = p % St::kWords;
             if (St::kWords % 2 != 0 && p >= 16 * St::kWords) break;
-            const int64_t at = ((sf_e + weight_row(ld_tile, row) * (uint32_t)sf_row +
-                                 (uint32_t)(ld_blk * St::kGroups)) & ~(int64_t)3) + 4 * wi;
-            const int64_t left = end - at;
+            const int64_t row_at = sf_e + weight_row(ld_tile, row) * (uint32_t)sf_row;
+            const int64_t at =
+                ((row_at + (uint32_t)(ld_blk * St::kGroups)) & ~(int64_t)3) + 4 * wi;
+            const int64_t left = row_at + sf_row - at;
             const int bytes = left < 0 ? 0 : left > 4 ? 4 : (int)left;
             cp_async4(sst + p * 4, sf + (bytes > 0 ? at : 0), bytes);
           }

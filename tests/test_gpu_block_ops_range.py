@@ -232,3 +232,23 @@ def test_norm_backward_of_large_and_tiny_rows(T, H, bd, eps):
         if t.dtype == BF:
             s = torch.ones_like(s)
         ref.check((t.double() * s.to(DEV)).to(F32 if t.dtype == F32 else BF), val * s, mag * s, name)
+
+
+# ------------------------------------------------------- 4-bit expert products
+
+@pytest.mark.parametrize("group", [16, 32, 64, 128])
+@pytest.mark.parametrize("K", [128, 384, 640, 1152])
+def test_matvec_rows_beside_a_row_without_scales(K, group):
+    """UE8M0 scales of 255 (NaN) in one weight row reach that row's output alone."""
+    g, N, R = gen(K + group), 40, 3
+    w = torch.randint(0, 256, (2, N, K // 2), generator=g).to(torch.uint8).to(DEV)
+    sf = torch.randint(110, 130, (2, N, K // group), generator=g).to(torch.uint8).to(DEV)
+    x = randn((2 * R, K), g, BF)
+    offsets = torch.tensor([0, R, 2 * R], dtype=torch.int32, device=DEV)
+    for n in (0, 9, N - 1):
+        s = sf.clone()
+        s[:, n] = 255
+        got = ops.expert_matvec_fp4(x, w, s, offsets, group=group, out_dtype=F32)
+        want, mag, _ = ref.expert_matvec(x, w, sf, group, offsets, None, 1, False, 2 * R)
+        rest = torch.arange(N) != n
+        ref.check(got[:, rest.to(DEV)], want[:, rest], mag[:, rest], f"row {n} without scales")
