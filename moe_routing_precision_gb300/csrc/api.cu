@@ -63,6 +63,7 @@ moe_status_t context(void* stream, LaunchCtx* ctx) {
   ctx->stream = static_cast<cudaStream_t>(stream);
   ctx->num_sms = d.num_sms;
   ctx->err = d.err;
+  ctx->device = dev;
   return MOE_OK;
 }
 

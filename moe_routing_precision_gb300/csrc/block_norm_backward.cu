@@ -15,8 +15,11 @@
 // SM); 321 us with one block per row and no ring.  What bounds the other types is the
 // chain of a row (its sums) and the instructions: all bf16 125 us, 83 %.
 #include "block/block_norm.cuh"
+#include "known.cuh"
 
 #include <cooperative_groups.h>
+
+#include <utility>
 
 namespace cg = cooperative_groups;
 
@@ -485,12 +488,13 @@ cudaError_t bwd_t(const LaunchCtx& c, const NormArgs& a) {
   static SmemOptIn opt_in;
   cudaError_t e = opt_in.once(kernel);
   if (e != cudaSuccess) return e;
-  // blocks per SM, looked up when the shape changes (1 us a call)
-  thread_local int known = -1, per_sm = 0;
-  if (known != a.H) {
+  // blocks per SM, looked up once for each device and width (1 us a call)
+  static Known<std::pair<int, int>, int> known;
+  int per_sm = 0;
+  if (!known.find({c.device, a.H}, &per_sm)) {
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, s.tpr * s.rows, smem);
     if (e != cudaSuccess) return e;
-    known = a.H;
+    known.put({c.device, a.H}, per_sm);
   }
   int64_t blocks = (a.T + s.rows - 1) / s.rows;
   const int64_t cap = (int64_t)c.num_sms * (per_sm > 0 ? per_sm : 1);

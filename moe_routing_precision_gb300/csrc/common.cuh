@@ -352,6 +352,7 @@ struct LaunchCtx {
   cudaStream_t stream;
   int num_sms;
   unsigned* err;  // device error word
+  int device;
 };
 
 // The device conversions on arbitrary f32 values, for tests (debug_cvt.cu).
