@@ -532,8 +532,10 @@ typedef enum moe_dtype {
  *   rstd_post, rstd_pre      [T] f32 out, each may be NULL; kept for the backward
  * Requires T >= 0, 1 <= H <= MOE_NORM_MAX_HIDDEN, T * H < 2^40, eps > 0 and
  * finite, scale finite, y or pre_weight given, n non-NULL exactly when
- * pre_weight is, and every tensor aligned to its element.  (16-byte aligned
- * tensors with H % 8 == 0 take 16-byte accesses.)
+ * pre_weight is, and every tensor aligned to its element.  Fastest with H % 8 == 0
+ * and every [T, H] and [H] tensor 32-byte aligned; with 16-byte alignment alone
+ * rows go element by element, but for forward calls of fewer than 2^19 elements
+ * and for H > 8192.
  */
 moe_status_t moe_block_norm(const void *residual, int32_t stream_dtype, const void *y,
                             int32_t block_dtype, int64_t num_tokens, int32_t hidden,

@@ -22,11 +22,13 @@
 // and their inverses, and the sigmoids e^x / (1 + e^x) stay in f32's range, and what
 // underflows is below 1e-29 of the row.  Other rows take the shifted form.
 //
-// At 65536 tokens of 256 experts (67 MB of scores) the exponentials and the
-// rows' index work bound both passes, not HBM: about 250 warp instructions per
-// token forward (26 us, 2.7 TB/s) and 470 for the sigmoid gradient (36 us, 3.9
-// TB/s).  The rows' next scores are in flight meanwhile; without them the
-// forward waited on its loads (43 us).
+// At 65536 tokens of 256 experts (67 MB of scores) instruction issue bounds both
+// passes, not HBM: 260 warp instructions per token forward (26 us, 2.7 TB/s; sigmoid 29
+// us) and 463 for the sigmoid gradient with the top-k weights (36 us, 3.9 TB/s; softmax
+// 32 us), about half of them on the exponentials, sums and scaling, the rest on the
+// row's form (maximum, votes), its walk and its selections.  Rows all in the shifted
+// form: 29 and 40 us forward, 36 and 49 us backward.  The rows' next scores are in
+// flight meanwhile; without them the forward waited on its loads (43 us).
 #include "block/block_ops.cuh"
 
 namespace moe {

@@ -11,7 +11,9 @@
 // TB/s, 98 % of a plain copy, through the ring with two rows per turn (176 us
 // with one block per row, whose loads stop while a row is summed; 206 us with
 // the ring but one row per turn and single bf16 conversions).  One token, H =
-// 4096: 3.1 us.
+// 4096: 2.9 us.  8192 tokens of widths that are no multiple of 8, all bf16 : f32 stream:
+// H = 1001 17 : 19 us, 2047 38 : 41, 7161 115 : 123.  Above 8192, one block per row, 4096
+// tokens: H = 12288 80 : 143 us, 16384 137 : 178 (their bytes 59 : 89 and 79 : 119).
 #include "block/block_norm.cuh"
 
 namespace moe {
@@ -356,8 +358,8 @@ bool fwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e
     return all && (a.H == 512 || a.H == 1024) ? fwd_ring<RT, YT, GEL, 8, 2, 0, true>(c, a, e)
                                               : fwd_ring<RT, YT, GEL, 8, 2, 0, false>(c, a, e);
   }
-  // the smallest block that holds the row; the next larger one, us at 8192 tokens:
-  // H = 250: 8.5 : 31, 1001: 16 : 32, 2047: 36 : 61 (a block's threads past the
+  // the smallest block that holds the row; the next larger one, us at 8192 tokens, all
+  // bf16: H = 250: 8.5 : 31, 1001: 16 : 32, 2047: 36 : 61 (a block's threads past the
   // row are idle, and fewer blocks fit an SM)
   if (a.H <= 256) return fwd_ring<RT, YT, GEL, 1, 4, 64, false>(c, a, e);
   if (a.H <= 1024) return fwd_ring<RT, YT, GEL, 1, 8, 128, false>(c, a, e);

@@ -13,7 +13,11 @@
 // Measured: 8192 tokens, H = 7168, f32 stream, bf16 block, gate per channel (1.06
 // GB): 161 us, 6.5 TB/s, 97 % of a plain copy (two rows of 86 KB in flight per
 // SM); 321 us with one block per row and no ring.  What bounds the other types is the
-// chain of a row (its sums) and the instructions: all bf16 125 us, 83 %.
+// chain of a row (its sums) and the instructions: all bf16 125 us, 83 %.  Widths that
+// are no multiple of 8 go element by element, 8192 tokens, all bf16 : f32 stream: H =
+// 1001 40 : 42 us, 2047 67 : 67, 7161 356 : 377.  Above 8192 rows go through the kernel
+// without the ring, whose threads' sums do not fit their registers: 4096 tokens, H =
+// 12288 342 : 379, 16384 470 : 516 (their bytes 89 : 134 and 119 : 178).
 #include "block/block_norm.cuh"
 #include "known.cuh"
 
@@ -276,11 +280,11 @@ __device__ __forceinline__ void ring_fill_piece(const RingState& r, const Ring& 
 }
 
 // ALL: rows that fill the threads, with every input: no conditions between the
-// loads (H = 7168, 8192 tokens, bf16: 137 us; 147 with them).
+// loads (H = 7168, 8192 tokens, bf16, two units: 127 us; 134 with them).
 // P: stages per row.  Two (U = 2, V = 8, one unit of every thread each) where two
 // whole rows do not fit: H = 7168, all f32, element gate, 4096 tokens 162 us; 251
 // without the ring.  Whole rows where they fit (half rows take two turns of the
-// copying thread: bf16, 8192 tokens 148 : 177 us).
+// copying thread: bf16, 8192 tokens, two units 127 : 134 us).
 template <class RT, class YT, bool GEL, int V, int U, int NT, int P, bool ALL>
 __global__ void __launch_bounds__(ring_max_threads(U, NT), ring_min_blocks(V, U, NT))
     norm_backward_ring_kernel(const NormArgs a, const Ring ring, unsigned* err) {
@@ -576,8 +580,9 @@ bool bwd_ring_8(const LaunchCtx& c, const NormArgs& a, cudaError_t* e) {
 template <class RT, class YT, bool GEL>
 bool bwd_ring_vec(const LaunchCtx& c, const NormArgs& a, int vec, cudaError_t* e) {
   if (vec == 8) return bwd_ring_8<RT, YT, GEL>(c, a, e);
-  // the smallest block that holds the row; the next larger one, us at 8192 tokens:
-  // H = 250: 32 : 48, 1001: 47 : 58, 2047: 72 : 107
+  // the smallest block that holds the row; the next larger one, us at 8192 tokens of
+  // f32 streams and bf16 blocks, at an earlier step: H = 250: 32 : 48, 1001: 47 : 58,
+  // 2047: 72 : 107
   if (a.H <= 256) return bwd_ring<RT, YT, GEL, 1, 4, 64, 1, false>(c, a, e);
   if (a.H <= 1024) return bwd_ring<RT, YT, GEL, 1, 8, 128, 1, false>(c, a, e);
   if (a.H <= 2048) return bwd_ring<RT, YT, GEL, 1, 8, 256, 1, false>(c, a, e);

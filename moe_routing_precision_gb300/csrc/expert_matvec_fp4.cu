@@ -29,11 +29,13 @@
 //
 // Measured: 64 tokens, top 8 of 256 experts, K = 2048, N = 7168, f32 scales per 128
 // (1.74 GB): 244 us, 7.1 TB/s, above a plain copy's rate (reads alone run faster).
-// One token, K = 7168, SwiGLU of 2 x 2048, UE8M0 scales per 32 (125 MB): 27 us, of
+// Groups of 16: f32 scales (2.4 GB) 388 us, 6.3 TB/s, UE8M0 (1.8 GB) 372 us, 4.9 TB/s:
+// the scaling of the groups' sums bounds those.
+// One token, K = 7168, SwiGLU of 2 x 2048, UE8M0 scales per 32 (125 MB): 28 us, of
 // which 8 us do not depend on N (launch, offsets, x, filling the rings); the
 // slope is 6.4 TB/s.  At that rate a scheduler issues two thirds of its slots;
 // what the warps execute per weight bounds it next: 64 conversions and 16 products
-// per 4096 weights among about 290 instructions.  A stage of 128 channels doubled
+// per 4096 weights among 264 instructions.  A stage of 128 channels doubled
 // the rest (42 us); cp.async for the codes filled the load queue ahead of the
 // shared-memory reads (batch 292 us); 8 warps could not hide the latencies (51 us).
 //

@@ -234,6 +234,51 @@ def test_norm_backward_of_large_and_tiny_rows(T, H, bd, eps):
         ref.check((t.double() * s.to(DEV)).to(F32 if t.dtype == F32 else BF), val * s, mag * s, name)
 
 
+@pytest.mark.parametrize("T,H", [(9, 512), (1500, 512), (700, 4096), (560, 7168), (4100, 520)])
+@pytest.mark.parametrize("sd,bd", [(BF, BF), (F32, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("by", [16, 48])
+def test_norm_of_views_at_16_bytes(T, H, sd, bd, by):
+    """Tensors that start at an odd multiple of 16 bytes, below and at sizes that take
+    the ring of staged rows."""
+    g = gen(T + H)
+    r, y, gate = randn((T, H), g, sd, 3.0), randn((T, H), g, bd), randn((T, H), g, bd)
+    w, v = 1 + randn((H,), g, std=0.2), 1 + randn((H,), g, std=0.2)
+    r, y, gate, w, v = (at_bytes(t, by) for t in (r, y, gate, w, v))
+    out = (at_bytes(torch.empty_like(r), by), at_bytes(torch.empty_like(y), by))
+    got = ops.block_norm(r, y, post_weight=w, gate=gate, gate_act="sigmoid", scale=0.5,
+                         pre_weight=v, out=out)
+    want = ref.norm_forward(r, y, w, gate, "sigmoid", 0.5, v, 1e-6)
+    for name, t in zip(("h", "n", "rstd_post", "rstd_pre"), got):
+        ref.check(t, *want[name], name)
+    h = got[0]
+    gh, gn = at_bytes(randn((T, H), g, sd), by), at_bytes(randn((T, H), g, bd), by)
+    grads = ops.block_norm_backward(gh, gn, h, y=y, post_weight=w, gate=gate, gate_act="sigmoid",
+                                    scale=0.5, pre_weight=v, rstd_post=got[2], rstd_pre=got[3])
+    want = ref.norm_backward(gh, gn, h, y, w, gate, "sigmoid", 0.5, v, got[2], got[3])
+    for name, t in zip(("grad_residual", "grad_y", "grad_post_weight", "grad_gate",
+                        "grad_pre_weight"), grads):
+        ref.check(t, *want[name], name)
+
+
+def test_inverse_root_and_sigmoid_to_a_few_ulp():
+    """rstd of rows of one channel is 1 / sqrt(y^2 + eps); h of a token-gated row of ones
+    on zeros is the sigmoid.  The root's argument has two roundings (each half an ulp of
+    it, a quarter of the result), the inverse root at most 2 ulp: 2.5 ulp of 2^-23.  The
+    sigmoid: e^-|x| 2 ulp, the sum and the reciprocal 1.5, the product 0.5: 4 ulp."""
+    T = 20000
+    e = torch.rand(T, generator=gen(1)) * 100 - 50
+    y = torch.pow(2.0, e)[:, None].to(DEV)
+    _, _, rp, _ = ops.block_norm(torch.zeros_like(y), y, post_weight=torch.ones(1, device=DEV),
+                                 eps=1e-38)
+    want = (y.cpu().double()[:, 0].square() + 1e-38).rsqrt()
+    assert bool(((rp.cpu().double() - want).abs() <= 2.5 * 2.0 ** -23 * want).all())
+    x = (torch.randn(T, generator=gen(2)) * 20).clamp(-80, 80)[:, None].to(DEV)
+    one = torch.ones(T, 1, device=DEV)
+    h, _, _, _ = ops.block_norm(torch.zeros_like(one), one, gate=x, gate_act="sigmoid")
+    want = torch.sigmoid(x.cpu().double())
+    assert bool(((h.cpu().double() - want).abs() <= 4 * 2.0 ** -23 * want).all())
+
+
 # ------------------------------------------------------- 4-bit expert products
 
 @pytest.mark.parametrize("group", [16, 32, 64, 128])
