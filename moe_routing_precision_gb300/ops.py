@@ -173,31 +173,35 @@ def _ptr(t):
     return None if t is None else (t.data_ptr() or None)
 
 
-def _empty(shape, dtype, like, stream=None, alloc=None):
-    """A tensor for a call whose kernels run on `stream` (None: the current one).
+def _on(stream, alloc):
+    """`alloc` (torch.empty, ...) for a call whose kernels run on `stream`.
 
-    On another stream than the current one it is allocated as that stream's own:
-    taken from the current stream's memory, its last user there might still be
-    running, and a workspace or an output that the caller drops would go back
+    On another stream than the current one a tensor is allocated as that stream's
+    own: taken from the current stream's memory, its last user there might still
+    be running, and a workspace or an output that the caller drops would go back
     to the current stream while the kernels are yet to write it.  The current
     stream is recorded on it, for the work the caller gives it there."""
-    alloc = alloc or torch.empty
     if stream is None:
-        return alloc(shape, dtype=dtype, device=like.device)
+        return alloc
     here = torch.cuda.current_stream()
     handle = _stream(stream) or 0
     if handle == here.cuda_stream:
-        return alloc(shape, dtype=dtype, device=like.device)
+        return alloc
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-    with torch.cuda.stream(stream):
-        t = alloc(shape, dtype=dtype, device=like.device)
-    t.record_stream(here)
-    return t
+
+    def there(*args, **kwargs):
+        with torch.cuda.stream(stream):
+            t = alloc(*args, **kwargs)
+        t.record_stream(here)
+        return t
+    return there
 
 
-def _like(t, stream=None):
-    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t, stream)
+def _empty(shape, dtype, like, stream=None):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _on(stream, torch.empty)(shape, dtype=dtype, device=like.device)
 
 
 # --------------------------------------------------------------------------
@@ -323,7 +327,7 @@ def route_expand_cast_workspace(T: int, E: int, k: int, like: torch.Tensor,
     """A zero-filled workspace for route_expand_cast_fp8 (its first 256 bytes
     are the fused path's control words, which must start at zero)."""
     n = int(lib().moe_route_expand_cast_fp8_workspace_bytes(T, E, k))
-    return _empty((max(n, 256),), torch.uint8, like, stream, torch.zeros)
+    return _on(stream, torch.zeros)(max(n, 256), dtype=torch.uint8, device=like.device)
 
 
 def route_expand_cast_fp8(scores: torch.Tensor, x: torch.Tensor, k: int, *, mode: int = PATH_AUTO,
@@ -628,24 +632,26 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
     if pre_weight is not None:
         _dev(pre_weight, "pre_weight", torch.float32, (H,))
     kind = GATE_NONE if gate is None else _gate_kind(gate, T, H, block_dtype)
+    empty, empty_like = _on(stream, torch.empty), _on(stream, torch.empty_like)
     h, n = out if out is not None else (None, None)
     if y is None:
         h = residual
     elif h is None:
-        h = _like(residual, stream)
+        h = empty_like(residual)
     else:
         _dev(h, "out[0]", residual.dtype, (T, H))
     if pre_weight is None:
         n = None
     elif n is None:
-        n = _like(y, stream) if y is not None else _empty((T, H), block_dtype, residual, stream)
+        n = (empty_like(y) if y is not None else
+             empty((T, H), dtype=block_dtype, device=residual.device))
     else:
         _dev(n, "out[1]", block_dtype, (T, H))
     rp = rn = None
     if post_weight is not None:
-        rp = _empty((T,), torch.float32, residual, stream)
+        rp = empty((T,), dtype=torch.float32, device=residual.device)
     if pre_weight is not None:
-        rn = _empty((T,), torch.float32, residual, stream)
+        rn = empty((T,), dtype=torch.float32, device=residual.device)
     rc = lib().moe_block_norm(_ptr(residual), sd, _ptr(y),
                               DT_F32 if block_dtype == torch.float32 else DT_BF16, T, H,
                               _ptr(post_weight), _ptr(gate), kind,
@@ -692,11 +698,12 @@ def block_norm_backward(grad_h, grad_n, h: torch.Tensor, *, y=None, post_weight=
         _dev(pre_weight, "pre_weight", torch.float32, (H,))
         _dev(rstd_pre, "rstd_pre", torch.float32, (T,))
     kind = GATE_NONE if gate is None else _gate_kind(gate, T, H, block.dtype)
-    gr = _like(h, stream)
-    gy = None if y is None else _like(y, stream)
-    gpw = None if post_weight is None else _like(post_weight, stream)
-    gg = None if gate is None else _like(gate, stream)
-    gnw = None if pre_weight is None else _like(pre_weight, stream)
+    empty_like = _on(stream, torch.empty_like)
+    gr = empty_like(h)
+    gy = None if y is None else empty_like(y)
+    gpw = None if post_weight is None else empty_like(post_weight)
+    gg = None if gate is None else empty_like(gate)
+    gnw = None if pre_weight is None else empty_like(pre_weight)
     ws_bytes = block_norm_backward_workspace_bytes(T, H)
     if workspace is None:
         workspace = _empty((ws_bytes,), torch.uint8, h, stream)
@@ -747,11 +754,12 @@ def balance_loss(scores: torch.Tensor, topk_idx: torch.Tensor, *, score_func: st
     k = topk_idx.shape[1]
     _dev(topk_idx, "topk_idx", torch.int32, (T, k))
     S = _sequences(seq_offsets, token_mask, T)
-    bal = _empty((S,), torch.float32, scores, stream)
-    z = _empty((S,), torch.float32, scores, stream)
-    counts = _empty((S, E), torch.int32, scores, stream)
-    probs = _empty((S, E), torch.float32, scores, stream)
-    tokens = _empty((S,), torch.int32, scores, stream)
+    empty, dev = _on(stream, torch.empty), scores.device
+    bal = empty((S,), dtype=torch.float32, device=dev)
+    z = empty((S,), dtype=torch.float32, device=dev)
+    counts = empty((S, E), dtype=torch.int32, device=dev)
+    probs = empty((S, E), dtype=torch.float32, device=dev)
+    tokens = empty((S,), dtype=torch.int32, device=dev)
     ws_bytes = balance_loss_workspace_bytes(T, E, S)
     if workspace is None and ws_bytes:
         workspace = _empty((ws_bytes,), torch.uint8, scores, stream)
@@ -797,7 +805,7 @@ def balance_loss_backward(scores: torch.Tensor, counts: torch.Tensor, tokens: to
             raise ValueError("grad_topk_weights needs topk_idx and topk_weights")
         _dev(topk_weights, "topk_weights", torch.float32, (T, k))
         _dev(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k))
-    g = out if out is not None else _like(scores, stream)
+    g = out if out is not None else _on(stream, torch.empty_like)(scores)
     _dev(g, "out", torch.float32, (T, E))
     rc = lib().moe_balance_loss_backward(
         _ptr(scores), T, E, k, _choice(score_func, _SCORE_FUNC, "score_func"), _ptr(seq_offsets),
@@ -826,7 +834,8 @@ def combine_backward(grad_out: torch.Tensor, y: torch.Tensor, topk_weights: torc
     if sorted_src is not None:
         _dev(sorted_src, "sorted_src", torch.int32, (R,))
     if out is None:
-        gy, gw = _like(y, stream), _like(topk_weights, stream)
+        empty_like = _on(stream, torch.empty_like)
+        gy, gw = empty_like(y), empty_like(topk_weights)
     else:
         gy, gw = out
         _dev(gy, "out[0]", torch.bfloat16, (R, H))
