@@ -613,7 +613,8 @@ def block_norm(residual: torch.Tensor, y: torch.Tensor | None = None, *, post_we
     float32, or [T, H] in y's type; gate_act "none" or "sigmoid".  residual and
     h are [T, H] bfloat16 or float32, y and n [T, H] bfloat16 or float32
     (block_dtype, y's own by default, else bfloat16); weights are [H] float32.
-    out: None or (h, n), where h may be residual itself.
+    out: None or (h, n), where h may be residual itself (without y h is residual and
+    out[0] is not used).
     -> (h, n, rstd_post, rstd_pre), None for what there is not."""
     sd = _dt(residual, "residual")
     T, H = _dev(residual, "residual", residual.dtype).shape

@@ -76,3 +76,34 @@ def test_calls_beside_other_work_of_the_current_stream(name):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["norm_many", "norm_backward", "balance", "matvec"])
+def test_calls_on_a_forked_stream_of_a_captured_graph(name):
+    """The capture forks to another stream for the call and joins again; the call's own
+    tensors are dropped during the capture."""
+    call = _calls()[name]
+    want = [t.clone() for t in _flat(call(None))]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        s.wait_stream(here)
+        call(s)
+        got = _flat(call(s))
+        here.wait_stream(s)
+        got = [t.clone() for t in got]
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    del graph
+    torch.cuda.synchronize()
+    again = _flat(call(s))
+    torch.cuda.synchronize()
+    for a, b in zip(again, want):
+        assert torch.equal(a, b)
