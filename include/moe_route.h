@@ -17,7 +17,9 @@
  * decode launch (moe_route_expand_cast_fp8), and the route map without a
  * workspace (moe_route_map_noalloc); and the operators around the routed
  * experts (moe_block_norm, moe_balance_loss and moe_combine's gradient, with
- * their backward passes, and moe_expert_matvec_fp4).
+ * their backward passes, and moe_expert_matvec_fp4), and a router with balance
+ * and groups before 8-bit integer experts (moe_router_gate with its backward pass,
+ * moe_cast_int8, moe_expert_matmul_int8).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -491,7 +493,8 @@ size_t moe_route_expand_cast_fp8_workspace_bytes(int64_t num_tokens, int32_t num
  * ------------------------------------------------------------------------
  * The operators around the routed experts: the block's norms with its gate and
  * residual scale, the router's balance loss with its gradient, the combine's
- * gradient, and the experts' products with 4-bit weights for decode batches.
+ * gradient, and the experts' products with 4-bit weights for decode batches; then
+ * the router with a bias for balance and groups, and the experts in 8-bit integers.
  * They have no counterpart on the pages; the formulas are given in full here.
  * The conventions above hold, with one widening: where a float argument says
  * "-inf allowed", -inf is an ordinary value.
@@ -695,6 +698,104 @@ moe_status_t moe_expert_matvec_fp4(const void *x, int64_t num_x, const uint8_t *
                                    int32_t num_experts, int32_t num_topk, int64_t num_rows,
                                    int32_t k_dim, int32_t n_dim, int32_t swiglu, void *out,
                                    int32_t out_dtype, void *stream);
+
+/* What a group of experts is ranked by in moe_router_gate. */
+#define MOE_GROUP_MAX 0  /* its largest s + bias                                  */
+#define MOE_GROUP_TOP2 1 /* the sum of its two largest (of one, if it has one)    */
+#define MOE_MAX_GROUPS 32
+
+/*
+ * moe_router_gate -- the router of a block with balanced and grouped experts:
+ *   s[t,e] = softmax over e of scores[t,e]            (MOE_SCORE_SOFTMAX), or
+ *            1 / (1 + exp(-scores[t,e]))              (MOE_SCORE_SIGMOID);
+ *            0 where scores[t,e] is -inf
+ *   c[t,e] = s[t,e] + bias[e]                         (bias NULL: s[t,e])
+ * The num_groups groups of E / num_groups consecutive experts are ranked by
+ * group_score over their experts with scores above -inf (a group without any
+ * comes last); the topk_groups first stay.  Of their experts the k with the largest
+ * c are selected, in descending order; experts with a score of -inf come last.
+ * Equal values go to the lower group and the lower expert.  Values are compared as
+ * real numbers: in f32, and in f64 where f32 cannot tell them apart.
+ *   topk_weights[t,j] = scale * s_j / sum_j' s_j'     (renormalize; 0 if the sum is 0)
+ *                       scale * s_j                   (otherwise)
+ * with s_j the score of the j-th selected expert: the bias decides the selection
+ * only.  The ratio of sigmoids keeps its digits however small they are.
+ *   scores [T,E] f32 (-inf allowed, +inf not); bias [E] f32, finite, may be NULL;
+ *   topk_idx [T,k] i32, topk_weights [T,k] f32
+ * Requires the E and k limits of moe_topk_gate, 1 <= num_groups <= MOE_MAX_GROUPS,
+ * E % num_groups == 0, 1 <= topk_groups <= num_groups, k <= E / num_groups *
+ * topk_groups and a finite scale.
+ */
+moe_status_t moe_router_gate(const float *scores, int64_t num_tokens, int32_t num_experts,
+                             int32_t num_topk, int32_t score_func, const float *bias,
+                             int32_t num_groups, int32_t topk_groups, int32_t group_score,
+                             int32_t renormalize, float scale, int32_t *topk_idx,
+                             float *topk_weights, void *stream);
+
+/*
+ * moe_router_gate_backward -- the score gradient of moe_router_gate's weights, for
+ * their gradient g = grad_topk_weights and e = topk_idx[t,j] (the selection and the
+ * bias get none).  With w and s as above:
+ *   renormalize: grad_scores[t,e] = w_j (g_j - sum_j' g_j' w_j' / scale) [* (1 - s_j)
+ *                                   for MOE_SCORE_SIGMOID]
+ *   otherwise:   grad_scores[t,e] = scale g_j s_j (1 - s_j)            (sigmoid)
+ *                grad_scores[t,e'] = s_e' (scale g_j [e' = e] - scale sum_j' g_j' s_j')
+ *                                    for every expert e'               (softmax)
+ * and 0 elsewhere; with add, that is added to add's entry (moe_balance_loss_backward's
+ * gradient, say).
+ *   scores [T,E] f32 as above; topk_idx [T,k] i32, a token's experts distinct;
+ *   grad_topk_weights [T,k] f32; add [T,E] f32, may be NULL
+ *   grad_scores [T,E] f32 out; may be add itself (in place)
+ * An index outside [0, E) is left out of every sum and sets MOE_DEVERR_EXPERT_RANGE.
+ * Requires the E and k limits of moe_topk_gate and a finite scale.
+ */
+moe_status_t moe_router_gate_backward(const float *scores, int64_t num_tokens,
+                                      int32_t num_experts, int32_t num_topk, int32_t score_func,
+                                      int32_t renormalize, float scale, const int32_t *topk_idx,
+                                      const float *grad_topk_weights, const float *add,
+                                      float *grad_scores, void *stream);
+
+/*
+ * moe_cast_int8 -- rows to 8-bit integers with one scale per row, for
+ * moe_expert_matmul_int8 (activations: a row per token; weights: a row per output):
+ *   a = max(max_c |x[t,c]|, 2^-96)
+ *   out_sf[t] = a / 127;  out[t,c] = rint(x[t,c] * (127 / a))
+ * each step in f32, rounded to nearest (ties to even): values in [-127, 127].
+ *   x [T,H] in dtype (MOE_DT_*), finite; out [T,H] i8; out_sf [T] f32
+ * Requires 0 <= T < 2^31, H >= 1, T * H < 2^40 and every tensor aligned to its element.
+ * Fastest with H % 8 == 0, x 16-byte and out 8-byte aligned.
+ */
+moe_status_t moe_cast_int8(const void *x, int32_t dtype, int64_t num_rows, int32_t hidden,
+                           int8_t *out, float *out_sf, void *stream);
+
+/*
+ * moe_expert_matmul_int8 -- products of routed 8-bit rows with their expert's 8-bit
+ * weights, with a scale per row of x and per output channel:
+ *   o[r, m] = (sum_c x[src(r), c] * w[e(r), m, c]) * x_sf[src(r)] * w_sf[e(r), m]
+ *   out[r, n] = o[r, n]                                        (M = N), or
+ *   out[r, n] = o[r, n] / (1 + exp(-o[r, n])) * o[r, N + n]    (swiglu: M = 2N)
+ * for the rows offsets[e] <= r < offsets[e+1] of every expert e, from one row per
+ * expert to all rows, rounded once to out_dtype.  Rows at or past offsets[E] are not
+ * written.  The sum of products is a sum of f32 in a fixed order; it is exact while no
+ * partial sum passes 2^24 (always so for K <= 1024).
+ *   x [num_x, K] i8, 16-byte aligned; x_sf [num_x] f32
+ *   w [E, M, K] i8, 16-byte aligned; w_sf [E, M] f32
+ *   offsets [E+1] i32, non-decreasing, within [0, num_rows], as the route maps
+ *   return it; NULL (E == 1 only): all num_rows rows
+ *   sorted_src: NULL: src(r) = r (num_x >= num_rows); or [num_rows] i32 as the route
+ *   maps return it: src(r) = sorted_src[r] / num_topk, and a negative entry gives
+ *   a row of zeros
+ *   out [num_rows, N] in out_dtype (MOE_OUT_*)
+ * Requires K % 16 == 0, 16 <= K <= 65536, num_rows < 2^31, E * M < 2^31 and the limits
+ * of E and k.  offsets beyond num_rows or a src outside [0, num_x) set
+ * MOE_DEVERR_POS_RANGE; such rows are not written, or are zero.
+ */
+moe_status_t moe_expert_matmul_int8(const int8_t *x, const float *x_sf, int64_t num_x,
+                                    const int8_t *w, const float *w_sf, const int32_t *offsets,
+                                    const int32_t *sorted_src, int32_t num_experts,
+                                    int32_t num_topk, int64_t num_rows, int32_t k_dim,
+                                    int32_t n_dim, int32_t swiglu, void *out, int32_t out_dtype,
+                                    void *stream);
 
 /* Test hooks of the fused path, process-wide, read at each launch:
  *   MOE_DEBUG_WAIT_TIMEOUT_NS: the bound of every wait (default 1e9 ns);

@@ -347,4 +347,138 @@ moe_status_t moe_expert_matvec_fp4(const void* x, int64_t num_x, const uint8_t* 
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
 
+moe_status_t moe_router_gate(const float* scores, int64_t num_tokens, int32_t num_experts,
+                             int32_t num_topk, int32_t score_func, const float* bias,
+                             int32_t num_groups, int32_t topk_groups, int32_t group_score,
+                             int32_t renormalize, float scale, int32_t* topk_idx,
+                             float* topk_weights, void* stream) {
+  if (num_tokens < 0 || num_tokens >= ((int64_t)1 << 31) || !experts_ok(num_experts, num_topk))
+    return MOE_ERR_INVALID_ARG;
+  if (score_func != MOE_SCORE_SOFTMAX && score_func != MOE_SCORE_SIGMOID)
+    return MOE_ERR_INVALID_ARG;
+  if (num_groups < 1 || num_groups > MOE_MAX_GROUPS || num_experts % num_groups != 0 ||
+      topk_groups < 1 || topk_groups > num_groups ||
+      num_topk > num_experts / num_groups * topk_groups)
+    return MOE_ERR_INVALID_ARG;
+  if (group_score != MOE_GROUP_MAX && group_score != MOE_GROUP_TOP2) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (num_tokens == 0) return MOE_OK;
+  if (!scores || !topk_idx || !topk_weights || !aligned(scores, 4) || !aligned(bias, 4) ||
+      !aligned(topk_idx, 4) || !aligned(topk_weights, 4))
+    return MOE_ERR_INVALID_ARG;
+  LaunchCtx c;
+  moe_status_t s = context(stream, &c);
+  if (s != MOE_OK) return s;
+  RouterArgs a;
+  a.scores = scores;
+  a.T = num_tokens;
+  a.E = num_experts;
+  a.k = num_topk;
+  a.func = score_func;
+  a.bias = bias;
+  a.G = num_groups;
+  a.g = topk_groups;
+  a.group_score = group_score;
+  a.renorm = renormalize != 0;
+  a.scale = scale;
+  a.idx = topk_idx;
+  a.w = topk_weights;
+  cudaError_t e = launch_router_gate(c, a);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+moe_status_t moe_router_gate_backward(const float* scores, int64_t num_tokens,
+                                      int32_t num_experts, int32_t num_topk, int32_t score_func,
+                                      int32_t renormalize, float scale, const int32_t* topk_idx,
+                                      const float* grad_topk_weights, const float* add,
+                                      float* grad_scores, void* stream) {
+  if (num_tokens < 0 || num_tokens >= ((int64_t)1 << 31) || !experts_ok(num_experts, num_topk))
+    return MOE_ERR_INVALID_ARG;
+  if (score_func != MOE_SCORE_SOFTMAX && score_func != MOE_SCORE_SIGMOID)
+    return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (num_tokens == 0) return MOE_OK;
+  if (!scores || !topk_idx || !grad_topk_weights || !grad_scores || !aligned(scores, 4) ||
+      !aligned(topk_idx, 4) || !aligned(grad_topk_weights, 4) || !aligned(add, 4) ||
+      !aligned(grad_scores, 4))
+    return MOE_ERR_INVALID_ARG;
+  LaunchCtx c;
+  moe_status_t s = context(stream, &c);
+  if (s != MOE_OK) return s;
+  RouterArgs a;
+  a.scores = scores;
+  a.T = num_tokens;
+  a.E = num_experts;
+  a.k = num_topk;
+  a.func = score_func;
+  a.renorm = renormalize != 0;
+  a.scale = scale;
+  a.idx = const_cast<int32_t*>(topk_idx);
+  a.grad_w = grad_topk_weights;
+  a.add = add;
+  a.grad_scores = grad_scores;
+  cudaError_t e = launch_router_gate_backward(c, a);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+moe_status_t moe_cast_int8(const void* x, int32_t dtype, int64_t num_rows, int32_t hidden,
+                           int8_t* out, float* out_sf, void* stream) {
+  if (!dtype_ok(dtype) || num_rows < 0 || hidden < 1) return MOE_ERR_INVALID_ARG;
+  if (num_rows >= ((int64_t)1 << 31) || num_rows >= ((int64_t)1 << 40) / hidden)
+    return MOE_ERR_UNSUPPORTED;
+  if (num_rows == 0) return MOE_OK;
+  if (!x || !out || !out_sf || !aligned(x, dtype_size(dtype)) || !aligned(out_sf, 4))
+    return MOE_ERR_INVALID_ARG;
+  LaunchCtx c;
+  moe_status_t s = context(stream, &c);
+  if (s != MOE_OK) return s;
+  cudaError_t e = launch_cast_int8(c, x, dtype == MOE_DT_F32, num_rows, hidden, out, out_sf);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+moe_status_t moe_expert_matmul_int8(const int8_t* x, const float* x_sf, int64_t num_x,
+                                    const int8_t* w, const float* w_sf, const int32_t* offsets,
+                                    const int32_t* sorted_src, int32_t num_experts,
+                                    int32_t num_topk, int64_t num_rows, int32_t k_dim,
+                                    int32_t n_dim, int32_t swiglu, void* out, int32_t out_dtype,
+                                    void* stream) {
+  if (out_dtype != MOE_OUT_BF16 && out_dtype != MOE_OUT_F32) return MOE_ERR_INVALID_ARG;
+  if (num_experts < 1 || num_experts > MOE_MAX_EXPERTS || num_topk < 1 ||
+      num_topk > MOE_MAX_TOPK || num_rows < 0 || num_x < 0 || n_dim < 1 || k_dim < 16 ||
+      k_dim % 16 != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (!offsets && num_experts != 1) return MOE_ERR_INVALID_ARG;
+  if (!sorted_src && num_x < num_rows) return MOE_ERR_INVALID_ARG;
+  if (k_dim > 65536 || num_rows >= ((int64_t)1 << 31) ||
+      (int64_t)num_experts * n_dim * (swiglu ? 2 : 1) >= ((int64_t)1 << 31))
+    return MOE_ERR_UNSUPPORTED;
+  if (num_rows == 0) return MOE_OK;
+  if ((num_x > 0 && (!x || !x_sf)) || !w || !w_sf || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_sf, 4) || !aligned(w_sf, 4) ||
+      !aligned(offsets, 4) || !aligned(sorted_src, 4) ||
+      !aligned(out, out_dtype == MOE_OUT_F32 ? 4 : 2))
+    return MOE_ERR_INVALID_ARG;
+  LaunchCtx c;
+  moe_status_t s = context(stream, &c);
+  if (s != MOE_OK) return s;
+  MatmulInt8Args a;
+  a.x = x;
+  a.x_sf = x_sf;
+  a.num_x = num_x;
+  a.w = w;
+  a.w_sf = w_sf;
+  a.offsets = offsets;
+  a.src = sorted_src;
+  a.E = num_experts;
+  a.k = num_topk;
+  a.R = num_rows;
+  a.K = k_dim;
+  a.N = n_dim;
+  a.swiglu = swiglu ? 1 : 0;
+  a.out = out;
+  a.out_f32 = out_dtype == MOE_OUT_F32;
+  cudaError_t e = launch_expert_matmul_int8(c, a);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
 }  // extern "C"

@@ -369,4 +369,44 @@ struct MatvecArgs {
 };
 cudaError_t launch_expert_matvec_fp4(const LaunchCtx& c, const MatvecArgs& a);
 
+// moe_router_gate and its backward (router_gate.cu).
+struct RouterArgs {
+  const float* scores = nullptr;
+  int64_t T = 0;
+  int E = 0, k = 0, func = 0;
+  const float* bias = nullptr;
+  int G = 1, g = 1, group_score = 0;
+  bool renorm = true;
+  float scale = 1.0f;
+  int32_t* idx = nullptr;  // written by the forward, read by the backward
+  float* w = nullptr;
+  // backward
+  const float* grad_w = nullptr;
+  const float* add = nullptr;
+  float* grad_scores = nullptr;
+};
+cudaError_t launch_router_gate(const LaunchCtx& c, const RouterArgs& a);
+cudaError_t launch_router_gate_backward(const LaunchCtx& c, const RouterArgs& a);
+
+// moe_cast_int8 (cast_int8.cu).
+cudaError_t launch_cast_int8(const LaunchCtx& c, const void* x, bool f32, int64_t T, int H,
+                             int8_t* out, float* sf);
+
+// moe_expert_matmul_int8 (expert_matmul_int8.cu).
+struct MatmulInt8Args {
+  const int8_t* x = nullptr;
+  const float* x_sf = nullptr;
+  int64_t num_x = 0;
+  const int8_t* w = nullptr;
+  const float* w_sf = nullptr;
+  const int32_t* offsets = nullptr;
+  const int32_t* src = nullptr;
+  int E = 1, k = 1;
+  int64_t R = 0;
+  int K = 0, N = 0, swiglu = 0;
+  void* out = nullptr;
+  bool out_f32 = false;
+};
+cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& a);
+
 }  // namespace moe

@@ -78,6 +78,13 @@ SIGNATURES = {
                                             _P, _P]),
     "moe_expert_matvec_fp4": (ctypes.c_int, [_P, _i64, _P, _P, _i32, _i32, _P, _P, _i32, _i32,
                                              _i64, _i32, _i32, _i32, _P, _i32, _P]),
+    "moe_router_gate": (ctypes.c_int, [_P, _i64, _i32, _i32, _i32, _P, _i32, _i32, _i32, _i32,
+                                       ctypes.c_float, _P, _P, _P]),
+    "moe_router_gate_backward": (ctypes.c_int, [_P, _i64, _i32, _i32, _i32, _i32, ctypes.c_float,
+                                                _P, _P, _P, _P, _P]),
+    "moe_cast_int8": (ctypes.c_int, [_P, _i32, _i64, _i32, _P, _P, _P]),
+    "moe_expert_matmul_int8": (ctypes.c_int, [_P, _P, _i64, _P, _P, _P, _P, _i32, _i32, _i64, _i32,
+                                              _i32, _i32, _P, _i32, _P]),
     "moe_peak_copy": (ctypes.c_int, [_P, _P, _sz, _P]),
     "moe_get_device_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -563,6 +570,7 @@ DT_BF16, DT_F32 = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = range(4)
 _GATE_ACT = {"none": 0, "sigmoid": 1}
 _SCORE_FUNC = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORE = {"max": 0, "top2": 1}
 WSF_F32, WSF_UE8M0 = 0, 1
 
 
@@ -897,6 +905,145 @@ def expert_matvec_fp4(x: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, offs
     return o
 
 
+def _one_device(first: torch.Tensor, *others):
+    """Every tensor (or None) on `first`'s device, and that the current one."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: all must be on one device")
+    here = _cuda_device() if _cuda_device is not None else torch.cuda.current_device()
+    if dev.index != here:
+        raise ValueError(f"tensors on {dev}, but the current device is cuda:{here}")
+
+
+def router_gate(scores: torch.Tensor, k: int, *, score_func: str = "softmax", bias=None,
+                num_groups: int = 1, topk_groups: int | None = None, group_score: str = "top2",
+                renormalize: bool = True, scale: float = 1.0, out_idx=None, out_w=None,
+                stream=None):
+    """The k experts of each token by score plus bias, from its best groups.
+
+    s is the softmax or the sigmoid of scores [T, E] float32 (-inf: a closed expert);
+    experts are selected by s + bias (bias [E] float32 or None), from the topk_groups
+    (None: all) of num_groups groups of consecutive experts whose largest s + bias
+    (group_score "max") or sum of the two largest ("top2") is largest.  Equal values
+    go to the lower group and expert.  The weights are scale * s of the selected
+    experts, divided by their sum with renormalize.
+    -> (idx [T, k] int32 in descending order, w [T, k] float32)."""
+    _dev(scores, "scores", torch.float32)
+    if scores.dim() != 2:
+        raise ValueError("scores must be [T, E]")
+    T, E = scores.shape
+    if bias is not None:
+        _dev(bias, "bias", torch.float32, (E,))
+    idx = out_idx if out_idx is not None else _empty((T, k), torch.int32, scores, stream)
+    _dev(idx, "out_idx", torch.int32, (T, k))
+    w = out_w if out_w is not None else _empty((T, k), torch.float32, scores, stream)
+    _dev(w, "out_w", torch.float32, (T, k))
+    _one_device(scores, bias, idx, w)
+    rc = lib().moe_router_gate(_ptr(scores), T, E, k,
+                               _choice(score_func, _SCORE_FUNC, "score_func"), _ptr(bias),
+                               num_groups, num_groups if topk_groups is None else topk_groups,
+                               _choice(group_score, _GROUP_SCORE, "group_score"),
+                               int(renormalize), scale, _ptr(idx), _ptr(w), _stream(stream))
+    _check(rc, "moe_router_gate")
+    return idx, w
+
+
+def router_gate_backward(scores: torch.Tensor, topk_idx: torch.Tensor,
+                         grad_topk_weights: torch.Tensor, *, score_func: str = "softmax",
+                         renormalize: bool = True, scale: float = 1.0, add=None, out=None,
+                         stream=None):
+    """The score gradient [T, E] float32 of router_gate's weights for their gradient
+    grad_topk_weights [T, k]: zero but for the selected experts, except for the
+    softmax without renormalize.  add [T, E] (balance_loss_backward's gradient, say)
+    is added; out may be add itself."""
+    _dev(scores, "scores", torch.float32)
+    if scores.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("scores must be [T, E] and topk_idx [T, k]")
+    T, E = scores.shape
+    k = topk_idx.shape[1]
+    _dev(topk_idx, "topk_idx", torch.int32, (T, k))
+    _dev(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k))
+    if add is not None:
+        _dev(add, "add", torch.float32, (T, E))
+    g = out if out is not None else _on(stream, torch.empty_like)(scores)
+    _dev(g, "out", torch.float32, (T, E))
+    _one_device(scores, topk_idx, grad_topk_weights, add, g)
+    rc = lib().moe_router_gate_backward(_ptr(scores), T, E, k,
+                                        _choice(score_func, _SCORE_FUNC, "score_func"),
+                                        int(renormalize), scale, _ptr(topk_idx),
+                                        _ptr(grad_topk_weights), _ptr(add), _ptr(g),
+                                        _stream(stream))
+    _check(rc, "moe_router_gate_backward")
+    return g
+
+
+def cast_int8(x: torch.Tensor, *, out=None, out_sf=None, stream=None):
+    """Rows to 8-bit integers with one scale per row: sf = max|x| / 127 and
+    q = round(x * (127 / max|x|)), ties to even.
+
+    x [T, H] bfloat16 or float32 -> (q [T, H] int8, sf [T] float32).  For weights
+    [E, M, K]: cast_int8(w.view(E * M, K)), a scale per output channel."""
+    dt = _dt(x, "x")
+    _dev(x, "x", x.dtype)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, H]")
+    T, H = x.shape
+    q = out if out is not None else _empty((T, H), torch.int8, x, stream)
+    _dev(q, "out", torch.int8, (T, H))
+    sf = out_sf if out_sf is not None else _empty((T,), torch.float32, x, stream)
+    _dev(sf, "out_sf", torch.float32, (T,))
+    _one_device(x, q, sf)
+    _check(lib().moe_cast_int8(_ptr(x), dt, T, H, _ptr(q), _ptr(sf), _stream(stream)),
+           "moe_cast_int8")
+    return q, sf
+
+
+def expert_matmul_int8(x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor,
+                       offsets=None, *, sorted_src=None, k: int = 1, swiglu: bool = False,
+                       out_dtype=torch.bfloat16, out=None, stream=None):
+    """Products of routed 8-bit rows with their expert's 8-bit weights, from one row
+    per expert to all rows.
+
+    x [num_x, K] int8 with x_sf [num_x] float32, w [E, M, K] int8 with w_sf [E, M]
+    float32, as cast_int8 writes them.  Rows are in the route map's order: offsets
+    [E+1] int32 (None: one expert, all rows).  Row r of the output reads x[r], or
+    with sorted_src [R] int32 x[sorted_src[r] // k] (a negative entry: a row of zeros).
+    swiglu: M = 2N, the gate's outputs first; out = silu(gate) * up.
+    -> out [R, N] bfloat16 or float32 (rows past offsets[E] not written)."""
+    _dev(x, "x", torch.int8)
+    _dev(w, "w", torch.int8)
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [rows, K] and w [E, M, K]")
+    X, K = x.shape
+    E, M = w.shape[0], w.shape[1]
+    _dev(w, "w", torch.int8, (E, M, K))
+    _dev(x_sf, "x_sf", torch.float32, (X,))
+    _dev(w_sf, "w_sf", torch.float32, (E, M))
+    if swiglu and M % 2:
+        raise ValueError("swiglu needs an even number of weight rows")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bfloat16 or float32")
+    if offsets is not None:
+        _dev(offsets, "offsets", torch.int32, (E + 1,))
+    R = X
+    if sorted_src is not None:
+        _dev(sorted_src, "sorted_src", torch.int32)
+        if sorted_src.dim() != 1:
+            raise ValueError("sorted_src must be [R]")
+        R = sorted_src.shape[0]
+    N = M // 2 if swiglu else M
+    o = out if out is not None else _empty((R, N), out_dtype, x, stream)
+    _dev(o, "out", out_dtype, (R, N))
+    _one_device(x, x_sf, w, w_sf, offsets, sorted_src, o)
+    rc = lib().moe_expert_matmul_int8(_ptr(x), _ptr(x_sf), X, _ptr(w), _ptr(w_sf), _ptr(offsets),
+                                      _ptr(sorted_src), E, k, R, K, N, int(swiglu), _ptr(o),
+                                      MOE_OUT_F32 if out_dtype == torch.float32 else MOE_OUT_BF16,
+                                      _stream(stream))
+    _check(rc, "moe_expert_matmul_int8")
+    return o
+
+
 def peak_copy(src: torch.Tensor, dst: torch.Tensor, *, stream=None):
     """Device copy of src's bytes into dst (the HBM roofline probe)."""
     if src.device.type != "cuda" or dst.device.type != "cuda":
@@ -927,4 +1074,5 @@ __all__ = ["lib", "MoeError", "topk_gate", "route_map", "route_map_workspace_byt
            "expand_cast_fp8", "swiglu_cast_fp8", "combine", "peak_copy", "device_status",
            "launch_count", "SIGNATURES", "block_norm", "block_norm_backward",
            "block_norm_backward_workspace_bytes", "balance_loss", "balance_loss_backward",
-           "balance_loss_workspace_bytes", "combine_backward", "expert_matvec_fp4"]
+           "balance_loss_workspace_bytes", "combine_backward", "expert_matvec_fp4",
+           "router_gate", "router_gate_backward", "cast_int8", "expert_matmul_int8"]
