@@ -786,9 +786,10 @@ moe_status_t moe_cast_int8(const void *x, int32_t dtype, int64_t num_rows, int32
  *   maps return it: src(r) = sorted_src[r] / num_topk, and a negative entry gives
  *   a row of zeros
  *   out [num_rows, N] in out_dtype (MOE_OUT_*)
- * Requires K % 16 == 0, 16 <= K <= 65536, num_rows < 2^31, E * M < 2^31 and the limits
- * of E and k.  offsets beyond num_rows or a src outside [0, num_x) set
- * MOE_DEVERR_POS_RANGE; such rows are not written, or are zero.
+ * Requires K % 16 == 0, 16 <= K <= 65536, num_rows < 2^31, E * M < 2^31 - 512 and the
+ * limits of E and k.  offsets beyond num_rows or a src outside [0, num_x) set
+ * MOE_DEVERR_POS_RANGE; such rows are not written, or are zero.  Every wait inside the
+ * kernel is bounded (1 s); one that runs out sets MOE_DEVERR_TIMEOUT.
  */
 moe_status_t moe_expert_matmul_int8(const int8_t *x, const float *x_sf, int64_t num_x,
                                     const int8_t *w, const float *w_sf, const int32_t *offsets,

@@ -450,7 +450,7 @@ moe_status_t moe_expert_matmul_int8(const int8_t* x, const float* x_sf, int64_t 
   if (!offsets && num_experts != 1) return MOE_ERR_INVALID_ARG;
   if (!sorted_src && num_x < num_rows) return MOE_ERR_INVALID_ARG;
   if (k_dim > 65536 || num_rows >= ((int64_t)1 << 31) ||
-      (int64_t)num_experts * n_dim * (swiglu ? 2 : 1) >= ((int64_t)1 << 31))
+      (int64_t)num_experts * n_dim * (swiglu ? 2 : 1) >= ((int64_t)1 << 31) - 512)
     return MOE_ERR_UNSUPPORTED;
   if (num_rows == 0) return MOE_OK;
   if ((num_x > 0 && (!x || !x_sf)) || !w || !w_sf || !out) return MOE_ERR_INVALID_ARG;

@@ -3,100 +3,508 @@
 //
 //   o[r, m] = (sum_c x[src(r), c] * w[e(r), m, c]) * x_sf[src(r)] * w_sf[e(r), m]
 //
-// The simple form: a warp per run of up to 4 rows of one expert and 4 outputs, each
-// lane 16 channels at a time, four products per dp4a.
-#include "block/block_ops.cuh"
+// sm_103a's tensor cores take no 8-bit integers (tcgen05.mma kind::i8 exists on other
+// parts only), and mma.sync's are far slower.  8-bit integers are exact in f16, and their
+// products and any sum below 2^24 in f32, so the products go to tcgen05.mma kind::f16:
+// the weights are the M operand, converted from shared into tensor memory on their way,
+// the rows of x the N operand, converted from global into shared memory.  Both are read
+// as bytes, which is what counts for few rows, where HBM bounds it.
+//
+// A tile is 2 x 128 outputs (two accumulators in the same lanes; with SwiGLU the gate's
+// and the up outputs of 128 channels, which one thread then holds) by up to NT rows.
+// One CTA per SM, its warps in roles joined by barriers:
+//   0-7    convert a stage of weights (a thread per weight row) into tensor memory, and
+//          write the finished tiles out; 4 warps per half
+//   8-11   gather, convert and store the rows of x
+//   12     asks for the weights (TMA, 128-byte swizzle)
+//   13     issues the products
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "block/tcgen05.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kRows = 4, kOuts = 4, kWarps = 8;
+constexpr int kWarps = 14;
+constexpr int kThreads = kWarps * 32;
+constexpr int kConvert = 8;          // warps 0 .. 7
+constexpr int kGather = 4;           // warps 8 .. 11
+constexpr int kBlockK = 128;         // channels per stage
+constexpr int kHalf = 128;           // outputs of one accumulator
+constexpr int kABytes = 2 * kHalf * kBlockK;
 
-__global__ void __launch_bounds__(kWarps * 32)
-    expert_matmul_simple_kernel(const MatmulInt8Args a, unsigned* err) {
+// NT rows per tile; SA stages of weights (bytes) and SB of rows (f16) in shared memory,
+// ST of weights (f16) in tensor memory, behind the two accumulators.
+template <int NT_, int SA_, int SB_, int ST_>
+struct Shape {
+  static constexpr int NT = NT_, SA = SA_, SB = SB_, ST = ST_;
+  static constexpr int kBBytes = NT * kBlockK * 2;
+  static constexpr int kColA = 2 * NT;  // first column of the weights
+  static_assert(kColA + ST * 128 <= 512, "tensor memory has 512 columns");
+};
+
+struct Smem {
+  uint32_t a, b, bars, xsf, totals, tmem, first, rows, total;
+};
+template <class S>
+__host__ __device__ inline Smem smem_layout(int E) {
+  Smem s;
+  s.a = 0;
+  s.b = s.a + S::SA * kABytes;
+  s.bars = s.b + S::SB * S::kBBytes;
+  s.xsf = s.bars + (2 * S::SA + 2 * S::SB + 2 * S::ST + 3) * 8;
+  s.totals = s.xsf + S::NT * 4;
+  s.tmem = s.totals + kWarps * 4;
+  s.first = s.tmem + 16 - (s.tmem & 7);
+  s.rows = s.first + (uint32_t)(E + 2) / 2 * 8;
+  s.total = s.rows + (uint32_t)E * 8;
+  return s;
+}
+
+// Four 8-bit integers to f16, in pairs: u = v + 128 in the low mantissa bits of 1024 is
+// 1024 + u, and 1152 off is v, exactly.
+__device__ __forceinline__ void int8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  const uint32_t p = __byte_perm(w, 0x64646464u, 0x4140), q = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 off = __half2half2(__ushort_as_half(0x6480));
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&p), off);
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&q), off);
+  lo = *reinterpret_cast<const uint32_t*>(&a);
+  hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c, int r,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(c), "r"(r), "r"(bar)
+      : "memory");
+}
+
+// Row r's row of x, or -1 for a row of zeros.
+__device__ __forceinline__ int64_t source_row(const MatmulInt8Args& a, int64_t r, unsigned* err) {
+  int64_t s = r;
+  if (a.src != nullptr) {
+    const int v = __ldg(a.src + r);
+    if (v < 0) return -1;
+    s = v / a.k;
+  }
+  if (s >= a.num_x) {
+    flag_error(err, MOE_DEVERR_POS_RANGE);
+    return -1;
+  }
+  return s;
+}
+
+__device__ __forceinline__ void store_out(const MatmulInt8Args& a, int64_t at, float v) {
+  if (a.out_f32)
+    static_cast<float*>(a.out)[at] = v;
+  else
+    static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Stage and phase of a ring, step by step.
+struct Ring {
+  int i = 0;
+  uint32_t phase = 0;
+  template <int N>
+  __device__ __forceinline__ void next() {
+    if (++i == N) i = 0, phase ^= 1u;
+  }
+};
+
+template <class S>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_matmul_kernel(const MatmulInt8Args a, const __grid_constant__ CUtensorMap map,
+                         unsigned* err) {
+  constexpr int NT = S::NT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const Smem L = smem_layout<S>(a.E);
+  const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
+  float* s_xsf = reinterpret_cast<float*>(smem + L.xsf);
+  int* first = reinterpret_cast<int*>(smem + L.first);
+  int2* rows_of = reinterpret_cast<int2*>(smem + L.rows);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  // barriers: weights in / out of a shared stage, rows in / out, weights in / out of a
+  // tensor-memory stage, accumulators full / free, and one to drain the products
+  const uint32_t a_full = sbase + L.bars, a_free = a_full + S::SA * 8;
+  const uint32_t b_full = a_free + S::SA * 8, b_free = b_full + S::SB * 8;
+  const uint32_t t_full = b_free + S::SB * 8, t_free = t_full + S::ST * 8;
+  const uint32_t c_full = t_free + S::ST * 8, c_free = c_full + 8, drain = c_free + 8;
+
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
+    for (int i = 0; i < S::SA; ++i) mbar_init_n(a_full + i * 8, 1), mbar_init_n(a_free + i * 8, kConvert);
+    for (int i = 0; i < S::SB; ++i) mbar_init_n(b_full + i * 8, kGather), mbar_init_n(b_free + i * 8, 1);
+    for (int i = 0; i < S::ST; ++i) mbar_init_n(t_full + i * 8, kConvert), mbar_init_n(t_free + i * 8, 1);
+    mbar_init_n(c_full, 1);
+    mbar_init_n(c_free, kConvert);
+    mbar_init_n(drain, 1);
+    mbar_init_done();
+  }
+  if (warp == 13) tmem_alloc(sbase + L.tmem);
   pdl_enter();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int e = blockIdx.y;
-  int64_t lo = 0, hi = a.R;
-  if (a.offsets != nullptr) {
-    lo = a.offsets[e], hi = a.offsets[e + 1];
-    if (lo < 0 || hi > a.R) flag_error(err, MOE_DEVERR_POS_RANGE);
-    if (lo < 0) lo = 0;
-    if (hi > a.R) hi = a.R;
+
+  // first[e]: runs of up to NT rows of the experts before e
+  {
+    constexpr int kPer = (MOE_MAX_EXPERTS + kThreads - 1) / kThreads;
+    int* totals = reinterpret_cast<int*>(smem + L.totals);
+    int runs[kPer] = {};
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = kPer * tid + i;
+      if (e >= a.E) continue;
+      int64_t lo = 0, hi = a.R;
+      if (a.offsets != nullptr) {
+        lo = __ldg(a.offsets + e);
+        hi = __ldg(a.offsets + e + 1);
+        if (lo < 0 || hi > a.R) flag_error(err, MOE_DEVERR_POS_RANGE);
+        if (lo < 0) lo = 0;
+        if (hi > a.R) hi = a.R;
+      }
+      rows_of[e] = make_int2((int)lo, (int)hi);
+      runs[i] = hi > lo ? (int)((hi - lo + NT - 1) / NT) : 0;
+      sum += runs[i];
+    }
+    const int own = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) totals[warp] = sum;
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    int before = sum - own;
+    for (int w = 0; w < warp; ++w) before += totals[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (kPer * tid + i <= a.E) first[kPer * tid + i] = before;
+      before += runs[i];
+    }
+    __syncthreads();
   }
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L.tmem);
   const int M = a.swiglu ? 2 * a.N : a.N;
-  const int per = a.swiglu ? kOuts / 2 : kOuts;
-  const int n0 = (blockIdx.x * kWarps + warp) * per;
-  if (n0 >= a.N) return;
-  int m[kOuts];
+  const int per_tile = a.swiglu ? kHalf : 2 * kHalf;
+  const int tiles = (a.N + per_tile - 1) / per_tile;
+  const int nblk = (a.K + kBlockK - 1) / kBlockK;
+  const int64_t items = (int64_t)first[a.E] * tiles;
+
+  // one item: an expert, a tile of outputs and a run of rows; an expert's runs of one
+  // tile follow one another, so that its weights are read once from HBM
+  struct Item {
+    int e, tile, n;
+    int64_t r0;
+  };
+  auto item_at = [&](int64_t it) {
+    const int q = (int)(it / tiles);
+    int e = 0;  // the last expert with first[e] <= q
+    for (int hi = a.E; hi - e > 1;) {
+      const int mid = (e + hi) >> 1;
+      if (first[mid] <= q)
+        e = mid;
+      else
+        hi = mid;
+    }
+    const int runs = first[e + 1] - first[e];
+    const int64_t local = it - (int64_t)first[e] * tiles;
+    Item m;
+    m.e = e;
+    m.tile = (int)(local / runs);
+    const int2 rows = rows_of[e];
+    const int run = (int)(local - (int64_t)m.tile * runs);
+    m.r0 = rows.x + (int64_t)run * NT;
+    m.n = (int)(rows.y - m.r0 < NT ? rows.y - m.r0 : NT);
+    return m;
+  };
+  bool ok = true;  // no wait ran out
+  auto wait = [&](uint32_t bar, uint32_t phase) {
+    if (ok && !mbar_wait(bar, phase)) {
+      ok = false;
+      flag_error(err, MOE_DEVERR_TIMEOUT);
+    }
+    return ok;
+  };
+  // the same for a whole warp, with one answer
+  auto wait_warp = [&](uint32_t bar, uint32_t phase) {
+    return ok = __all_sync(0xFFFFFFFFu, wait(bar, phase));
+  };
+
+  if (warp < kConvert) {
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + (uint32_t)((warp & 3) * 32) * kTmemLane;
+    Ring ra, rt;
+    uint32_t c_phase = 0;
+    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const Item m = item_at(it);
+      // the scales of the run's rows, asked for early
+      float my_xsf = 0.0f;
+      if (tid < m.n) {
+        const int64_t s = source_row(a, m.r0 + tid, err);
+        if (s >= 0) my_xsf = __ldg(a.x_sf + s);
+      }
+      const int n0 = m.tile * per_tile + row, n1 = n0 + kHalf;  // n1 without SwiGLU
+      const float* wsf = a.w_sf + (int64_t)m.e * M;
+      const float w0 = n0 < a.N ? __ldg(wsf + n0) : 0.0f;
+      const float w1 = a.swiglu ? (n0 < a.N ? __ldg(wsf + a.N + n0) : 0.0f)
+                                : (n1 < a.N ? __ldg(wsf + n1) : 0.0f);
+      for (int kb = 0; kb < nblk; ++kb) {
+        if (!wait_warp(a_full + ra.i * 8, ra.phase)) break;
+        const uint32_t at = sbase + L.a + (uint32_t)(ra.i * kABytes + half * (kABytes / 2) + row * 128);
+        uint32_t f[2][32];
 #pragma unroll
-  for (int j = 0; j < kOuts; ++j) {
-    const int n = n0 + (a.swiglu ? j / 2 : j);
-    m[j] = (n < a.N ? n : a.N - 1) + (a.swiglu && (j & 1) ? a.N : 0);
-  }
-  for (int64_t r0 = lo; r0 < hi; r0 += kRows) {
-    int64_t s[kRows];
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = lds_v4(at + (uint32_t)((c ^ (row & 7)) << 4));
+          uint32_t* o = f[c >> 2] + (c & 3) * 8;
+          int8x4_to_f16(v.x, o[0], o[1]);
+          int8x4_to_f16(v.y, o[2], o[3]);
+          int8x4_to_f16(v.z, o[4], o[5]);
+          int8x4_to_f16(v.w, o[6], o[7]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(a_free + ra.i * 8);
+        if (!wait_warp(t_free + rt.i * 8, rt.phase ^ 1u)) break;
+        tc_after_sync();
+        const uint32_t to = lanes + (uint32_t)(S::kColA + rt.i * 128 + half * 64);
+        tmem_store32(to, f[0]);
+        tmem_store32(to + 32, f[1]);
+        tmem_store_wait();
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(t_full + rt.i * 8);
+        ra.next<S::SA>();
+        rt.next<S::ST>();
+      }
+      // ---- the tile's outputs: this warp's lanes, half of its columns
+      if (tid < NT) s_xsf[tid] = my_xsf;
+      ok = named_and(1, kConvert * 32, ok);
+      if (ok && wait_warp(c_full, c_phase)) {
+        tc_after_sync();
+        for (int c = half * (NT / 2); c < (half + 1) * (NT / 2) && c < m.n; c += 16) {
+          float x[16], y[16];
+          __syncwarp();
+          tmem_load16x2(lanes + c, lanes + NT + c, x, y);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      s[i] = -1;
-      if (r0 + i >= hi) continue;
-      s[i] = r0 + i;
-      if (a.src != nullptr) s[i] = a.src[r0 + i] < 0 ? -1 : a.src[r0 + i] / a.k;
-      if (s[i] >= a.num_x) {
-        flag_error(err, MOE_DEVERR_POS_RANGE);
-        s[i] = -1;
+          for (int j = 0; j < 16; ++j) {
+            if (c + j >= m.n) break;
+            const float xs = s_xsf[c + j];
+            const float p = x[j] * xs * w0, q = y[j] * xs * w1;
+            const int64_t to = (m.r0 + c + j) * a.N;
+            if (a.swiglu) {
+              if (n0 < a.N) store_out(a, to + n0, p / (1.0f + expf(-p)) * q);
+            } else {
+              if (n0 < a.N) store_out(a, to + n0, p);
+              if (n1 < a.N) store_out(a, to + n1, q);
+            }
+          }
+        }
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c_free);
+      }
+      c_phase ^= 1u;
+      // the scales may be written over; the converting warps leave together
+      ok = named_and(1, kConvert * 32, ok);
+    }
+  } else if (warp < kConvert + kGather) {
+    constexpr int kUnits = NT * 8 / 128;  // 16-channel units per thread and stage
+    const int g = tid - kConvert * 32, c = g & 7, r0 = g >> 3;
+    Ring rb;
+    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const Item m = item_at(it);
+      const int8_t* from[kUnits];
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int r = r0 + 16 * u;
+        from[u] = nullptr;
+        if (r < m.n) {
+          const int64_t s = source_row(a, m.r0 + r, err);
+          if (s >= 0) from[u] = a.x + s * a.K + c * 16;
+        }
+      }
+      uint4 v[kUnits];
+      auto fetch = [&](int kb) {
+        const int k0 = kb * kBlockK;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          v[u] = make_uint4(0, 0, 0, 0);
+          if (from[u] != nullptr && k0 + c * 16 < a.K) v[u] = ld_v4(from[u] + k0);
+        }
+      };
+      fetch(0);
+      for (int kb = 0; kb < nblk; ++kb) {
+        if (!wait_warp(b_free + rb.i * 8, rb.phase ^ 1u)) break;
+        // channels 64 to 127 lie in a second block of rows; the lanes of its units store
+        // their odd half first, so that 8 lanes meet 8 different groups of banks
+        const uint32_t blk = sbase + L.b + (uint32_t)(rb.i * S::kBBytes + (c >> 2) * (NT * 128));
+        const int odd = c >> 2;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          const int r = r0 + 16 * u;
+          if (r >= m.n) break;
+          uint32_t f[8];
+          int8x4_to_f16(v[u].x, f[0], f[1]);
+          int8x4_to_f16(v[u].y, f[2], f[3]);
+          int8x4_to_f16(v[u].z, f[4], f[5]);
+          int8x4_to_f16(v[u].w, f[6], f[7]);
+          const uint32_t rowat = blk + (uint32_t)(r * 128);
+          const int ch = (c & 3) * 2;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int hh = h ^ odd;
+            sts_v4(rowat + (uint32_t)(((ch + hh) ^ (r & 7)) << 4), hh ? f[4] : f[0],
+                   hh ? f[5] : f[1], hh ? f[6] : f[2], hh ? f[7] : f[3]);
+          }
+        }
+        if (kb + 1 < nblk) fetch(kb + 1);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_full + rb.i * 8);
+        rb.next<S::SB>();
       }
     }
-    int acc[kRows][kOuts] = {};
-    for (int c = lane * 16; c < a.K; c += 512) {
-      uint4 xv[kRows];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)
-        xv[i] = s[i] >= 0 ? ld_v4(a.x + s[i] * a.K + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < kOuts; ++j) {
-        const uint4 wv = ld_v4(a.w + ((int64_t)e * M + m[j]) * a.K + c);
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          acc[i][j] = __dp4a((int)wv.x, (int)xv[i].x, acc[i][j]);
-          acc[i][j] = __dp4a((int)wv.y, (int)xv[i].y, acc[i][j]);
-          acc[i][j] = __dp4a((int)wv.z, (int)xv[i].z, acc[i][j]);
-          acc[i][j] = __dp4a((int)wv.w, (int)xv[i].w, acc[i][j]);
+  } else if (warp == 12) {
+    if (lane == 0) {
+      Ring ra;
+      int64_t asked = 0;
+      for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        const Item m = item_at(it);
+        // rows past the expert's last output are another's, or past the tensor and zero:
+        // their products are not stored
+        const int r0 = m.e * M + m.tile * per_tile;
+        const int r1 = a.swiglu ? r0 + a.N : r0 + kHalf;
+        for (int kb = 0; kb < nblk; ++kb) {
+          if (!wait(a_free + ra.i * 8, ra.phase ^ 1u)) break;
+          const uint32_t bar = a_full + ra.i * 8, dst = sbase + L.a + (uint32_t)(ra.i * kABytes);
+          const bool box_ok = MOE_DBG_OK(dst % 1024 == 0 && dst + kABytes <= sbase + L.b, err);
+          mbar_expect(bar, box_ok ? kABytes : 0);
+          if (box_ok) {
+            tma_box(dst, &map, kb * kBlockK, r0, bar);
+            tma_box(dst + kABytes / 2, &map, kb * kBlockK, r1, bar);
+          }
+          ++asked;
+          ra.next<S::SA>();
+        }
+      }
+      if (!ok) {
+        // what may still be on its way: the last SA stages, each waited for (bounded)
+        for (int i = 0; i < S::SA && i < asked; ++i) {
+          if (ra.i == 0) ra.i = S::SA, ra.phase ^= 1u;
+          --ra.i;
+          (void)mbar_wait(a_full + ra.i * 8, ra.phase);
         }
       }
     }
+  } else {
+    if (lane == 0) {
+      Ring rb, rt;
+      uint32_t c_phase = 0;
+      bool any = false;
+      for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        const Item m = item_at(it);
+        const uint32_t idesc = tc_idesc_f16(kHalf, (m.n + 15) / 16 * 16);
+        if (!wait(c_free, c_phase ^ 1u)) break;
+        for (int kb = 0; kb < nblk; ++kb) {
+          if (!wait(b_full + rb.i * 8, rb.phase)) break;
+          if (!wait(t_full + rt.i * 8, rt.phase)) break;
+          tc_after_sync();
+          const uint64_t b0 = tc_desc_sw128(sbase + L.b + (uint32_t)(rb.i * S::kBBytes));
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      float o[kOuts];
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < kOuts; ++j) {
-        const int sum = (int)__reduce_add_sync(0xFFFFFFFFu, acc[i][j]);
-        o[j] = s[i] >= 0 ? (float)sum * a.x_sf[s[i]] * a.w_sf[(int64_t)e * M + m[j]] : 0.0f;
+            for (int s = 0; s < kBlockK / 16; ++s)
+              tc_mma_f16(tmem + (uint32_t)(h * NT),
+                         tmem + (uint32_t)(S::kColA + rt.i * 128 + h * 64 + s * 8),
+                         b0 + (uint64_t)((s >> 2) * (NT * 128) >> 4) + (uint64_t)((s & 3) * 2),
+                         idesc, kb > 0 || s > 0);
+          any = true;
+          tc_commit(b_free + rb.i * 8);
+          tc_commit(t_free + rt.i * 8);
+          rb.next<S::SB>();
+          rt.next<S::ST>();
+        }
+        if (!ok) break;
+        tc_commit(c_full);
+        c_phase ^= 1u;
       }
-      if (r0 + i >= hi || lane >= per || n0 + lane >= a.N) continue;
-      float v = o[0];
-#pragma unroll
-      for (int j = 0; j < kOuts; ++j)
-        if (!a.swiglu && lane == j) v = o[j];
-      if (a.swiglu) {
-        const float g = lane ? o[2] : o[0], u = lane ? o[3] : o[1];
-        v = g / (1.0f + expf(-g)) * u;
+      if (!ok && any) {  // the products in flight end before tensor memory is given back
+        tc_commit(drain);
+        (void)mbar_wait(drain, 0);
       }
-      const int64_t at = (r0 + i) * a.N + n0 + lane;
-      if (a.out_f32)
-        static_cast<float*>(a.out)[at] = v;
-      else
-        static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
     }
   }
+  __syncwarp();
+  tc_before_sync();
+  __syncthreads();
+  if (warp == 13) {
+    tc_after_sync();
+    tmem_free(tmem);
+  }
+}
+
+// The weights as a tensor of rows of K bytes, in boxes of 128 rows of 128 bytes.
+cudaError_t weight_map(const MatmulInt8Args& a, CUtensorMap* map) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(fn)
+                                                                    : nullptr;
+  }();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.E * a.N * (a.swiglu ? 2 : 1)};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.K};
+  const cuuint32_t box[2] = {kBlockK, kHalf}, unit[2] = {1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(a.w), dims,
+                            strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <class S>
+cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a) {
+  auto* kernel = expert_matmul_kernel<S>;
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.once(kernel);
+  if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  e = weight_map(a, &map);
+  if (e != cudaSuccess) return e;
+  const int per_tile = a.swiglu ? kHalf : 2 * kHalf;
+  int64_t runs = (a.offsets ? a.E : 1) + a.R / S::NT;
+  if (runs > a.R) runs = a.R;
+  const int64_t items = runs * ((a.N + per_tile - 1) / per_tile);
+  const int64_t blocks = items < c.num_sms ? items : c.num_sms;
+  return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, smem_layout<S>(a.E).total, c.stream,
+                    a, map, c.err);
 }
 
 }  // namespace
 
 cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& a) {
-  const int per = kWarps * (a.swiglu ? kOuts / 2 : kOuts);
-  return launch_pdl(expert_matmul_simple_kernel, dim3((unsigned)((a.N + per - 1) / per), a.E),
-                    kWarps * 32, 0, c.stream, a, c.err);
+  // few rows per expert: short tiles, and more weights on their way
+  if (a.R <= 24 * (int64_t)a.E) return launch_t<Shape<32, 5, 4, 3>>(c, a);
+  return launch_t<Shape<128, 3, 3, 2>>(c, a);
 }
 
 }  // namespace moe
