@@ -15,9 +15,10 @@
 // One CTA per SM, its warps in roles joined by barriers:
 //   0-7    convert a stage of weights (a thread per weight row) into tensor memory, and
 //          write the finished tiles out; 4 warps per half
-//   8-11   gather, convert and store the rows of x
-//   12     asks for the weights (TMA, 128-byte swizzle)
-//   13     issues the products
+//   8-15   gather, convert and store the rows of x
+//   16     asks for the weights (TMA, 128-byte swizzle)
+//   17-18  issue the products of one half each: what one waits for does not keep the
+//          tensor cores from the other's
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -26,10 +27,10 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 14;
+constexpr int kWarps = 19;
 constexpr int kThreads = kWarps * 32;
 constexpr int kConvert = 8;          // warps 0 .. 7
-constexpr int kGather = 4;           // warps 8 .. 11
+constexpr int kGather = 8;           // warps 8 .. 15
 constexpr int kBlockK = 128;         // channels per stage
 constexpr int kHalf = 128;           // outputs of one accumulator
 constexpr int kABytes = 2 * kHalf * kBlockK;
@@ -53,7 +54,7 @@ __host__ __device__ inline Smem smem_layout(int E) {
   s.a = 0;
   s.b = s.a + S::SA * kABytes;
   s.bars = s.b + S::SB * S::kBBytes;
-  s.xsf = s.bars + (2 * S::SA + 2 * S::SB + 2 * S::ST + 3) * 8;
+  s.xsf = s.bars + (2 * S::SA + 2 * S::SB + 4 * S::ST + 4) * 8;
   s.totals = s.xsf + S::NT * 4;
   s.tmem = s.totals + kWarps * 4;
   s.first = s.tmem + 16 - (s.tmem & 7);
@@ -139,24 +140,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   int2* rows_of = reinterpret_cast<int2*>(smem + L.rows);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-  // barriers: weights in / out of a shared stage, rows in / out, weights in / out of a
-  // tensor-memory stage, accumulators full / free, and one to drain the products
+  // barriers: weights in / out of a shared stage, rows in / out, a half's weights in / out
+  // of a tensor-memory stage, accumulators full / free, and two to drain the products
   const uint32_t a_full = sbase + L.bars, a_free = a_full + S::SA * 8;
   const uint32_t b_full = a_free + S::SA * 8, b_free = b_full + S::SB * 8;
-  const uint32_t t_full = b_free + S::SB * 8, t_free = t_full + S::ST * 8;
-  const uint32_t c_full = t_free + S::ST * 8, c_free = c_full + 8, drain = c_free + 8;
+  const uint32_t t_full = b_free + S::SB * 8, t_free = t_full + 2 * S::ST * 8;
+  const uint32_t c_full = t_free + 2 * S::ST * 8, c_free = c_full + 8, drain = c_free + 8;
 
   if (tid == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     for (int i = 0; i < S::SA; ++i) mbar_init_n(a_full + i * 8, 1), mbar_init_n(a_free + i * 8, kConvert);
-    for (int i = 0; i < S::SB; ++i) mbar_init_n(b_full + i * 8, kGather), mbar_init_n(b_free + i * 8, 1);
-    for (int i = 0; i < S::ST; ++i) mbar_init_n(t_full + i * 8, kConvert), mbar_init_n(t_free + i * 8, 1);
-    mbar_init_n(c_full, 1);
+    for (int i = 0; i < S::SB; ++i) mbar_init_n(b_full + i * 8, kGather), mbar_init_n(b_free + i * 8, 2);
+    for (int i = 0; i < 2 * S::ST; ++i) mbar_init_n(t_full + i * 8, kConvert / 2), mbar_init_n(t_free + i * 8, 1);
+    mbar_init_n(c_full, 2);
     mbar_init_n(c_free, kConvert);
     mbar_init_n(drain, 1);
+    mbar_init_n(drain + 8, 1);
     mbar_init_done();
   }
-  if (warp == 13) tmem_alloc(sbase + L.tmem);
+  if (warp == kWarps - 1) tmem_alloc(sbase + L.tmem);
   pdl_enter();
 
   // first[e]: runs of up to NT rows of the experts before e
@@ -268,27 +270,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < nblk; ++kb) {
         if (!wait_warp(a_full + ra.i * 8, ra.phase)) break;
         const uint32_t at = sbase + L.a + (uint32_t)(ra.i * kABytes + half * (kABytes / 2) + row * 128);
-        uint32_t f[2][32];
+        uint4 v[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 v = lds_v4(at + (uint32_t)((c ^ (row & 7)) << 4));
-          uint32_t* o = f[c >> 2] + (c & 3) * 8;
-          int8x4_to_f16(v.x, o[0], o[1]);
-          int8x4_to_f16(v.y, o[2], o[3]);
-          int8x4_to_f16(v.z, o[4], o[5]);
-          int8x4_to_f16(v.w, o[6], o[7]);
-        }
+        for (int c = 0; c < 8; ++c) v[c] = lds_v4(at + (uint32_t)((c ^ (row & 7)) << 4));
+        uint32_t f[32];
+        auto convert = [&](int c0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t* o = f + c * 8;
+            int8x4_to_f16(v[c0 + c].x, o[0], o[1]);
+            int8x4_to_f16(v[c0 + c].y, o[2], o[3]);
+            int8x4_to_f16(v[c0 + c].z, o[4], o[5]);
+            int8x4_to_f16(v[c0 + c].w, o[6], o[7]);
+          }
+        };
+        convert(0);
         __syncwarp();
         if (lane == 0) mbar_arrive(a_free + ra.i * 8);
-        if (!wait_warp(t_free + rt.i * 8, rt.phase ^ 1u)) break;
+        if (!wait_warp(t_free + (half * S::ST + rt.i) * 8, rt.phase ^ 1u)) break;
         tc_after_sync();
         const uint32_t to = lanes + (uint32_t)(S::kColA + rt.i * 128 + half * 64);
-        tmem_store32(to, f[0]);
-        tmem_store32(to + 32, f[1]);
+        tmem_store32(to, f);
+        convert(4);
+        tmem_store32(to + 32, f);
         tmem_store_wait();
         tc_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(t_full + rt.i * 8);
+        if (lane == 0) mbar_arrive(t_full + (half * S::ST + rt.i) * 8);
         ra.next<S::SA>();
         rt.next<S::ST>();
       }
@@ -324,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = named_and(1, kConvert * 32, ok);
     }
   } else if (warp < kConvert + kGather) {
-    constexpr int kUnits = NT * 8 / 128;  // 16-channel units per thread and stage
+    // a thread's units of 16 channels of a stage: rows r0, r0 + kStep, ..
+    constexpr int kStep = kGather * 4, kUnits = NT > kStep ? NT / kStep : 1;
     const int g = tid - kConvert * 32, c = g & 7, r0 = g >> 3;
     Ring rb;
     for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
@@ -332,15 +341,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int8_t* from[kUnits];
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int r = r0 + 16 * u;
+        const int r = r0 + kStep * u;
         from[u] = nullptr;
         if (r < m.n) {
           const int64_t s = source_row(a, m.r0 + r, err);
           if (s >= 0) from[u] = a.x + s * a.K + c * 16;
         }
       }
-      uint4 v[kUnits];
-      auto fetch = [&](int kb) {
+      auto fetch = [&](uint4 (&v)[kUnits], int kb) {
         const int k0 = kb * kBlockK;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
@@ -348,16 +356,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (from[u] != nullptr && k0 + c * 16 < a.K) v[u] = ld_v4(from[u] + k0);
         }
       };
-      fetch(0);
-      for (int kb = 0; kb < nblk; ++kb) {
-        if (!wait_warp(b_free + rb.i * 8, rb.phase ^ 1u)) break;
+      // one stage from registers that were asked for two stages before
+      auto stage = [&](uint4 (&v)[kUnits], int kb) {
+        if (!wait_warp(b_free + rb.i * 8, rb.phase ^ 1u)) return;
         // channels 64 to 127 lie in a second block of rows; the lanes of its units store
         // their odd half first, so that 8 lanes meet 8 different groups of banks
         const uint32_t blk = sbase + L.b + (uint32_t)(rb.i * S::kBBytes + (c >> 2) * (NT * 128));
         const int odd = c >> 2;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-          const int r = r0 + 16 * u;
+          const int r = r0 + kStep * u;
           if (r >= m.n) break;
           uint32_t f[8];
           int8x4_to_f16(v[u].x, f[0], f[1]);
@@ -373,14 +381,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                    hh ? f[5] : f[1], hh ? f[6] : f[2], hh ? f[7] : f[3]);
           }
         }
-        if (kb + 1 < nblk) fetch(kb + 1);
+        fetch(v, kb + 2);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_full + rb.i * 8);
         rb.next<S::SB>();
+      };
+      uint4 v0[kUnits], v1[kUnits];
+      fetch(v0, 0);
+      fetch(v1, 1);
+      for (int kb = 0; kb < nblk && ok; kb += 2) {
+        stage(v0, kb);
+        if (kb + 1 < nblk && ok) stage(v1, kb + 1);
       }
     }
-  } else if (warp == 12) {
+  } else if (warp == kConvert + kGather) {
     if (lane == 0) {
       Ring ra;
       int64_t asked = 0;
@@ -414,6 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     if (lane == 0) {
+      const int h = warp - (kWarps - 2);
+      const uint32_t th_full = t_full + h * S::ST * 8, th_free = t_free + h * S::ST * 8;
       Ring rb, rt;
       uint32_t c_phase = 0;
       bool any = false;
@@ -423,20 +440,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(c_free, c_phase ^ 1u)) break;
         for (int kb = 0; kb < nblk; ++kb) {
           if (!wait(b_full + rb.i * 8, rb.phase)) break;
-          if (!wait(t_full + rt.i * 8, rt.phase)) break;
+          if (!wait(th_full + rt.i * 8, rt.phase)) break;
           tc_after_sync();
           const uint64_t b0 = tc_desc_sw128(sbase + L.b + (uint32_t)(rb.i * S::kBBytes));
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int s = 0; s < kBlockK / 16; ++s)
-              tc_mma_f16(tmem + (uint32_t)(h * NT),
-                         tmem + (uint32_t)(S::kColA + rt.i * 128 + h * 64 + s * 8),
-                         b0 + (uint64_t)((s >> 2) * (NT * 128) >> 4) + (uint64_t)((s & 3) * 2),
-                         idesc, kb > 0 || s > 0);
+          for (int s = 0; s < kBlockK / 16; ++s)
+            tc_mma_f16(tmem + (uint32_t)(h * NT),
+                       tmem + (uint32_t)(S::kColA + rt.i * 128 + h * 64 + s * 8),
+                       b0 + (uint64_t)((s >> 2) * (NT * 128) >> 4) + (uint64_t)((s & 3) * 2),
+                       idesc, kb > 0 || s > 0);
           any = true;
           tc_commit(b_free + rb.i * 8);
-          tc_commit(t_free + rt.i * 8);
+          tc_commit(th_free + rt.i * 8);
           rb.next<S::SB>();
           rt.next<S::ST>();
         }
@@ -445,15 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         c_phase ^= 1u;
       }
       if (!ok && any) {  // the products in flight end before tensor memory is given back
-        tc_commit(drain);
-        (void)mbar_wait(drain, 0);
+        tc_commit(drain + h * 8);
+        (void)mbar_wait(drain + h * 8, 0);
       }
     }
   }
   __syncwarp();
   tc_before_sync();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == kWarps - 1) {
     tc_after_sync();
     tmem_free(tmem);
   }
