@@ -36,25 +36,29 @@ constexpr int kHalf = 128;           // outputs of one accumulator
 constexpr int kABytes = 2 * kHalf * kBlockK;
 
 // NT rows per tile; SA stages of weights (bytes) and SB of rows (f16) in shared memory,
-// ST of weights (f16) in tensor memory, behind the two accumulators.
-template <int NT_, int SA_, int SB_, int ST_>
+// ST of weights (f16) in tensor memory, behind the two accumulators.  SPLIT: the CTAs of
+// a cluster take equal parts of K of one tile and add their sums up.
+template <int NT_, int SA_, int SB_, int ST_, bool SPLIT_>
 struct Shape {
   static constexpr int NT = NT_, SA = SA_, SB = SB_, ST = ST_;
+  static constexpr bool SPLIT = SPLIT_;
+  static constexpr int kPartBytes = SPLIT ? 2 * NT * kHalf * 4 : 0;
   static constexpr int kBBytes = NT * kBlockK * 2;
   static constexpr int kColA = 2 * NT;  // first column of the weights
   static_assert(kColA + ST * 128 <= 512, "tensor memory has 512 columns");
 };
 
 struct Smem {
-  uint32_t a, b, bars, xsf, totals, tmem, first, rows, total;
+  uint32_t a, b, part, bars, xsf, totals, tmem, first, rows, total;
 };
 template <class S>
 __host__ __device__ inline Smem smem_layout(int E) {
   Smem s;
   s.a = 0;
   s.b = s.a + S::SA * kABytes;
-  s.bars = s.b + S::SB * S::kBBytes;
-  s.xsf = s.bars + (2 * S::SA + 2 * S::SB + 4 * S::ST + 4) * 8;
+  s.part = s.b + S::SB * S::kBBytes;
+  s.bars = s.part + S::kPartBytes;
+  s.xsf = s.bars + (2 * S::SA + 2 * S::SB + 4 * S::ST + 6) * 8;
   s.totals = s.xsf + S::NT * 4;
   s.tmem = s.totals + kWarps * 4;
   s.first = s.tmem + 16 - (s.tmem & 7);
@@ -146,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t b_full = a_free + S::SA * 8, b_free = b_full + S::SB * 8;
   const uint32_t t_full = b_free + S::SB * 8, t_free = t_full + 2 * S::ST * 8;
   const uint32_t c_full = t_free + 2 * S::ST * 8, c_free = c_full + 8, drain = c_free + 8;
+  const uint32_t p_full = drain + 16, p_free = p_full + 8;  // SPLIT: sums written, read
 
   if (tid == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
@@ -156,9 +161,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init_n(c_free, kConvert);
     mbar_init_n(drain, 1);
     mbar_init_n(drain + 8, 1);
+    if (S::SPLIT) {
+      mbar_init_n(p_full, kConvert * (int)cluster_size());
+      mbar_init_n(p_free, kConvert * (int)cluster_size());
+    }
     mbar_init_done();
   }
   if (warp == kWarps - 1) tmem_alloc(sbase + L.tmem);
+  __syncwarp();
+  if (S::SPLIT) cluster_sync();  // the barriers, before a peer arrives at one
   pdl_enter();
 
   // first[e]: runs of up to NT rows of the experts before e
@@ -208,6 +219,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = (a.N + per_tile - 1) / per_tile;
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
   const int64_t items = (int64_t)first[a.E] * tiles;
+  // this CTA's items, and its part of their channels
+  const int ctas = S::SPLIT ? (int)cluster_size() : 1, rank = S::SPLIT ? (int)cluster_rank() : 0;
+  const int64_t item0 = blockIdx.x / ctas, item_step = gridDim.x / ctas;
+  const int kb0 = nblk * rank / ctas, kb1 = nblk * (rank + 1) / ctas;
 
   // one item: an expert, a tile of outputs and a run of rows; an expert's runs of one
   // tile follow one another, so that its weights are read once from HBM
@@ -232,8 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     m.tile = (int)(local / runs);
     const int2 rows = rows_of[e];
     const int run = (int)(local - (int64_t)m.tile * runs);
-    m.r0 = rows.x + (int64_t)run * NT;
-    m.n = (int)(rows.y - m.r0 < NT ? rows.y - m.r0 : NT);
+    // equal runs, in whole 16 rows
+    const int per = ((rows.y - rows.x + runs - 1) / runs + 15) / 16 * 16;
+    m.r0 = rows.x + (int64_t)run * per;
+    m.n = (int)(rows.y - m.r0 < per ? rows.y - m.r0 : per);
     return m;
   };
   bool ok = true;  // no wait ran out
@@ -254,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + (uint32_t)((warp & 3) * 32) * kTmemLane;
     Ring ra, rt;
     uint32_t c_phase = 0;
-    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+    for (int64_t it = item0; it < items && ok; it += item_step) {
       const Item m = item_at(it);
       // the scales of the run's rows, asked for early
       float my_xsf = 0.0f;
@@ -267,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float w0 = n0 < a.N ? __ldg(wsf + n0) : 0.0f;
       const float w1 = a.swiglu ? (n0 < a.N ? __ldg(wsf + a.N + n0) : 0.0f)
                                 : (n1 < a.N ? __ldg(wsf + n1) : 0.0f);
-      for (int kb = 0; kb < nblk; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait_warp(a_full + ra.i * 8, ra.phase)) break;
         const uint32_t at = sbase + L.a + (uint32_t)(ra.i * kABytes + half * (kABytes / 2) + row * 128);
         uint4 v[8];
@@ -303,8 +320,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the tile's outputs: this warp's lanes, half of its columns
       if (tid < NT) s_xsf[tid] = my_xsf;
       ok = named_and(1, kConvert * 32, ok);
+      auto finish = [&](float p, float q, float xs, float u0, float u1, int64_t at, int n) {
+        // p and q: the sums of output n and, behind it, of its partner
+        p *= xs * u0, q *= xs * u1;
+        if (a.swiglu) {
+          if (n < a.N) store_out(a, at + n, p / (1.0f + expf(-p)) * q);
+        } else {
+          if (n < a.N) store_out(a, at + n, p);
+          if (n + kHalf < a.N) store_out(a, at + n + kHalf, q);
+        }
+      };
+      if (S::SPLIT && ok) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(p_free, c_phase ^ 1u));
+        if (!ok) flag_error(err, MOE_DEVERR_TIMEOUT);
+      }
       if (ok && wait_warp(c_full, c_phase)) {
         tc_after_sync();
+        float* part = reinterpret_cast<float*>(smem + L.part);
         for (int c = half * (NT / 2); c < (half + 1) * (NT / 2) && c < m.n; c += 16) {
           float x[16], y[16];
           __syncwarp();
@@ -312,20 +344,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             if (c + j >= m.n) break;
-            const float xs = s_xsf[c + j];
-            const float p = x[j] * xs * w0, q = y[j] * xs * w1;
-            const int64_t to = (m.r0 + c + j) * a.N;
-            if (a.swiglu) {
-              if (n0 < a.N) store_out(a, to + n0, p / (1.0f + expf(-p)) * q);
+            if constexpr (S::SPLIT) {
+              part[(c + j) * kHalf + row] = x[j];
+              part[(NT + c + j) * kHalf + row] = y[j];
             } else {
-              if (n0 < a.N) store_out(a, to + n0, p);
-              if (n1 < a.N) store_out(a, to + n1, q);
+              finish(x[j], y[j], s_xsf[c + j], w0, w1, (m.r0 + c + j) * a.N, n0);
             }
           }
         }
         tc_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(c_free);
+        if constexpr (S::SPLIT) {
+          if (lane < ctas) cluster_arrive(cluster_map(p_full, lane));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(p_full, c_phase));
+          if (!ok) flag_error(err, MOE_DEVERR_TIMEOUT);
+          if (ok) {
+            // this CTA's share of the tile: pairs of sums, added in the CTAs' order
+            const int pairs = m.n * kHalf;
+            const int p0 = pairs * rank / ctas, p1 = pairs * (rank + 1) / ctas;
+            const int l = (p0 + tid) & (kHalf - 1), n = m.tile * per_tile + l;
+            const float u0 = n < a.N ? __ldg(wsf + n) : 0.0f;
+            const int partner = a.swiglu ? a.N + n : n + kHalf;
+            const float u1 = partner < M ? __ldg(wsf + partner) : 0.0f;
+            const uint32_t at = sbase + L.part;
+            for (int p = p0 + tid; p < p1; p += kConvert * 32) {
+              float x = 0.0f, y = 0.0f;
+              for (int r = 0; r < ctas; ++r) {
+                const uint32_t from = cluster_map(at + (uint32_t)p * 4, r);
+                x += cluster_load(from);
+                y += cluster_load(from + NT * kHalf * 4);
+              }
+              const int c = p / kHalf;
+              finish(x, y, s_xsf[c], u0, u1, (m.r0 + c) * a.N, n);
+            }
+          }
+          __syncwarp();
+          if (lane < ctas) cluster_arrive(cluster_map(p_free, lane));
+        }
       }
       c_phase ^= 1u;
       // the scales may be written over; the converting warps leave together
@@ -336,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kStep = kGather * 4, kUnits = NT > kStep ? NT / kStep : 1;
     const int g = tid - kConvert * 32, c = g & 7, r0 = g >> 3;
     Ring rb;
-    for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+    for (int64_t it = item0; it < items && ok; it += item_step) {
       const Item m = item_at(it);
       const int8_t* from[kUnits];
 #pragma unroll
@@ -353,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
           v[u] = make_uint4(0, 0, 0, 0);
-          if (from[u] != nullptr && k0 + c * 16 < a.K) v[u] = ld_v4(from[u] + k0);
+          if (from[u] != nullptr && kb < kb1 && k0 + c * 16 < a.K) v[u] = ld_v4(from[u] + k0);
         }
       };
       // one stage from registers that were asked for two stages before
@@ -388,24 +444,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         rb.next<S::SB>();
       };
       uint4 v0[kUnits], v1[kUnits];
-      fetch(v0, 0);
-      fetch(v1, 1);
-      for (int kb = 0; kb < nblk && ok; kb += 2) {
+      fetch(v0, kb0);
+      fetch(v1, kb0 + 1);
+      for (int kb = kb0; kb < kb1 && ok; kb += 2) {
         stage(v0, kb);
-        if (kb + 1 < nblk && ok) stage(v1, kb + 1);
+        if (kb + 1 < kb1 && ok) stage(v1, kb + 1);
       }
     }
   } else if (warp == kConvert + kGather) {
     if (lane == 0) {
       Ring ra;
       int64_t asked = 0;
-      for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      for (int64_t it = item0; it < items && ok; it += item_step) {
         const Item m = item_at(it);
         // rows past the expert's last output are another's, or past the tensor and zero:
         // their products are not stored
         const int r0 = m.e * M + m.tile * per_tile;
         const int r1 = a.swiglu ? r0 + a.N : r0 + kHalf;
-        for (int kb = 0; kb < nblk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait(a_free + ra.i * 8, ra.phase ^ 1u)) break;
           const uint32_t bar = a_full + ra.i * 8, dst = sbase + L.a + (uint32_t)(ra.i * kABytes);
           const bool box_ok = MOE_DBG_OK(dst % 1024 == 0 && dst + kABytes <= sbase + L.b, err);
@@ -434,11 +490,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring rb, rt;
       uint32_t c_phase = 0;
       bool any = false;
-      for (int64_t it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      for (int64_t it = item0; it < items && ok; it += item_step) {
         const Item m = item_at(it);
         const uint32_t idesc = tc_idesc_f16(kHalf, (m.n + 15) / 16 * 16);
         if (!wait(c_free, c_phase ^ 1u)) break;
-        for (int kb = 0; kb < nblk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait(b_full + rb.i * 8, rb.phase)) break;
           if (!wait(th_full + rt.i * 8, rt.phase)) break;
           tc_after_sync();
@@ -448,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_mma_f16(tmem + (uint32_t)(h * NT),
                        tmem + (uint32_t)(S::kColA + rt.i * 128 + h * 64 + s * 8),
                        b0 + (uint64_t)((s >> 2) * (NT * 128) >> 4) + (uint64_t)((s & 3) * 2),
-                       idesc, kb > 0 || s > 0);
+                       idesc, kb > kb0 || s > 0);
           any = true;
           tc_commit(b_free + rb.i * 8);
           tc_commit(th_free + rt.i * 8);
@@ -468,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_before_sync();
   __syncthreads();
+  if (S::SPLIT) cluster_sync();  // no peer reads or arrives here any more
   if (warp == kWarps - 1) {
     tc_after_sync();
     tmem_free(tmem);
@@ -496,8 +553,48 @@ cudaError_t weight_map(const MatmulInt8Args& a, CUtensorMap* map) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A launch of `blocks` CTAs in clusters of `ctas`.
 template <class S>
-cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a) {
+struct Config {
+  cudaLaunchConfig_t c = {};
+  cudaLaunchAttribute attr[2];
+  Config(int E, int64_t blocks, int ctas) {
+    c.gridDim = dim3((unsigned)blocks);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem_layout<S>(E).total;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    c.attrs = attr;
+    c.numAttrs = S::SPLIT ? 2 : 1;
+  }
+};
+
+// How many clusters of 2, 4 or 8 CTAs the device runs at once: one CTA per SM, and fewer
+// SMs than a die's that a cluster can share.  Asked once per process and size.
+template <class S>
+cudaError_t clusters_at_once(const LaunchCtx& c, int ctas, int* n) {
+  static std::atomic<int> known[4];
+  std::atomic<int>& slot = known[ctas == 2 ? 1 : ctas == 4 ? 2 : 3];
+  *n = slot.load(std::memory_order_relaxed);
+  if (*n > 0) return cudaSuccess;
+  auto* kernel = expert_matmul_kernel<S>;
+  cudaError_t e = allow_max_dynamic_smem(kernel);
+  if (e != cudaSuccess) return e;
+  Config<S> cfg(MOE_MAX_EXPERTS, (int64_t)c.num_sms / ctas * ctas, ctas);
+  // the query takes no launch attribute but the cluster's
+  cfg.attr[0] = cfg.attr[1];
+  cfg.c.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg.c);
+  if (e == cudaSuccess) slot.store(*n, std::memory_order_relaxed);
+  return e;
+}
+
+// `ctas` CTAs per item (a cluster, if more than one).
+template <class S>
+cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a, int64_t groups, int ctas) {
   auto* kernel = expert_matmul_kernel<S>;
   static SmemOptIn opt_in;
   cudaError_t e = opt_in.once(kernel);
@@ -505,21 +602,41 @@ cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a) {
   CUtensorMap map;
   e = weight_map(a, &map);
   if (e != cudaSuccess) return e;
-  const int per_tile = a.swiglu ? kHalf : 2 * kHalf;
-  int64_t runs = (a.offsets ? a.E : 1) + a.R / S::NT;
-  if (runs > a.R) runs = a.R;
-  const int64_t items = runs * ((a.N + per_tile - 1) / per_tile);
-  const int64_t blocks = items < c.num_sms ? items : c.num_sms;
-  return launch_pdl(kernel, dim3((unsigned)blocks), kThreads, smem_layout<S>(a.E).total, c.stream,
-                    a, map, c.err);
+  Config<S> cfg(a.E, groups * ctas, ctas);
+  cfg.c.stream = c.stream;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg.c, kernel, a, map, c.err);
 }
 
 }  // namespace
 
 cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& a) {
-  // few rows per expert: short tiles, and more weights on their way
-  if (a.R <= 24 * (int64_t)a.E) return launch_t<Shape<32, 5, 4, 3>>(c, a);
-  return launch_t<Shape<128, 3, 3, 2>>(c, a);
+  using Whole = Shape<128, 3, 3, 2, false>;
+  using Split = Shape<32, 4, 4, 3, true>;
+  const int per_tile = a.swiglu ? kHalf : 2 * kHalf;
+  const int64_t tiles = (a.N + per_tile - 1) / per_tile;
+  auto items = [&](int nt) {
+    int64_t runs = (a.offsets ? a.E : 1) + (a.R + nt - 1) / nt - 1;
+    if (runs > a.R) runs = a.R;
+    return runs * tiles;
+  };
+  // Few tiles: a cluster shares each one's channels, as long as all clusters run at once
+  // (E = 1, one row, us, 1 : 2 : 4 : 8 CTAs per tile: K = N = 4096 28 : 18 : 12.4 : two
+  // rounds 18; K = 7168, N = 256 46 : 27 : 16.6 : 11.7.  With tiles for 128 CTAs, 1 token
+  // of 8 experts: 49 : two rounds 56 : 94 : 130).
+  const int nblk = (a.K + kBlockK - 1) / kBlockK;
+  const int64_t split = items(Split::NT);
+  int ctas = 1;
+  for (int s = 2; s <= 8 && s <= nblk; s *= 2) {
+    if (split * s > c.num_sms) break;
+    int fit = 0;
+    const cudaError_t e = clusters_at_once<Split>(c, s, &fit);
+    if (e != cudaSuccess) return e;
+    if (split <= fit) ctas = s;
+  }
+  if (ctas > 1) return launch_t<Split>(c, a, split, ctas);
+  const int64_t whole = items(Whole::NT);
+  return launch_t<Whole>(c, a, whole < c.num_sms ? whole : c.num_sms, 1);
 }
 
 }  // namespace moe
