@@ -720,7 +720,8 @@ moe_status_t moe_expert_matvec_fp4(const void *x, int64_t num_x, const uint8_t *
  *                       scale * s_j                   (otherwise)
  * with s_j the score of the j-th selected expert: the bias decides the selection
  * only.  The ratio of sigmoids keeps its digits however small they are.
- *   scores [T,E] f32 (-inf allowed, +inf not); bias [E] f32, finite, may be NULL;
+ *   scores [T,E] f32 (-inf allowed, +inf not); bias [E] f32, below 2^100 in magnitude,
+ *   may be NULL;
  *   topk_idx [T,k] i32, topk_weights [T,k] f32
  * Requires the E and k limits of moe_topk_gate, 1 <= num_groups <= MOE_MAX_GROUPS,
  * E % num_groups == 0, 1 <= topk_groups <= num_groups, k <= E / num_groups *

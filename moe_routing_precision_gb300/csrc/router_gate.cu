@@ -7,11 +7,10 @@
 //   w_j = scale s_j / sum s, or scale s_j
 //
 // The selection is that of the real numbers.  Without a bias c orders the experts as
-// x does, and they are compared by x, exactly.  Otherwise c is taken in f32, whose
-// error is bounded (kErr below); where two values at a border of the selection lie
-// closer than that and are not the same (x, bias), the token is decided again in f64,
-// one value per candidate, which f32's spacing makes rare: about one token in a
-// thousand for 8 of 256 experts.
+// x does, and they are compared by x, exactly.  Otherwise c is taken in f32 with a
+// bounded error (score_err); where two values at a border of the selection lie closer
+// than that, the token is decided again in f64, one value per candidate, which is rare:
+// about one token in a thousand for 8 of 256 experts.
 //
 // One warp per token, lane l holding the V consecutive experts l V .. l V + V - 1, so
 // that a group is a run of lanes.  The selection is topk_warp.cuh's: a lower bound of
@@ -25,139 +24,215 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;
+#ifndef KB
+#define KB 4
+#endif
+constexpr int kBlocks = KB;
 constexpr float kInf = __builtin_huge_valf();
+constexpr float kLog2e = 1.4426950408889634f;
 
-// |f32 c - c| <= kErr[func] * (largest s of the row) + 2^-23 |c|.
-// Sigmoid: expf, the reciprocal and two products, each within 2 ulp of s <= 1.
-// Softmax: x - max is off by up to 2^-24 |x - max|, which e^ turns into a relative
-// error of that size: below 100 * 2^-24 as far as e^ does not vanish, plus the sum's.
+// |f32 c - c| <= score_err + 2^-23 |c|.  Both forms take 2^y and 1 / y from the hardware
+// estimates (2 ulp and 1 ulp).
+// Sigmoid: e = 2^(-x log2 e) is off by (3 |x| + 4) 2^-24 e, which moves s by less than
+// s (1 - s) times that, under 2^-23; the sum and the estimate of its inverse add 3 * 2^-24.
+// Softmax: e = 2^((x - max) log2 e) in the same way, |x - max| e^(x - max) < 0.37, relative
+// to the largest score; the sum of 1024 terms and its inverse add 2^-20 of s.
 __device__ __forceinline__ float score_err(int func, float top) {
-  return func == MOE_SCORE_SIGMOID ? 0x1p-20f : 0x1p-16f * top;
+  return func == MOE_SCORE_SIGMOID ? 0x1p-21f : 0x1p-19f * top;
+}
+__device__ __forceinline__ float exp2_est(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_est(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Two values of a group or of two groups: the largest and the second.
+// The largest and the second of a group.
 struct Top2 {
   float a, b;
 };
+__device__ __forceinline__ void merge(Top2& t, float v) {
+  t.b = fmaxf(t.b, fminf(t.a, v));
+  t.a = fmaxf(t.a, v);
+}
 __device__ __forceinline__ void merge(Top2& t, Top2 o) {
-  const float lo = fminf(t.a, o.a);
+  t.b = fmaxf(fminf(t.a, o.a), fmaxf(t.b, o.b));
   t.a = fmaxf(t.a, o.a);
-  t.b = fmaxf(lo, fmaxf(t.b, o.b));
 }
 __device__ __forceinline__ float group_value(const Top2& t, int kind) {
   return kind == MOE_GROUP_TOP2 && t.b > -kInf ? t.a + t.b : t.a;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+  return key_score(__reduce_max_sync(kAll, score_key(v)));
 }
 __device__ __forceinline__ float warp_min(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fminf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+  return key_score(__reduce_min_sync(kAll, score_key(v)));
 }
-__device__ __forceinline__ double warp_sum64(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
+
+// ------------------------------------------------ what f32 cannot tell, in f64
 
 __device__ __forceinline__ double sigmoid64(double x) {
   const double e = exp(-fabs(x));
   return x < 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);
 }
-
-// One token's scores as every step of the kernel sees them.
-struct Token {
-  const float* row;
-  const float* bias;
-  int func;
-  float m;         // largest x (softmax)
-  double z;        // sum of exp(x - m) in f64, 0 until it is needed
-};
-
-// c of expert e in f64.
-__device__ __noinline__ double choice64(const Token& t, int e) {
-  const float x = t.row[e];
+// c of an expert with score x; m and z: the softmax's largest x and sum of exp(x - m).
+__device__ __forceinline__ double choice64(int func, float x, const float* bias, int e, float m,
+                                           double z) {
   if (x == -kInf) return -__builtin_huge_val();
-  const double s = t.func == MOE_SCORE_SIGMOID ? sigmoid64((double)x)
-                                               : exp((double)x - (double)t.m) / t.z;
-  return t.bias ? s + (double)t.bias[e] : s;
+  const double s =
+      func == MOE_SCORE_SIGMOID ? sigmoid64((double)x) : exp((double)x - (double)m) / z;
+  return bias ? s + (double)__ldg(bias + e) : s;
 }
-// The softmax's sum in f64.
-__device__ __noinline__ double sum64(const Token& t, int E, int lane) {
+__device__ __forceinline__ double sum64(const float* row, int E, float m, int lane) {
   double z = 0.0;
-  for (int e = lane; e < E; e += 32) z += exp((double)t.row[e] - (double)t.m);
-  return warp_sum64(z);
+  for (int e = lane; e < E; e += 32) z += exp((double)__ldg(row + e) - (double)m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
+  return z;
 }
 
-// The groups of rank < g, by values one per lane (lane i < G), in f64: a bit per group.
-__device__ __noinline__ uint32_t groups64(const Token& t, int E, int G, int g, int kind,
-                                          int lane) {
-  const int n = E / G;
-  double v = 0.0;
-  // each group in turn by the whole warp
-  for (int i = 0; i < G; ++i) {
-    double a = -__builtin_huge_val(), b = a;
-    for (int e = lane; e < n; e += 32) {
-      const double c = choice64(t, i * n + e);
+// An order-preserving integer of a non-NaN value; 0 is below all of them.
+__device__ __forceinline__ unsigned long long order64(double d) {
+  const long long b = __double_as_longlong(d + 0.0);  // -0 + 0 = +0
+  return (unsigned long long)b ^ ((unsigned long long)(b >> 63) | (1ull << 63));
+}
+
+// The groups at the border decided again.  Lane i < G is group i: `sure` those that stay
+// whatever the errors, `near` those that may; lane j < C holds expert e of a near group,
+// all that may be among its group's two largest.  s_v, s_e: scratch of 32.
+__device__ __noinline__ uint32_t groups64(const float* row, const float* bias, int func, float m,
+                                          int E, int n, int g, int kind, uint32_t sure,
+                                          uint32_t near, int C, int e, int lane, double* s_v,
+                                          int* s_e) {
+  const double z = func == MOE_SCORE_SOFTMAX ? sum64(row, E, m, lane) : 1.0;
+  const double none = -__builtin_huge_val();
+  if (lane < C) {
+    s_v[lane] = choice64(func, __ldg(row + e), bias, e, m, z);
+    s_e[lane] = e / n;
+  }
+  __syncwarp();
+  unsigned long long key = 0ull;
+  if ((near >> lane) & 1u) {
+    double a = none, b = none;
+    for (int j = 0; j < C; ++j) {
+      if (s_e[j] != lane) continue;
+      const double c = s_v[j];
       if (c > a) {
         b = a, a = c;
       } else if (c > b) {
         b = c;
       }
     }
+    key = order64(kind == MOE_GROUP_TOP2 && b > none ? a + b : a);
+  }
+  int rank = __popc(sure);
+  for (uint32_t left = near; left; left &= left - 1) {
+    const int i = __ffs(left) - 1;
+    const unsigned long long o = __shfl_sync(kAll, key, i);
+    rank += o > key || (o == key && i < lane) ? 1 : 0;
+  }
+  return sure | __ballot_sync(kAll, ((near >> lane) & 1u) && rank < g);
+}
+
+// The same for all groups from scratch.
+__device__ __noinline__ uint32_t all_groups64(const float* row, const float* bias, int func,
+                                              float m, int E, int G, int g, int kind, int lane) {
+  const double z = func == MOE_SCORE_SOFTMAX ? sum64(row, E, m, lane) : 1.0;
+  const double none = -__builtin_huge_val();
+  const int n = E / G;
+  unsigned long long key = 0ull;
+  for (int i = 0; i < G; ++i) {  // each group in turn by the whole warp
+    double a = none, b = none;
+    for (int e = i * n + lane; e < (i + 1) * n; e += 32) {
+      const double c = choice64(func, __ldg(row + e), bias, e, m, z);
+      b = fmax(b, fmin(a, c));
+      a = fmax(a, c);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const double oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
-      const double lo = fmin(a, oa);
+      b = fmax(fmin(a, oa), fmax(b, ob));
       a = fmax(a, oa);
-      b = fmax(lo, fmax(b, ob));
     }
-    const double s = kind == MOE_GROUP_TOP2 && b > -__builtin_huge_val() ? a + b : a;
-    if (lane == i) v = s;
+    if (lane == i) key = order64(kind == MOE_GROUP_TOP2 && b > none ? a + b : a);
   }
   int rank = 0;
   for (int i = 0; i < G; ++i) {
-    const double o = __shfl_sync(kAll, v, i);
-    rank += o > v || (o == v && i < lane) ? 1 : 0;
+    const unsigned long long o = __shfl_sync(kAll, key, i);
+    rank += o > key || (o == key && i < lane) ? 1 : 0;
   }
   return __ballot_sync(kAll, lane < G && rank < g);
 }
 
-// The k winners of the open groups one after the other in f64, the r-th in lane r.
-__device__ __noinline__ int select64(const Token& t, int E, int G, uint32_t open, int k,
-                                     int lane, double* list) {
-  // list: this warp's values, [E], retired ones NaN
-  const int n = E / G;
-  for (int e = lane; e < E; e += 32)
-    list[e] = (open >> (e / n)) & 1u ? choice64(t, e) : __longlong_as_double(-1ll);
+// Whether all scores of a row are one value, and all biases: then ties are exact.
+__device__ __noinline__ bool one_value(const float* row, const float* bias, int E, int lane) {
+  float xl = kInf, xh = -kInf, bl = kInf, bh = -kInf;
+  for (int e = lane; e < E; e += 32) {
+    const float x = __ldg(row + e), b = bias ? __ldg(bias + e) : 0.0f;
+    xl = fminf(xl, x), xh = fmaxf(xh, x), bl = fminf(bl, b), bh = fmaxf(bh, b);
+  }
+  return warp_min(xl) == warp_max(xh) && warp_min(bl) == warp_max(bh);
+}
+
+// Ranks of C candidates, expert e in lane < C: by x (exact), or by c in f64.
+__device__ __noinline__ int rank64(const float* row, const float* bias, int func, float m, int E,
+                                   bool by_x, int e, int C, int lane) {
+  const double z = !by_x && func == MOE_SCORE_SOFTMAX ? sum64(row, E, m, lane) : 1.0;
+  unsigned long long d = 0ull;
+  if (lane < C) {
+    const float x = __ldg(row + e);
+    d = by_x ? score_key(x) : order64(choice64(func, x, bias, e, m, z));
+  }
+  int rank = 0;
+  for (int j = 0; j < C; ++j) {
+    const unsigned long long od = __shfl_sync(kAll, d, j);
+    const int oe = __shfl_sync(kAll, e, j);
+    rank += od > d || (od == d && oe < e) ? 1 : 0;
+  }
+  return rank;
+}
+
+// The k winners of the open groups one after the other, the r-th in lane r, where there
+// are more candidates than lanes.  list: [E], order-preserving integers.
+__device__ __noinline__ int select64(const float* row, const float* bias, int func, float m,
+                                     int E, int n, uint32_t open, int k, int lane,
+                                     unsigned long long* list) {
+  const double z = func == MOE_SCORE_SOFTMAX ? sum64(row, E, m, lane) : 1.0;
+  for (int e = lane; e < E; e += 32) {
+    unsigned long long key = 0ull;
+    if ((open >> (e / n)) & 1u)
+      key = order64(choice64(func, __ldg(row + e), bias, e, m, z));
+    list[e] = key;
+  }
   __syncwarp();
-  int mine = -1;
+  int mine = 0;
   for (int r = 0; r < k; ++r) {
-    double best = -__builtin_huge_val();
-    int at = -1;
-    for (int e = lane; e < E; e += 32) {
-      const double c = list[e];
-      if (c == c && (at < 0 || c > best)) best = c, at = e;
-    }
+    unsigned long long best = 0ull;
+    int at = E;
+    for (int e = lane; e < E; e += 32)
+      if (list[e] > best) best = list[e], at = e;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const double ob = __shfl_xor_sync(kAll, best, o);
+      const unsigned long long ob = __shfl_xor_sync(kAll, best, o);
       const int oa = __shfl_xor_sync(kAll, at, o);
-      if (oa >= 0 && (at < 0 || ob > best || (ob == best && oa < at))) best = ob, at = oa;
+      if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
     }
     if (lane == r) mine = at;
-    if (lane == 0) list[at] = __longlong_as_double(-1ll);
+    if (lane == 0) list[at] = 0ull;
     __syncwarp();
   }
   return mine;
 }
 
-// The scores of the selected experts (one per lane, e < 0: none) for the weights: s
-// itself, or with `ratio` s times a factor that all of them share.
+// ------------------------------------------------------------------- weights
+
+// The scores of the selected experts (one per lane, have: this lane's is one) for the
+// weights: s itself, or with `ratio` s times a factor that all of them share.
 __device__ __forceinline__ float weight_score(int func, bool ratio, float x, bool have, float m,
                                               float z_inv) {
   if (func == MOE_SCORE_SOFTMAX) {
@@ -171,280 +246,339 @@ __device__ __forceinline__ float weight_score(int func, bool ratio, float x, boo
   return have && x > -kInf ? expf(lo - top) * rcp_f32(1.0f + expf(-fabsf(x))) : 0.0f;
 }
 
+// ------------------------------------------------------------------- forward
+
 struct WarpScratch {
-  unsigned long long cand[32];
-  float x[32];
+  float c[36];  // the candidates' c, then -inf up to a multiple of four
+  float by_rank[36];
+  double v64[32];
+  int e[32];
 };
 
-// V experts per lane.  VEC: E = 32 V, V % 4 == 0 and 16-byte aligned rows.
-template <int V, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32)
+// V experts per lane.  VEC: E = 32 V, V % 4 == 0 and 16-byte aligned rows.  KFIX > 0: k.
+// FULL: with a bias, and groups that are a power of two of whole lanes.
+template <int V, bool VEC, int KFIX, bool FULL>
+__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? kBlocks : V <= 16 ? 2 : 1)
     router_gate_kernel(const RouterArgs a) {
-  __shared__ WarpScratch s_scratch[kWarps];
-  extern __shared__ double s_list[];  // [kWarps][E]
+  __shared__ __align__(16) WarpScratch s_scratch[kWarps];
+  extern __shared__ unsigned long long s_list[];  // [kWarps][E]
   pdl_enter();
   const int lane = threadIdx.x & 31, wib = threadIdx.x >> 5;
   WarpScratch& ws = s_scratch[wib];
   const int E = VEC ? 32 * V : a.E;
-  const int k = a.k, n = E / a.G;
-  double* list = s_list + (size_t)wib * E;
+  const int k = KFIX > 0 ? KFIX : a.k, n = E / a.G;
+  unsigned long long* list = s_list + (size_t)wib * E;
   float* s_c = reinterpret_cast<float*>(list);
-  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  // lanes per group, where a group is a power of two of whole lanes
+  const int warps = (int)((gridDim.x * blockDim.x) >> 5);
+  // groups that are a power of two of whole lanes are merged by shuffles; others
+  // through shared memory by L lanes each
   const int run = n % V == 0 ? n / V : 0;
-  const bool runs = run > 0 && (run & (run - 1)) == 0;
-  int L = 32;  // lanes that share a group otherwise
+  const bool runs = FULL || (run > 0 && (run & (run - 1)) == 0);
+  int L = 32;
   while (L > 1 && L * a.G > 32) L >>= 1;
+  const int width = runs ? run : L;  // lanes of a group
+  const int my_group = lane / (runs ? run : L), from_lane = (lane * width) & 31;
+  const uint32_t inv_n = ((1u << 21) + n - 1) / n;  // e / n = e inv_n >> 21 for e < 1024
+  const int present = VEC ? V : (E - lane * V < 0 ? 0 : E - lane * V > V ? V : E - lane * V);
+  const bool by_x = !FULL && a.bias == nullptr;  // c orders the experts as x does
   float bias[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    bias[i] = a.bias != nullptr && e < E ? __ldg(a.bias + e) : 0.0f;
-  }
-  const bool by_x = a.bias == nullptr;  // c orders the experts as x does
-  const bool need_c = !by_x || (a.G > 1 && a.group_score == MOE_GROUP_TOP2);
+  for (int i = 0; i < V; ++i)
+    bias[i] = !by_x && i < present ? __ldg(a.bias + lane * V + i) : 0.0f;
+  const bool grouped = FULL || a.g < a.G;
+  const bool need_c = !by_x || (grouped && a.group_score == MOE_GROUP_TOP2);
   const bool need_z = a.func == MOE_SCORE_SOFTMAX && (need_c || !a.renorm);
+  const float none = __int_as_float(0x7FFFFFFF);  // NaN: a slot that is no candidate
 
-  for (int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < a.T; t += warps) {
-    Token tok;
-    tok.row = a.scores + t * E;
-    tok.bias = a.bias;
-    tok.func = a.func;
-    tok.m = 0.0f;
-    tok.z = 0.0;
+  int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const float* row = a.scores + t * E;
+  int32_t* idx_out = a.idx + t * k;
+  float* w_out = a.w + t * k;
+  for (; t < a.T; t += warps, row += (int64_t)warps * E, idx_out += (int64_t)warps * k,
+                  w_out += (int64_t)warps * k) {
     float x[V];
     if constexpr (VEC) {
 #pragma unroll
       for (int h = 0; h < V / 4; ++h) {
-        const float4 f =
-            __ldg(reinterpret_cast<const float4*>(tok.row + lane * V + 4 * h));
+        const float4 f = __ldg(reinterpret_cast<const float4*>(row + lane * V + 4 * h));
         x[4 * h] = f.x, x[4 * h + 1] = f.y, x[4 * h + 2] = f.z, x[4 * h + 3] = f.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        x[i] = e < E ? __ldg(tok.row + e) : -kInf;
-      }
+      for (int i = 0; i < V; ++i) x[i] = i < present ? __ldg(row + lane * V + i) : -kInf;
     }
-    // ---- scores and choices
-    float c[V];
-    float top = 1.0f, z_inv = 0.0f;
-    if (a.func == MOE_SCORE_SOFTMAX && need_z) {
-      float m = x[0];
+    // ---- c, and the softmax's largest x and inverse sum
+    float c[V], m = 0.0f, z_inv = 0.0f, err = 0.0f;
+    if (need_z) {
+      m = x[0];
 #pragma unroll
       for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
       m = warp_max(m);
       if (m == -kInf) m = 0.0f;
-      tok.m = m;
       float z = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        c[i] = expf(x[i] - m);
+        c[i] = exp2_est((x[i] - m) * kLog2e);
         z += c[i];
       }
       z = warp_sum(z);
       z_inv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
-      top = z_inv;
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = x[i] > -kInf ? c[i] * z_inv + bias[i] : -kInf;
+      for (int i = 0; i < V; ++i) c[i] = x[i] > -kInf ? __fmaf_rn(c[i], z_inv, bias[i]) : -kInf;
+      err = score_err(a.func, z_inv);
     } else if (need_c) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = x[i] > -kInf ? sigmoid_f32(x[i]) + bias[i] : -kInf;
+      for (int i = 0; i < V; ++i) {
+        // -inf where x is -inf, by a bound that no other x brings below 2^126
+        c[i] = fminf(rcp_est(1.0f + exp2_est(x[i] * -kLog2e)) + bias[i],
+                     __fmaf_rn(x[i], 0x1p-60f, 0x1p127f));
+      }
+      err = score_err(a.func, 1.0f);
     }
     if (!need_c) {
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = x[i];
     }
-    const float err = need_c ? score_err(a.func, top) : 0.0f;
 
     // ---- groups
     uint32_t open = kAll;
-    if (a.G > 1 && a.g < a.G) {
+    Top2 l2 = {-kInf, -kInf};  // the lane's two largest c
+    if (grouped) {
       Top2 g2 = {-kInf, -kInf};
       if (runs) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) merge(g2, Top2{c[i], -kInf});
-        for (int o = 1; o < run; o <<= 1)
-          merge(g2, Top2{__shfl_xor_sync(kAll, g2.a, o), __shfl_xor_sync(kAll, g2.b, o)});
+        for (int i = 0; i < V; ++i) merge(g2, c[i]);
+        l2 = g2;
       } else {
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (lane * V + i < E) s_c[lane * V + i] = c[i];
+          if (i < present) s_c[lane * V + i] = c[i];
         __syncwarp();
-        const int gi = lane / L;
-        if (gi < a.G)
-          for (int e = lane % L; e < n; e += L) merge(g2, Top2{s_c[gi * n + e], -kInf});
-        for (int o = 1; o < L; o <<= 1)
-          merge(g2, Top2{__shfl_xor_sync(kAll, g2.a, o), __shfl_xor_sync(kAll, g2.b, o)});
+        if (my_group < a.G)
+          for (int e = lane % L; e < n; e += L) merge(g2, s_c[my_group * n + e]);
       }
-      const float mine = group_value(g2, a.group_score);
-      const float gv = __shfl_sync(kAll, mine, (lane * (runs ? run : L)) & 31);
-      int rank = 0;
-      bool near = false;  // to a group on the other side of the border
-      for (int i = 0; i < a.G; ++i) {
-        const float o = __shfl_sync(kAll, gv, i);
-        rank += o > gv || (o == gv && i < lane) ? 1 : 0;
+      for (int o = 1; o < width; o <<= 1)
+        merge(g2, Top2{__shfl_xor_sync(kAll, g2.a, o), __shfl_xor_sync(kAll, g2.b, o)});
+      const float gv = __shfl_sync(kAll, group_value(g2, a.group_score), from_lane);
+      // the groups of the g largest distinct values; more than g of them: ties
+      const uint32_t gkey = lane < a.G ? score_key(gv) : 0u;
+      uint32_t edge_in = 0, left = gkey;
+      for (int r = 0; r < a.g; ++r) {
+        edge_in = __reduce_max_sync(kAll, left);
+        if (left == edge_in) left = 0u;
+        if (__popc(__ballot_sync(kAll, gkey > 0u && left == 0u)) >= a.g) break;
       }
-      const bool in = lane < a.G && rank < a.g;
-      open = __ballot_sync(kAll, in);
+      open = __ballot_sync(kAll, gkey > 0u && left == 0u);
+      const uint32_t edge_out = __reduce_max_sync(kAll, left);
+      const bool ties = __popc(open) > a.g;
+      if (ties) {  // of the last value, the first groups
+        uint32_t last = __ballot_sync(kAll, gkey == edge_in);
+        open &= ~last;
+        for (int r = __popc(open); r < a.g; ++r, last &= last - 1) open |= last & (0u - last);
+      }
       if (need_c) {
         // the lowest inside against the highest outside
-        const float low = warp_min(in ? gv : kInf);
-        const float high = warp_max(lane < a.G && !in ? gv : -kInf);
-        near = low - high <= 4.0f * err + 0x1p-21f * fmaxf(fabsf(low), fabsf(high)) &&
-               high > -kInf;
-      }
-      if (near) {
-        // unless the whole row is one value: those ties are exact
-        float xl = kInf, xh = -kInf, bl = kInf, bh = -kInf;
+        const float low = key_score(edge_in);
+        const float high = ties ? low : edge_out ? key_score(edge_out) : -kInf;
+        const float tol = 4.0f * err + 0x1p-21f * fmaxf(fabsf(low), fabsf(high));
+        if (high > -kInf && low - high <= tol) {
+          if (!one_value(row, a.bias, E, lane)) {
+            const uint32_t near = __ballot_sync(
+                kAll, lane < a.G && gv <= low + tol && gv >= high - tol);
+            // the near groups' experts that may be among the two largest: from the second
+            // (the first, where only that counts, or there is no second) down to the error
+            const float second =
+                a.group_score == MOE_GROUP_TOP2 && g2.b > -kInf ? g2.b : g2.a;
+            const float edge = __shfl_sync(kAll, second, from_lane) - tol;
+            uint32_t take = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (lane * V + i >= E) continue;
-          xl = fminf(xl, x[i]), xh = fmaxf(xh, x[i]);
-          bl = fminf(bl, bias[i]), bh = fmaxf(bh, bias[i]);
-        }
-        if (warp_min(xl) != warp_max(xh) || warp_min(bl) != warp_max(bh)) {
-          if (a.func == MOE_SCORE_SOFTMAX) tok.z = sum64(tok, E, lane);
-          open = groups64(tok, E, a.G, a.g, a.group_score, lane);
+            for (int i = 0; i < V; ++i) {
+              const int gi = (int)((uint32_t)(lane * V + i) * inv_n >> 21) & 31;
+              const float from = __shfl_sync(kAll, edge, gi);
+              if (i < present && (near >> gi & 1u) && c[i] >= from) take |= 1u << i;
+            }
+            const int nt = __popc(take), end = warp_incl_scan(nt, lane);
+            const int C = __shfl_sync(kAll, end, 31);
+            __syncwarp();
+            int at = end - nt;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if ((take >> i) & 1u && at < 32) ws.e[at++] = lane * V + i;
+            __syncwarp();
+            const int e = lane < C ? ws.e[lane] : 0;
+            __syncwarp();
+            if (C <= 32)
+              open = groups64(row, a.bias, a.func, m, E, n, a.g, a.group_score, open & ~near,
+                              near, C, e, lane, ws.v64, ws.e);
+            else  // a bundle of equal experts: each group in turn
+              open = all_groups64(row, a.bias, a.func, m, E, a.G, a.g, a.group_score, lane);
+          }
         }
       }
     }
 
-    // ---- keys: c, or x without a bias; 0 for closed groups and absent slots
-    uint32_t key[V], lmax = 0;
+    // ---- candidates: from here on c is what the experts are compared by, NaN where no
+    // expert can be selected
+    if (by_x && need_c) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      const bool in = (VEC || e < E) && (a.G == 1 || (open >> (e / n)) & 1u);
-      key[i] = in ? score_key(by_x ? x[i] : c[i]) : 0u;
-      lmax = max(lmax, key[i]);
+      for (int i = 0; i < V; ++i) c[i] = x[i];
     }
-    // the k-th largest distinct value among the lanes' maxima, less what the errors
-    // of two values may hide
-    uint32_t theta = 0;
-    {
-      uint32_t lm = lmax;
-      for (int r = 0; r < k; ++r) {
-        theta = __reduce_max_sync(kAll, lm);
-        if (lm == theta) lm = 0u;
+    bool in = present > 0;  // this lane has any
+    if (grouped && runs) {
+      in = in && ((open >> my_group) & 1u);
+    } else if (grouped) {
+      in = false;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const bool yes =
+            i < present && (open >> ((uint32_t)(lane * V + i) * inv_n >> 21)) & 1u;
+        c[i] = yes ? c[i] : none;
+        in = in || yes;
       }
-    }
-    if (!by_x && theta > 0) {
-      const float f = key_score(theta);
-      theta = f > -kInf ? score_key(f - (2.0f * err + 0x1p-22f * fabsf(f))) : theta;
-    }
-    uint32_t cmask = 0;
+    } else if (!VEC) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] != 0u && key[i] >= theta) cmask |= 1u << i;
-    const int nc = __popc(cmask);
-    const int C = (int)__reduce_add_sync(kAll, (unsigned)nc);
-    int sel = -1, slot_out = -1;  // this lane's selected expert and its slot
-    bool again = false;           // f32 cannot tell
-    __syncwarp();
-    if (C <= 32) {
-      int slot = warp_incl_scan(nc, lane) - nc;
+      for (int i = 0; i < V; ++i) c[i] = i < present ? c[i] : none;
+    }
+    if (!(grouped && runs) || (by_x && need_c)) {
+      l2.a = l2.b = -kInf;
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (cmask & (1u << i)) {
-          ws.cand[slot] = ((unsigned long long)key[i] << 32) | (uint32_t) ~(uint32_t)(lane * V + i);
-          ws.x[slot++] = x[i];
-        }
+        if (c[i] == c[i]) merge(l2, c[i]);
+    }
+    // the k-th largest distinct value among the lanes' two largest: k experts reach it
+    uint32_t head = in ? score_key(l2.a) : 0u, next = in && l2.b > -kInf ? score_key(l2.b) : 0u;
+    uint32_t theta = 0;
+#pragma unroll
+    for (int r = 0; r < (KFIX > 0 ? KFIX : 1); ++r) {
+      theta = __reduce_max_sync(kAll, head);
+      if (head == theta) head = next, next = 0u;
+    }
+    if constexpr (KFIX == 0) {
+      for (int r = 1; r < k; ++r) {
+        theta = __reduce_max_sync(kAll, head);
+        if (head == theta) head = next, next = 0u;
+      }
+    }
+    // less what the errors of two values may hide
+    float from = theta ? key_score(theta) : -kInf;
+    if (!by_x && from > -kInf) from -= 2.0f * err + 0x1p-22f * fabsf(from);
+    if (!in || (!VEC && present == 0)) from = none;
+    uint32_t cmask = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) cmask |= c[i] >= from ? 1u << i : 0u;
+    // the candidates' experts, one after the other
+    int C = 0;
+    for (uint32_t left = cmask;;) {
+      const uint32_t b = __ballot_sync(kAll, left != 0u);
+      if (b == 0u) break;
+      const int at = C + __popc(b & ((1u << lane) - 1u));
+      if (left != 0u && at < 32) ws.e[at] = lane * V + __ffs(left) - 1;
+      left &= left - 1;
+      C += __popc(b);
+    }
+    const float twice = 2.0f * err;
+    int sel = 0, slot = k;  // this lane's selected expert and its place (k: none)
+    float xs = -kInf;       // and its score
+    if (C <= 32) {
       __syncwarp();
-      const unsigned long long cand = lane < C ? ws.cand[lane] : 0ull;
-      const float cx = lane < C ? ws.x[lane] : 0.0f;
+      float v = -kInf;
+      if (lane < C) {
+        sel = ws.e[lane];
+        xs = v = __ldg(row + sel);
+        if (!by_x && v > -kInf)
+          v = a.func == MOE_SCORE_SIGMOID ? rcp_est(1.0f + exp2_est(xs * -kLog2e))
+                                          : exp2_est((xs - m) * kLog2e) * z_inv;
+        if (!by_x) v += __ldg(a.bias + sel);
+      }
+      ws.c[lane] = v;
+      if (lane < 4) ws.c[32 + lane] = -kInf;
+      __syncwarp();
       int rank = 0;
-      for (int j = 0; j < C; ++j) rank += ws.cand[j] > cand ? 1 : 0;
-      const int e = (int)~(uint32_t)cand;
-      if (!by_x) {
-        // neighbours in rank that are too close, and not the same x and bias
-        __syncwarp();
-        if (lane < C) {
-          ws.cand[rank] = cand;
-          ws.x[rank] = cx;
-        }
+      for (int j = 0; j < C; j += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(ws.c + j);
+        rank += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
+      }
+      // m equal values leave their next m - 1 ranks free, which the sum of 2^rank shows
+      const uint32_t taken =
+          __reduce_add_sync(kAll, lane < C && rank < k ? 1u << rank : 0u);
+      bool again = taken != kAll >> (32 - k);
+      if (!by_x && !again) {
+        // neighbours in rank that are too close
+        if (lane < C) ws.by_rank[rank] = v;
         __syncwarp();
         bool near = false;
         if (lane < k && lane + 1 < C) {
-          const unsigned long long p = ws.cand[lane], q = ws.cand[lane + 1];
-          const float cp = key_score((uint32_t)(p >> 32)), cq = key_score((uint32_t)(q >> 32));
-          near = cq > -kInf && cp - cq <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(cp), fabsf(cq));
-          if (near && ws.x[lane] == ws.x[lane + 1] &&
-              __ldg(a.bias + (int)~(uint32_t)p) == __ldg(a.bias + (int)~(uint32_t)q))
-            near = false;
+          const float p = ws.by_rank[lane], q = ws.by_rank[lane + 1];
+          near = q > -kInf && p - q <= twice + 0x1p-22f * fmaxf(fabsf(p), fabsf(q));
         }
         again = __any_sync(kAll, near);
       }
-      if (again) {
-        if (a.func == MOE_SCORE_SOFTMAX && tok.z == 0.0) tok.z = sum64(tok, E, lane);
-        const double d = lane < C ? choice64(tok, e) : 0.0;
-        rank = 0;
-        for (int j = 0; j < C; ++j) {
-          const double od = __shfl_sync(kAll, d, j);
-          const int oe = __shfl_sync(kAll, e, j);
-          rank += od > d || (od == d && oe < e) ? 1 : 0;
-        }
-      }
-      if (lane < C && rank < k) {
-        sel = e;
-        slot_out = rank;
-      }
+      if (again) rank = rank64(row, a.bias, a.func, m, E, by_x, sel, C, lane);
+      slot = lane < C ? rank : k;
     } else {
-      // many candidates: round by round, one more round for the border
-      float last_c = 0.0f, last_x = 0.0f, last_b = 0.0f;
-      for (int r = 0; r <= k; ++r) {
-        uint32_t best = 0;
-        int at = 0;
+      // more candidates than lanes (equal values, or k near the number of lanes): round
+      // by round, one more for the border, and as many more as lie too close to it
+      bool again = false, more = false;
+      float last = kInf, edge = kInf;
+      int r = 0;
+      for (;; ++r) {
+        float best = -kInf;
+        int at = V;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (key[i] > best) best = key[i], at = i;
-        const uint32_t m = __reduce_max_sync(kAll, best);
-        const int win = (int)__reduce_min_sync(
-            kAll, best == m ? (uint32_t)(lane * V + at) : 0xFFFFFFFFu);
-        if (m == 0u) break;
-        if (!by_x) {
-          const float wc = key_score(m), wx = __ldg(tok.row + win), wb = __ldg(a.bias + win);
-          if (r > 0 && wc > -kInf && !(wx == last_x && wb == last_b) &&
-              last_c - wc <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(wc), fabsf(last_c)))
-            again = true;
-          last_c = wc, last_x = wx, last_b = wb;
-        }
-        if (r == k) break;
-        if (lane == r) sel = win, slot_out = r;
-        if (win / V == lane) {
+          if (c[i] >= from && (at == V || c[i] > best)) best = c[i], at = i;
+        const uint32_t key = at < V ? score_key(best) : 0u;
+        const uint32_t win = __reduce_max_sync(kAll, key);
+        if (win == 0u) break;
+        const float v = key_score(win);
+        const bool near = !by_x && v > -kInf &&
+                          last - v <= twice + 0x1p-22f * fmaxf(fabsf(last), fabsf(v));
+        if (r <= k) again = again || near;
+        if (r == k - 1) edge = v;
+        // past the k-th: only those that may change places with it
+        if (r >= k && (!again || edge - v > twice + 0x1p-22f * fmaxf(fabsf(edge), fabsf(v))))
+          break;
+        more = r == 32;  // no lane left
+        if (more) break;
+        last = v;
+        const int e = (int)__reduce_min_sync(kAll, key == win ? (uint32_t)(lane * V + at) : ~0u);
+        if (lane == r) sel = e, slot = r;
 #pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (lane * V + i == win) key[i] = 0u;
-        }
+        for (int i = 0; i < V; ++i)
+          if (lane * V + i == e) c[i] = none;
       }
-      if (again) {
-        if (a.func == MOE_SCORE_SOFTMAX && tok.z == 0.0) tok.z = sum64(tok, E, lane);
-        sel = select64(tok, E, a.G, open, k, lane, list);
-        slot_out = lane < k ? lane : -1;
+      if (again && more) {
+        // the border hides more experts than there are lanes
+        sel = select64(row, a.bias, a.func, m, E, n, open, k, lane, list);
+        slot = lane;
+      } else if (again) {
+        const int C2 = r < 32 ? r : 32;
+        const int rank = rank64(row, a.bias, a.func, m, E, by_x, sel, C2, lane);
+        slot = lane < C2 ? rank : k;
       }
     }
 
     // ---- weights
-    const bool have = slot_out >= 0;
-    const float xs = have ? __ldg(tok.row + sel) : -kInf;
-    float w = weight_score(a.func, a.renorm, xs, have, tok.m, z_inv);
+    const bool have = slot < k;
+    if (C > 32) xs = have ? __ldg(row + sel) : -kInf;
+    float w = weight_score(a.func, a.renorm, xs, have, m, z_inv);
     if (a.renorm) {
+      // the largest score's factor is in [1/2, 1]
       const float sum = warp_sum(w);
-      w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
+      w = sum > 0.0f ? w * rcp_f32(sum) : 0.0f;
     }
     if (have) {
-      a.idx[t * k + slot_out] = sel;
-      a.w[t * k + slot_out] = w * a.scale;
+      idx_out[slot] = sel;
+      w_out[slot] = w * a.scale;
     }
     __syncwarp();
   }
 }
 
-template <int V, bool VEC>
-cudaError_t launch_v(const LaunchCtx& c, const RouterArgs& a) {
-  auto* kernel = router_gate_kernel<V, VEC>;
+template <int V, bool VEC, int KFIX, bool FULL>
+cudaError_t launch_k(const LaunchCtx& c, const RouterArgs& a) {
+  auto* kernel = router_gate_kernel<V, VEC, KFIX, FULL>;
   const size_t smem = (size_t)kWarps * a.E * 8;
   if (smem > 40 * 1024) {
     static SmemOptIn opt_in;
@@ -455,13 +589,26 @@ cudaError_t launch_v(const LaunchCtx& c, const RouterArgs& a) {
   return launch_pdl(kernel, dim3((unsigned)(need < cap ? need : cap)), kWarps * 32, smem, c.stream,
                     a);
 }
+template <int V, bool VEC>
+cudaError_t launch_v(const LaunchCtx& c, const RouterArgs& a) {
+  if constexpr (V >= 4 && V <= 8) {
+    const int n = a.E / a.G, run = n % V == 0 ? n / V : 0;
+    const bool full = a.bias && a.g < a.G && run > 0 && (run & (run - 1)) == 0;
+    if (a.k == 8)
+      return full ? launch_k<V, VEC, 8, true>(c, a) : launch_k<V, VEC, 8, false>(c, a);
+    if (full) return launch_k<V, VEC, 0, true>(c, a);
+  }
+  return launch_k<V, VEC, 0, false>(c, a);
+}
 
 // ------------------------------------------------------------------ backward
 
 // One warp per token.  The row is copied (or zeroed) first; the selected entries are
 // then written over by their lanes, from add's values read before.  For the softmax
-// without renormalisation every entry changes.
-template <int VEC>
+// without renormalisation every entry changes.  U > 0: rows of whole, 16-byte aligned
+// fours, at most 128 U; add's row (and the softmax's) is asked for before the selected
+// experts are known.
+template <int U>
 __global__ void __launch_bounds__(kWarps * 32)
     router_gate_backward_kernel(const RouterArgs a, unsigned* err) {
   pdl_enter();
@@ -472,30 +619,52 @@ __global__ void __launch_bounds__(kWarps * 32)
   const float* row = a.scores + t * E;
   const float* add = a.add ? a.add + t * E : nullptr;
   float* out = a.grad_scores + t * E;
-  int e = -1;
-  float g = 0.0f, x = -kInf, before = 0.0f;
-  if (lane < k) {
-    e = a.idx[t * k + lane];
-    if (e < 0 || e >= E) {
-      flag_error(err, MOE_DEVERR_EXPERT_RANGE);
-      e = -1;
+  const bool dense = a.func == MOE_SCORE_SOFTMAX && !a.renorm;
+  const bool copy = dense || add != out;
+  int e = lane < k ? a.idx[t * k + lane] : -1;
+  float g = lane < k ? a.grad_w[t * k + lane] : 0.0f;
+  float4 v[U > 0 ? U : 1];
+  float4 x4[U > 0 ? U : 1];
+  if constexpr (U > 0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = u * 128 + lane * 4;
+      v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (add && copy && c < E) v[u] = *reinterpret_cast<const float4*>(add + c);
+      x4[u] = make_float4(-kInf, -kInf, -kInf, -kInf);
+      if (dense && c < E) x4[u] = __ldg(reinterpret_cast<const float4*>(row + c));
     }
   }
-  const bool have = e >= 0;
-  if (have) {
-    g = a.grad_w[t * k + lane];
-    x = row[e];
-    if (add) before = add[e];
+  if (lane < k && (e < 0 || e >= E)) {
+    flag_error(err, MOE_DEVERR_EXPERT_RANGE);
+    e = -1;
   }
-  const bool dense = a.func == MOE_SCORE_SOFTMAX && !a.renorm;
+  const bool have = e >= 0;
+  const float x = have ? row[e] : -kInf;
+  const float before = have && add ? add[e] : 0.0f;
+  if (!have) g = 0.0f;
   float m = 0.0f, z_inv = 0.0f;
   if (dense) {
     m = -kInf;
-    for (int c = lane; c < E; c += 32) m = fmaxf(m, row[c]);
-    m = warp_max(m);
-    if (m == -kInf) m = 0.0f;
     float z = 0.0f;
-    for (int c = lane; c < E; c += 32) z += expf(row[c] - m);
+    if constexpr (U > 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        m = fmaxf(m, fmaxf(fmaxf(x4[u].x, x4[u].y), fmaxf(x4[u].z, x4[u].w)));
+      m = warp_max(m);
+      if (m == -kInf) m = 0.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        x4[u].x = expf(x4[u].x - m), x4[u].y = expf(x4[u].y - m);
+        x4[u].z = expf(x4[u].z - m), x4[u].w = expf(x4[u].w - m);
+        z += (x4[u].x + x4[u].y) + (x4[u].z + x4[u].w);
+      }
+    } else {
+      for (int c = lane; c < E; c += 32) m = fmaxf(m, row[c]);
+      m = warp_max(m);
+      if (m == -kInf) m = 0.0f;
+      for (int c = lane; c < E; c += 32) z += expf(row[c] - m);
+    }
     z = warp_sum(z);
     z_inv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
   }
@@ -507,45 +676,64 @@ __global__ void __launch_bounds__(kWarps * 32)
   const float dot = warp_sum(g * w);  // sum_j g_j w_j / scale, or sum_j g_j s_j
   float d = a.scale * w * (a.renorm || dense ? g - dot : g);
   if (a.func == MOE_SCORE_SIGMOID) d *= sigmoid_f32(-x);
-  if (dense) {
-    const float f = a.scale * dot;
-    for (int c = lane; c < E; c += 32)
-      out[c] = (add ? add[c] : 0.0f) - expf(row[c] - m) * z_inv * f;
-  } else if (add != out) {
-    if constexpr (VEC == 4) {
-      for (int c = lane * 4; c < E; c += 128) {
-        const uint4 v = add ? ld_once_v4(add + c) : make_uint4(0, 0, 0, 0);
-        st_stream_v4(out + c, v);
+  const float f = dense ? -a.scale * dot * z_inv : 0.0f;
+  if (copy) {
+    if constexpr (U > 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = u * 128 + lane * 4;
+        if (dense) {
+          v[u].x = __fmaf_rn(x4[u].x, f, v[u].x), v[u].y = __fmaf_rn(x4[u].y, f, v[u].y);
+          v[u].z = __fmaf_rn(x4[u].z, f, v[u].z), v[u].w = __fmaf_rn(x4[u].w, f, v[u].w);
+        }
+        if (c < E)
+          st_stream_v4(out + c, make_uint4(__float_as_uint(v[u].x), __float_as_uint(v[u].y),
+                                           __float_as_uint(v[u].z), __float_as_uint(v[u].w)));
       }
     } else {
-      for (int c = lane; c < E; c += 32) out[c] = add ? add[c] : 0.0f;
+      for (int c = lane; c < E; c += 32)
+        out[c] = (add ? add[c] : 0.0f) + (dense ? expf(row[c] - m) * f : 0.0f);
     }
   }
   __syncwarp();
   if (have) out[e] = before + d;
 }
 
+template <int U>
+cudaError_t launch_backward(const LaunchCtx& c, const RouterArgs& a) {
+  return launch_pdl(router_gate_backward_kernel<U>, dim3((unsigned)((a.T + kWarps - 1) / kWarps)),
+                    kWarps * 32, 0, c.stream, a, c.err);
+}
+
 }  // namespace
 
 cudaError_t launch_router_gate(const LaunchCtx& c, const RouterArgs& a) {
   const bool al = reinterpret_cast<uintptr_t>(a.scores) % 16 == 0;
-  if (a.E <= 32) return launch_v<1, false>(c, a);
-  if (a.E <= 64) return launch_v<2, false>(c, a);
-  if (a.E <= 128) return a.E == 128 && al ? launch_v<4, true>(c, a) : launch_v<4, false>(c, a);
-  if (a.E <= 256) return a.E == 256 && al ? launch_v<8, true>(c, a) : launch_v<8, false>(c, a);
-  if (a.E <= 512) return a.E == 512 && al ? launch_v<16, true>(c, a) : launch_v<16, false>(c, a);
+  switch ((a.E + 31) / 32) {
+    case 1: return launch_v<1, false>(c, a);
+    case 2: return launch_v<2, false>(c, a);
+    case 3: return launch_v<3, false>(c, a);
+    case 4: return a.E == 128 && al ? launch_v<4, true>(c, a) : launch_v<4, false>(c, a);
+    case 5: return launch_v<5, false>(c, a);
+    case 6: return launch_v<6, false>(c, a);
+    case 7: return launch_v<7, false>(c, a);
+    case 8: return a.E == 256 && al ? launch_v<8, true>(c, a) : launch_v<8, false>(c, a);
+    default: break;
+  }
+  if (a.E <= 384) return launch_v<12, false>(c, a);
+  if (a.E <= 512) return launch_v<16, false>(c, a);
   return launch_v<32, false>(c, a);
 }
 
 cudaError_t launch_router_gate_backward(const LaunchCtx& c, const RouterArgs& a) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.add) |
-                       reinterpret_cast<uintptr_t>(a.grad_scores);
-  const unsigned blocks = (unsigned)((a.T + kWarps - 1) / kWarps);
-  if (a.E % 4 == 0 && at % 16 == 0)
-    return launch_pdl(router_gate_backward_kernel<4>, dim3(blocks), kWarps * 32, 0, c.stream, a,
-                      c.err);
-  return launch_pdl(router_gate_backward_kernel<1>, dim3(blocks), kWarps * 32, 0, c.stream, a,
-                    c.err);
+                       reinterpret_cast<uintptr_t>(a.grad_scores) |
+                       reinterpret_cast<uintptr_t>(a.scores);
+  if (a.E % 4 != 0 || at % 16 != 0) return launch_backward<0>(c, a);
+  if (a.E <= 128) return launch_backward<1>(c, a);
+  if (a.E <= 256) return launch_backward<2>(c, a);
+  if (a.E <= 512) return launch_backward<4>(c, a);
+  return launch_backward<8>(c, a);
 }
 
 }  // namespace moe
