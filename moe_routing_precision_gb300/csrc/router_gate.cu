@@ -24,10 +24,6 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;
-#ifndef KB
-#define KB 4
-#endif
-constexpr int kBlocks = KB;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -255,10 +251,162 @@ struct WarpScratch {
   int e[32];
 };
 
-// V experts per lane.  VEC: E = 32 V, V % 4 == 0 and 16-byte aligned rows.  KFIX > 0: k.
-// FULL: with a bias, and groups that are a power of two of whole lanes.
-template <int V, bool VEC, int KFIX, bool FULL>
-__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? kBlocks : V <= 16 ? 2 : 1)
+// f32 c of one expert, as the kernel takes it; -inf where x is -inf (for the sigmoid by a
+// bound that no other x brings below 2^126).
+__device__ __forceinline__ float choice32(int func, float x, float b, float m, float z_inv) {
+  return func == MOE_SCORE_SIGMOID
+             ? fminf(rcp_est(1.0f + exp2_est(x * -kLog2e)) + b, __fmaf_rn(x, 0x1p-60f, 0x1p127f))
+             : (x > -kInf ? __fmaf_rn(exp2_est((x - m) * kLog2e), z_inv, b) : -kInf);
+}
+
+// One token with every border looked at, by one warp: where f32 cannot tell, in f64.
+// list: [E] words of scratch.
+__device__ __noinline__ void careful_token(const RouterArgs& a, int64_t t, int lane,
+                                           WarpScratch& ws, unsigned long long* list) {
+  const int E = a.E, k = a.k, n = E / a.G;
+  const float* row = a.scores + t * E;
+  float* c = reinterpret_cast<float*>(list);
+  const bool by_x = a.bias == nullptr;  // c orders the experts as x does
+  const bool grouped = a.g < a.G;
+  const bool need_c = !by_x || (grouped && a.group_score == MOE_GROUP_TOP2);
+  float m = 0.0f, z_inv = 0.0f, err = 0.0f;
+  __syncwarp();
+  if (a.func == MOE_SCORE_SOFTMAX) {
+    m = -kInf;
+    for (int e = lane; e < E; e += 32) m = fmaxf(m, __ldg(row + e));
+    m = warp_max(m);
+    if (m == -kInf) m = 0.0f;
+    float z = 0.0f;
+    for (int e = lane; e < E; e += 32) z += exp2_est((__ldg(row + e) - m) * kLog2e);
+    z = warp_sum(z);
+    z_inv = z > 0.0f ? rcp_f32(z) : 0.0f;
+  }
+  for (int e = lane; e < E; e += 32) {
+    const float x = __ldg(row + e);
+    c[e] = need_c ? choice32(a.func, x, by_x ? 0.0f : __ldg(a.bias + e), m, z_inv) : x;
+  }
+  if (need_c) err = score_err(a.func, a.func == MOE_SCORE_SIGMOID ? 1.0f : z_inv);
+  __syncwarp();
+
+  // ---- groups, one per lane
+  uint32_t open = kAll >> (32 - a.G);
+  if (grouped) {
+    Top2 g2 = {-kInf, -kInf};
+    if (lane < a.G)
+      for (int e = 0; e < n; ++e) merge(g2, c[lane * n + e]);
+    const float gv = group_value(g2, a.group_score);
+    int rank = 0;
+    for (int i = 0; i < a.G; ++i) {
+      const float o = __shfl_sync(kAll, gv, i);
+      rank += o > gv || (o == gv && i < lane) ? 1 : 0;
+    }
+    open = __ballot_sync(kAll, lane < a.G && rank < a.g);
+    const uint32_t at_low = __ballot_sync(kAll, lane < a.G && rank == a.g - 1);
+    const uint32_t at_high = __ballot_sync(kAll, lane < a.G && rank == a.g);
+    const float low = __shfl_sync(kAll, gv, __ffs(at_low) - 1);
+    const float high = __shfl_sync(kAll, gv, __ffs(at_high) - 1);
+    const float tol = 4.0f * err + 0x1p-21f * fmaxf(fabsf(low), fabsf(high));
+    // unless the whole row is one value: those ties are exact
+    if (need_c && high > -kInf && low - high <= tol && !one_value(row, a.bias, E, lane)) {
+      const uint32_t near =
+          __ballot_sync(kAll, lane < a.G && gv <= low + tol && gv >= high - tol);
+      // the near groups' experts that may be among the two largest: from the second (the
+      // first, where only that counts, or there is no second) down to the error
+      const float edge = (a.group_score == MOE_GROUP_TOP2 && g2.b > -kInf ? g2.b : g2.a) - tol;
+      int C = 0;
+      for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane, gi = e / n;
+        const float from = __shfl_sync(kAll, edge, gi & 31);
+        const bool take = e < E && (near >> (gi & 31) & 1u) && c[e] >= from;
+        const uint32_t b = __ballot_sync(kAll, take);
+        const int at = C + __popc(b & ((1u << lane) - 1u));
+        if (take && at < 32) ws.e[at] = e;
+        C += __popc(b);
+      }
+      __syncwarp();
+      const int e = lane < C ? ws.e[lane] : 0;
+      __syncwarp();
+      if (C <= 32)
+        open = groups64(row, a.bias, a.func, m, E, n, a.g, a.group_score, open & ~near, near, C, e,
+                        lane, ws.v64, ws.e);
+      else  // a bundle of equal experts: each group in turn
+        open = all_groups64(row, a.bias, a.func, m, E, a.G, a.g, a.group_score, lane);
+    }
+  }
+
+  // ---- the experts of open groups, round by round: the k largest, one more for the
+  // border, and as many more as lie too close to it
+  const float none = __int_as_float(0x7FFFFFFF), twice = 2.0f * err;
+  __syncwarp();
+  for (int e = lane; e < E; e += 32)
+    c[e] = !((open >> (e / n)) & 1u) ? none : by_x ? __ldg(row + e) : c[e];
+  __syncwarp();
+  bool again = false, more = false;
+  float last = 0.0f, edge = 0.0f;
+  int sel = 0, slot = k, r = 0;
+  for (;; ++r) {
+    uint32_t best = 0;
+    int at = 0;
+    for (int e = lane; e < E; e += 32) {
+      const float v = c[e];
+      const uint32_t key = v == v ? score_key(v) : 0u;
+      if (key > best) best = key, at = e;
+    }
+    const uint32_t win = __reduce_max_sync(kAll, best);
+    if (win == 0u) break;
+    const float v = key_score(win);
+    const bool near = r > 0 && !by_x && v > -kInf &&
+                      last - v <= twice + 0x1p-22f * fmaxf(fabsf(last), fabsf(v));
+    if (r <= k) again = again || near;
+    if (r == k - 1) edge = v;
+    // past the k-th: only those that may change places with it
+    if (r >= k && (!again || edge - v > twice + 0x1p-22f * fmaxf(fabsf(edge), fabsf(v)))) break;
+    more = r == 32;  // no lane left
+    if (more) break;
+    last = v;
+    const int e = (int)__reduce_min_sync(kAll, best == win ? (uint32_t)at : ~0u);
+    if (lane == r) sel = e, slot = r;
+    if (lane == 0) c[e] = none;
+    __syncwarp();
+  }
+  if (again && more) {
+    // the border hides more experts than there are lanes
+    sel = select64(row, a.bias, a.func, m, E, n, open, k, lane, list);
+    slot = lane;
+  } else if (again) {
+    const int rank = rank64(row, a.bias, a.func, m, E, by_x, sel, r, lane);
+    slot = lane < r ? rank : k;
+  }
+
+  // ---- weights
+  const bool have = slot < k;
+  const float xs = have ? __ldg(row + sel) : -kInf;
+  float w = weight_score(a.func, a.renorm, xs, have, m, z_inv);
+  if (a.renorm) {
+    const float sum = warp_sum(w);
+    w = sum > 0.0f ? w * rcp_f32(sum) : 0.0f;
+  }
+  if (have) {
+    a.idx[t * k + slot] = sel;
+    a.w[t * k + slot] = w * a.scale;
+  }
+  __syncwarp();
+}
+
+// How the experts are compared: by x; by c of a sigmoid; by c of a softmax.
+constexpr int kByX = 0, kSigmoid = 1, kSoftmax = 2;
+
+// One warp per token.  V experts per lane; VEC: E = 32 V, V % 4 == 0 and 16-byte aligned
+// rows; KFIX > 0: k.  A token with more unsettled experts than a warp has lanes is noted
+// and done again at the end (careful_token, 10 us), which keeps that work's registers out
+// of the loop.
+//
+// 65536 tokens, 8 of 256 experts (67 MB; us): by x alone 26; sigmoid and bias 41; with 8
+// groups 49.  Instruction issue bounds it, 600 per token and 70 % of the slots.  A border
+// decided in f64 costs its warp 1.2 us for experts and 3 us for groups.  16 lanes per
+// token, two tokens per warp, were slower (71: registers), as was asking for a row ahead.
+template <int V, bool VEC, int KFIX, int MODE>
+__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
     router_gate_kernel(const RouterArgs a) {
   __shared__ __align__(16) WarpScratch s_scratch[kWarps];
   extern __shared__ unsigned long long s_list[];  // [kWarps][E]
@@ -273,83 +421,80 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? kBlocks : V <= 16 ? 2 : 
   // groups that are a power of two of whole lanes are merged by shuffles; others
   // through shared memory by L lanes each
   const int run = n % V == 0 ? n / V : 0;
-  const bool runs = FULL || (run > 0 && (run & (run - 1)) == 0);
+  const bool runs = run > 0 && (run & (run - 1)) == 0;
   int L = 32;
   while (L > 1 && L * a.G > 32) L >>= 1;
   const int width = runs ? run : L;  // lanes of a group
-  const int my_group = lane / (runs ? run : L), from_lane = (lane * width) & 31;
+  const int my_group = lane / width, from_lane = (lane * width) & 31;
   const uint32_t inv_n = ((1u << 21) + n - 1) / n;  // e / n = e inv_n >> 21 for e < 1024
   const int present = VEC ? V : (E - lane * V < 0 ? 0 : E - lane * V > V ? V : E - lane * V);
-  const bool by_x = !FULL && a.bias == nullptr;  // c orders the experts as x does
+  const bool by_x = MODE == kByX || a.bias == nullptr;
+  const bool grouped = a.g < a.G;
   float bias[V];
+  if constexpr (MODE != kByX) {
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    bias[i] = !by_x && i < present ? __ldg(a.bias + lane * V + i) : 0.0f;
-  const bool grouped = FULL || a.g < a.G;
-  const bool need_c = !by_x || (grouped && a.group_score == MOE_GROUP_TOP2);
-  const bool need_z = a.func == MOE_SCORE_SOFTMAX && (need_c || !a.renorm);
+    for (int i = 0; i < V; ++i)
+      bias[i] = !by_x && i < present ? __ldg(a.bias + lane * V + i) : 0.0f;
+  }
   const float none = __int_as_float(0x7FFFFFFF);  // NaN: a slot that is no candidate
+  uint32_t careful = 0;                           // tokens to be done again
 
-  int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const float* row = a.scores + t * E;
-  int32_t* idx_out = a.idx + t * k;
-  float* w_out = a.w + t * k;
-  for (; t < a.T; t += warps, row += (int64_t)warps * E, idx_out += (int64_t)warps * k,
-                  w_out += (int64_t)warps * k) {
-    float x[V];
-    if constexpr (VEC) {
+  const int64_t t0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  int64_t t = t0;
+  for (int turn = 0; t < a.T; t += warps, ++turn) {
+    const float* row = a.scores + t * E;
+    float c[V];
+    auto load_x = [&]() {
+      if constexpr (VEC) {
 #pragma unroll
-      for (int h = 0; h < V / 4; ++h) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(row + lane * V + 4 * h));
-        x[4 * h] = f.x, x[4 * h + 1] = f.y, x[4 * h + 2] = f.z, x[4 * h + 3] = f.w;
+        for (int h = 0; h < V / 4; ++h) {
+          const float4 f = __ldg(reinterpret_cast<const float4*>(row + lane * V + 4 * h));
+          c[4 * h] = f.x, c[4 * h + 1] = f.y, c[4 * h + 2] = f.z, c[4 * h + 3] = f.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = i < present ? __ldg(row + lane * V + i) : -kInf;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = i < present ? __ldg(row + lane * V + i) : -kInf;
-    }
+    };
+    load_x();
     // ---- c, and the softmax's largest x and inverse sum
-    float c[V], m = 0.0f, z_inv = 0.0f, err = 0.0f;
-    if (need_z) {
-      m = x[0];
+    float m = 0.0f, z_inv = 0.0f, err = 0.0f;
+    if (MODE == kSoftmax || (MODE == kByX && a.func == MOE_SCORE_SOFTMAX && !a.renorm)) {
+      m = c[0];
 #pragma unroll
-      for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
+      for (int i = 1; i < V; ++i) m = fmaxf(m, c[i]);
       m = warp_max(m);
       if (m == -kInf) m = 0.0f;
-      float z = 0.0f;
+      float z = 0.0f, ex[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        c[i] = exp2_est((x[i] - m) * kLog2e);
-        z += c[i];
+        ex[i] = exp2_est((c[i] - m) * kLog2e);
+        z += ex[i];
       }
       z = warp_sum(z);
-      z_inv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
+      z_inv = z > 0.0f ? rcp_f32(z) : 0.0f;
+      if constexpr (MODE == kSoftmax) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = x[i] > -kInf ? __fmaf_rn(c[i], z_inv, bias[i]) : -kInf;
-      err = score_err(a.func, z_inv);
-    } else if (need_c) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        // -inf where x is -inf, by a bound that no other x brings below 2^126
-        c[i] = fminf(rcp_est(1.0f + exp2_est(x[i] * -kLog2e)) + bias[i],
-                     __fmaf_rn(x[i], 0x1p-60f, 0x1p127f));
+        for (int i = 0; i < V; ++i) c[i] = c[i] > -kInf ? __fmaf_rn(ex[i], z_inv, bias[i]) : -kInf;
+        err = score_err(MOE_SCORE_SOFTMAX, z_inv);
       }
-      err = score_err(a.func, 1.0f);
-    }
-    if (!need_c) {
+    } else if constexpr (MODE == kSigmoid) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = x[i];
+      for (int i = 0; i < V; ++i)
+        c[i] = choice32(MOE_SCORE_SIGMOID, c[i], bias[i], 0.0f, 0.0f);
+      err = score_err(MOE_SCORE_SIGMOID, 1.0f);
     }
 
-    // ---- groups
-    uint32_t open = kAll;
-    Top2 l2 = {-kInf, -kInf};  // the lane's two largest c
-    if (grouped) {
-      Top2 g2 = {-kInf, -kInf};
-      if (runs) {
+    // ---- the lane's two largest, and the groups
+    Top2 l2 = {c[0], -kInf};
 #pragma unroll
-        for (int i = 0; i < V; ++i) merge(g2, c[i]);
-        l2 = g2;
-      } else {
+    for (int i = 1; i < V; ++i) merge(l2, c[i]);
+    uint32_t open = kAll;
+    bool settled = true;  // f32 tells
+    if (grouped) {
+      Top2 g2 = l2;
+      if (!runs) {
+        g2 = Top2{-kInf, -kInf};
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -367,52 +512,57 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? kBlocks : V <= 16 ? 2 : 
       for (int r = 0; r < a.g; ++r) {
         edge_in = __reduce_max_sync(kAll, left);
         if (left == edge_in) left = 0u;
-        if (__popc(__ballot_sync(kAll, gkey > 0u && left == 0u)) >= a.g) break;
       }
-      open = __ballot_sync(kAll, gkey > 0u && left == 0u);
+      open = __ballot_sync(kAll, gkey >= edge_in && gkey > 0u);
       const uint32_t edge_out = __reduce_max_sync(kAll, left);
-      const bool ties = __popc(open) > a.g;
-      if (ties) {  // of the last value, the first groups
-        uint32_t last = __ballot_sync(kAll, gkey == edge_in);
-        open &= ~last;
-        for (int r = __popc(open); r < a.g; ++r, last &= last - 1) open |= last & (0u - last);
-      }
-      if (need_c) {
+      const bool ties = __popc(open) != a.g;
+      if constexpr (MODE == kByX) {
+        if (ties) {  // of the last value that has a place, the first groups
+          uint32_t all = kAll >> (32 - a.G);
+          open = 0u;
+          for (int r = 0; r < a.g; ++r) {
+            const uint32_t best =
+                __reduce_max_sync(kAll, (all >> lane & 1u) ? gkey : 0u);
+            const uint32_t who = __ballot_sync(kAll, gkey == best) & all;
+            open |= who & (0u - who);
+            all &= ~(who & (0u - who));
+          }
+        }
+      } else {
         // the lowest inside against the highest outside
-        const float low = key_score(edge_in);
-        const float high = ties ? low : edge_out ? key_score(edge_out) : -kInf;
+        const float low = key_score(edge_in), high = edge_out ? key_score(edge_out) : -kInf;
         const float tol = 4.0f * err + 0x1p-21f * fmaxf(fabsf(low), fabsf(high));
-        if (high > -kInf && low - high <= tol) {
-          if (!one_value(row, a.bias, E, lane)) {
-            const uint32_t near = __ballot_sync(
-                kAll, lane < a.G && gv <= low + tol && gv >= high - tol);
-            // the near groups' experts that may be among the two largest: from the second
-            // (the first, where only that counts, or there is no second) down to the error
-            const float second =
-                a.group_score == MOE_GROUP_TOP2 && g2.b > -kInf ? g2.b : g2.a;
-            const float edge = __shfl_sync(kAll, second, from_lane) - tol;
-            uint32_t take = 0;
+        if (ties || (high > -kInf && low - high <= tol)) {
+          // the near groups' experts that may be among the two largest: from the second
+          // (the first, where only that counts, or there is no second) down to the error
+          const uint32_t near =
+              __ballot_sync(kAll, lane < a.G && fabsf(gv - low) <= 2.0f * tol);
+          const float second = a.group_score == MOE_GROUP_TOP2 && g2.b > -kInf ? g2.b : g2.a;
+          const float edge = __shfl_sync(kAll, second, from_lane) - tol;
+          uint32_t take = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const int gi = (int)((uint32_t)(lane * V + i) * inv_n >> 21) & 31;
-              const float from = __shfl_sync(kAll, edge, gi);
-              if (i < present && (near >> gi & 1u) && c[i] >= from) take |= 1u << i;
-            }
-            const int nt = __popc(take), end = warp_incl_scan(nt, lane);
-            const int C = __shfl_sync(kAll, end, 31);
-            __syncwarp();
-            int at = end - nt;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-              if ((take >> i) & 1u && at < 32) ws.e[at++] = lane * V + i;
-            __syncwarp();
-            const int e = lane < C ? ws.e[lane] : 0;
-            __syncwarp();
-            if (C <= 32)
-              open = groups64(row, a.bias, a.func, m, E, n, a.g, a.group_score, open & ~near,
-                              near, C, e, lane, ws.v64, ws.e);
-            else  // a bundle of equal experts: each group in turn
-              open = all_groups64(row, a.bias, a.func, m, E, a.G, a.g, a.group_score, lane);
+          for (int i = 0; i < V; ++i) {
+            const int gi = (int)((uint32_t)(lane * V + i) * inv_n >> 21) & 31;
+            const float from = __shfl_sync(kAll, edge, gi);
+            if (i < present && (near >> gi & 1u) && c[i] >= from) take |= 1u << i;
+          }
+          int C = 0;
+          for (uint32_t more = take;;) {
+            const uint32_t b = __ballot_sync(kAll, more != 0u);
+            if (b == 0u) break;
+            const int at = C + __popc(b & ((1u << lane) - 1u));
+            if (more != 0u && at < 32) ws.e[at] = lane * V + __ffs(more) - 1;
+            more &= more - 1;
+            C += __popc(b);
+          }
+          __syncwarp();
+          const int e = lane < C ? ws.e[lane] : 0;
+          __syncwarp();
+          settled = C <= 32 && low > -kInf;
+          if (settled) {
+            const uint32_t sure = __ballot_sync(kAll, gkey > 0u && gv > low + 2.0f * tol);
+            open = groups64(row, by_x ? nullptr : a.bias, a.func, m, E, n, a.g, a.group_score,
+                            sure, near, C, e, lane, ws.v64, ws.e);
           }
         }
       }
@@ -420,31 +570,29 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? kBlocks : V <= 16 ? 2 : 
 
     // ---- candidates: from here on c is what the experts are compared by, NaN where no
     // expert can be selected
-    if (by_x && need_c) {
+    if (MODE != kByX && by_x) {
+      load_x();
+      l2 = Top2{c[0], -kInf};
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = x[i];
+      for (int i = 1; i < V; ++i) merge(l2, c[i]);
     }
     bool in = present > 0;  // this lane has any
     if (grouped && runs) {
       in = in && ((open >> my_group) & 1u);
     } else if (grouped) {
       in = false;
+      l2 = Top2{-kInf, -kInf};
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const bool yes =
             i < present && (open >> ((uint32_t)(lane * V + i) * inv_n >> 21)) & 1u;
+        if (yes) merge(l2, c[i]);
         c[i] = yes ? c[i] : none;
         in = in || yes;
       }
     } else if (!VEC) {
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = i < present ? c[i] : none;
-    }
-    if (!(grouped && runs) || (by_x && need_c)) {
-      l2.a = l2.b = -kInf;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (c[i] == c[i]) merge(l2, c[i]);
     }
     // the k-th largest distinct value among the lanes' two largest: k experts reach it
     uint32_t head = in ? score_key(l2.a) : 0u, next = in && l2.b > -kInf ? score_key(l2.b) : 0u;
@@ -463,7 +611,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? kBlocks : V <= 16 ? 2 : 
     // less what the errors of two values may hide
     float from = theta ? key_score(theta) : -kInf;
     if (!by_x && from > -kInf) from -= 2.0f * err + 0x1p-22f * fabsf(from);
-    if (!in || (!VEC && present == 0)) from = none;
+    if (!in) from = none;
     uint32_t cmask = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) cmask |= c[i] >= from ? 1u << i : 0u;
@@ -477,52 +625,38 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? kBlocks : V <= 16 ? 2 : 
       left &= left - 1;
       C += __popc(b);
     }
-    const float twice = 2.0f * err;
-    int sel = 0, slot = k;  // this lane's selected expert and its place (k: none)
-    float xs = -kInf;       // and its score
-    if (C <= 32) {
-      __syncwarp();
-      float v = -kInf;
-      if (lane < C) {
-        sel = ws.e[lane];
-        xs = v = __ldg(row + sel);
-        if (!by_x && v > -kInf)
-          v = a.func == MOE_SCORE_SIGMOID ? rcp_est(1.0f + exp2_est(xs * -kLog2e))
-                                          : exp2_est((xs - m) * kLog2e) * z_inv;
-        if (!by_x) v += __ldg(a.bias + sel);
-      }
-      ws.c[lane] = v;
-      if (lane < 4) ws.c[32 + lane] = -kInf;
-      __syncwarp();
-      int rank = 0;
-      for (int j = 0; j < C; j += 4) {
-        const float4 o = *reinterpret_cast<const float4*>(ws.c + j);
-        rank += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
-      }
-      // m equal values leave their next m - 1 ranks free, which the sum of 2^rank shows
-      const uint32_t taken =
-          __reduce_add_sync(kAll, lane < C && rank < k ? 1u << rank : 0u);
-      bool again = taken != kAll >> (32 - k);
-      if (!by_x && !again) {
-        // neighbours in rank that are too close
-        if (lane < C) ws.by_rank[rank] = v;
-        __syncwarp();
-        bool near = false;
-        if (lane < k && lane + 1 < C) {
-          const float p = ws.by_rank[lane], q = ws.by_rank[lane + 1];
-          near = q > -kInf && p - q <= twice + 0x1p-22f * fmaxf(fabsf(p), fabsf(q));
-        }
-        again = __any_sync(kAll, near);
-      }
-      if (again) rank = rank64(row, a.bias, a.func, m, E, by_x, sel, C, lane);
-      slot = lane < C ? rank : k;
-    } else {
-      // more candidates than lanes (equal values, or k near the number of lanes): round
-      // by round, one more for the border, and as many more as lie too close to it
-      bool again = false, more = false;
-      float last = kInf, edge = kInf;
-      int r = 0;
-      for (;; ++r) {
+    __syncwarp();
+    int sel = 0;
+    float xs = -kInf, v = -kInf;  // the candidate's x and what it is compared by
+    if (lane < C) {
+      sel = ws.e[lane];
+      xs = v = __ldg(row + sel);
+      if (!by_x)
+        v = choice32(MODE == kSigmoid ? MOE_SCORE_SIGMOID : MOE_SCORE_SOFTMAX, xs,
+                     __ldg(a.bias + sel), m, z_inv);
+    }
+    ws.c[lane] = v;
+    ws.by_rank[lane] = none;
+    __syncwarp();
+    int rank = 0;
+    for (int j = 0; j < C; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(ws.c + j);
+      rank += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
+    }
+    if (lane < C) ws.by_rank[rank] = v;
+    __syncwarp();
+    // an empty rank follows equal values; and neighbours that are too close
+    bool bad = false;
+    if (lane < k && lane + 1 < C) {
+      const float p = ws.by_rank[lane], q = ws.by_rank[lane + 1];
+      bad = q != q || (!by_x && q > -kInf &&
+                       p - q <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(p), fabsf(q)));
+    }
+    if (C > 32) {
+      // many equal values, or k near the number of lanes: round by round, and one more
+      // for the border
+      float last = 0.0f;
+      for (int r = 0; r <= k; ++r) {
         float best = -kInf;
         int at = V;
 #pragma unroll
@@ -531,37 +665,28 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? kBlocks : V <= 16 ? 2 : 
         const uint32_t key = at < V ? score_key(best) : 0u;
         const uint32_t win = __reduce_max_sync(kAll, key);
         if (win == 0u) break;
-        const float v = key_score(win);
-        const bool near = !by_x && v > -kInf &&
-                          last - v <= twice + 0x1p-22f * fmaxf(fabsf(last), fabsf(v));
-        if (r <= k) again = again || near;
-        if (r == k - 1) edge = v;
-        // past the k-th: only those that may change places with it
-        if (r >= k && (!again || edge - v > twice + 0x1p-22f * fmaxf(fabsf(edge), fabsf(v))))
-          break;
-        more = r == 32;  // no lane left
-        if (more) break;
-        last = v;
+        const float top = key_score(win);
+        if (r > 0 && !by_x && top > -kInf &&
+            last - top <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(last), fabsf(top)))
+          settled = false;
+        last = top;
         const int e = (int)__reduce_min_sync(kAll, key == win ? (uint32_t)(lane * V + at) : ~0u);
-        if (lane == r) sel = e, slot = r;
+        if (lane == r) sel = e, xs = __ldg(row + e);
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (lane * V + i == e) c[i] = none;
       }
-      if (again && more) {
-        // the border hides more experts than there are lanes
-        sel = select64(row, a.bias, a.func, m, E, n, open, k, lane, list);
-        slot = lane;
-      } else if (again) {
-        const int C2 = r < 32 ? r : 32;
-        const int rank = rank64(row, a.bias, a.func, m, E, by_x, sel, C2, lane);
-        slot = lane < C2 ? rank : k;
-      }
+      rank = lane;
+    } else if (__any_sync(kAll, bad) && settled) {
+      rank = rank64(row, a.bias, a.func, m, E, by_x, sel, C, lane);
+    }
+    if (!settled) {
+      careful |= 1u << turn;
+      continue;
     }
 
     // ---- weights
-    const bool have = slot < k;
-    if (C > 32) xs = have ? __ldg(row + sel) : -kInf;
+    const bool have = lane < C && rank < k;  // C > 32: lane r has the r-th
     float w = weight_score(a.func, a.renorm, xs, have, m, z_inv);
     if (a.renorm) {
       // the largest score's factor is in [1/2, 1]
@@ -569,36 +694,43 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? kBlocks : V <= 16 ? 2 : 
       w = sum > 0.0f ? w * rcp_f32(sum) : 0.0f;
     }
     if (have) {
-      idx_out[slot] = sel;
-      w_out[slot] = w * a.scale;
+      a.idx[t * k + rank] = sel;
+      a.w[t * k + rank] = w * a.scale;
     }
-    __syncwarp();
   }
+  for (; careful; careful &= careful - 1)
+    careful_token(a, t0 + (int64_t)(__ffs(careful) - 1) * warps, lane, ws, list);
 }
 
-template <int V, bool VEC, int KFIX, bool FULL>
-cudaError_t launch_k(const LaunchCtx& c, const RouterArgs& a) {
-  auto* kernel = router_gate_kernel<V, VEC, KFIX, FULL>;
+template <int V, bool VEC, int KFIX, int MODE>
+cudaError_t launch_m(const LaunchCtx& c, const RouterArgs& a) {
+  auto* kernel = router_gate_kernel<V, VEC, KFIX, MODE>;
   const size_t smem = (size_t)kWarps * a.E * 8;
   if (smem > 40 * 1024) {
     static SmemOptIn opt_in;
     const cudaError_t e = opt_in.once(kernel);
     if (e != cudaSuccess) return e;
   }
-  const int64_t need = (a.T + kWarps - 1) / kWarps, cap = (int64_t)c.num_sms * 8;
-  return launch_pdl(kernel, dim3((unsigned)(need < cap ? need : cap)), kWarps * 32, smem, c.stream,
-                    a);
+  // two rounds of blocks, and at most 32 tokens per warp
+  const int64_t need = (a.T + kWarps - 1) / kWarps;
+  int64_t blocks = (int64_t)c.num_sms * 8;
+  if (blocks > need) blocks = need;
+  if (blocks < (need + 31) / 32) blocks = (need + 31) / 32;
+  return launch_pdl(kernel, dim3((unsigned)blocks), kWarps * 32, smem, c.stream, a);
+}
+template <int V, bool VEC, int KFIX>
+cudaError_t launch_k(const LaunchCtx& c, const RouterArgs& a) {
+  if (!a.bias && (a.g == a.G || a.group_score == MOE_GROUP_MAX))
+    return launch_m<V, VEC, KFIX, kByX>(c, a);
+  return a.func == MOE_SCORE_SIGMOID ? launch_m<V, VEC, KFIX, kSigmoid>(c, a)
+                                     : launch_m<V, VEC, KFIX, kSoftmax>(c, a);
 }
 template <int V, bool VEC>
 cudaError_t launch_v(const LaunchCtx& c, const RouterArgs& a) {
-  if constexpr (V >= 4 && V <= 8) {
-    const int n = a.E / a.G, run = n % V == 0 ? n / V : 0;
-    const bool full = a.bias && a.g < a.G && run > 0 && (run & (run - 1)) == 0;
-    if (a.k == 8)
-      return full ? launch_k<V, VEC, 8, true>(c, a) : launch_k<V, VEC, 8, false>(c, a);
-    if (full) return launch_k<V, VEC, 0, true>(c, a);
+  if constexpr (V == 8) {
+    if (a.k == 8) return launch_k<V, VEC, 8>(c, a);
   }
-  return launch_k<V, VEC, 0, false>(c, a);
+  return launch_k<V, VEC, 0>(c, a);
 }
 
 // ------------------------------------------------------------------ backward
@@ -709,17 +841,15 @@ cudaError_t launch_backward(const LaunchCtx& c, const RouterArgs& a) {
 
 cudaError_t launch_router_gate(const LaunchCtx& c, const RouterArgs& a) {
   const bool al = reinterpret_cast<uintptr_t>(a.scores) % 16 == 0;
-  switch ((a.E + 31) / 32) {
-    case 1: return launch_v<1, false>(c, a);
-    case 2: return launch_v<2, false>(c, a);
-    case 3: return launch_v<3, false>(c, a);
-    case 4: return a.E == 128 && al ? launch_v<4, true>(c, a) : launch_v<4, false>(c, a);
-    case 5: return launch_v<5, false>(c, a);
-    case 6: return launch_v<6, false>(c, a);
-    case 7: return launch_v<7, false>(c, a);
-    case 8: return a.E == 256 && al ? launch_v<8, true>(c, a) : launch_v<8, false>(c, a);
-    default: break;
-  }
+  // the fewest experts per lane; a few widths more than powers of two, as groups are then
+  // more often whole lanes
+  if (a.E <= 32) return launch_v<1, false>(c, a);
+  if (a.E <= 64) return launch_v<2, false>(c, a);
+  if (a.E <= 96) return launch_v<3, false>(c, a);
+  if (a.E <= 128) return launch_v<4, false>(c, a);
+  if (a.E <= 160) return launch_v<5, false>(c, a);
+  if (a.E <= 192) return launch_v<6, false>(c, a);
+  if (a.E <= 256) return a.E == 256 && al ? launch_v<8, true>(c, a) : launch_v<8, false>(c, a);
   if (a.E <= 384) return launch_v<12, false>(c, a);
   if (a.E <= 512) return launch_v<16, false>(c, a);
   return launch_v<32, false>(c, a);
