@@ -269,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kConvert) {
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (uint32_t)((warp & 3) * 32) * kTmemLane;
+    // this thread's row in a stage, at the first 16 bytes' place under the swizzle
+    const uint32_t a_at = sbase + L.a + (uint32_t)(half * (kABytes / 2) + row * 128 + ((row & 7) << 4));
     Ring ra, rt;
     uint32_t c_phase = 0;
     for (int64_t it = item0; it < items && ok; it += item_step) {
@@ -286,19 +288,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 : (n1 < a.N ? __ldg(wsf + n1) : 0.0f);
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait_warp(a_full + ra.i * 8, ra.phase)) break;
-        const uint32_t at = sbase + L.a + (uint32_t)(ra.i * kABytes + half * (kABytes / 2) + row * 128);
+        const uint32_t at = a_at + (uint32_t)(ra.i * kABytes);
         uint4 v[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = lds_v4(at + (uint32_t)((c ^ (row & 7)) << 4));
+        for (int c = 0; c < 8; ++c) v[c] = lds_v4(at ^ (uint32_t)(c << 4));
         uint32_t f[32];
         auto convert = [&](int c0) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
+            // units 4 to 7 with their two groups exchanged, as the rows' are
             uint32_t* o = f + c * 8;
-            int8x4_to_f16(v[c0 + c].x, o[0], o[1]);
-            int8x4_to_f16(v[c0 + c].y, o[2], o[3]);
-            int8x4_to_f16(v[c0 + c].z, o[4], o[5]);
-            int8x4_to_f16(v[c0 + c].w, o[6], o[7]);
+            uint32_t *p = c0 ? o + 4 : o, *q = c0 ? o : o + 4;
+            int8x4_to_f16(v[c0 + c].x, p[0], p[1]);
+            int8x4_to_f16(v[c0 + c].y, p[2], p[3]);
+            int8x4_to_f16(v[c0 + c].z, q[0], q[1]);
+            int8x4_to_f16(v[c0 + c].w, q[2], q[3]);
           }
         };
         convert(0);
@@ -388,64 +392,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = named_and(1, kConvert * 32, ok);
     }
   } else if (warp < kConvert + kGather) {
-    // a thread's units of 16 channels of a stage: rows r0, r0 + kStep, ..
+    // A warp takes 4 rows x 8 units of 16 channels of a stage (8 lanes per row: whole lines
+    // asked for at once, half lines took twice as long), and every 32nd row after them.
+    // A unit becomes two 16-byte groups of f16; units 4 to 7 lie in a second block of rows,
+    // with their groups exchanged, so that the 8 lanes of a store meet 8 different groups
+    // of banks.  The weights' channels are exchanged in the same way: a sum has no order.
     constexpr int kStep = kGather * 4, kUnits = NT > kStep ? NT / kStep : 1;
-    const int g = tid - kConvert * 32, c = g & 7, r0 = g >> 3;
+    const int c = lane & 7, r0 = (warp - kConvert) * 4 + (lane >> 3);
+    const uint32_t to0 = sbase + L.b + (uint32_t)((c >> 2) * (NT * 128) + r0 * 128 +
+                                                  ((((c & 3) * 2 + (c >> 2)) ^ (r0 & 7)) << 4));
+    const uint32_t to1 = to0 ^ 16u;
     Ring rb;
     for (int64_t it = item0; it < items && ok; it += item_step) {
       const Item m = item_at(it);
       const int8_t* from[kUnits];
+      uint32_t rows = 0;  // units that have a row; the others stay zero
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
         const int r = r0 + kStep * u;
-        from[u] = nullptr;
-        if (r < m.n) {
-          const int64_t s = source_row(a, m.r0 + r, err);
-          if (s >= 0) from[u] = a.x + s * a.K + c * 16;
-        }
+        const int64_t s = r < m.n ? source_row(a, m.r0 + r, err) : -1;
+        if (s >= 0) rows |= 1u << u;
+        from[u] = a.x + (s >= 0 ? s : 0) * a.K + c * 16 + (int64_t)kb0 * kBlockK;
       }
-      auto fetch = [&](uint4 (&v)[kUnits], int kb) {
-        const int k0 = kb * kBlockK;
+      uint4 v0[kUnits], v1[kUnits];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          v[u] = make_uint4(0, 0, 0, 0);
-          if (from[u] != nullptr && kb < kb1 && k0 + c * 16 < a.K) v[u] = ld_v4(from[u] + k0);
+      for (int u = 0; u < kUnits; ++u) v0[u] = v1[u] = make_uint4(0, 0, 0, 0);
+      // asks for block kb; `from` is at block kb - ahead
+      auto fetch = [&](uint4 (&v)[kUnits], int kb, int ahead) {
+        if (kb >= kb1) return;
+        if ((kb + 1) * kBlockK <= a.K) {
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u)
+            if ((rows >> u) & 1u) v[u] = ld_v4(from[u] + ahead * kBlockK);
+        } else {
+          const bool in = kb * kBlockK + c * 16 < a.K;
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u)
+            v[u] = in && ((rows >> u) & 1u) ? ld_v4(from[u] + ahead * kBlockK)
+                                            : make_uint4(0, 0, 0, 0);
         }
       };
       // one stage from registers that were asked for two stages before
       auto stage = [&](uint4 (&v)[kUnits], int kb) {
         if (!wait_warp(b_free + rb.i * 8, rb.phase ^ 1u)) return;
-        // channels 64 to 127 lie in a second block of rows; the lanes of its units store
-        // their odd half first, so that 8 lanes meet 8 different groups of banks
-        const uint32_t blk = sbase + L.b + (uint32_t)(rb.i * S::kBBytes + (c >> 2) * (NT * 128));
-        const int odd = c >> 2;
+        const uint32_t blk = (uint32_t)(rb.i * S::kBBytes);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-          const int r = r0 + kStep * u;
-          if (r >= m.n) break;
+          if (kStep * u >= m.n) break;
           uint32_t f[8];
           int8x4_to_f16(v[u].x, f[0], f[1]);
           int8x4_to_f16(v[u].y, f[2], f[3]);
           int8x4_to_f16(v[u].z, f[4], f[5]);
           int8x4_to_f16(v[u].w, f[6], f[7]);
-          const uint32_t rowat = blk + (uint32_t)(r * 128);
-          const int ch = (c & 3) * 2;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int hh = h ^ odd;
-            sts_v4(rowat + (uint32_t)(((ch + hh) ^ (r & 7)) << 4), hh ? f[4] : f[0],
-                   hh ? f[5] : f[1], hh ? f[6] : f[2], hh ? f[7] : f[3]);
-          }
+          sts_v4(to0 + blk + u * (kStep * 128), f[0], f[1], f[2], f[3]);
+          sts_v4(to1 + blk + u * (kStep * 128), f[4], f[5], f[6], f[7]);
+          from[u] += kBlockK;
         }
-        fetch(v, kb + 2);
+        fetch(v, kb + 2, 1);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_full + rb.i * 8);
         rb.next<S::SB>();
       };
-      uint4 v0[kUnits], v1[kUnits];
-      fetch(v0, kb0);
-      fetch(v1, kb0 + 1);
+      fetch(v0, kb0, 0);
+      fetch(v1, kb0 + 1, 1);
       for (int kb = kb0; kb < kb1 && ok; kb += 2) {
         stage(v0, kb);
         if (kb + 1 < kb1 && ok) stage(v1, kb + 1);
