@@ -1,4 +1,5 @@
-// tcgen05.cuh -- tensor memory and the 5th-generation tensor cores, one CTA.
+// tcgen05.cuh -- tensor memory and the 5th-generation tensor cores, for one CTA and for a
+// pair (the two CTAs of a cluster of two).
 #pragma once
 
 #include "block_ops.cuh"
@@ -65,6 +66,19 @@ __device__ __forceinline__ void tmem_load16x2(uint32_t a, uint32_t b, float (&x)
       : "memory");
 }
 
+// 16 columns, complete on return.
+__device__ __forceinline__ void tmem_load16(uint32_t a, float (&x)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]),
+        "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]),
+        "=f"(x[14]), "=f"(x[15])
+      : "r"(a)
+      : "memory");
+}
+
 // D[128 lanes, N columns] (+)= A[128, 16] B[N, 16]^T, f16 into f32: A in tensor memory
 // (two channels per column), B in shared memory.
 __device__ __forceinline__ void tc_mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -74,6 +88,33 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d, uint32_t a, uint64_t b, u
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
+}
+// The same by a pair: 256 rows of A, 128 in each CTA's tensor memory, N rows of B, half in
+// each CTA's shared memory at the same address; D's rows are where A's are.  Issued in the
+// first CTA.  The other forms below are the pair's counterparts of those above; the
+// commit arrives at the barrier in both CTAs.
+__device__ __forceinline__ void tc2_mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc2_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem2_alloc(uint32_t at) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(at)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem2_free(uint32_t tmem) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 // Instruction descriptor: f32 sums of f16 products, both operands channel-major.
 __device__ __forceinline__ uint32_t tc_idesc_f16(int m, int n) {
@@ -141,6 +182,11 @@ __device__ __forceinline__ float cluster_load(uint32_t addr) {
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
+}
+// The same for operands of the tensor cores, which a proxy fence or tcgen05's has ordered
+// before: no release of other memory to the cluster (which cost a stage 1 us).
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // mbar_wait for arrivals from the whole cluster.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {

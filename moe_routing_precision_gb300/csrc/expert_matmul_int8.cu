@@ -19,10 +19,8 @@
 //   16     asks for the weights (TMA, 128-byte swizzle)
 //   17-18  issue the products of one half each: what one waits for does not keep the
 //          tensor cores from the other's
-#include <cuda.h>
-#include <cuda_fp16.h>
-
-#include "block/tcgen05.cuh"
+#include <cstdlib>
+#include "block/matmul_int8.cuh"
 
 namespace moe {
 namespace {
@@ -31,7 +29,6 @@ constexpr int kWarps = 19;
 constexpr int kThreads = kWarps * 32;
 constexpr int kConvert = 8;          // warps 0 .. 7
 constexpr int kGather = 8;           // warps 8 .. 15
-constexpr int kBlockK = 128;         // channels per stage
 constexpr int kHalf = 128;           // outputs of one accumulator
 constexpr int kABytes = 2 * kHalf * kBlockK;
 
@@ -66,70 +63,6 @@ __host__ __device__ inline Smem smem_layout(int E) {
   s.total = s.rows + (uint32_t)E * 8;
   return s;
 }
-
-// Four 8-bit integers to f16, in pairs: u = v + 128 in the low mantissa bits of 1024 is
-// 1024 + u, and 1152 off is v, exactly.
-__device__ __forceinline__ void int8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  w ^= 0x80808080u;
-  const uint32_t p = __byte_perm(w, 0x64646464u, 0x4140), q = __byte_perm(w, 0x64646464u, 0x4342);
-  const __half2 off = __half2half2(__ushort_as_half(0x6480));
-  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&p), off);
-  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&q), off);
-  lo = *reinterpret_cast<const uint32_t*>(&a);
-  hi = *reinterpret_cast<const uint32_t*>(&b);
-}
-
-__device__ __forceinline__ uint4 lds_v4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
-}
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c, int r,
-                                        uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(c), "r"(r), "r"(bar)
-      : "memory");
-}
-
-// Row r's row of x, or -1 for a row of zeros.
-__device__ __forceinline__ int64_t source_row(const MatmulInt8Args& a, int64_t r, unsigned* err) {
-  int64_t s = r;
-  if (a.src != nullptr) {
-    const int v = __ldg(a.src + r);
-    if (v < 0) return -1;
-    s = v / a.k;
-  }
-  if (s >= a.num_x) {
-    flag_error(err, MOE_DEVERR_POS_RANGE);
-    return -1;
-  }
-  return s;
-}
-
-__device__ __forceinline__ void store_out(const MatmulInt8Args& a, int64_t at, float v) {
-  if (a.out_f32)
-    static_cast<float*>(a.out)[at] = v;
-  else
-    static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
-// Stage and phase of a ring, step by step.
-struct Ring {
-  int i = 0;
-  uint32_t phase = 0;
-  template <int N>
-  __device__ __forceinline__ void next() {
-    if (++i == N) i = 0, phase ^= 1u;
-  }
-};
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -172,87 +105,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (S::SPLIT) cluster_sync();  // the barriers, before a peer arrives at one
   pdl_enter();
 
-  // first[e]: runs of up to NT rows of the experts before e
-  {
-    constexpr int kPer = (MOE_MAX_EXPERTS + kThreads - 1) / kThreads;
-    int* totals = reinterpret_cast<int*>(smem + L.totals);
-    int runs[kPer] = {};
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = kPer * tid + i;
-      if (e >= a.E) continue;
-      int64_t lo = 0, hi = a.R;
-      if (a.offsets != nullptr) {
-        lo = __ldg(a.offsets + e);
-        hi = __ldg(a.offsets + e + 1);
-        if (lo < 0 || hi > a.R) flag_error(err, MOE_DEVERR_POS_RANGE);
-        if (lo < 0) lo = 0;
-        if (hi > a.R) hi = a.R;
-      }
-      rows_of[e] = make_int2((int)lo, (int)hi);
-      runs[i] = hi > lo ? (int)((hi - lo + NT - 1) / NT) : 0;
-      sum += runs[i];
-    }
-    const int own = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (lane == 31) totals[warp] = sum;
-    tc_before_sync();
-    __syncthreads();
-    tc_after_sync();
-    int before = sum - own;
-    for (int w = 0; w < warp; ++w) before += totals[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (kPer * tid + i <= a.E) first[kPer * tid + i] = before;
-      before += runs[i];
-    }
-    __syncthreads();
-  }
+  const ItemList list = {first, rows_of, a.E};
+  list.build<kThreads, NT>(a, reinterpret_cast<int*>(smem + L.totals), err);
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L.tmem);
   const int M = a.swiglu ? 2 * a.N : a.N;
   const int per_tile = a.swiglu ? kHalf : 2 * kHalf;
   const int tiles = (a.N + per_tile - 1) / per_tile;
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
-  const int64_t items = (int64_t)first[a.E] * tiles;
+  const int64_t items = (int64_t)list.runs() * tiles;
   // this CTA's items, and its part of their channels
   const int ctas = S::SPLIT ? (int)cluster_size() : 1, rank = S::SPLIT ? (int)cluster_rank() : 0;
   const int64_t item0 = blockIdx.x / ctas, item_step = gridDim.x / ctas;
   const int kb0 = nblk * rank / ctas, kb1 = nblk * (rank + 1) / ctas;
 
-  // one item: an expert, a tile of outputs and a run of rows; an expert's runs of one
-  // tile follow one another, so that its weights are read once from HBM
-  struct Item {
-    int e, tile, n;
-    int64_t r0;
-  };
-  auto item_at = [&](int64_t it) {
-    const int q = (int)(it / tiles);
-    int e = 0;  // the last expert with first[e] <= q
-    for (int hi = a.E; hi - e > 1;) {
-      const int mid = (e + hi) >> 1;
-      if (first[mid] <= q)
-        e = mid;
-      else
-        hi = mid;
-    }
-    const int runs = first[e + 1] - first[e];
-    const int64_t local = it - (int64_t)first[e] * tiles;
-    Item m;
-    m.e = e;
-    m.tile = (int)(local / runs);
-    const int2 rows = rows_of[e];
-    const int run = (int)(local - (int64_t)m.tile * runs);
-    // equal runs, in whole 16 rows
-    const int per = ((rows.y - rows.x + runs - 1) / runs + 15) / 16 * 16;
-    m.r0 = rows.x + (int64_t)run * per;
-    m.n = (int)(rows.y - m.r0 < per ? rows.y - m.r0 : per);
-    return m;
-  };
+  auto item_at = [&](int64_t it) { return list.at(it, tiles); };
   bool ok = true;  // no wait ran out
   auto wait = [&](uint32_t bar, uint32_t phase) {
     if (ok && !mbar_wait(bar, phase)) {
@@ -541,28 +407,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The weights as a tensor of rows of K bytes, in boxes of 128 rows of 128 bytes.
-cudaError_t weight_map(const MatmulInt8Args& a, CUtensorMap* map) {
-  using Encode = decltype(&cuTensorMapEncodeTiled);
-  static const Encode encode = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                           cudaEnableDefault, &found);
-    return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(fn)
-                                                                    : nullptr;
-  }();
-  if (encode == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {(cuuint64_t)a.K, (cuuint64_t)a.E * a.N * (a.swiglu ? 2 : 1)};
-  const cuuint64_t strides[1] = {(cuuint64_t)a.K};
-  const cuuint32_t box[2] = {kBlockK, kHalf}, unit[2] = {1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(a.w), dims,
-                            strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // A launch of `blocks` CTAs in clusters of `ctas`.
 template <class S>
 struct Config {
@@ -610,7 +454,7 @@ cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a, int64_t groups
   cudaError_t e = opt_in.once(kernel);
   if (e != cudaSuccess) return e;
   CUtensorMap map;
-  e = weight_map(a, &map);
+  e = weight_map(a, kHalf, &map);
   if (e != cudaSuccess) return e;
   Config<S> cfg(a.E, groups * ctas, ctas);
   cfg.c.stream = c.stream;
@@ -645,6 +489,7 @@ cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& 
     if (split <= fit) ctas = s;
   }
   if (ctas > 1) return launch_t<Split>(c, a, split, ctas);
+  if (getenv("MMP")) return launch_expert_matmul_int8_pair(c, a);
   const int64_t whole = items(Whole::NT);
   return launch_t<Whole>(c, a, whole < c.num_sms ? whole : c.num_sms, 1);
 }
