@@ -72,6 +72,38 @@ __device__ __forceinline__ void store_out(const MatmulInt8Args& a, int64_t at, f
     static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// 16 columns of one thread's output channel: x[j], scaled, into rows row + j (j < rows),
+// channel ch.  Two rows share a conversion, and the address goes from row to row.
+template <bool F32>
+__device__ __forceinline__ void store_column16(const MatmulInt8Args& a, const float (&v)[16],
+                                               int64_t row, int rows, int ch) {
+  const int64_t at = row * a.N + ch;
+  if constexpr (F32) {
+    float* o = static_cast<float*>(a.out) + at;
+#pragma unroll
+    for (int j = 0; j < 16; ++j, o += a.N)
+      if (j < rows) *o = v[j];
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      const uint32_t w = pack_bf16x2_rn(v[j], v[j + 1]);
+      if (j < rows) *o = (uint16_t)w;
+      o += a.N;
+      if (j + 1 < rows) *o = (uint16_t)(w >> 16);
+      o += a.N;
+    }
+  }
+}
+// The scales of 16 rows from shared memory (16-byte aligned).
+__device__ __forceinline__ void load_scales16(const float* s, float (&v)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float4 f = *reinterpret_cast<const float4*>(s + 4 * q);
+    v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+  }
+}
+
 // Stage and phase of a ring, step by step.
 struct Ring {
   int i = 0;

@@ -55,7 +55,7 @@ __host__ __device__ inline Smem smem_layout(int E) {
   s.b = s.a + S::SA * kABytes;
   s.part = s.b + S::SB * S::kBBytes;
   s.bars = s.part + S::kPartBytes;
-  s.xsf = s.bars + (2 * S::SA + 2 * S::SB + 4 * S::ST + 6) * 8;
+  s.xsf = s.bars + (2 * S::SA + 2 * S::SB + 4 * S::ST + 6) * 8;  // 16-byte aligned
   s.totals = s.xsf + S::NT * 4;
   s.tmem = s.totals + kWarps * 4;
   s.first = s.tmem + 16 - (s.tmem & 7);
@@ -64,7 +64,7 @@ __host__ __device__ inline Smem smem_layout(int E) {
   return s;
 }
 
-template <class S>
+template <class S, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_matmul_kernel(const MatmulInt8Args a, const __grid_constant__ CUtensorMap map,
                          unsigned* err) {
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // p and q: the sums of output n and, behind it, of its partner
         p *= xs * u0, q *= xs * u1;
         if (a.swiglu) {
-          if (n < a.N) store_out(a, at + n, p / (1.0f + expf(-p)) * q);
+          if (n < a.N) store_out(a, at + n, p * sigmoid_f32(p) * q);
         } else {
           if (n < a.N) store_out(a, at + n, p);
           if (n + kHalf < a.N) store_out(a, at + n + kHalf, q);
@@ -211,15 +211,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           float x[16], y[16];
           __syncwarp();
           tmem_load16x2(lanes + c, lanes + NT + c, x, y);
+          const int rows = m.n - c < 16 ? m.n - c : 16;
+          if constexpr (S::SPLIT) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c + j >= m.n) break;
-            if constexpr (S::SPLIT) {
+            for (int j = 0; j < 16; ++j) {
+              if (j >= rows) break;
               part[(c + j) * kHalf + row] = x[j];
               part[(NT + c + j) * kHalf + row] = y[j];
-            } else {
-              finish(x[j], y[j], s_xsf[c + j], w0, w1, (m.r0 + c + j) * a.N, n0);
             }
+          } else {
+            float xs[16];
+            load_scales16(s_xsf + c, xs);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] *= xs[j] * w0, y[j] *= xs[j] * w1;
+            if (a.swiglu) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = x[j] * sigmoid_f32(x[j]) * y[j];
+            }
+            if (n0 < a.N) store_column16<F32>(a, x, m.r0 + c, rows, n0);
+            if (!a.swiglu && n1 < a.N) store_column16<F32>(a, y, m.r0 + c, rows, n1);
           }
         }
         tc_before_sync();
@@ -434,7 +444,7 @@ cudaError_t clusters_at_once(const LaunchCtx& c, int ctas, int* n) {
   std::atomic<int>& slot = known[ctas == 2 ? 1 : ctas == 4 ? 2 : 3];
   *n = slot.load(std::memory_order_relaxed);
   if (*n > 0) return cudaSuccess;
-  auto* kernel = expert_matmul_kernel<S>;
+  auto* kernel = expert_matmul_kernel<S, false>;
   cudaError_t e = allow_max_dynamic_smem(kernel);
   if (e != cudaSuccess) return e;
   Config<S> cfg(MOE_MAX_EXPERTS, (int64_t)c.num_sms / ctas * ctas, ctas);
@@ -447,9 +457,9 @@ cudaError_t clusters_at_once(const LaunchCtx& c, int ctas, int* n) {
 }
 
 // `ctas` CTAs per item (a cluster, if more than one).
-template <class S>
-cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a, int64_t groups, int ctas) {
-  auto* kernel = expert_matmul_kernel<S>;
+template <class S, bool F32>
+cudaError_t launch_f(const LaunchCtx& c, const MatmulInt8Args& a, int64_t groups, int ctas) {
+  auto* kernel = expert_matmul_kernel<S, F32>;
   static SmemOptIn opt_in;
   cudaError_t e = opt_in.once(kernel);
   if (e != cudaSuccess) return e;
@@ -460,6 +470,10 @@ cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a, int64_t groups
   cfg.c.stream = c.stream;
   count_launches(1);
   return cudaLaunchKernelEx(&cfg.c, kernel, a, map, c.err);
+}
+template <class S>
+cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a, int64_t groups, int ctas) {
+  return a.out_f32 ? launch_f<S, true>(c, a, groups, ctas) : launch_f<S, false>(c, a, groups, ctas);
 }
 
 }  // namespace

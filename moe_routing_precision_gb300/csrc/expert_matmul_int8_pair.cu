@@ -9,18 +9,19 @@
 // memory, half in each: a product is 256 x 256 x 16 in 128 clocks, every converted value
 // feeds 256 others, and one thread of the pair issues 8 products per wait.
 //
-// Warps 0-7 convert the weights (a thread per weight row) and write the finished tile out,
-// 8-15 gather and convert rows, both in two sets of 4 that take the stages in turn; 16
-// asks for the weights (TMA), 17 issues the products (first CTA).  With SwiGLU a CTA holds 64 gate and the 64 up rows of
+// Warps 0-7 convert the weights (a thread per weight row), 8-15 write finished tiles out,
+// 16-23 gather and convert rows; the converting and the gathering warps are two sets of 4
+// that take the stages in turn.  24 asks for the weights (TMA), 25 issues the products
+// (first CTA).  With SwiGLU a CTA holds 64 gate and the 64 up rows of
 // the same channels, in runs of 8 lanes by turns, so that lane l's partner is l ^ 8.
 #include "block/matmul_int8.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 18;
+constexpr int kConvert = 8, kFinish = 8, kGather = 8;  // warps
+constexpr int kWarps = kConvert + kFinish + kGather + 2;
 constexpr int kThreads = kWarps * 32;
-constexpr int kConvert = 8, kGather = 8;
 constexpr int kStages = 4;     // of weights (bytes), rows (f16) and weights (f16)
 constexpr int kRowsMax = 256;  // rows of a tile
 constexpr int kOuts = 128;     // outputs of a CTA
@@ -38,7 +39,7 @@ __host__ __device__ inline Smem smem_layout(int E) {
   s.a = 0;
   s.b = s.a + kStages * kABytes;
   s.bars = s.b + kStages * kBBytes;
-  s.xsf = s.bars + (4 * kStages + 4) * 8;
+  s.xsf = s.bars + (4 * kStages + 4) * 8;  // 16-byte aligned
   s.totals = s.xsf + kRowsMax * 4;
   s.tmem = s.totals + kWarps * 4;
   s.first = s.tmem + 16 - (s.tmem & 7);
@@ -47,6 +48,7 @@ __host__ __device__ inline Smem smem_layout(int E) {
   return s;
 }
 
+template <bool SWIGLU, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_matmul_pair_kernel(const MatmulInt8Args a, const __grid_constant__ CUtensorMap map,
                               unsigned* err) {
@@ -69,12 +71,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     for (int i = 0; i < kStages; ++i) {
       mbar_init_n(a_full + i * 8, 1);
-      mbar_init_n(a_free + i * 8, kConvert / 2);
-      mbar_init_n(full + i * 8, kConvert + kGather);
+      mbar_init_n(a_free + i * 8, 4);
+      mbar_init_n(full + i * 8, 2 * (4 + 4));
       mbar_init_n(done + i * 8, 1);
     }
     mbar_init_n(c_full, 1);
-    mbar_init_n(c_free, 2 * kConvert);
+    mbar_init_n(c_free, 2 * kFinish);
     mbar_init_n(drain, 1);
     mbar_init_done();
   }
@@ -85,8 +87,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_enter();
   list.build<kThreads, kRowsMax>(a, reinterpret_cast<int*>(smem + L.totals), err);
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L.tmem);
-  const int M = a.swiglu ? 2 * a.N : a.N;
-  const int per_tile = a.swiglu ? kOuts : 2 * kOuts;  // of the pair
+  const int M = SWIGLU ? 2 * a.N : a.N;
+  const int per_tile = SWIGLU ? kOuts : 2 * kOuts;  // of the pair
   const int tiles = (a.N + per_tile - 1) / per_tile;
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
   const int64_t items = (int64_t)list.runs() * tiles;
@@ -110,97 +112,121 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kConvert) {
     const int l = (warp & 3) * 32 + lane, set = warp >> 2;
     const uint32_t lanes = tmem + (uint32_t)((warp & 3) * 32) * kTmemLane;
-    const bool up = a.swiglu && (l & 8);
-    const int src = a.swiglu ? (l & 8) * 8 + (l >> 4) * 8 + (l & 7) : l;  // weight row in a stage
+    const int src = SWIGLU ? (l & 8) * 8 + (l >> 4) * 8 + (l & 7) : l;  // weight row in a stage
     const uint32_t a_at = sbase + L.a + (uint32_t)(src * 128 + ((src & 7) << 4));
     Ring ra;
     ra.next<kStages>(set);
-    int turn = set;  // this set's first stage of the item
+    // every other stage, of all items
+    const int64_t stages = item0 < items ? ((items - 1 - item0) / item_step + 1) * nblk : 0;
+    for (int64_t s = set; s < stages; s += 2) {
+      if (!wait_warp(a_full + ra.i * 8, ra.phase)) break;
+      const uint32_t at = a_at + (uint32_t)(ra.i * kABytes);
+      const uint32_t to = lanes + (uint32_t)(kColA + ra.i * (kBlockK / 2));
+      uint32_t f[32];
+      // 64 channels; of the second 64 the two 8s of each 16 exchanged, as the rows' are
+      auto convert = [&](auto second) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          constexpr int first = second ? 4 : 0;
+          const uint4 v = lds_v4(at ^ (uint32_t)((first + c) << 4));
+          uint32_t *p = f + c * 8 + first, *q = f + c * 8 + 4 - first;
+          int8x4_to_f16(v.x, p[0], p[1]);
+          int8x4_to_f16(v.y, p[2], p[3]);
+          int8x4_to_f16(v.z, q[0], q[1]);
+          int8x4_to_f16(v.w, q[2], q[3]);
+        }
+      };
+      convert(std::integral_constant<bool, false>());
+      if (!wait_warp(done + ra.i * 8, ra.phase ^ 1u)) break;
+      tc_after_sync();
+      tmem_store32(to, f);
+      convert(std::integral_constant<bool, true>());
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_free + ra.i * 8);
+      tmem_store32(to + 32, f);
+      tmem_store_wait();
+      tc_before_sync();
+      __syncwarp();
+      if (lane == 0) pair_arrive(cluster_map(full + ra.i * 8, 0));
+      ra.next<kStages>(2);
+    }
+  } else if (warp < kConvert + kFinish) {
+    // ---- the tiles' outputs: a warp's lanes, every other 16 of the columns
+    const int l = (warp & 3) * 32 + lane, turn = (warp >> 2) & 1, t = tid - kConvert * 32;
+    const uint32_t lanes = tmem + (uint32_t)((warp & 3) * 32) * kTmemLane;
+    const bool up = SWIGLU && (l & 8);
     uint32_t c_phase = 0;
     for (int64_t it = item0; it < items && ok; it += item_step) {
       const Item m = list.at(it, tiles);
-      // the scales of the run's rows, asked for early
       float my_xsf = 0.0f;
-      if (tid < m.n) {
-        const int64_t s = source_row(a, m.r0 + tid, err);
+      if (t < m.n) {
+        const int64_t s = source_row(a, m.r0 + t, err);
         if (s >= 0) my_xsf = __ldg(a.x_sf + s);
       }
       const int n0 = m.tile * per_tile + rank * (per_tile / 2) +
-                     (a.swiglu ? (l >> 4) * 8 + (l & 7) : l);
+                     (SWIGLU ? (l >> 4) * 8 + (l & 7) : l);
       const float* wsf = a.w_sf + (int64_t)m.e * M;
       const float w0 = n0 < a.N ? __ldg(wsf + n0) : 0.0f;
-      const float w1 = a.swiglu && n0 < a.N ? __ldg(wsf + a.N + n0) : 0.0f;
-      int kb = turn;
-      for (; kb < nblk; kb += 2) {
-        if (!wait_warp(a_full + ra.i * 8, ra.phase)) break;
-        const uint32_t at = a_at + (uint32_t)(ra.i * kABytes);
-        const uint32_t to = lanes + (uint32_t)(kColA + ra.i * (kBlockK / 2));
-        uint32_t f[32];
-        // 64 channels; of the second 64 the two 8s of each 16 exchanged, as the rows' are
-        auto convert = [&](auto second) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            constexpr int first = second ? 4 : 0;
-            const uint4 v = lds_v4(at ^ (uint32_t)((first + c) << 4));
-            uint32_t *p = f + c * 8 + first, *q = f + c * 8 + 4 - first;
-            int8x4_to_f16(v.x, p[0], p[1]);
-            int8x4_to_f16(v.y, p[2], p[3]);
-            int8x4_to_f16(v.z, q[0], q[1]);
-            int8x4_to_f16(v.w, q[2], q[3]);
-          }
-        };
-        convert(std::integral_constant<bool, false>());
-        if (!wait_warp(done + ra.i * 8, ra.phase ^ 1u)) break;
-        tc_after_sync();
-        tmem_store32(to, f);
-        convert(std::integral_constant<bool, true>());
-        __syncwarp();
-        if (lane == 0) mbar_arrive(a_free + ra.i * 8);
-        tmem_store32(to + 32, f);
-        tmem_store_wait();
-        tc_before_sync();
-        __syncwarp();
-        if (lane == 0) pair_arrive(cluster_map(full + ra.i * 8, 0));
-        ra.next<kStages>(2);
-      }
-      turn = kb - nblk;
-      // ---- the tile's outputs: this warp's lanes, every other 16 of the columns
-      s_xsf[tid] = my_xsf;
-      ok = named_and(1, kConvert * 32, ok);
+      const float w1 = SWIGLU && n0 < a.N ? __ldg(wsf + a.N + n0) : 0.0f;
+      s_xsf[t] = my_xsf;
+      ok = named_and(1, kFinish * 32, ok);
       if (ok && wait_warp(c_full, c_phase)) {
         tc_after_sync();
-        for (int c = set * 16; c < m.n; c += 32) {
+        for (int c = turn * 16; c < m.n; c += 32) {
           float x[16];
           __syncwarp();
           tmem_load16(lanes + c, x);
-          if (a.swiglu) {
+          if (c + 32 >= m.n) {  // the last of them: the next tile's products may begin
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) pair_arrive(cluster_map(c_free, 0));
+          }
+          const int rows = m.n - c < 16 ? m.n - c : 16;
+          float xs[16];
+          load_scales16(s_xsf + c, xs);
+          if constexpr (SWIGLU) {
             // of two columns the gate's lane finishes the first, the up lane the second
+            float v[16];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
               const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? x[j] : x[j + 1], 8);
-              const int col = c + j + (up ? 1 : 0);
-              if (col >= m.n || n0 >= a.N) continue;
-              const float xs = s_xsf[col];
-              const float g = (up ? got : x[j]) * xs * w0, u = (up ? x[j + 1] : got) * xs * w1;
-              store_out(a, (m.r0 + col) * a.N + n0, g / (1.0f + expf(-g)) * u);
+              const float s = up ? xs[j + 1] : xs[j];
+              const float g = (up ? got : x[j]) * s * w0, u = (up ? x[j + 1] : got) * s * w1;
+              v[j / 2] = g * sigmoid_f32(g) * u;
+            }
+            if (n0 < a.N) {
+              const int64_t at = (m.r0 + c + (up ? 1 : 0)) * a.N + n0;
+              const int mine = up ? rows - 1 : rows;  // columns j = 0, 2, .. below it
+#pragma unroll
+              for (int j = 0; j < 8; j += 2) {
+                if constexpr (F32) {
+                  float* o = static_cast<float*>(a.out) + at + 2 * j * (int64_t)a.N;
+                  if (2 * j < mine) *o = v[j];
+                  if (2 * j + 2 < mine) o[2 * (int64_t)a.N] = v[j + 1];
+                } else {
+                  uint16_t* o = static_cast<uint16_t*>(a.out) + at + 2 * j * (int64_t)a.N;
+                  const uint32_t w = pack_bf16x2_rn(v[j], v[j + 1]);
+                  if (2 * j < mine) *o = (uint16_t)w;
+                  if (2 * j + 2 < mine) o[2 * (int64_t)a.N] = (uint16_t)(w >> 16);
+                }
+              }
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              if (c + j >= m.n) break;
-              if (n0 < a.N) store_out(a, (m.r0 + c + j) * a.N + n0, x[j] * s_xsf[c + j] * w0);
-            }
+            for (int j = 0; j < 16; ++j) x[j] *= xs[j] * w0;
+            if (n0 < a.N) store_column16<F32>(a, x, m.r0 + c, rows, n0);
           }
         }
-        tc_before_sync();
-        __syncwarp();
-        if (lane == 0) pair_arrive(cluster_map(c_free, 0));
+        if (turn * 16 >= m.n) {  // no column here
+          __syncwarp();
+          if (lane == 0) pair_arrive(cluster_map(c_free, 0));
+        }
       }
       c_phase ^= 1u;
-      // the scales may be written over; the converting warps leave together
-      ok = named_and(1, kConvert * 32, ok);
+      // the scales may be written over; the finishing warps leave together
+      ok = named_and(1, kFinish * 32, ok);
     }
-  } else if (warp < kConvert + kGather) {
+  } else if (warp < kConvert + kFinish + kGather) {
     // as in the one-CTA form: 4 rows x 8 units of 16 channels per warp, every 16th row
     constexpr int kStep = kGather / 2 * 4, kUnits = kRowsMax / 2 / kStep;
     const int set = (warp >> 2) & 1, c = lane & 7, r0 = (warp & 3) * 4 + (lane >> 3);
@@ -264,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       turn = kb - nblk;
     }
-  } else if (warp == kConvert + kGather) {
+  } else if (warp == kConvert + kFinish + kGather) {
     if (lane == 0) {
       Ring ra;
       int64_t asked = 0;
@@ -273,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rows past the expert's last output are another's, or past the tensor and zero:
         // their products are not stored
         const int r0 = m.e * M + m.tile * per_tile + rank * (per_tile / 2);
-        const int r1 = a.swiglu ? r0 + a.N : r0 + kOuts / 2;
+        const int r1 = SWIGLU ? r0 + a.N : r0 + kOuts / 2;
         for (int kb = 0; kb < nblk; ++kb) {
           if (!wait(a_free + ra.i * 8, ra.phase ^ 1u)) break;
           const uint32_t bar = a_full + ra.i * 8, dst = sbase + L.a + (uint32_t)(ra.i * kABytes);
@@ -338,16 +364,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-}  // namespace
-
-cudaError_t launch_expert_matmul_int8_pair(const LaunchCtx& c, const MatmulInt8Args& a) {
+template <bool SWIGLU, bool F32>
+cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a) {
+  auto* kernel = expert_matmul_pair_kernel<SWIGLU, F32>;
   static SmemOptIn opt_in;
-  cudaError_t e = opt_in.once(expert_matmul_pair_kernel);
+  cudaError_t e = opt_in.once(kernel);
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   e = weight_map(a, kOuts / 2, &map);
   if (e != cudaSuccess) return e;
-  const int per_tile = a.swiglu ? kOuts : 2 * kOuts;
+  const int per_tile = SWIGLU ? kOuts : 2 * kOuts;
   int64_t runs = (a.offsets ? a.E : 1) + (a.R + kRowsMax - 1) / kRowsMax - 1;
   if (runs > a.R) runs = a.R;
   const int64_t items = runs * ((a.N + per_tile - 1) / per_tile), pairs = c.num_sms / 2;
@@ -365,7 +391,14 @@ cudaError_t launch_expert_matmul_int8_pair(const LaunchCtx& c, const MatmulInt8A
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   count_launches(1);
-  return cudaLaunchKernelEx(&cfg, expert_matmul_pair_kernel, a, map, c.err);
+  return cudaLaunchKernelEx(&cfg, kernel, a, map, c.err);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_matmul_int8_pair(const LaunchCtx& c, const MatmulInt8Args& a) {
+  if (a.swiglu) return a.out_f32 ? launch_t<true, true>(c, a) : launch_t<true, false>(c, a);
+  return a.out_f32 ? launch_t<false, true>(c, a) : launch_t<false, false>(c, a);
 }
 
 }  // namespace moe
