@@ -34,7 +34,8 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
+               : "r"(a)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -72,21 +73,22 @@ __device__ __forceinline__ void store_out(const MatmulInt8Args& a, int64_t at, f
     static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// 16 columns of one thread's output channel: x[j], scaled, into rows row + j (j < rows),
-// channel ch.  Two rows share a conversion, and the address goes from row to row.
-template <bool F32>
-__device__ __forceinline__ void store_column16(const MatmulInt8Args& a, const float (&v)[16],
-                                               int64_t row, int rows, int ch) {
+// COLS columns of one thread's output channel into rows row + j (j < rows), channel ch.
+// Two rows share a conversion, and the address goes from row to row (a product per store
+// and a conversion each took the tile of 256 x 256, K = 2048, longer than its products).
+template <bool F32, int COLS>
+__device__ __forceinline__ void store_column(const MatmulInt8Args& a, const float (&v)[COLS],
+                                             int64_t row, int rows, int ch) {
   const int64_t at = row * a.N + ch;
   if constexpr (F32) {
     float* o = static_cast<float*>(a.out) + at;
 #pragma unroll
-    for (int j = 0; j < 16; ++j, o += a.N)
+    for (int j = 0; j < COLS; ++j, o += a.N)
       if (j < rows) *o = v[j];
   } else {
     uint16_t* o = static_cast<uint16_t*>(a.out) + at;
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
+    for (int j = 0; j < COLS; j += 2) {
       const uint32_t w = pack_bf16x2_rn(v[j], v[j + 1]);
       if (j < rows) *o = (uint16_t)w;
       o += a.N;
@@ -175,7 +177,9 @@ struct ItemList {
   }
 
   __device__ __forceinline__ Item at(int64_t it, int tiles) const {
-    const int q = (int)(it / tiles);
+    // 32-bit divisions where they do (a 64-bit one takes longer than the search)
+    const bool narrow = it < (int64_t)1 << 32;
+    const int q = narrow ? (int)((uint32_t)it / (uint32_t)tiles) : (int)(it / tiles);
     int e = 0;  // the last expert with first[e] <= q
     for (int hi = E; hi - e > 1;) {
       const int mid = (e + hi) >> 1;
@@ -188,7 +192,7 @@ struct ItemList {
     const int64_t local = it - (int64_t)first[e] * tiles;
     Item m;
     m.e = e;
-    m.tile = (int)(local / n);
+    m.tile = narrow ? (int)((uint32_t)local / (uint32_t)n) : (int)(local / n);
     const int2 span = rows[e];
     const int run = (int)(local - (int64_t)m.tile * n);
     const int per = ((span.y - span.x + n - 1) / n + 15) / 16 * 16;

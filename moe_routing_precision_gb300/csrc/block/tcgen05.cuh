@@ -183,8 +183,8 @@ __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
-// The same for operands of the tensor cores, which a proxy fence or tcgen05's has ordered
-// before: no release of other memory to the cluster (which cost a stage 1 us).
+// The same for operands of the tensor cores, which a proxy fence or tcgen05's fence has
+// ordered before: no release of other memory to the cluster (which took a stage 1 us).
 __device__ __forceinline__ void pair_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

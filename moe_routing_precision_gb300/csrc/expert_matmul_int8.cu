@@ -17,9 +17,15 @@
 //          write the finished tiles out; 4 warps per half
 //   8-15   gather, convert and store the rows of x
 //   16     asks for the weights (TMA, 128-byte swizzle)
-//   17-18  issue the products of one half each: what one waits for does not keep the
-//          tensor cores from the other's
-#include <cstdlib>
+//   17-18  issue the products of one half each: a product takes at least the 61 clocks
+//          that its weights take out of tensor memory, and what one issuer waits for does
+//          not keep the tensor cores from the other's (one issuer: 620 : 496 us, 64 tokens,
+//          top 8 of 256, K = 2048, N = 7168)
+// Measured: 64 tokens, top 8 of 256, K = 7168, SwiGLU of 2 x 2048 (6.5 GB): 945 us, 6.9
+// TB/s, and K = 2048, N = 7168 (3.3 GB) 521 us: HBM bounds them.  One token: 50 us for 235
+// MB: 5 us until the first weights are there, 128 tiles for 152 SMs, then 5.5 TB/s.  16
+// converting warps in two sets were slower for long runs (308 : 336 us), as were tiles of
+// 32, 64 or 96 rows (no faster for few rows).  Long runs: expert_matmul_int8_pair.cu.
 #include "block/matmul_int8.cuh"
 
 namespace moe {
@@ -172,8 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         convert(0);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(a_free + ra.i * 8);
         if (!wait_warp(t_free + (half * S::ST + rt.i) * 8, rt.phase ^ 1u)) break;
         tc_after_sync();
         const uint32_t to = lanes + (uint32_t)(S::kColA + rt.i * 128 + half * 64);
@@ -183,7 +187,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_store_wait();
         tc_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(t_full + (half * S::ST + rt.i) * 8);
+        // the weights' place is free only now, when the stores have taken what was loaded: an
+        // arrival beside the loads may be moved before them
+        if (lane == 0) {
+          mbar_arrive(t_full + (half * S::ST + rt.i) * 8);
+          mbar_arrive(a_free + ra.i * 8);
+        }
         ra.next<S::SA>();
         rt.next<S::ST>();
       }
@@ -220,16 +229,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               part[(NT + c + j) * kHalf + row] = y[j];
             }
           } else {
-            float xs[16];
-            load_scales16(s_xsf + c, xs);
+            // 4 columns at a time: a run may have few rows
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] *= xs[j] * w0, y[j] *= xs[j] * w1;
-            if (a.swiglu) {
+            for (int j = 0; j < 16; j += 4) {
+              if (j >= rows) break;
+              const float4 xs = *reinterpret_cast<const float4*>(s_xsf + c + j);
+              const float s[4] = {xs.x, xs.y, xs.z, xs.w};
+              float p[4], q[4];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = x[j] * sigmoid_f32(x[j]) * y[j];
+              for (int i = 0; i < 4; ++i) {
+                p[i] = x[j + i] * s[i] * w0, q[i] = y[j + i] * s[i] * w1;
+                if (a.swiglu) p[i] = p[i] * sigmoid_f32(p[i]) * q[i];
+              }
+              if (n0 < a.N) store_column<F32, 4>(a, p, m.r0 + c + j, rows - j, n0);
+              if (!a.swiglu && n1 < a.N) store_column<F32, 4>(a, q, m.r0 + c + j, rows - j, n1);
             }
-            if (n0 < a.N) store_column16<F32>(a, x, m.r0 + c, rows, n0);
-            if (!a.swiglu && n1 < a.N) store_column16<F32>(a, y, m.r0 + c, rows, n1);
           }
         }
         tc_before_sync();
@@ -479,7 +493,7 @@ cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a, int64_t groups
 }  // namespace
 
 cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& a) {
-  using Whole = Shape<128, 3, 3, 2, false>;
+  using Whole = Shape<128, 4, 2, 2, false>;
   using Split = Shape<32, 4, 4, 3, true>;
   const int per_tile = a.swiglu ? kHalf : 2 * kHalf;
   const int64_t tiles = (a.N + per_tile - 1) / per_tile;
@@ -503,7 +517,11 @@ cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& 
     if (split <= fit) ctas = s;
   }
   if (ctas > 1) return launch_t<Split>(c, a, split, ctas);
-  if (getenv("MMP")) return launch_expert_matmul_int8_pair(c, a);
+  // Long runs of rows: a pair of CTAs per tile (us, one CTA : a pair; 256 experts, K = 7168,
+  // SwiGLU of 2 x 2048: 64 rows per expert on average 1532 : 1720, 80 1621 : 1772, 128 2086 :
+  // 1963, 256 3507 : 2850; one expert, K = N = 4096: 128 rows 22 : 22, 256 35 : 27; 16 experts
+  // of 1024 rows, K = N = 256: 17 : 19, its start counts).
+  if (a.R > 104 * (int64_t)a.E && a.K > 512) return launch_expert_matmul_int8_pair(c, a);
   const int64_t whole = items(Whole::NT);
   return launch_t<Whole>(c, a, whole < c.num_sms ? whole : c.num_sms, 1);
 }

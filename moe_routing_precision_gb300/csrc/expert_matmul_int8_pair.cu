@@ -2,12 +2,18 @@
 // long runs of rows: a pair of CTAs shares one tile.
 //
 // With one CTA per tile a product of 128 x 128 x 16 takes 64 clocks of the tensor cores
-// and as long to read its weights from tensor memory, and each converted row of x feeds
-// 256 outputs: shared memory (1250 clocks per 128 channels, of which 1024 in the products)
-// and the waits on its barriers bound it at 1.3 PFLOP/s.  Here the weights of 256 outputs
-// lie in the two CTAs' tensor memory, 128 each, and up to 256 rows of x in their shared
-// memory, half in each: a product is 256 x 256 x 16 in 128 clocks, every converted value
-// feeds 256 others, and one thread of the pair issues 8 products per wait.
+// and as long to read its weights from tensor memory, each converted row of x feeds 256
+// outputs, and two threads issue 8 products per wait each: 1.35 PFLOP/s.  Here the weights
+// of 256 outputs lie in the two CTAs' tensor memory, 128 each, and up to 256 rows of x in
+// their shared memory, half in each: a product is 256 x 256 x 16 in 128 clocks, every
+// converted value feeds 256 others, and one thread of the pair issues 8 products per wait.
+//
+// Measured: 4096 rows, K = N = 7168: 218 us, 1.93 PFLOP/s, as fast as the measured rate of
+// a library's f16 product (1.89); 8192 tokens, top 8 of 256, K = 7168, SwiGLU of 2 x 2048:
+// 2850 us, 1.35 PFLOP/s (runs of 150 to 450 rows do not fill tiles of 256, and a stage of
+// few rows takes as long as its weights' conversion, 950 clocks); the down products, K =
+// 2048, N = 7168: 1607 us, 1.2 PFLOP/s (also the tile's end: its sums are read before the
+// next tile's products may begin).
 //
 // Warps 0-7 convert the weights (a thread per weight row), 8-15 write finished tiles out,
 // 16-23 gather and convert rows; the converting and the gathering warps are two sets of 4
@@ -72,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init_n(a_full + i * 8, 1);
       mbar_init_n(a_free + i * 8, 4);
-      mbar_init_n(full + i * 8, 2 * (4 + 4));
+      mbar_init_n(full + i * 8, 2 * (4 + 4));  // a set of converting and one of gathering warps
       mbar_init_n(done + i * 8, 1);
     }
     mbar_init_n(c_full, 1);
@@ -141,13 +147,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_after_sync();
       tmem_store32(to, f);
       convert(std::integral_constant<bool, true>());
-      __syncwarp();
-      if (lane == 0) mbar_arrive(a_free + ra.i * 8);
       tmem_store32(to + 32, f);
       tmem_store_wait();
       tc_before_sync();
       __syncwarp();
-      if (lane == 0) pair_arrive(cluster_map(full + ra.i * 8, 0));
+      // the weights' place is free only now: an arrival beside the loads was moved before
+      // them, and the next weights overtook the second half
+      if (lane == 0) {
+        pair_arrive(cluster_map(full + ra.i * 8, 0));
+        mbar_arrive(a_free + ra.i * 8);
+      }
       ra.next<kStages>(2);
     }
   } else if (warp < kConvert + kFinish) {
@@ -214,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) x[j] *= xs[j] * w0;
-            if (n0 < a.N) store_column16<F32>(a, x, m.r0 + c, rows, n0);
+            if (n0 < a.N) store_column<F32, 16>(a, x, m.r0 + c, rows, n0);
           }
         }
         if (turn * 16 >= m.n) {  // no column here

@@ -907,13 +907,13 @@ def expert_matvec_fp4(x: torch.Tensor, w: torch.Tensor, w_sf: torch.Tensor, offs
 
 def _one_device(first: torch.Tensor, *others):
     """Every tensor (or None) on `first`'s device, and that the current one."""
-    dev = first.device
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: all must be on one device")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}: all must be on one device")
     here = _cuda_device() if _cuda_device is not None else torch.cuda.current_device()
-    if dev.index != here:
-        raise ValueError(f"tensors on {dev}, but the current device is cuda:{here}")
+    if dev != here:
+        raise ValueError(f"tensors on {first.device}, but the current device is cuda:{here}")
 
 
 def router_gate(scores: torch.Tensor, k: int, *, score_func: str = "softmax", bias=None,
