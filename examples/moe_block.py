@@ -1,6 +1,6 @@
-"""One MoE block, trained for a few steps and then decoded with 4-bit experts.
+"""One MoE block, trained for a few steps and then run with 4-bit and 8-bit experts.
 
-    python examples/moe_block.py            # both, with the losses printed
+    python examples/moe_block.py            # all of it, with the losses printed
 
 The block, in the order its kernels run (residual stream r, [T, H]):
 
@@ -18,6 +18,12 @@ passes: block_norm_backward, combine_backward, the experts', the router's
 (balance_loss_backward, which takes the top-k weights' gradient with it) and
 block_norm_backward again.  Decoding quantises the trained experts once with
 the library's own FP4 cast and then runs every step in its kernels.
+
+With router="sigmoid" the experts are selected by sigmoid scores plus a bias, from
+the best of their groups (router_gate, router_gate_backward); the bias is no
+parameter of the loss: after a step it moves towards the experts that got fewer
+tokens.  serve_int8 runs the block with experts in 8-bit integers (cast_int8,
+expert_matmul_int8), for a decoding step as for a whole prompt.
 """
 from __future__ import annotations
 
@@ -48,7 +54,12 @@ class Block:
     group: int = 32
     device: str = "cuda"
     seed: int = 0
+    router: str = "softmax"   # or "sigmoid": with a bias for balance, and groups
+    groups: int = 1
+    topk_groups: int = 1
+    route_scale: float = 1.0
     p: dict = field(default_factory=dict)
+    bias: torch.Tensor | None = None
 
     def __post_init__(self):
         g = torch.Generator().manual_seed(self.seed)
@@ -62,6 +73,7 @@ class Block:
                       router=randn(H, E, std=H ** -0.5),
                       up=randn(E, 2 * N, H, std=H ** -0.5),      # gate rows, then up rows
                       down=randn(E, H, N, std=N ** -0.5))
+        self.bias = torch.zeros(E, device=self.device)
 
 
 def swiglu(x):
@@ -69,12 +81,20 @@ def swiglu(x):
     return gate * torch.sigmoid(gate) * up
 
 
+def route(b: Block, scores):
+    """The tokens' experts and weights."""
+    if b.router == "softmax":
+        return ops.topk_gate(scores, b.k)
+    return ops.router_gate(scores, b.k, score_func="sigmoid", bias=b.bias, num_groups=b.groups,
+                           topk_groups=b.topk_groups, scale=b.route_scale)
+
+
 def forward(b: Block, r, seq_offsets, token_mask=None):
     """The block's output h and what its backward pass needs."""
     p = b.p
     _, n, _, rstd_pre = ops.block_norm(r, pre_weight=p["pre"])
     scores = n.float() @ p["router"]
-    idx, w = ops.topk_gate(scores, b.k)
+    idx, w = route(b, scores)
     counts, offsets, pos, src = ops.route_map(idx, b.E)
     rows = n[(src // b.k).long()]
     ends = offsets.tolist()
@@ -87,7 +107,8 @@ def forward(b: Block, r, seq_offsets, token_mask=None):
     y = ops.combine(y_e, w, pos)
     h, _, rstd_post, _ = ops.block_norm(r, y, post_weight=p["post"], gate=p["gate"],
                                         gate_act="sigmoid", scale=b.scale)
-    losses = ops.balance_loss(scores, idx, seq_offsets=seq_offsets, token_mask=token_mask)
+    losses = ops.balance_loss(scores, idx, score_func=b.router, seq_offsets=seq_offsets,
+                              token_mask=token_mask)
     saved = dict(r=r, n=n, rstd_pre=rstd_pre, scores=scores, idx=idx, w=w, ends=ends, pos=pos,
                  src=src, rows=rows, pre_act=pre_act, y_e=y_e, y=y, rstd_post=rstd_post, h=h,
                  losses=losses, seq_offsets=seq_offsets, token_mask=token_mask)
@@ -118,11 +139,17 @@ def backward(b: Block, s: dict, grad_h):
     grad_n = ops.combine(grad_rows, torch.ones_like(s["w"]), s["pos"], F32)
     _, _, counts, _, tokens = s["losses"]
     S = tokens.numel()
-    grad_scores = ops.balance_loss_backward(
-        s["scores"], counts, tokens, torch.full((S,), b.balance_coef / S, device=grad_h.device),
-        torch.full((S,), b.z_coef / S, device=grad_h.device), seq_offsets=s["seq_offsets"],
-        token_mask=s["token_mask"], topk_idx=s["idx"], topk_weights=s["w"],
-        grad_topk_weights=grad_w)
+    kw = dict(score_func=b.router, seq_offsets=s["seq_offsets"], token_mask=s["token_mask"])
+    coefs = (torch.full((S,), b.balance_coef / S, device=grad_h.device),
+             torch.full((S,), b.z_coef / S, device=grad_h.device))
+    if b.router == "softmax":
+        grad_scores = ops.balance_loss_backward(s["scores"], counts, tokens, *coefs, **kw,
+                                                topk_idx=s["idx"], topk_weights=s["w"],
+                                                grad_topk_weights=grad_w)
+    else:
+        grad_scores = ops.balance_loss_backward(s["scores"], counts, tokens, *coefs, **kw, k=b.k)
+        ops.router_gate_backward(s["scores"], s["idx"], grad_w, score_func="sigmoid",
+                                 scale=b.route_scale, add=grad_scores, out=grad_scores)
     g["router"] = s["n"].float().T @ grad_scores
     grad_n += grad_scores @ p["router"].T
     grad_r2, _, _, _, g["pre"] = ops.block_norm_backward(
@@ -147,6 +174,9 @@ def train(b: Block, steps: int = 8, tokens: int = 192, lr: float = 0.5, say=prin
         _, g = backward(b, s, err / err.numel())
         for name, grad in g.items():
             b.p[name] -= lr * grad * tokens ** 0.5
+        if b.router == "sigmoid":
+            load = s["losses"][2].sum(0).float()
+            b.bias += 0.01 * torch.sign(load.mean() - load)
         history.append(float(total))
         say(f"step {step}: loss {float(loss):.5f}  balance {float(balance.mean()):.4f}  "
             f"z {float(z.mean()):.4f}  total {history[-1]:.5f}")
@@ -182,6 +212,33 @@ def decode(b: Block, q: dict, r):
     return h
 
 
+def quantise_int8(b: Block) -> dict:
+    """The experts in 8-bit integers, once: a scale per output channel."""
+    out = {}
+    for name in ("up", "down"):
+        w = b.p[name]
+        E, M, K = w.shape
+        q, sf = ops.cast_int8(w.view(E * M, K))
+        out[name] = (q.view(E, M, K), sf.view(E, M))
+    return out
+
+
+def serve_int8(b: Block, q: dict, r):
+    """The block for r [T, H] with 8-bit experts, a decoding step or a prompt: every step in
+    the library's kernels but the router's product."""
+    p = b.p
+    _, n, _, _ = ops.block_norm(r, pre_weight=p["pre"])
+    idx, w = route(b, (n.float() @ p["router"]).contiguous())
+    _, offsets, pos, src = ops.route_map(idx, b.E)
+    act = ops.expert_matmul_int8(*ops.cast_int8(n), *q["up"], offsets, sorted_src=src, k=b.k,
+                                 swiglu=True)
+    y_e = ops.expert_matmul_int8(*ops.cast_int8(act), *q["down"], offsets)
+    y = ops.combine(y_e, w, pos)
+    h, _, _, _ = ops.block_norm(r, y, post_weight=p["post"], gate=p["gate"], gate_act="sigmoid",
+                                scale=b.scale)
+    return h
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=8)
@@ -196,6 +253,12 @@ def main():
     h = decode(b, q, r)
     rel = float((h - with_bf16).norm() / (with_bf16 - r).norm())
     print(f"decoded 4 tokens with 4-bit experts: relative to the bf16 block's update {rel:.3f}")
+    h = serve_int8(b, quantise_int8(b), r)
+    rel = float((h - with_bf16).norm() / (with_bf16 - r).norm())
+    print(f"the same with 8-bit experts: {rel:.3f}")
+    grouped = Block(router="sigmoid", groups=4, topk_groups=2, route_scale=2.0)
+    train(grouped, a.steps, a.tokens)
+    serve_int8(grouped, quantise_int8(grouped), torch.randn(300, grouped.H, device=b.device))
     assert ops.device_status() == 0
 
 

@@ -763,7 +763,8 @@ moe_status_t moe_router_gate_backward(const float *scores, int64_t num_tokens,
  *   out_sf[t] = a / 127;  out[t,c] = rint(x[t,c] * (127 / a))
  * each step in f32, rounded to nearest (ties to even): values in [-127, 127].
  *   x [T,H] in dtype (MOE_DT_*), finite; out [T,H] i8; out_sf [T] f32
- * Requires 0 <= T < 2^31, H >= 1, T * H < 2^40 and every tensor aligned to its element.
+ * Requires 0 <= T < 2^31, 1 <= H <= 2^30, T * H < 2^40 and every tensor aligned to its
+ * element.
  * Fastest with H % 8 == 0, x 16-byte and out 8-byte aligned.
  */
 moe_status_t moe_cast_int8(const void *x, int32_t dtype, int64_t num_rows, int32_t hidden,

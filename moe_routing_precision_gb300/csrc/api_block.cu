@@ -424,7 +424,8 @@ moe_status_t moe_router_gate_backward(const float* scores, int64_t num_tokens,
 moe_status_t moe_cast_int8(const void* x, int32_t dtype, int64_t num_rows, int32_t hidden,
                            int8_t* out, float* out_sf, void* stream) {
   if (!dtype_ok(dtype) || num_rows < 0 || hidden < 1) return MOE_ERR_INVALID_ARG;
-  if (num_rows >= ((int64_t)1 << 31) || num_rows >= ((int64_t)1 << 40) / hidden)
+  if (num_rows >= ((int64_t)1 << 31) || hidden > 1 << 30 ||
+      num_rows >= ((int64_t)1 << 40) / hidden)
     return MOE_ERR_UNSUPPORTED;
   if (num_rows == 0) return MOE_OK;
   if (!x || !out || !out_sf || !aligned(x, dtype_size(dtype)) || !aligned(out_sf, 4))

@@ -219,7 +219,7 @@ __device__ __noinline__ int select64(const float* row, const float* bias, int fu
       if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
     }
     if (lane == r) mine = at;
-    if (lane == 0) list[at] = 0ull;
+    if (lane == 0 && at < E) list[at] = 0ull;
     __syncwarp();
   }
   return mine;
@@ -639,15 +639,16 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
     ws.by_rank[lane] = none;
     __syncwarp();
     int rank = 0;
-    for (int j = 0; j < C; j += 4) {
+    const int held = C <= 32 ? C : 0;  // candidates one per lane
+    for (int j = 0; j < held; j += 4) {
       const float4 o = *reinterpret_cast<const float4*>(ws.c + j);
       rank += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
     }
-    if (lane < C) ws.by_rank[rank] = v;
+    if (lane < held) ws.by_rank[rank] = v;
     __syncwarp();
     // an empty rank follows equal values; and neighbours that are too close
     bool bad = false;
-    if (lane < k && lane + 1 < C) {
+    if (lane < k && lane + 1 < held) {
       const float p = ws.by_rank[lane], q = ws.by_rank[lane + 1];
       bad = q != q || (!by_x && q > -kInf &&
                        p - q <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(p), fabsf(q)));
