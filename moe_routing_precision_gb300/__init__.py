@@ -15,7 +15,9 @@ declared in ``include/moe_route.h``:
 Around them, the operators of an MoE block in training and decoding:
 ``block_norm`` (the norms before and after the block, with its gate and
 residual scale), ``balance_loss``, ``combine_backward`` and the backward
-passes, and ``expert_matvec_fp4`` (products with 4-bit expert weights).
+passes, ``expert_matvec_fp4`` (products with 4-bit expert weights), ``router_gate``
+with its backward pass (a bias for balance, groups), ``cast_int8`` and
+``expert_matmul_int8`` (products with 8-bit expert weights).
 
 ``ops`` is the thin Python binding (argument marshalling only); it loads the
 in-tree shared library and raises if it is missing.  ``workloads`` draws the
