@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t blk = (uint32_t)(rb.i * S::kBBytes);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-          if (kStep * u >= m.n) break;
+          if (kStep * u + (warp - kConvert) * 4 >= m.n) break;  // this warp's rows
           uint32_t f[8];
           int8x4_to_f16(v[u].x, f[0], f[1]);
           int8x4_to_f16(v[u].y, f[2], f[3]);
