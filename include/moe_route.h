@@ -744,8 +744,9 @@ moe_status_t moe_router_gate(const float *scores, int64_t num_tokens, int32_t nu
  *                                    for every expert e'               (softmax)
  * and 0 elsewhere; with add, that is added to add's entry (moe_balance_loss_backward's
  * gradient, say).
- *   scores [T,E] f32 as above; topk_idx [T,k] i32, a token's experts distinct;
- *   grad_topk_weights [T,k] f32; add [T,E] f32, may be NULL
+ * (an expert that a token names twice gets both gradients).
+ *   scores [T,E] f32 as above; topk_idx [T,k] i32; grad_topk_weights [T,k] f32;
+ *   add [T,E] f32, may be NULL
  *   grad_scores [T,E] f32 out; may be add itself (in place)
  * An index outside [0, E) is left out of every sum and sets MOE_DEVERR_EXPERT_RANGE.
  * Requires the E and k limits of moe_topk_gate and a finite scale.

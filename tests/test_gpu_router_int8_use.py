@@ -315,6 +315,33 @@ def test_products_write_their_rows_only(rows):
             check(out[:rows - 2], want[:rows - 2], mag[:rows - 2] / 8, "products")
 
 
+@pytest.mark.parametrize("func", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("shape", [(1, 8, 8), (6, 256, 8), (9, 40, 7), (5, 33, 16), (7, 512, 12),
+                                   (3, 200, 16), (6, 1024, 32), (2, 1024, 3)])
+def test_router_gradient_of_an_expert_named_twice(shape, func, renorm):
+    """Both gradients reach the entry, in place too; entries named not at all between
+    others and tokens that share no warp evenly."""
+    T, E, k = shape
+    r = gen(T * E + k)
+    x = torch.randn(T, E, generator=r) * 3
+    idx = torch.randint(0, max(1, min(E, k // 2)), (T, k), generator=r, dtype=I32)
+    idx[-1, 0] = -1
+    gw = torch.randn(T, k, generator=r)
+    add = torch.randn(T, E, generator=r) * 0.1
+    args = dict(score_func=func, renormalize=renorm, scale=2.5)
+    for a in (None, add):
+        want, mag = ref.gate_grad(x, idx, gw, func, renorm, 2.5, a)
+        got = ops.router_gate_backward(x.to(DEV), idx.to(DEV), gw.to(DEV),
+                                       add=None if a is None else a.to(DEV), **args)
+        assert ops.device_status() == ops.MOE_DEVERR_EXPERT_RANGE
+        check(got, want, mag, "grad_scores")
+    same = add.to(DEV)
+    ops.router_gate_backward(x.to(DEV), idx.to(DEV), gw.to(DEV), add=same, out=same, **args)
+    assert ops.device_status() == ops.MOE_DEVERR_EXPERT_RANGE
+    check(same, want, mag, "in place")
+
+
 def test_under_the_debug_bounds_library():
     """The same kernels with their internal checks compiled in report nothing."""
     env = dict(os.environ, MOE_DEBUG_BOUNDS="1")
