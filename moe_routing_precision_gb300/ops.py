@@ -916,6 +916,11 @@ def _one_device(first: torch.Tensor, *others):
         raise ValueError(f"tensors on {first.device}, but the current device is cuda:{here}")
 
 
+def _result(out, name: str, shape, dtype, like, stream):
+    """The caller's output, checked, or a new one, which needs no check."""
+    return _empty(shape, dtype, like, stream) if out is None else _dev(out, name, dtype, shape)
+
+
 def router_gate(scores: torch.Tensor, k: int, *, score_func: str = "softmax", bias=None,
                 num_groups: int = 1, topk_groups: int | None = None, group_score: str = "top2",
                 renormalize: bool = True, scale: float = 1.0, out_idx=None, out_w=None,
@@ -935,11 +940,9 @@ def router_gate(scores: torch.Tensor, k: int, *, score_func: str = "softmax", bi
     T, E = scores.shape
     if bias is not None:
         _dev(bias, "bias", torch.float32, (E,))
-    idx = out_idx if out_idx is not None else _empty((T, k), torch.int32, scores, stream)
-    _dev(idx, "out_idx", torch.int32, (T, k))
-    w = out_w if out_w is not None else _empty((T, k), torch.float32, scores, stream)
-    _dev(w, "out_w", torch.float32, (T, k))
-    _one_device(scores, bias, idx, w)
+    idx = _result(out_idx, "out_idx", (T, k), torch.int32, scores, stream)
+    w = _result(out_w, "out_w", (T, k), torch.float32, scores, stream)
+    _one_device(scores, bias, out_idx, out_w)
     rc = lib().moe_router_gate(_ptr(scores), T, E, k,
                                _choice(score_func, _SCORE_FUNC, "score_func"), _ptr(bias),
                                num_groups, num_groups if topk_groups is None else topk_groups,
@@ -966,9 +969,8 @@ def router_gate_backward(scores: torch.Tensor, topk_idx: torch.Tensor,
     _dev(grad_topk_weights, "grad_topk_weights", torch.float32, (T, k))
     if add is not None:
         _dev(add, "add", torch.float32, (T, E))
-    g = out if out is not None else _on(stream, torch.empty_like)(scores)
-    _dev(g, "out", torch.float32, (T, E))
-    _one_device(scores, topk_idx, grad_topk_weights, add, g)
+    g = _result(out, "out", (T, E), torch.float32, scores, stream)
+    _one_device(scores, topk_idx, grad_topk_weights, add, out)
     rc = lib().moe_router_gate_backward(_ptr(scores), T, E, k,
                                         _choice(score_func, _SCORE_FUNC, "score_func"),
                                         int(renormalize), scale, _ptr(topk_idx),
@@ -989,11 +991,9 @@ def cast_int8(x: torch.Tensor, *, out=None, out_sf=None, stream=None):
     if x.dim() != 2:
         raise ValueError("x must be [rows, H]")
     T, H = x.shape
-    q = out if out is not None else _empty((T, H), torch.int8, x, stream)
-    _dev(q, "out", torch.int8, (T, H))
-    sf = out_sf if out_sf is not None else _empty((T,), torch.float32, x, stream)
-    _dev(sf, "out_sf", torch.float32, (T,))
-    _one_device(x, q, sf)
+    q = _result(out, "out", (T, H), torch.int8, x, stream)
+    sf = _result(out_sf, "out_sf", (T,), torch.float32, x, stream)
+    _one_device(x, out, out_sf)
     _check(lib().moe_cast_int8(_ptr(x), dt, T, H, _ptr(q), _ptr(sf), _stream(stream)),
            "moe_cast_int8")
     return q, sf
@@ -1013,11 +1013,10 @@ def expert_matmul_int8(x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_s
     -> out [R, N] bfloat16 or float32 (rows past offsets[E] not written)."""
     _dev(x, "x", torch.int8)
     _dev(w, "w", torch.int8)
-    if x.dim() != 2 or w.dim() != 3:
+    if x.dim() != 2 or w.dim() != 3 or w.shape[2] != x.shape[1]:
         raise ValueError("x must be [rows, K] and w [E, M, K]")
     X, K = x.shape
-    E, M = w.shape[0], w.shape[1]
-    _dev(w, "w", torch.int8, (E, M, K))
+    E, M, _ = w.shape
     _dev(x_sf, "x_sf", torch.float32, (X,))
     _dev(w_sf, "w_sf", torch.float32, (E, M))
     if swiglu and M % 2:
@@ -1033,9 +1032,8 @@ def expert_matmul_int8(x: torch.Tensor, x_sf: torch.Tensor, w: torch.Tensor, w_s
             raise ValueError("sorted_src must be [R]")
         R = sorted_src.shape[0]
     N = M // 2 if swiglu else M
-    o = out if out is not None else _empty((R, N), out_dtype, x, stream)
-    _dev(o, "out", out_dtype, (R, N))
-    _one_device(x, x_sf, w, w_sf, offsets, sorted_src, o)
+    o = _result(out, "out", (R, N), out_dtype, x, stream)
+    _one_device(x, x_sf, w, w_sf, offsets, sorted_src, out)
     rc = lib().moe_expert_matmul_int8(_ptr(x), _ptr(x_sf), X, _ptr(w), _ptr(w_sf), _ptr(offsets),
                                       _ptr(sorted_src), E, k, R, K, N, int(swiglu), _ptr(o),
                                       MOE_OUT_F32 if out_dtype == torch.float32 else MOE_OUT_BF16,
