@@ -12,10 +12,12 @@
 // than that, the token is decided again in f64, one value per candidate, which is rare:
 // about one token in a thousand for 8 of 256 experts.
 //
-// One warp per token, lane l holding the V consecutive experts l V .. l V + V - 1, so
-// that a group is a run of lanes.  The selection is topk_warp.cuh's: a lower bound of
-// the k-th value from the lanes' maxima leaves a few candidates, one per lane, ranked
-// against one another.
+// A token has a warp, or 8 or 16 lanes of one, lane l holding the V consecutive experts
+// l V .. l V + V - 1, so that a group is a run of lanes.  The selection is topk_warp.cuh's:
+// a lower bound of the k-th value from the lanes' two largest leaves a few candidates,
+// ranked against one another.
+#include <type_traits>
+
 #include "block/block_ops.cuh"
 #include "topk_warp.cuh"
 
@@ -24,6 +26,8 @@ namespace {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr int kWarps = 8;
+// Several tokens per warp: tokens per SM from which on, warps of a block, blocks per SM.
+constexpr int kLanesFrom = 12, kLaneWarps = 4, kLaneBlocks = 4;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -401,10 +405,11 @@ constexpr int kByX = 0, kSigmoid = 1, kSoftmax = 2;
 // and done again at the end (careful_token, 10 us), which keeps that work's registers out
 // of the loop.
 //
-// 65536 tokens, 8 of 256 experts (67 MB; us): by x alone 26; sigmoid and bias 41; with 8
-// groups 49.  Instruction issue bounds it, 600 per token and 70 % of the slots.  A border
-// decided in f64 costs its warp 1.2 us for experts and 3 us for groups.  16 lanes per
-// token, two tokens per warp, were slower (71: registers), as was asking for a row ahead.
+// For few tokens, for selections by x, and for numbers of experts and groups that
+// router_gate_lanes_kernel does not divide.  65536 tokens, 8 of 256 experts (67 MB; us):
+// by x alone 26; sigmoid and bias 42; with 8 groups 50.  Instruction issue bounds it, 640
+// per token and 70 % of the slots.  A border decided in f64 costs its warp 1.2 us for
+// experts and 3 us for groups.  Asking for a row ahead was slower.
 template <int V, bool VEC, int KFIX, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
     router_gate_kernel(const RouterArgs a) {
@@ -703,6 +708,385 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
     careful_token(a, t0 + (int64_t)(__ffs(careful) - 1) * warps, lane, ws, list);
 }
 
+// ------------------------------------------- forward, several tokens per warp
+
+template <int L, class F>
+__device__ __forceinline__ float lanes_reduce(float v, F f) {
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) v = f(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// One token's candidates, and its winners in their order.
+struct TokenScratch {
+  float v[32];        // what they are compared by
+  uint32_t at[32];    // expert | place in the warp's rows << 16
+  float by_rank[20];  // the values of the first L + 1
+  float x[16];
+  int e[16];
+};
+
+// E = L V experts by L lanes per token, 32 / L tokens per warp, each lane V consecutive
+// experts; groups are runs of whole lanes (L % G == 0); k <= L, a bias.  What a token takes
+// beyond its scores, the groups' ranks, the bound of the k-th value, the candidates' ranks
+// and the weights, serves all tokens of the warp.  Rows come by coalesced asynchronous
+// copies into shared memory, each lane's run padded so that reading 16 bytes per lane
+// meets no bank twice, and the next rows are asked for once the candidates' x is taken.
+//
+// 65536 tokens, 8 of 256 experts, sigmoid and bias: 8 groups 30 us (router_gate_kernel:
+// 50), one group 26 (42); 322 instructions per token against 640, 60 % of the issue slots
+// with 16 warps per SM.  80 registers and 24 warps were slower (34: spills).  Below about
+// 12 tokens per SM a token per warp is as fast or faster (1024 tokens 4.3 against 5.1 us,
+// 4096 9.9 against 8.2).  Nearly equal borders, one token in a thousand, are decided in
+// f64 by the whole warp where they are met.
+template <int L, int V, int MODE>
+__global__ void __launch_bounds__(kLaneWarps * 32, kLaneBlocks)
+    router_gate_lanes_kernel(const RouterArgs a) {
+  constexpr int Q = 32 / L, E = L * V, S = 32 / L, kStride = (V / 4) % 2 ? V : V + 4;
+  struct Warp {
+    float x[32 * kStride];
+    TokenScratch q[Q];
+  };
+  __shared__ __align__(16) float s_bias[L * kStride];
+  __shared__ __align__(16) Warp s_warp[kLaneWarps];
+  static_assert(sizeof(s_warp[0].x) >= E * 8 && sizeof(s_warp[0].q) >= sizeof(WarpScratch),
+                "careful_token's scratch");
+  pdl_enter();
+  const int lane = threadIdx.x & 31, q = lane / L, j = lane % L;
+  Warp& ws = s_warp[threadIdx.x >> 5];
+  TokenScratch& tok = ws.q[q];
+  const int k = a.k, width = L / a.G;
+  const bool grouped = a.g < a.G;
+  const int warps = (int)((gridDim.x * blockDim.x) >> 5);
+  const int64_t b0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int64_t batches = (a.T + Q - 1) / Q;
+  const uint32_t x_to = (uint32_t)__cvta_generic_to_shared(ws.x);
+  auto ask = [&](int64_t b) {  // the rows of a batch; past the last token the last row again
+    if (b < batches) {
+#pragma unroll
+      for (int i = 0; i < Q * E / 128; ++i) {
+        const int c = i * 32 + lane, row = c / (E / 4), at = c % (E / 4);
+        const int64_t t = b * Q + row < a.T ? b * Q + row : a.T - 1;
+        cp_async16(x_to + (uint32_t)((row * L + at / (V / 4)) * kStride + at % (V / 4) * 4) * 4,
+                   a.scores + t * E + at * 4);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  ask(b0);
+  for (int e = threadIdx.x; e < E; e += blockDim.x)
+    s_bias[e / V * kStride + e % V] = a.bias ? __ldg(a.bias + e) : 0.0f;
+  __syncthreads();
+  uint32_t careful = 0;  // tokens to be done again
+
+  int64_t b = b0;
+  for (int turn = 0; b < batches; b += warps, ++turn) {
+    const int64_t t = b * Q + q;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+    // ---- c
+    const float4* my_x = reinterpret_cast<const float4*>(ws.x + lane * kStride);
+    const float4* my_b = reinterpret_cast<const float4*>(s_bias + j * kStride);
+    float c[V];
+    float m = 0.0f, z_inv = 0.0f, err, x_min = kInf;
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) {
+      const float4 f = my_x[h];
+      c[4 * h] = f.x, c[4 * h + 1] = f.y, c[4 * h + 2] = f.z, c[4 * h + 3] = f.w;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) x_min = fminf(x_min, c[i]);
+    if constexpr (MODE == kSoftmax) {
+      m = c[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) m = fmaxf(m, c[i]);
+      m = lanes_reduce<L>(m, [](float u, float w) { return fmaxf(u, w); });
+      if (m == -kInf) m = 0.0f;
+      float z = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        c[i] = exp2_est((c[i] - m) * kLog2e);
+        z += c[i];
+      }
+      z = lanes_reduce<L>(z, [](float u, float w) { return u + w; });
+      z_inv = z > 0.0f ? rcp_f32(z) : 0.0f;
+      err = score_err(MOE_SCORE_SOFTMAX, z_inv);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = rcp_est(1.0f + exp2_est(c[i] * -kLog2e));
+      err = score_err(MOE_SCORE_SIGMOID, 1.0f);
+    }
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) {
+      const float4 f = my_b[h];
+      const float bias[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c[4 * h + i] = MODE == kSoftmax ? __fmaf_rn(c[4 * h + i], z_inv, bias[i])
+                                        : c[4 * h + i] + bias[i];
+    }
+    if (__any_sync(kAll, x_min == -kInf)) {
+#pragma unroll
+      for (int h = 0; h < V / 4; ++h) {
+        const float4 f = my_x[h];
+        c[4 * h] = f.x == -kInf ? -kInf : c[4 * h];
+        c[4 * h + 1] = f.y == -kInf ? -kInf : c[4 * h + 1];
+        c[4 * h + 2] = f.z == -kInf ? -kInf : c[4 * h + 2];
+        c[4 * h + 3] = f.w == -kInf ? -kInf : c[4 * h + 3];
+      }
+    }
+    // ---- the lane's two largest, and the groups
+    Top2 l2 = {fmaxf(c[0], c[1]), fminf(c[0], c[1])};
+#pragma unroll
+    for (int i = 2; i < V; i += 2) {
+      const float hi = fmaxf(c[i], c[i + 1]), lo = fminf(c[i], c[i + 1]);
+      l2.b = fmaxf(fmaxf(l2.b, lo), fminf(l2.a, hi));
+      l2.a = fmaxf(l2.a, hi);
+    }
+    bool in = true;
+    if (grouped) {
+      Top2 g2 = l2;
+      for (int o = 1; o < width; o <<= 1)
+        merge(g2, Top2{__shfl_xor_sync(kAll, g2.a, o), __shfl_xor_sync(kAll, g2.b, o)});
+      const float gv = group_value(g2, a.group_score);
+      int rank = 0;
+      for (int o = width; o < L; o += width) {
+        const float other = __shfl_xor_sync(kAll, gv, o);
+        rank += other > gv || (other == gv && (lane ^ o) < lane) ? 1 : 0;
+      }
+      in = rank < a.g;
+      // the lowest inside against the highest outside
+      const float low = lanes_reduce<L>(in ? gv : kInf,
+                                        [](float u, float w) { return fminf(u, w); });
+      const float high = lanes_reduce<L>(in ? -kInf : gv,
+                                         [](float u, float w) { return fmaxf(u, w); });
+      const float tol = 4.0f * err + 0x1p-21f * fmaxf(fabsf(low), fabsf(high));
+      uint32_t near = __ballot_sync(kAll, high > -kInf && low - high <= tol);
+      while (near) {  // rare
+        const int w = (__ffs(near) - 1) / L;
+        near &= ~((kAll >> (32 - L)) << (w * L));
+        const int64_t tw = b * Q + w < a.T ? b * Q + w : a.T - 1;
+        const float* row = a.scores + tw * E;
+        const float mw = __shfl_sync(kAll, m, w * L);
+        // the near groups' experts that may be among the two largest: from the second (the
+        // first, where only that counts, or there is no second) down to the error
+        const bool close = q == w && fabsf(gv - low) <= 2.0f * tol;
+        const float edge =
+            (a.group_score == MOE_GROUP_TOP2 && g2.b > -kInf ? g2.b : g2.a) - tol;
+        uint32_t take = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) take |= close && c[i] >= edge ? 1u << i : 0u;
+        int n = 0;
+        for (;;) {
+          const uint32_t some = __ballot_sync(kAll, take != 0u);
+          if (some == 0u) break;
+          const int at = n + __popc(some & ((1u << lane) - 1u));
+          if (take != 0u && at < 32) ws.q[w].at[at] = (uint32_t)(j * V + __ffs(take) - 1);
+          take &= take - 1;
+          n += __popc(some);
+        }
+        uint32_t maybe = 0, sure = 0;  // a bit per group
+        for (int i = 0; i < a.G; ++i) {
+          const int of = w * L + i * width;
+          maybe |= __shfl_sync(kAll, close ? 1u : 0u, of) << i;
+          sure |= __shfl_sync(kAll, gv > low + 2.0f * tol ? 1u : 0u, of) << i;
+        }
+        __syncwarp();
+        const int e = lane < n ? (int)ws.q[w].at[lane] : 0;
+        __syncwarp();
+        uint32_t open = 0;
+        bool known = true;
+        if (n <= 32 && __shfl_sync(kAll, low, w * L) > -kInf)
+          open = groups64(row, a.bias, a.func, mw, E, E / a.G, a.g, a.group_score, sure, maybe, n,
+                          e, lane, reinterpret_cast<double*>(ws.q[w].v),
+                          reinterpret_cast<int*>(ws.q[w].by_rank));
+        else if (!one_value(row, a.bias, E, lane))  // else these ties are exact
+          open = all_groups64(row, a.bias, a.func, mw, E, a.G, a.g, a.group_score, lane);
+        else
+          known = false;
+        if (q == w && known) in = (open >> (j / width)) & 1u;
+        __syncwarp();
+      }
+    }
+    // ---- candidates: the k-th largest among the lanes' two largest is reached by k experts
+    if (!in) l2 = Top2{-kInf, -kInf};
+    int rank_a = 0, rank_b = 1;
+#pragma unroll
+    for (int o = 1; o < L; ++o) {
+      const float oa = __shfl_xor_sync(kAll, l2.a, o), ob = __shfl_xor_sync(kAll, l2.b, o);
+      rank_a += (oa > l2.a ? 1 : 0) + (ob > l2.a ? 1 : 0);
+      rank_b += (oa > l2.b ? 1 : 0) + (ob > l2.b ? 1 : 0);
+    }
+    auto larger = [](float u, float w) { return fmaxf(u, w); };
+    float theta = lanes_reduce<L>(rank_b < k ? l2.b : rank_a < k ? l2.a : kInf,
+                                  [](float u, float w) { return fminf(u, w); });
+    // fewer than k finite values: settled with care
+    const bool lost = !(theta > -kInf && theta < kInf);
+    uint32_t mine;
+    int upto, C;
+    float from;
+    auto collect = [&]() {
+      // less what the errors of two values may hide
+      from = theta - (2.0f * err + 0x1p-22f * fabsf(theta));
+      if (!in || lost) from = __int_as_float(0x7FFFFFFF);
+      mine = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) mine |= c[i] >= from ? 1u << i : 0u;
+      upto = __popc(mine);
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, upto, o, L);
+        if (j >= o) upto += v;
+      }
+      C = __shfl_sync(kAll, upto, L - 1, L);
+    };
+    collect();
+    // one token in a hundred has more than the scratch holds: the bound by bisection
+    bool again = false;
+    if (__any_sync(kAll, C > 32)) {
+      float lo = theta, hi = lanes_reduce<L>(l2.a, larger);
+      for (int i = 0; i < 12 && __any_sync(kAll, C > 32 || C < k); ++i) {
+        if (C > 32) lo = theta;
+        if (C < k) hi = theta;
+        if (C > 32 || C < k) theta = 0.5f * (lo + hi);
+        collect();
+      }
+      int reach = 0;  // the bound itself: k experts reach it, not the margin alone
+#pragma unroll
+      for (int i = 0; i < V; ++i) reach += in && c[i] >= theta ? 1 : 0;
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) reach += __shfl_xor_sync(kAll, reach, o);
+      again = reach < k;
+    }
+    again = again || C > 32 || C < k;
+    if (again) C = 0, mine = 0u;
+    int put = upto - __popc(mine);
+    while (mine) {
+      const int i = __ffs(mine) - 1;
+      mine &= mine - 1;
+      tok.at[put++] = (uint32_t)(j * V + i) | (uint32_t)(lane * kStride + i) << 16;
+    }
+    for (int r = j; r <= k; r += L) tok.by_rank[r] = __int_as_float(0x7FFFFFFF);
+    const int most = (int)__reduce_max_sync(kAll, (uint32_t)C);
+    __syncwarp();
+    float xs[S], v[S];
+    int e[S], rank[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      xs[s] = v[s] = -kInf;
+      e[s] = 0, rank[s] = 32;
+      if (s * L < most) {
+        const int r = s * L + j;
+        if (r < C) {
+          const uint32_t at = tok.at[r];
+          e[s] = (int)(at & 0xFFFFu);
+          xs[s] = ws.x[at >> 16];
+          v[s] = choice32(MODE == kSigmoid ? MOE_SCORE_SIGMOID : MOE_SCORE_SOFTMAX, xs[s],
+                          s_bias[(int)(at >> 16) - q * L * kStride], m, z_inv);
+        }
+        tok.v[r] = v[s];
+      }
+    }
+    __syncwarp();
+    ask(b + warps);
+    auto ranks = [&](auto count) {
+#pragma unroll
+      for (int s = 0; s < count.value; ++s) rank[s] = 0;
+      for (int o = 0; o < most; o += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(tok.v + o);
+#pragma unroll
+        for (int s = 0; s < count.value; ++s)
+          rank[s] += (u.x > v[s] ? 1 : 0) + (u.y > v[s] ? 1 : 0) + (u.z > v[s] ? 1 : 0) +
+                     (u.w > v[s] ? 1 : 0);
+      }
+    };
+    if (S == 2 || most <= 2 * L)
+      ranks(std::integral_constant<int, 2>());
+    else if (most <= 3 * L)
+      ranks(std::integral_constant<int, S < 3 ? S : 3>());
+    else
+      ranks(std::integral_constant<int, S>());
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      if (s * L + j >= C) rank[s] = 32;
+      if (rank[s] <= k) tok.by_rank[rank[s]] = v[s];
+      if (rank[s] < k) tok.e[rank[s]] = e[s], tok.x[rank[s]] = xs[s];
+    }
+    __syncwarp();
+    // an empty rank follows equal values; and neighbours that are too close
+    bool bad = false;
+    if (j < k && j + 1 < C) {
+      const float p = tok.by_rank[j], n = tok.by_rank[j + 1];
+      bad = n != n || (n > -kInf && p - n <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(p), fabsf(n)));
+    }
+    uint32_t near = __ballot_sync(kAll, bad);
+    while (near) {  // one token in a thousand
+      const int w = (__ffs(near) - 1) / L;
+      near &= ~((kAll >> (32 - L)) << (w * L));
+      const int64_t tw = b * Q + w < a.T ? b * Q + w : a.T - 1;
+      const int Cw = __shfl_sync(kAll, C, w * L);
+      const float* row = a.scores + tw * E;
+      const int ew = lane < Cw ? (int)(ws.q[w].at[lane] & 0xFFFFu) : 0;
+      const int rw = rank64(row, a.bias, a.func, __shfl_sync(kAll, m, w * L), E,
+                            a.bias == nullptr, ew, Cw, lane);
+      if (lane < Cw && rw < k) ws.q[w].e[rw] = ew, ws.q[w].x[rw] = __ldg(row + ew);
+      __syncwarp();
+    }
+    // ---- weights, the r-th winner's by lane r
+    const bool have = j < k && !again;
+    const float x = have ? tok.x[j] : -kInf;
+    float w = 0.0f;
+    if (MODE == kSoftmax) {
+      const float top = a.renorm ? lanes_reduce<L>(x, larger) : m;
+      if (x > -kInf) w = expf(x - top) * (a.renorm ? 1.0f : z_inv);
+    } else {
+      const float lo = fminf(x, 0.0f);
+      const float top = a.renorm ? lanes_reduce<L>(lo, larger) : 0.0f;
+      if (x > -kInf) w = expf(lo - top) * rcp_f32(1.0f + expf(-fabsf(x)));
+    }
+    if (a.renorm) {
+      const float sum = lanes_reduce<L>(w, [](float u, float y) { return u + y; });
+      w = sum > 0.0f ? w * rcp_f32(sum) : 0.0f;
+    }
+    if (have && t < a.T) {
+      a.idx[t * k + j] = tok.e[j];
+      a.w[t * k + j] = w * a.scale;
+    }
+    const uint32_t redo = __ballot_sync(kAll, again && j == 0 && t < a.T);
+#pragma unroll
+    for (int w2 = 0; w2 < Q; ++w2) careful |= (redo >> (w2 * L) & 1u) << (turn * Q + w2);
+    __syncwarp();
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+  for (; careful; careful &= careful - 1) {
+    const int at = __ffs(careful) - 1;
+    careful_token(a, (b0 + (int64_t)(at / Q) * warps) * Q + at % Q, lane,
+                  *reinterpret_cast<WarpScratch*>(ws.q),
+                  reinterpret_cast<unsigned long long*>(ws.x));
+  }
+}
+
+template <int L, int V, int MODE>
+cudaError_t launch_lanes(const LaunchCtx& c, const RouterArgs& a) {
+  constexpr int Q = 32 / L;
+  // at most 32 tokens per warp
+  const int64_t need = ((a.T + Q - 1) / Q + kLaneWarps - 1) / kLaneWarps;
+  int64_t blocks = (int64_t)c.num_sms * kLaneBlocks;
+  if (blocks > need) blocks = need;
+  if (blocks < (need + L - 1) / L) blocks = (need + L - 1) / L;
+  return launch_pdl(router_gate_lanes_kernel<L, V, MODE>, dim3((unsigned)blocks), kLaneWarps * 32,
+                    0, c.stream, a);
+}
+template <int L, int V>
+cudaError_t launch_lanes(const LaunchCtx& c, const RouterArgs& a) {
+  return a.func == MOE_SCORE_SIGMOID ? launch_lanes<L, V, kSigmoid>(c, a)
+                                     : launch_lanes<L, V, kSoftmax>(c, a);
+}
+
 template <int V, bool VEC, int KFIX, int MODE>
 cudaError_t launch_m(const LaunchCtx& c, const RouterArgs& a) {
   auto* kernel = router_gate_kernel<V, VEC, KFIX, MODE>;
@@ -735,13 +1119,6 @@ cudaError_t launch_v(const LaunchCtx& c, const RouterArgs& a) {
 }
 
 // ------------------------------------------------------------------ backward
-
-template <int L, class F>
-__device__ __forceinline__ float lanes_reduce(float v, F f) {
-#pragma unroll
-  for (int o = 1; o < L; o <<= 1) v = f(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
 
 // L >= k lanes per token, 32 / L tokens per warp: what a token takes beyond its row (the
 // scores, weights and sums of the selected experts) serves all of them.  A row is copied
@@ -902,6 +1279,22 @@ cudaError_t launch_backward_u(const LaunchCtx& c, const RouterArgs& a) {
 
 cudaError_t launch_router_gate(const LaunchCtx& c, const RouterArgs& a) {
   const bool al = reinterpret_cast<uintptr_t>(a.scores) % 16 == 0;
+  // compared by c, and tokens enough: several per warp, where groups are whole lanes and
+  // the lanes' two largest of the open groups are at least k values
+  if (al && (a.bias || (a.g < a.G && a.group_score == MOE_GROUP_TOP2)) &&
+      a.T > kLanesFrom * (int64_t)c.num_sms) {
+    if (a.k <= 8 && 8 % a.G == 0 && a.k * a.G <= 16 * a.g) {
+      if (a.E == 64) return launch_lanes<8, 8>(c, a);
+      if (a.E == 128) return launch_lanes<8, 16>(c, a);
+      if (a.E == 160) return launch_lanes<8, 20>(c, a);
+      if (a.E == 192) return launch_lanes<8, 24>(c, a);
+      if (a.E == 256) return launch_lanes<8, 32>(c, a);
+    }
+    if (a.k <= 16 && 16 % a.G == 0 && a.k * a.G <= 32 * a.g) {
+      if (a.E == 384) return launch_lanes<16, 24>(c, a);
+      if (a.E == 512) return launch_lanes<16, 32>(c, a);
+    }
+  }
   // the fewest experts per lane; a few widths more than powers of two, as groups are then
   // more often whole lanes
   if (a.E <= 32) return launch_v<1, false>(c, a);

@@ -342,6 +342,61 @@ def test_router_gradient_of_an_expert_named_twice(shape, func, renorm):
     check(same, want, mag, "in place")
 
 
+def many_scores(kind, T, E, r):
+    x = torch.randn(T, E, generator=r) * 2
+    if kind == "few digits":  # equal values, with the bias of an untrained router
+        return x.bfloat16().float(), torch.zeros(E)
+    if kind == "closed":
+        x[torch.rand(T, E, generator=r) < 0.4] = -float("inf")
+        x[::5, 3:] = -float("inf")
+        x[7] = -float("inf")
+    elif kind == "one value":  # nearly: borders that f32 cannot tell
+        x[::2] = 0.75
+        x[1::4] = 0.75 + 1e-7 * torch.randn(E, generator=r)
+        return x, torch.zeros(E)
+    elif kind == "in one place":  # all large values in an eighth of the row
+        x[:, E // 8:E // 4] += 9
+    elif kind == "saturated":
+        x *= 20
+    return x, torch.randn(E, generator=r) * 0.05
+
+
+@pytest.mark.parametrize("kind", ["plain", "few digits", "closed", "one value", "in one place",
+                                  "saturated"])
+@pytest.mark.parametrize("case", [(64, 8, 8, 4), (128, 3, 4, 1), (160, 6, 8, 3), (192, 8, 1, 1),
+                                  (256, 8, 8, 4), (256, 8, 2, 1), (256, 1, 1, 1), (384, 16, 16, 8),
+                                  (512, 9, 8, 3), (512, 8, 1, 1)])
+def test_router_of_many_tokens(case, kind):
+    """More tokens than SMs many times over, not a multiple of any warp's: the 64-bit
+    selection for every token, with each score and group rule."""
+    E, k, G, g = case
+    T = 13 * torch.cuda.get_device_properties(0).multi_processor_count + 3
+    x, bias = many_scores(kind, T, E, gen(E + k))
+    for i, (func, gs) in enumerate([("sigmoid", "top2"), ("softmax", "max"), ("sigmoid", "max"),
+                                    ("softmax", "top2")]):
+        b = None if i == 3 or (i == 0 and kind == "saturated") else bias
+        some = torch.arange(i % 2, T, 2)  # the oracle takes its time: every other token
+        want, w = ref.gate(x[some], k, func, b, G, g, gs, i % 2 == 0, 2.5)
+        idx, got = ops.router_gate(x.to(DEV), k, score_func=func, num_groups=G, topk_groups=g,
+                                   bias=None if b is None else b.to(DEV), group_score=gs,
+                                   renormalize=i % 2 == 0, scale=2.5)
+        assert torch.equal(idx.cpu()[some].long(), want), (func, gs)
+        check(got.cpu()[some], w, w, "weights")
+
+
+def test_router_of_many_tokens_as_of_few():
+    """A token's result does not depend on how many tokens come with it."""
+    r = gen(5)
+    x = (torch.randn(5000, 256, generator=r) * 2).to(DEV)
+    b = (torch.randn(256, generator=r) * 0.1).to(DEV)
+    args = dict(score_func="sigmoid", bias=b, num_groups=8, topk_groups=4)
+    idx, w = ops.router_gate(x, 8, **args)
+    for at in (0, 1, 2047, 4999):
+        one, ow = ops.router_gate(x[at:at + 1].contiguous(), 8, **args)
+        assert torch.equal(one[0], idx[at])
+        check(ow[0], cpu64(w[at]), cpu64(w[at]), "weights")
+
+
 def test_under_the_debug_bounds_library():
     """The same kernels with their internal checks compiled in report nothing."""
     env = dict(os.environ, MOE_DEBUG_BOUNDS="1")
