@@ -12,7 +12,7 @@
 // than that, the token is decided again in f64, one value per candidate, which is rare:
 // about one token in a thousand for 8 of 256 experts.
 //
-// A token has a warp, or 8 or 16 lanes of one, lane l holding the V consecutive experts
+// A token has a warp, or 4 to 16 lanes of one, lane l holding the V consecutive experts
 // l V .. l V + V - 1, so that a group is a run of lanes.  The selection is topk_warp.cuh's:
 // a lower bound of the k-th value from the lanes' two largest leaves a few candidates,
 // ranked against one another.
@@ -730,7 +730,7 @@ struct TokenScratch {
 };
 
 // E = L V experts by L lanes per token, 32 / L tokens per warp, each lane V consecutive
-// experts; groups are runs of whole lanes (L % G == 0); k <= L, a bias.  What a token takes
+// experts and S candidates; groups are runs of whole lanes (L % G == 0); k <= L, a bias.  What a token takes
 // beyond its scores, the groups' ranks, the bound of the k-th value, the candidates' ranks
 // and the weights, serves all tokens of the warp.  Rows come by coalesced asynchronous
 // copies into shared memory, each lane's run padded so that reading 16 bytes per lane
@@ -745,7 +745,7 @@ struct TokenScratch {
 template <int L, int V, int MODE>
 __global__ void __launch_bounds__(kLaneWarps * 32, kLaneBlocks)
     router_gate_lanes_kernel(const RouterArgs a) {
-  constexpr int Q = 32 / L, E = L * V, S = 32 / L, kStride = (V / 4) % 2 ? V : V + 4;
+  constexpr int Q = 32 / L, E = L * V, S = (E < 32 ? E : 32) / L, kStride = (V / 4) % 2 ? V : V + 4;
   struct Warp {
     float x[32 * kStride];
     TokenScratch q[Q];
@@ -1283,7 +1283,10 @@ cudaError_t launch_router_gate(const LaunchCtx& c, const RouterArgs& a) {
   // the lanes' two largest of the open groups are at least k values
   if (al && (a.bias || (a.g < a.G && a.group_score == MOE_GROUP_TOP2)) &&
       a.T > kLanesFrom * (int64_t)c.num_sms) {
+    if (a.E == 16 && a.k <= 4 && 4 % a.G == 0 && a.k * a.G <= 8 * a.g)
+      return launch_lanes<4, 4>(c, a);
     if (a.k <= 8 && 8 % a.G == 0 && a.k * a.G <= 16 * a.g) {
+      if (a.E == 32) return launch_lanes<8, 4>(c, a);
       if (a.E == 64) return launch_lanes<8, 8>(c, a);
       if (a.E == 128) return launch_lanes<8, 16>(c, a);
       if (a.E == 160) return launch_lanes<8, 20>(c, a);

@@ -365,7 +365,8 @@ def many_scores(kind, T, E, r):
                                   "saturated"])
 @pytest.mark.parametrize("case", [(64, 8, 8, 4), (128, 3, 4, 1), (160, 6, 8, 3), (192, 8, 1, 1),
                                   (256, 8, 8, 4), (256, 8, 2, 1), (256, 1, 1, 1), (384, 16, 16, 8),
-                                  (512, 9, 8, 3), (512, 8, 1, 1)])
+                                  (512, 9, 8, 3), (512, 8, 1, 1), (16, 2, 1, 1), (16, 4, 4, 2),
+                                  (32, 8, 8, 4), (32, 3, 2, 1), (16, 5, 2, 2)])
 def test_router_of_many_tokens(case, kind):
     """More tokens than SMs many times over, not a multiple of any warp's: the 64-bit
     selection for every token, with each score and group rule."""
