@@ -519,8 +519,16 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
         if (left == edge_in) left = 0u;
       }
       open = __ballot_sync(kAll, gkey >= edge_in && gkey > 0u);
-      const uint32_t edge_out = __reduce_max_sync(kAll, left);
       const bool ties = __popc(open) != a.g;
+      if (MODE != kByX && ties) {  // the g-th largest value, each group counted
+        left = gkey;
+        for (int count = 0; count < a.g;) {
+          edge_in = __reduce_max_sync(kAll, left);
+          count += __popc(__ballot_sync(kAll, left == edge_in));
+          if (left == edge_in) left = 0u;
+        }
+      }
+      const uint32_t edge_out = __reduce_max_sync(kAll, left);
       if constexpr (MODE == kByX) {
         if (ties) {  // of the last value that has a place, the first groups
           uint32_t all = kAll >> (32 - a.G);
