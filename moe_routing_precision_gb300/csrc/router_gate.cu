@@ -63,8 +63,24 @@ __device__ __forceinline__ void merge(Top2& t, Top2 o) {
   t.b = fmaxf(fminf(t.a, o.a), fmaxf(t.b, o.b));
   t.a = fmaxf(t.a, o.a);
 }
+__device__ __forceinline__ bool both_count(const Top2& t, int kind) {
+  return kind == MOE_GROUP_TOP2 && t.b > -kInf;
+}
 __device__ __forceinline__ float group_value(const Top2& t, int kind) {
-  return kind == MOE_GROUP_TOP2 && t.b > -kInf ? t.a + t.b : t.a;
+  return both_count(t, kind) ? t.a + t.b : t.a;
+}
+// How far group_value may be off, err being score_err: by the errors of its one or two
+// values, which their sum does not show where they cancel (biases of both signs).  3 * 2^-24
+// of each covers the rounding of s + bias, of the sum, and of the sum plus or minus this.
+__device__ __forceinline__ float group_err(const Top2& t, int kind, float err) {
+  const float size = fabsf(t.a) + (both_count(t, kind) ? fabsf(t.b) : 0.0f);
+  return t.a > -kInf ? __fmaf_rn(0x1p-22f, size, 2.0f * err) : 0.0f;
+}
+// The value from which on an expert of a group at the border may be one of those that count:
+// the second (the first, where only that counts) less what the errors of two values may hide.
+__device__ __forceinline__ float group_edge(const Top2& t, int kind, float err) {
+  const float v = both_count(t, kind) ? t.b : t.a;
+  return v - __fmaf_rn(0x1p-21f, fabsf(v), 2.0f * err);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -305,18 +321,17 @@ __device__ __noinline__ void careful_token(const RouterArgs& a, int64_t t, int l
       rank += o > gv || (o == gv && i < lane) ? 1 : 0;
     }
     open = __ballot_sync(kAll, lane < a.G && rank < a.g);
-    const uint32_t at_low = __ballot_sync(kAll, lane < a.G && rank == a.g - 1);
-    const uint32_t at_high = __ballot_sync(kAll, lane < a.G && rank == a.g);
-    const float low = __shfl_sync(kAll, gv, __ffs(at_low) - 1);
-    const float high = __shfl_sync(kAll, gv, __ffs(at_high) - 1);
-    const float tol = 4.0f * err + 0x1p-21f * fmaxf(fabsf(low), fabsf(high));
+    // the least that a group inside may be against the most that one outside may be
+    const bool in = rank < a.g;
+    const float spread = group_err(g2, a.group_score, err);
+    const float low = warp_min(lane < a.G && in ? gv - spread : kInf);
+    const float high = warp_max(lane < a.G && !in ? gv + spread : -kInf);
     // unless the whole row is one value: those ties are exact
-    if (need_c && high > -kInf && low - high <= tol && !one_value(row, a.bias, E, lane)) {
-      const uint32_t near =
-          __ballot_sync(kAll, lane < a.G && gv <= low + tol && gv >= high - tol);
-      // the near groups' experts that may be among the two largest: from the second (the
-      // first, where only that counts, or there is no second) down to the error
-      const float edge = (a.group_score == MOE_GROUP_TOP2 && g2.b > -kInf ? g2.b : g2.a) - tol;
+    if (need_c && high > -kInf && low <= high && !one_value(row, a.bias, E, lane)) {
+      const uint32_t near = __ballot_sync(
+          kAll, lane < a.G && (in ? gv - spread <= high : gv + spread >= low));
+      // the near groups' experts that may be among the two largest
+      const float edge = group_edge(g2, a.group_score, err);
       int C = 0;
       for (int e0 = 0; e0 < E; e0 += 32) {
         const int e = e0 + lane, gi = e / n;
@@ -512,6 +527,9 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
         merge(g2, Top2{__shfl_xor_sync(kAll, g2.a, o), __shfl_xor_sync(kAll, g2.b, o)});
       const float gv = __shfl_sync(kAll, group_value(g2, a.group_score), from_lane);
       // the groups of the g largest distinct values; more than g of them: ties
+      [[maybe_unused]] const float spread =
+          MODE == kByX ? 0.0f
+                       : __shfl_sync(kAll, group_err(g2, a.group_score, err), from_lane);
       const uint32_t gkey = lane < a.G ? score_key(gv) : 0u;
       uint32_t edge_in = 0, left = gkey;
       for (int r = 0; r < a.g; ++r) {
@@ -528,7 +546,6 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
           if (left == edge_in) left = 0u;
         }
       }
-      const uint32_t edge_out = __reduce_max_sync(kAll, left);
       if constexpr (MODE == kByX) {
         if (ties) {  // of the last value that has a place, the first groups
           uint32_t all = kAll >> (32 - a.G);
@@ -542,16 +559,17 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
           }
         }
       } else {
-        // the lowest inside against the highest outside
-        const float low = key_score(edge_in), high = edge_out ? key_score(edge_out) : -kInf;
-        const float tol = 4.0f * err + 0x1p-21f * fmaxf(fabsf(low), fabsf(high));
-        if (ties || (high > -kInf && low - high <= tol)) {
-          // the near groups' experts that may be among the two largest: from the second
-          // (the first, where only that counts, or there is no second) down to the error
-          const uint32_t near =
-              __ballot_sync(kAll, lane < a.G && fabsf(gv - low) <= 2.0f * tol);
-          const float second = a.group_score == MOE_GROUP_TOP2 && g2.b > -kInf ? g2.b : g2.a;
-          const float edge = __shfl_sync(kAll, second, from_lane) - tol;
+        // the least that a group inside may be against the most that one outside may be;
+        // of ties at the border each group is on both sides
+        const bool inside = lane < a.G && gkey >= edge_in;
+        const bool outside = lane < a.G && (ties ? gkey <= edge_in : gkey < edge_in);
+        const float low = warp_min(inside ? gv - spread : kInf);
+        const float high = warp_max(outside ? gv + spread : -kInf);
+        if (ties || (high > -kInf && low <= high)) {
+          // the near groups' experts that may be among the two largest
+          const uint32_t near = __ballot_sync(
+              kAll, (inside && gv - spread <= high) || (outside && gv + spread >= low));
+          const float edge = __shfl_sync(kAll, group_edge(g2, a.group_score, err), from_lane);
           uint32_t take = 0;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
@@ -573,7 +591,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
           __syncwarp();
           settled = C <= 32 && low > -kInf;
           if (settled) {
-            const uint32_t sure = __ballot_sync(kAll, gkey > 0u && gv > low + 2.0f * tol);
+            const uint32_t sure = __ballot_sync(kAll, inside) & ~near;
             open = groups64(row, by_x ? nullptr : a.bias, a.func, m, E, n, a.g, a.group_score,
                             sure, near, C, e, lane, ws.v64, ws.e);
           }
@@ -866,24 +884,22 @@ __global__ void __launch_bounds__(kLaneWarps * 32, kLaneBlocks)
         rank += other > gv || (other == gv && (lane ^ o) < lane) ? 1 : 0;
       }
       in = rank < a.g;
-      // the lowest inside against the highest outside
-      const float low = lanes_reduce<L>(in ? gv : kInf,
+      // the least that a group inside may be against the most that one outside may be
+      const float spread = group_err(g2, a.group_score, err);
+      const float low = lanes_reduce<L>(in ? gv - spread : kInf,
                                         [](float u, float w) { return fminf(u, w); });
-      const float high = lanes_reduce<L>(in ? -kInf : gv,
+      const float high = lanes_reduce<L>(in ? -kInf : gv + spread,
                                          [](float u, float w) { return fmaxf(u, w); });
-      const float tol = 4.0f * err + 0x1p-21f * fmaxf(fabsf(low), fabsf(high));
-      uint32_t near = __ballot_sync(kAll, high > -kInf && low - high <= tol);
+      uint32_t near = __ballot_sync(kAll, high > -kInf && low <= high);
       while (near) {  // rare
         const int w = (__ffs(near) - 1) / L;
         near &= ~((kAll >> (32 - L)) << (w * L));
         const int64_t tw = b * Q + w < a.T ? b * Q + w : a.T - 1;
         const float* row = a.scores + tw * E;
         const float mw = __shfl_sync(kAll, m, w * L);
-        // the near groups' experts that may be among the two largest: from the second (the
-        // first, where only that counts, or there is no second) down to the error
-        const bool close = q == w && fabsf(gv - low) <= 2.0f * tol;
-        const float edge =
-            (a.group_score == MOE_GROUP_TOP2 && g2.b > -kInf ? g2.b : g2.a) - tol;
+        // the near groups' experts that may be among the two largest
+        const bool close = q == w && (in ? gv - spread <= high : gv + spread >= low);
+        const float edge = group_edge(g2, a.group_score, err);
         uint32_t take = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) take |= close && c[i] >= edge ? 1u << i : 0u;
@@ -900,14 +916,14 @@ __global__ void __launch_bounds__(kLaneWarps * 32, kLaneBlocks)
         for (int i = 0; i < a.G; ++i) {
           const int of = w * L + i * width;
           maybe |= __shfl_sync(kAll, close ? 1u : 0u, of) << i;
-          sure |= __shfl_sync(kAll, gv > low + 2.0f * tol ? 1u : 0u, of) << i;
+          sure |= __shfl_sync(kAll, in && !close ? 1u : 0u, of) << i;
         }
         __syncwarp();
         const int e = lane < n ? (int)ws.q[w].at[lane] : 0;
         __syncwarp();
         uint32_t open = 0;
         bool known = true;
-        if (n <= 32 && __shfl_sync(kAll, low, w * L) > -kInf)
+        if (n <= 32)
           open = groups64(row, a.bias, a.func, mw, E, E / a.G, a.g, a.group_score, sure, maybe, n,
                           e, lane, reinterpret_cast<double*>(ws.q[w].v),
                           reinterpret_cast<int*>(ws.q[w].by_rank));
