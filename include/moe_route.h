@@ -778,8 +778,9 @@ moe_status_t moe_cast_int8(const void *x, int32_t dtype, int64_t num_rows, int32
  *   out[r, n] = o[r, n]                                        (M = N), or
  *   out[r, n] = o[r, n] / (1 + exp(-o[r, n])) * o[r, N + n]    (swiglu: M = 2N)
  * for the rows offsets[e] <= r < offsets[e+1] of every expert e, from one row per
- * expert to all rows, rounded once to out_dtype.  Rows at or past offsets[E] are not
- * written.  The sum of products is a sum of f32 in a fixed order; it is exact while no
+ * expert to all rows, rounded once to out_dtype; the scales are multiplied in the order
+ * given, each product in f32.  Rows at or past offsets[E] are not written.  The sum of
+ * products is a sum of f32 in a fixed order; it is exact while no
  * partial sum passes 2^24 (always so for K <= 1024).
  *   x [num_x, K] i8, 16-byte aligned; x_sf [num_x] f32
  *   w [E, M, K] i8, 16-byte aligned; w_sf [E, M] f32

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = named_and(1, kConvert * 32, ok);
       auto finish = [&](float p, float q, float xs, float u0, float u1, int64_t at, int n) {
         // p and q: the sums of output n and, behind it, of its partner
-        p *= xs * u0, q *= xs * u1;
+        p = p * xs * u0, q = q * xs * u1;
         if (a.swiglu) {
           if (n < a.N) store_out(a, at + n, p * sigmoid_f32(p) * q);
         } else {

@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] *= xs[j] * w0;
+            for (int j = 0; j < 16; ++j) x[j] = x[j] * xs[j] * w0;
             if (n0 < a.N) store_column<F32, 16>(a, x, m.r0 + c, rows, n0);
           }
         }
