@@ -176,7 +176,7 @@ struct ItemList {
     __syncthreads();
   }
 
-  __device__ __forceinline__ Item at(int64_t it, int tiles) const {
+  __host__ __device__ __forceinline__ Item at(int64_t it, int tiles) const {
     // 32-bit divisions where they do (a 64-bit one takes longer than the search)
     const bool narrow = it < (int64_t)1 << 32;
     const int q = narrow ? (int)((uint32_t)it / (uint32_t)tiles) : (int)(it / tiles);
@@ -195,7 +195,7 @@ struct ItemList {
     m.tile = narrow ? (int)((uint32_t)local / (uint32_t)n) : (int)(local / n);
     const int2 span = rows[e];
     const int run = (int)(local - (int64_t)m.tile * n);
-    const int per = ((span.y - span.x + n - 1) / n + 15) / 16 * 16;
+    const int per = ((span.y - span.x - 1) / n + 16) / 16 * 16;  // rows up to 2^31 - 1
     m.r0 = span.x + (int64_t)run * per;
     const int64_t left = span.y - m.r0;
     m.n = (int)(left < 0 ? 0 : left < per ? left : per);
