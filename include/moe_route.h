@@ -106,7 +106,7 @@ typedef enum moe_out_dtype {
 #define MOE_DEVERR_POS_RANGE 0x2u    /* expand/combine: pos >= num_rows         */
 #define MOE_DEVERR_DUPLICATE_EXPERT 0x4u /* route_map: a token names an expert twice */
 #define MOE_DEVERR_ROWS_SHORT 0x8u   /* route_map_aligned: num_rows < padded total */
-#define MOE_DEVERR_TIMEOUT 0x10u     /* fused decode path: a bounded wait ran out */
+#define MOE_DEVERR_TIMEOUT 0x10u     /* a bounded wait inside a kernel ran out */
 #define MOE_DEVERR_BOUNDS 0x20u      /* debug-bounds library only: an internal index
                                         or alignment check failed, access skipped */
 
@@ -793,7 +793,8 @@ moe_status_t moe_cast_int8(const void *x, int32_t dtype, int64_t num_rows, int32
  * Requires K % 16 == 0, 16 <= K <= 65536, num_rows < 2^31, E * M < 2^31 - 512 and the
  * limits of E and k.  offsets beyond num_rows or a src outside [0, num_x) set
  * MOE_DEVERR_POS_RANGE; such rows are not written, or are zero.  Every wait inside the
- * kernel is bounded (1 s); one that runs out sets MOE_DEVERR_TIMEOUT.
+ * kernel is bounded (1 s); one that runs out sets MOE_DEVERR_TIMEOUT, and the kernel ends
+ * once its copies and products in flight have (out is then unspecified).
  */
 moe_status_t moe_expert_matmul_int8(const int8_t *x, const float *x_sf, int64_t num_x,
                                     const int8_t *w, const float *w_sf, const int32_t *offsets,
@@ -802,13 +803,18 @@ moe_status_t moe_expert_matmul_int8(const int8_t *x, const float *x_sf, int64_t 
                                     int32_t n_dim, int32_t swiglu, void *out, int32_t out_dtype,
                                     void *stream);
 
-/* Test hooks of the fused path, process-wide, read at each launch:
- *   MOE_DEBUG_WAIT_TIMEOUT_NS: the bound of every wait (default 1e9 ns);
+/* Test hooks of the fused path and of moe_expert_matmul_int8, process-wide, read at each
+ * launch:
+ *   MOE_DEBUG_WAIT_TIMEOUT_NS: the bound of every wait of theirs (default 1e9 ns), but for
+ *   those for the work in flight of a kernel that gives up, which stay at 1e9 ns;
  *   MOE_DEBUG_SKIP_ROUTE_SIGNAL: nonzero = block 0 never signals "routed", so
- *   the copy blocks' waits run out (the failure path, without a fault).
+ *   the copy blocks' waits run out (the failure path, without a fault);
+ *   MOE_DEBUG_WEIGHT_STAGES: how many stages of 128 channels of weights each CTA of the 8-bit
+ *   products asks for in all, so that the waits for the next one run out; -1 (default): all.
  * Returns MOE_ERR_INVALID_ARG for an unknown key or a value out of range. */
 #define MOE_DEBUG_WAIT_TIMEOUT_NS 1
 #define MOE_DEBUG_SKIP_ROUTE_SIGNAL 2
+#define MOE_DEBUG_WEIGHT_STAGES 3
 moe_status_t moe_debug_set(int32_t key, int64_t value);
 
 /*

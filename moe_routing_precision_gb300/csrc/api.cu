@@ -568,6 +568,11 @@ moe_status_t moe_debug_set(int32_t key, int64_t value) {
     g_decode_skip_signal.store(value != 0 ? 1 : 0);
     return MOE_OK;
   }
+  if (key == MOE_DEBUG_WEIGHT_STAGES) {
+    if (value < -1) return MOE_ERR_INVALID_ARG;
+    g_matmul_int8_stages.store(value < 0 ? INT64_MAX : value);
+    return MOE_OK;
+  }
   return MOE_ERR_INVALID_ARG;
 }
 

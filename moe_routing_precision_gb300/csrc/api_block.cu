@@ -478,6 +478,8 @@ moe_status_t moe_expert_matmul_int8(const int8_t* x, const float* x_sf, int64_t 
   a.swiglu = swiglu ? 1 : 0;
   a.out = out;
   a.out_f32 = out_dtype == MOE_OUT_F32;
+  a.wait_ns = (uint64_t)g_decode_timeout_ns.load();
+  a.stages = g_matmul_int8_stages.load();
   cudaError_t e = launch_expert_matmul_int8(c, a);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }

@@ -222,8 +222,9 @@ __device__ __forceinline__ uint64_t now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Waits for the phase `parity` of the barrier; false if that took over a second.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+// Waits for the phase `parity` of the barrier; false if that took over a second (`bound` ns).
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
+                                          uint64_t bound = 1000000000ull) {
   uint64_t begin = 0;
   for (;;) {
     uint32_t done;
@@ -236,7 +237,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     if (done) return true;
     const uint64_t t = now_ns();
     if (begin == 0) begin = t;
-    if (t - begin > 1000000000ull) return false;
+    if (t - begin > bound) return false;
   }
 }
 // Copies `bytes` (a multiple of 16) from global to shared memory, both 16-byte
@@ -406,6 +407,10 @@ struct MatmulInt8Args {
   int K = 0, N = 0, swiglu = 0;
   void* out = nullptr;
   bool out_f32 = false;
+  // test hooks (moe_debug_set): the bound of every wait, and how many stages of weights a
+  // CTA asks for
+  uint64_t wait_ns = 1000000000ull;
+  int64_t stages = INT64_MAX;
 };
 cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& a);
 

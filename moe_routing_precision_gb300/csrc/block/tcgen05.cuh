@@ -108,6 +108,12 @@ __device__ __forceinline__ void tc2_commit(uint32_t bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// The same at this CTA's barrier alone.
+__device__ __forceinline__ void tc2_commit_here(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void tmem2_alloc(uint32_t at) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(at)
                : "memory");
@@ -189,7 +195,8 @@ __device__ __forceinline__ void pair_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // mbar_wait for arrivals from the whole cluster.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  uint64_t bound = 1000000000ull) {
   uint64_t begin = 0;
   for (;;) {
     uint32_t done;
@@ -203,7 +210,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity)
     if (done) return true;
     const uint64_t t = now_ns();
     if (begin == 0) begin = t;
-    if (t - begin > 1000000000ull) return false;
+    if (t - begin > bound) return false;
   }
 }
 

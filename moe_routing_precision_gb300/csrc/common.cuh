@@ -362,6 +362,8 @@ cudaError_t launch_debug_cvt(const LaunchCtx& c, int fmt, const float* in, uint8
 // Fused decode path (decode_fused.cu) and its test hooks.
 extern std::atomic<int64_t> g_decode_timeout_ns;
 extern std::atomic<int> g_decode_skip_signal;
+// A test hook of the 8-bit products (expert_matmul_int8.cu).
+extern std::atomic<int64_t> g_matmul_int8_stages;
 size_t decode_fused_smem(int64_t T, int E, int k, int H, int num_sms, int* blocks, int* tpb);
 cudaError_t launch_decode_fused(const LaunchCtx& c, const float* scores, int64_t T, int E, int k,
                                 const void* x, int H, int32_t* idx, float* w, int32_t* counts,

@@ -30,6 +30,9 @@
 #include "block/matmul_int8.cuh"
 
 namespace moe {
+
+std::atomic<int64_t> g_matmul_int8_stages{INT64_MAX};
+
 namespace {
 
 constexpr int kWarps = 19;
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto item_at = [&](int64_t it) { return list.at(it, tiles); };
   bool ok = true;  // no wait ran out
   auto wait = [&](uint32_t bar, uint32_t phase) {
-    if (ok && !mbar_wait(bar, phase)) {
+    if (ok && !mbar_wait(bar, phase, a.wait_ns)) {
       ok = false;
       flag_error(err, MOE_DEVERR_TIMEOUT);
     }
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (S::SPLIT && ok) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(p_free, c_phase ^ 1u));
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(p_free, c_phase ^ 1u, a.wait_ns));
         if (!ok) flag_error(err, MOE_DEVERR_TIMEOUT);
       }
       if (ok && wait_warp(c_full, c_phase)) {
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(c_free);
         if constexpr (S::SPLIT) {
           if (lane < ctas) cluster_arrive(cluster_map(p_full, lane));
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(p_full, c_phase));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(p_full, c_phase, a.wait_ns));
           if (!ok) flag_error(err, MOE_DEVERR_TIMEOUT);
           if (ok) {
             // this CTA's share of the tile: pairs of sums, added in the CTAs' order
@@ -356,13 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       Ring ra;
       int64_t asked = 0;
-      for (int64_t it = item0; it < items && ok; it += item_step) {
+      for (int64_t it = item0; it < items && ok && asked < a.stages; it += item_step) {
         const Item m = item_at(it);
         // rows past the expert's last output are another's, or past the tensor and zero:
         // their products are not stored
         const int r0 = m.e * M + m.tile * per_tile;
         const int r1 = a.swiglu ? r0 + a.N : r0 + kHalf;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        const int end = a.stages - asked < kb1 - kb0 ? kb0 + (int)(a.stages - asked) : kb1;
+        for (int kb = kb0; kb < end; ++kb) {
           if (!wait(a_free + ra.i * 8, ra.phase ^ 1u)) break;
           const uint32_t bar = a_full + ra.i * 8, dst = sbase + L.a + (uint32_t)(ra.i * kABytes);
           const bool box_ok = MOE_DBG_OK(dst % 1024 == 0 && dst + kABytes <= sbase + L.b, err);
@@ -375,13 +379,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           ra.next<S::SA>();
         }
       }
-      if (!ok) {
-        // what may still be on its way: the last SA stages, each waited for (bounded)
-        for (int i = 0; i < S::SA && i < asked; ++i) {
-          if (ra.i == 0) ra.i = S::SA, ra.phase ^= 1u;
-          --ra.i;
-          (void)mbar_wait(a_full + ra.i * 8, ra.phase);
-        }
+      // what may still be on its way, if another warp gave up: the last SA stages, each waited
+      // for (bounded)
+      for (int i = 0; i < S::SA && i < asked; ++i) {
+        if (ra.i == 0) ra.i = S::SA, ra.phase ^= 1u;
+        --ra.i;
+        (void)mbar_wait(a_full + ra.i * 8, ra.phase);
       }
     }
   } else {
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(c_full);
         c_phase ^= 1u;
       }
-      if (!ok && any) {  // the products in flight end before tensor memory is given back
+      if (any) {  // the products in flight end before tensor memory is given back
         tc_commit(drain + h * 8);
         (void)mbar_wait(drain + h * 8, 0);
       }

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     flag_error(err, MOE_DEVERR_TIMEOUT);
   };
   auto wait = [&](uint32_t bar, uint32_t phase) {
-    if (ok && !mbar_wait(bar, phase)) failed();
+    if (ok && !mbar_wait(bar, phase, a.wait_ns)) failed();
     return ok;
   };
   auto wait_warp = [&](uint32_t bar, uint32_t phase) {
@@ -303,13 +303,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       Ring ra;
       int64_t asked = 0;
-      for (int64_t it = item0; it < items && ok; it += item_step) {
+      for (int64_t it = item0; it < items && ok && asked < a.stages; it += item_step) {
         const Item m = list.at(it, tiles);
         // rows past the expert's last output are another's, or past the tensor and zero:
         // their products are not stored
         const int r0 = m.e * M + m.tile * per_tile + rank * (per_tile / 2);
         const int r1 = SWIGLU ? r0 + a.N : r0 + kOuts / 2;
-        for (int kb = 0; kb < nblk; ++kb) {
+        const int end = a.stages - asked < nblk ? (int)(a.stages - asked) : nblk;
+        for (int kb = 0; kb < end; ++kb) {
           if (!wait(a_free + ra.i * 8, ra.phase ^ 1u)) break;
           const uint32_t bar = a_full + ra.i * 8, dst = sbase + L.a + (uint32_t)(ra.i * kABytes);
           const bool box_ok = MOE_DBG_OK(dst % 1024 == 0 && dst + kABytes <= sbase + L.b, err);
@@ -322,13 +323,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           ra.next<kStages>();
         }
       }
-      if (!ok) {
-        // what may still be on its way: the last stages, each waited for (bounded)
-        for (int i = 0; i < kStages && i < asked; ++i) {
-          if (ra.i == 0) ra.i = kStages, ra.phase ^= 1u;
-          --ra.i;
-          (void)mbar_wait(a_full + ra.i * 8, ra.phase);
-        }
+      // what may still be on its way, if another warp gave up: the last stages, each waited
+      // for (bounded)
+      for (int i = 0; i < kStages && i < asked; ++i) {
+        if (ra.i == 0) ra.i = kStages, ra.phase ^= 1u;
+        --ra.i;
+        (void)mbar_wait(a_full + ra.i * 8, ra.phase);
       }
     }
   } else if (rank == 0) {
@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc2_commit(c_full);
         c_phase ^= 1u;
       }
-      if (!ok && any) {  // the products in flight end before tensor memory is given back
-        tc2_commit(drain);
+      if (any) {  // the products in flight end before either CTA gives its memory back
+        tc2_commit_here(drain);
         (void)mbar_wait(drain, 0);
       }
     }

@@ -326,7 +326,7 @@ def sf_empty(rows: int, G: int, flags: int, ld: int | None, like: torch.Tensor, 
 
 
 PATH_AUTO, PATH_FUSED, PATH_SEPARATE, PATH_REPLICATED, PATH_CHAINED = 0, 1, 2, 3, 4
-DEBUG_WAIT_TIMEOUT_NS, DEBUG_SKIP_ROUTE_SIGNAL = 1, 2
+DEBUG_WAIT_TIMEOUT_NS, DEBUG_SKIP_ROUTE_SIGNAL, DEBUG_WEIGHT_STAGES = 1, 2, 3
 
 
 def route_expand_cast_workspace(T: int, E: int, k: int, like: torch.Tensor,

@@ -61,3 +61,31 @@ def test_scales_one_after_the_other(form, swiglu):
     tol = 16 * 2.0 ** -24 * mag + 2.0 ** -148 * (1 + up)
     assert (got[::3] == 0).all()
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
+
+
+@pytest.fixture
+def hooks():
+    yield ops.debug_set
+    ops.debug_set(ops.DEBUG_WEIGHT_STAGES, -1)
+    ops.debug_set(ops.DEBUG_WAIT_TIMEOUT_NS, 1_000_000_000)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("form", forms.FORMS)
+def test_waits_that_run_out_end_in_an_error(form, swiglu, hooks):
+    """Weights that no CTA asks for past its first stages: every warp's waits run out, the
+    copies and products in flight end, and the next call is right."""
+    p = forms.inputs(form, swiglu, sms(), 3)
+    want = run(p, swiglu, F32)
+    assert ops.device_status() == 0
+    hooks(ops.DEBUG_WAIT_TIMEOUT_NS, 2_000_000)
+    # none at all; fewer than a ring; fewer than, and more than, a tile's
+    for stages in (0, 1, 3, 4, 6, 11):
+        hooks(ops.DEBUG_WEIGHT_STAGES, stages)
+        if form == "cluster" and stages > 1:
+            continue                     # a CTA has one tile's share: two or five blocks
+        run(p, swiglu, F32)
+        assert ops.device_status() == ops.MOE_DEVERR_TIMEOUT, stages
+        hooks(ops.DEBUG_WEIGHT_STAGES, -1)
+        got = run(p, swiglu, F32)
+        assert ops.device_status() == 0 and torch.equal(got, want), stages
