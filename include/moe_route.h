@@ -817,6 +817,16 @@ moe_status_t moe_expert_matmul_int8(const int8_t *x, const float *x_sf, int64_t 
 #define MOE_DEBUG_WEIGHT_STAGES 3
 moe_status_t moe_debug_set(int32_t key, int64_t value);
 
+/* Which form of its kernel moe_expert_matmul_int8 takes on the current device for a call
+ * with these sizes and offsets given, for tests: a cluster of CTAs per tile, each with a
+ * part of the channels (few tiles); a CTA per tile; or a pair of CTAs per tile (more than
+ * 104 rows per expert, counting every row of out). */
+#define MOE_MATMUL_INT8_CLUSTER 1
+#define MOE_MATMUL_INT8_CTA 2
+#define MOE_MATMUL_INT8_PAIR 3
+moe_status_t moe_debug_matmul_int8_form(int32_t num_experts, int64_t num_rows, int32_t k_dim,
+                                        int32_t n_dim, int32_t swiglu, int32_t *form);
+
 /*
  * moe_debug_cvt -- the device's value conversions on arbitrary f32 input, for
  * tests: out[i] = the E4M3FN code (MOE_DEBUG_CVT_E4M3: round to nearest even,

@@ -484,4 +484,26 @@ moe_status_t moe_expert_matmul_int8(const int8_t* x, const float* x_sf, int64_t 
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
 
+moe_status_t moe_debug_matmul_int8_form(int32_t num_experts, int64_t num_rows, int32_t k_dim,
+                                        int32_t n_dim, int32_t swiglu, int32_t* form) {
+  if (num_experts < 1 || num_experts > MOE_MAX_EXPERTS || num_rows < 1 ||
+      num_rows >= ((int64_t)1 << 31) || k_dim < 16 || k_dim > 65536 || n_dim < 1 || !form)
+    return MOE_ERR_INVALID_ARG;
+  LaunchCtx c;
+  moe_status_t s = context(nullptr, &c);
+  if (s != MOE_OK) return s;
+  MatmulInt8Args a;
+  static const int32_t given = 0;
+  a.offsets = &given;  // not read: the form goes by the sizes
+  a.E = num_experts;
+  a.R = num_rows;
+  a.K = k_dim;
+  a.N = n_dim;
+  a.swiglu = swiglu ? 1 : 0;
+  int f = 0, ctas = 0;
+  cudaError_t e = expert_matmul_int8_form(c, a, &f, &ctas);
+  *form = f;
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
 }  // extern "C"

@@ -413,5 +413,8 @@ struct MatmulInt8Args {
   int64_t stages = INT64_MAX;
 };
 cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& a);
+// The form that it takes (MOE_MATMUL_INT8_*), by the sizes alone, and a cluster's CTAs.
+cudaError_t expert_matmul_int8_form(const LaunchCtx& c, const MatmulInt8Args& a, int* form,
+                                    int* ctas);
 
 }  // namespace moe

@@ -494,39 +494,54 @@ cudaError_t launch_t(const LaunchCtx& c, const MatmulInt8Args& a, int64_t groups
   return a.out_f32 ? launch_f<S, true>(c, a, groups, ctas) : launch_f<S, false>(c, a, groups, ctas);
 }
 
+using Whole = Shape<128, 4, 2, 2, false>;
+using Split = Shape<32, 4, 4, 3, true>;
+
+// Tiles times runs of at most nt rows, at most.
+int64_t items_at_most(const MatmulInt8Args& a, int nt) {
+  const int per_tile = a.swiglu ? kHalf : 2 * kHalf;
+  int64_t runs = (a.offsets ? a.E : 1) + (a.R + nt - 1) / nt - 1;
+  if (runs > a.R) runs = a.R;
+  return runs * ((a.N + per_tile - 1) / per_tile);
+}
+
 }  // namespace
 
-cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& a) {
-  using Whole = Shape<128, 4, 2, 2, false>;
-  using Split = Shape<32, 4, 4, 3, true>;
-  const int per_tile = a.swiglu ? kHalf : 2 * kHalf;
-  const int64_t tiles = (a.N + per_tile - 1) / per_tile;
-  auto items = [&](int nt) {
-    int64_t runs = (a.offsets ? a.E : 1) + (a.R + nt - 1) / nt - 1;
-    if (runs > a.R) runs = a.R;
-    return runs * tiles;
-  };
+cudaError_t expert_matmul_int8_form(const LaunchCtx& c, const MatmulInt8Args& a, int* form,
+                                    int* ctas) {
   // Few tiles: a cluster shares each one's channels, as long as all clusters run at once
   // (E = 1, one row, us, 1 : 2 : 4 : 8 CTAs per tile: K = N = 4096 28 : 18 : 12.4 : two
   // rounds 18; K = 7168, N = 256 46 : 27 : 16.6 : 11.7.  With tiles for 128 CTAs, 1 token
   // of 8 experts: 49 : two rounds 56 : 94 : 130).
   const int nblk = (a.K + kBlockK - 1) / kBlockK;
-  const int64_t split = items(Split::NT);
-  int ctas = 1;
+  const int64_t split = items_at_most(a, Split::NT);
+  *ctas = 1;
   for (int s = 2; s <= 8 && s <= nblk; s *= 2) {
     if (split * s > c.num_sms) break;
     int fit = 0;
     const cudaError_t e = clusters_at_once<Split>(c, s, &fit);
     if (e != cudaSuccess) return e;
-    if (split <= fit) ctas = s;
+    if (split <= fit) *ctas = s;
   }
-  if (ctas > 1) return launch_t<Split>(c, a, split, ctas);
   // Long runs of rows: a pair of CTAs per tile (us, one CTA : a pair; 256 experts, K = 7168,
   // SwiGLU of 2 x 2048: 64 rows per expert on average 1532 : 1720, 80 1621 : 1772, 128 2086 :
   // 1963, 256 3507 : 2850; one expert, K = N = 4096: 128 rows 22 : 22, 256 35 : 27; 16 experts
-  // of 1024 rows, K = N = 256: 17 : 19, its start counts).
-  if (a.R > 104 * (int64_t)a.E && a.K > 512) return launch_expert_matmul_int8_pair(c, a);
-  const int64_t whole = items(Whole::NT);
+  // of 1024 rows, K = N = 256: 17 : 19, its start counts).  The host knows the rows of out
+  // alone: rows that no expert has (a padded layout, a worst-case buffer) count as its rows.
+  *form = *ctas > 1                                ? MOE_MATMUL_INT8_CLUSTER
+          : a.R > 104 * (int64_t)a.E && a.K > 512 ? MOE_MATMUL_INT8_PAIR
+                                                   : MOE_MATMUL_INT8_CTA;
+  return cudaSuccess;
+}
+
+cudaError_t launch_expert_matmul_int8(const LaunchCtx& c, const MatmulInt8Args& a) {
+  int form = 0, ctas = 1;
+  const cudaError_t e = expert_matmul_int8_form(c, a, &form, &ctas);
+  if (e != cudaSuccess) return e;
+  if (form == MOE_MATMUL_INT8_CLUSTER)
+    return launch_t<Split>(c, a, items_at_most(a, Split::NT), ctas);
+  if (form == MOE_MATMUL_INT8_PAIR) return launch_expert_matmul_int8_pair(c, a);
+  const int64_t whole = items_at_most(a, Whole::NT);
   return launch_t<Whole>(c, a, whole < c.num_sms ? whole : c.num_sms, 1);
 }
 

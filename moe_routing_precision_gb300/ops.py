@@ -59,6 +59,8 @@ SIGNATURES = {
                                                  _P]),
     "moe_route_expand_cast_fp8_workspace_bytes": (ctypes.c_size_t, [_i64, _i32, _i32]),
     "moe_debug_set": (ctypes.c_int, [_i32, _i64]),
+    "moe_debug_matmul_int8_form": (ctypes.c_int, [_i32, _i64, _i32, _i32, _i32,
+                                                  ctypes.POINTER(_i32)]),
     "moe_debug_cvt": (ctypes.c_int, [_i32, _P, _P, _i64, _P]),
     "swiglu_cast_fp8_ex": (ctypes.c_int, [_P, _i64, _i32, _P, _P, ctypes.c_uint32, _i64, _i32,
                                           ctypes.c_float, _P, _P, _i32, _P]),
@@ -381,6 +383,15 @@ def debug_cvt(values: torch.Tensor, fmt: int, out=None, stream=None) -> torch.Te
 
 def debug_set(key: int, value: int) -> None:
     _check(lib().moe_debug_set(key, int(value)), "moe_debug_set")
+
+
+def debug_matmul_int8_form(E: int, R: int, K: int, N: int, swiglu: bool) -> str:
+    """Which form of its kernel expert_matmul_int8 takes on the current device, for tests:
+    "cluster", "cta" or "pair" (of CTAs per tile)."""
+    form = ctypes.c_int32()
+    _check(lib().moe_debug_matmul_int8_form(E, R, K, N, int(swiglu), ctypes.byref(form)),
+           "moe_debug_matmul_int8_form")
+    return ("cluster", "cta", "pair")[form.value - 1]
 
 
 def expand_cast_fp8_ex_workspace_bytes(T: int, H: int, sf_flags: int) -> int:
@@ -1068,7 +1079,7 @@ def launch_count() -> int:
 __all__ = ["lib", "MoeError", "topk_gate", "route_map", "route_map_workspace_bytes",
            "route_map_aligned", "expand_cast_fp8_padded", "expand_cast_fp8_ex",
            "expand_cast_fp8_ex_workspace_bytes", "swiglu_cast_fp8_ex", "sf_empty",
-           "route_expand_cast_fp8", "route_expand_cast_workspace", "debug_set", "debug_cvt", "expand_cast_fp4", "swiglu_cast_fp4",
+           "route_expand_cast_fp8", "route_expand_cast_workspace", "debug_set", "debug_matmul_int8_form", "debug_cvt", "expand_cast_fp4", "swiglu_cast_fp4",
            "expand_cast_fp8", "swiglu_cast_fp8", "combine", "peak_copy", "device_status",
            "launch_count", "SIGNATURES", "block_norm", "block_norm_backward",
            "block_norm_backward_workspace_bytes", "balance_loss", "balance_loss_backward",

@@ -16,7 +16,7 @@ def outputs(tiles, swiglu):
 
 
 def shape(form, swiglu, sms):
-    """-> offsets (list), K, N."""
+    """-> offsets (list), K, N.  K ends inside a block of 128 channels."""
     if form == "cluster":      # two runs x tiles, at least two CTAs for each
         return [0, 0, 5, 5, 13], 1040, outputs(max(1, sms // 32), swiglu)
     if form == "cta":          # 7 experts with rows, of at most 104 on average
@@ -26,9 +26,10 @@ def shape(form, swiglu, sms):
     return ends, 784, outputs(sms * 3 // 16, swiglu)      # 7 blocks, the last of 16 channels
 
 
-def inputs(form, swiglu, sms, seed, lim=40, extra=0):
+def inputs(form, swiglu, sms, seed, lim=40, extra=0, K=None):
     """x, x_sf, w, w_sf, offsets with `extra` rows behind the last expert's."""
-    ends, K, N = shape(form, swiglu, sms)
+    ends, k, N = shape(form, swiglu, sms)
+    K = k if K is None else K
     r = torch.Generator().manual_seed(seed)
     E, M, R = len(ends) - 1, N * (2 if swiglu else 1), ends[-1] + extra
 
