@@ -715,7 +715,8 @@ moe_status_t moe_expert_matvec_fp4(const void *x, int64_t num_x, const uint8_t *
  * comes last); the topk_groups first stay.  Of their experts the k with the largest
  * c are selected, in descending order; experts with a score of -inf come last.
  * Equal values go to the lower group and the lower expert.  Values are compared as
- * real numbers: in f32, and in f64 where f32 cannot tell them apart.
+ * real numbers: in f32, and in f64 where f32 cannot tell them apart (also where the two
+ * largest of a group nearly cancel, by biases of both signs).
  *   topk_weights[t,j] = scale * s_j / sum_j' s_j'     (renormalize; 0 if the sum is 0)
  *                       scale * s_j                   (otherwise)
  * with s_j the score of the j-th selected expert: the bias decides the selection
@@ -743,8 +744,7 @@ moe_status_t moe_router_gate(const float *scores, int64_t num_tokens, int32_t nu
  *                grad_scores[t,e'] = s_e' (scale g_j [e' = e] - scale sum_j' g_j' s_j')
  *                                    for every expert e'               (softmax)
  * and 0 elsewhere; with add, that is added to add's entry (moe_balance_loss_backward's
- * gradient, say).
- * (an expert that a token names twice gets both gradients).
+ * gradient, say).  An expert that a token names twice gets both gradients.
  *   scores [T,E] f32 as above; topk_idx [T,k] i32; grad_topk_weights [T,k] f32;
  *   add [T,E] f32, may be NULL
  *   grad_scores [T,E] f32 out; may be add itself (in place)
@@ -795,6 +795,9 @@ moe_status_t moe_cast_int8(const void *x, int32_t dtype, int64_t num_rows, int32
  * MOE_DEVERR_POS_RANGE; such rows are not written, or are zero.  Every wait inside the
  * kernel is bounded (1 s); one that runs out sets MOE_DEVERR_TIMEOUT, and the kernel ends
  * once its copies and products in flight have (out is then unspecified).
+ * The kernel's form goes by num_rows, as the host does not know the experts' rows: with far
+ * more rows in the buffer than experts have (padding, a buffer for the worst case), a form
+ * for longer runs is taken than theirs.
  */
 moe_status_t moe_expert_matmul_int8(const int8_t *x, const float *x_sf, int64_t num_x,
                                     const int8_t *w, const float *w_sf, const int32_t *offsets,

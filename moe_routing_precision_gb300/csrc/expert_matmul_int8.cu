@@ -23,8 +23,9 @@
 //          top 8 of 256, K = 2048, N = 7168)
 // Measured: 64 tokens, top 8 of 256, K = 7168, SwiGLU of 2 x 2048 (6.5 GB): 939 us, 6.9
 // TB/s, and K = 2048, N = 7168 (3.3 GB) 510 us: HBM bounds them.  One token: 49 us for 235
-// MB: 5 us until the first weights are there, then 5.5 TB/s; smaller tiles, one for each of
-// 152 SMs, or six stages of weights were no faster.  16 converting warps in two sets were
+// MB, which a kernel that only reads them takes 45 us for (5.3 TB/s; the rate for so few bytes
+// bounds it, then the 5 us until the first weights are there and their conversion); smaller
+// tiles, one for each of 152 SMs, or six stages of weights were no faster.  16 converting warps in two sets were
 // slower for long runs (308 : 336 us), as were tiles of 32, 64 or 96 rows (no faster for few
 // rows).  Long runs: expert_matmul_int8_pair.cu.
 #include "block/matmul_int8.cuh"

@@ -8,12 +8,12 @@
 // their shared memory, half in each: a product is 256 x 256 x 16 in 128 clocks, every
 // converted value feeds 256 others, and one thread of the pair issues 8 products per wait.
 //
-// Measured: 4096 rows, K = N = 7168: 216 us, 1.95 PFLOP/s, as fast as the measured rate of
+// Measured: 4096 rows, K = N = 7168: 218 us, 1.93 PFLOP/s, as fast as the measured rate of
 // a library's f16 product (1.89); 8192 tokens, top 8 of 256, K = 7168, SwiGLU of 2 x 2048:
-// 2850 us, 1.35 PFLOP/s (runs of 150 to 450 rows do not fill tiles of 256, and a stage of
-// few rows takes as long as its weights' conversion, 950 clocks); the down products, K =
-// 2048, N = 7168: 1590 us, 1.2 PFLOP/s (also the tile's end: its sums are read before the
-// next tile's products may begin).
+// 2820 us, 1.36 PFLOP/s, and 2985 us once the power limit is reached (1950 MHz of 2070).  An expert's 257 to 400 rows are two runs, each of whose stages takes as
+// long as its weights' conversion, 950 clocks, and not the products' 520 to 800.  The down
+// products, K = 2048, N = 7168: 1600 us, 1.2 PFLOP/s (also the tile's end: its sums are read
+// before the next tile's products may begin).
 //
 // Warps 0-7 convert the weights (a thread per weight row), 8-15 write finished tiles out,
 // 16-23 gather and convert rows; the converting and the gathering warps are two sets of 4

@@ -31,12 +31,15 @@ constexpr int kLanesFrom = 12, kLaneWarps = 4, kLaneBlocks = 4;
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 
-// |f32 c - c| <= score_err + 2^-23 |c|.  Both forms take 2^y and 1 / y from the hardware
-// estimates (2 ulp and 1 ulp).
+// A difference of two f32 c is off by at most 2 score_err + 2^-23 (|c| + |c'|).  Both forms
+// take 2^y and 1 / y from the hardware estimates (2 ulp and 1 ulp).
 // Sigmoid: e = 2^(-x log2 e) is off by (3 |x| + 4) 2^-24 e, which moves s by less than
 // s (1 - s) times that, under 2^-23; the sum and the estimate of its inverse add 3 * 2^-24.
-// Softmax: e = 2^((x - max) log2 e) in the same way, |x - max| e^(x - max) < 0.37, relative
-// to the largest score; the sum of 1024 terms and its inverse add 2^-20 of s.
+// Softmax: e = 2^((x - max) log2 e) in the same way, |x - max| e^(x - max) < 0.37: within
+// 5.1 * 2^-24 of the largest score for each.  The sum of 1024 terms (at most 36 roundings in
+// sequence), the terms' own errors and the inverse put all scores of a row off by one factor,
+// within 43 * 2^-24, and so the difference of two by that part of the largest: 54 * 2^-24 in
+// all, against 64 * 2^-24.
 __device__ __forceinline__ float score_err(int func, float top) {
   return func == MOE_SCORE_SIGMOID ? 0x1p-21f : 0x1p-19f * top;
 }
@@ -422,9 +425,11 @@ constexpr int kByX = 0, kSigmoid = 1, kSoftmax = 2;
 //
 // For few tokens, for selections by x, and for numbers of experts and groups that
 // router_gate_lanes_kernel does not divide.  65536 tokens, 8 of 256 experts (67 MB; us):
-// by x alone 26; sigmoid and bias 42; with 8 groups 50.  Instruction issue bounds it, 640
-// per token and 70 % of the slots.  A border decided in f64 costs its warp 1.2 us for
-// experts and 3 us for groups.  Asking for a row ahead was slower.
+// by x alone 26; sigmoid and bias 42; with 8 groups 50 (640 instructions per token, 70 % of
+// the issue slots; the rest waits in one token's chain of reductions).  k = 32: 373, for k
+// rounds of reductions, and as many again where there are more than 32 candidates.  A
+// border decided in f64 costs its warp 1.2 us for experts and 3 us for groups.  Asking for a
+// row ahead was slower.
 template <int V, bool VEC, int KFIX, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 4 : V <= 16 ? 2 : 1)
     router_gate_kernel(const RouterArgs a) {
@@ -756,17 +761,18 @@ struct TokenScratch {
 };
 
 // E = L V experts by L lanes per token, 32 / L tokens per warp, each lane V consecutive
-// experts and S candidates; groups are runs of whole lanes (L % G == 0); k <= L, a bias.  What a token takes
-// beyond its scores, the groups' ranks, the bound of the k-th value, the candidates' ranks
-// and the weights, serves all tokens of the warp.  Rows come by coalesced asynchronous
+// experts and S candidates; groups are runs of whole lanes (L % G == 0); k <= L; a bias, or
+// groups by the sum of two.  What a token takes beyond its scores, the groups' ranks, the
+// bound of the k-th value, the candidates' ranks and the weights, serves all tokens of the
+// warp.  Rows come by coalesced asynchronous
 // copies into shared memory, each lane's run padded so that reading 16 bytes per lane
 // meets no bank twice, and the next rows are asked for once the candidates' x is taken.
 //
 // 65536 tokens, 8 of 256 experts, sigmoid and bias: 8 groups 30 us (router_gate_kernel:
-// 50), one group 26 (42); 322 instructions per token against 640, 60 % of the issue slots
-// with 16 warps per SM.  80 registers and 24 warps were slower (34: spills).  Below about
-// 12 tokens per SM a token per warp is as fast or faster (1024 tokens 4.3 against 5.1 us,
-// 4096 9.9 against 8.2).  Nearly equal borders, one token in a thousand, are decided in
+// 50), one group 26 (42); 322 instructions per token against 640, 60 % of the issue slots:
+// 18 us of issue, and latency that 16 warps per SM do not cover.  80 registers and 24 warps
+// were slower (34: spills).  Below about 12 tokens per SM a token per warp is as fast or
+// faster (1024 tokens 4.3 against 5.1 us, 4096 9.9 against 8.2).  Nearly equal borders, one token in a thousand, are decided in
 // f64 by the whole warp where they are met.
 template <int L, int V, int MODE>
 __global__ void __launch_bounds__(kLaneWarps * 32, kLaneBlocks)
