@@ -10,10 +10,11 @@
 //
 // Measured: 4096 rows, K = N = 7168: 218 us, 1.93 PFLOP/s, as fast as the measured rate of
 // a library's f16 product (1.89); 8192 tokens, top 8 of 256, K = 7168, SwiGLU of 2 x 2048:
-// 2820 us, 1.36 PFLOP/s, and 2985 us once the power limit is reached (1950 MHz of 2070).  An expert's 257 to 400 rows are two runs, each of whose stages takes as
-// long as its weights' conversion, 950 clocks, and not the products' 520 to 800.  The down
-// products, K = 2048, N = 7168: 1600 us, 1.2 PFLOP/s (also the tile's end: its sums are read
-// before the next tile's products may begin).
+// 2820 us, 1.36 PFLOP/s, and 2985 us once the power limit is reached (1950 MHz of 2070).  An
+// expert's 257 to 400 rows are two runs, each of whose stages takes as long as its weights'
+// conversion, 950 clocks, and not the products' 520 to 800.  The down products, K = 2048,
+// N = 7168: 1600 us, 1.2 PFLOP/s (also the tile's end: its sums are read before the next
+// tile's products may begin).
 //
 // Warps 0-7 convert the weights (a thread per weight row), 8-15 write finished tiles out,
 // 16-23 gather and convert rows; the converting and the gathering warps are two sets of 4
